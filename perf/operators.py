@@ -1,0 +1,497 @@
+"""The 4-bit KV cache and the eviction operators, as cases that can be timed and compared.
+
+Four operators, each in a plain form (elementary torch operations in 32 bits,
+rounded once) and through the library's entry points (``own``):
+
+* ``write``    new K/V rows quantised into the 4-bit paged cache and read back;
+* ``decode``   attention of one or several new tokens over the 4-bit cache;
+* ``weights``  the attention weight that the new tokens give to every cached
+               token, summed over query heads (bf16, 8-bit and 4-bit K);
+* ``evict``    the tokens to keep under a budget, chosen by accumulated weight,
+               and the move of their rows into the sequence's kept blocks; with
+               ``then_decode`` on the 4-bit cache, followed by the step's decode.
+
+4-bit format: a (block, KV head) tile holds, after each other, E2M1 codes
+[block_size][dim/2] (element 2i in the low nibble of byte i) and E4M3 group
+scales [block_size][dim/16]; value = code * group scale * scale[KV head].
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+KV_BYTES = {"bf16": 2.0, "fp8": 1.0, "fp4": 9.0 / 16.0}
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def _case(name, op, batch, hq, hkv, dim, bs, lo, hi, kv="fp4", q=1, budget=0, recent=0,
+          accumulate=False, then_decode=False):
+    c = dict(op=op, batch=batch, hq=hq, hkv=hkv, dim=dim, bs=bs, lo=lo, hi=hi, kv=kv, q=q,
+             budget=budget, recent=recent, accumulate=accumulate, then_decode=then_decode)
+    return dict(c, name=name) if name else c
+
+
+def listed():
+    return [
+        # the KV write of one decode step of an 8B-class layer, 64 sequences: latency
+        _case("write_step_b64", "write", 64, 32, 8, 128, 16, 1, 1),
+        # a prefill chunk of four prompts written at once, odd lengths
+        _case("write_prompts", "write", 4, 32, 8, 128, 16, 1531, 2047),
+        # the smallest decode: four short sequences, one KV head, head dim 64
+        _case("decode_tiny", "decode", 4, 4, 1, 64, 16, 1, 33),
+        # one decode step of an 8B-class layer, ragged lengths
+        _case("decode_8b_b64", "decode", 64, 32, 8, 128, 16, 128, 2048),
+        # long contexts of a 70B-class layer: the largest cache
+        _case("decode_70b_b32", "decode", 32, 64, 8, 128, 16, 8192, 32768),
+        # four new tokens a sequence over 32-token blocks
+        _case("decode_q4_b16", "decode", 16, 32, 8, 128, 32, 1001, 9001, q=4),
+        # the weights of one step on a small 8-bit cache, 8-token blocks, three new tokens
+        _case("weights_small_fp8", "weights", 3, 16, 8, 64, 8, 37, 301, kv="fp8", q=3,
+              accumulate=True),
+        # the weights of one step of an 8B-class layer, bf16 cache
+        _case("weights_8b_b64", "weights", 64, 32, 8, 128, 16, 128, 2048, kv="bf16"),
+        # the same for long contexts on the 4-bit cache of a 70B-class layer
+        _case("weights_70b_b8_fp4", "weights", 8, 64, 8, 128, 16, 8192, 32768),
+        # every sequence of an 8B-class batch cut to at most 512 tokens
+        _case("evict_8b_b64", "evict", 64, 32, 8, 128, 16, 128, 2048, kv="bf16", budget=512,
+              recent=64),
+        # a few long contexts cut to 4,096 tokens
+        _case("evict_70b_b8", "evict", 8, 64, 8, 128, 16, 8192, 32768, kv="bf16", budget=4096,
+              recent=256),
+        # one sequence over its budget by a little, then its decode step: latency
+        _case("evict_decode_fp4", "evict", 1, 32, 8, 128, 16, 1061, 1061, budget=1024, recent=33,
+              then_decode=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "decode", "decode", "weights", "evict"])
+    hkv = rng.choice([1, 2, 4, 8])
+    hq = hkv * rng.choice([1, 2, 4, 8])
+    dim, bs = rng.choice([64, 128]), rng.choice([8, 16, 32])
+    if op == "write":
+        batch = _log(rng, 1, 64)
+        hi = _log(rng, 1, 8192 // batch)
+        return _case(None, op, batch, hq, hkv, dim, bs, max(1, hi // 2), hi)
+    hi = _log(rng, 2, 32768)
+    batch = max(1, min(_log(rng, 1, 256), (80000 if op == "evict" else 200000) // hi))
+    lo = rng.randint(1, hi)
+    if op == "decode":
+        return _case(None, op, batch, hq, hkv, dim, bs, lo, hi, q=rng.randint(1, min(lo, 8)))
+    if op == "weights":
+        return _case(None, op, batch, hq, hkv, dim, bs, lo, hi,
+                     kv=rng.choice(["bf16", "fp8", "fp4"]), q=rng.randint(1, min(lo, 4)),
+                     accumulate=rng.random() < 0.5)
+    budget = _log(rng, 1, hi)
+    then = rng.random() < 0.5
+    return _case(None, op, batch, hq, hkv, dim, bs, lo, hi, kv="fp4" if then else "bf16",
+                 budget=budget, recent=rng.randint(0, budget), then_decode=then)
+
+
+def _lens(c):
+    """The case's lengths: uniform in [lo, hi], drawn from its sizes alone."""
+    r = random.Random("%(op)s %(batch)d %(hq)d %(hkv)d %(dim)d %(bs)d %(lo)d %(hi)d" % c)
+    return [r.randint(c["lo"], c["hi"]) for _ in range(c["batch"])]
+
+
+def work(c):
+    lens, hkv, dim, q = _lens(c), c["hkv"], c["dim"], c["q"]
+    tok, row = sum(lens), hkv * dim
+    rows = 2 * c["batch"] * q * c["hq"] * dim  # bytes of q, or of out
+    tables = 4 * sum(-(-n // c["bs"]) for n in lens) + 4 * c["batch"]
+    if c["op"] == "write":  # the rows read, the cache rows written and read, the values written
+        return {"bytes": 2 * tok * row * (2 + KV_BYTES["fp4"]) * 2 + 16 * tok, "flops": 0}
+    if c["op"] == "decode":
+        return {"bytes": 2 * tok * row * KV_BYTES["fp4"] + 2 * rows + tables,
+                "flops": 4 * tok * c["hq"] * dim * q}
+    if c["op"] == "weights":
+        return {"bytes": tok * row * KV_BYTES[c["kv"]] + rows + tables
+                + tok * (8 if c["accumulate"] else 4), "flops": 2 * tok * c["hq"] * dim * q}
+    kept = sum(min(n, c["budget"]) for n in lens)
+    moved = 2 * kept * row * KV_BYTES[c["kv"]]
+    b = {"bytes": 4 * tok + 4 * kept + 2 * moved + tables, "flops": 0}
+    if c["then_decode"]:
+        b = {"bytes": b["bytes"] + moved + 2 * rows, "flops": 4 * kept * c["hq"] * dim}
+    return b
+
+
+# ---------------------------------------------------------------- inputs
+
+
+def _e2m1(a):
+    """E2M1 code (0..7) of a magnitude, to nearest, ties to even codes, saturating."""
+    up = [(a > 0.25), (a >= 0.75), (a > 1.25), (a >= 1.75), (a > 2.5), (a >= 3.5), (a > 5.0)]
+    return sum(u.to(torch.uint8) for u in up)
+
+
+def _quantise(x, s):
+    """Rows x [..., heads, dim] -> (sign and code as uint8 nibbles, group scales float32)."""
+    g = x.float().unflatten(-1, (-1, 16))
+    s = s.view(-1, 1)
+    sf = (g.abs().amax(-1) / (6.0 * s)).clamp(max=448.0).to(torch.float8_e4m3fn).float()
+    step = (sf * s).unsqueeze(-1)
+    a = torch.where(step > 0, g.abs() / step, torch.zeros_like(g))
+    code = _e2m1(a) | (torch.signbit(g).to(torch.uint8) << 3)
+    return code.flatten(-2), sf
+
+
+def _lut(device, dtype=torch.float32):
+    v = torch.tensor(E2M1, dtype=dtype, device=device)
+    return torch.cat([v, -v])
+
+
+def _pack(code, sf, nb, hkv, bs, dim):
+    """Codes and scales of nb * bs token rows as 4-bit cache tiles (uint8)."""
+    c = code.view(nb, bs, hkv, dim // 2, 2).transpose(1, 2)
+    c = (c[..., 0] | (c[..., 1] << 4)).reshape(nb, hkv, bs * dim // 2)
+    f = sf.to(torch.float8_e4m3fn).view(torch.uint8).view(nb, bs, hkv, dim // 16).transpose(1, 2)
+    return torch.cat([c, f.reshape(nb, hkv, bs * dim // 16)], -1).view(nb, hkv, bs, -1)
+
+
+def _normal(shape, g, dev, spread=None):
+    x = torch.randn(shape, generator=g, device=dev)
+    if spread is not None:
+        x = x * spread
+    return x.to(torch.bfloat16)
+
+
+def _cache(c, nb, s, g, dev):
+    """One cache of nb blocks of N(0, 1) rows in the case's type. Keys and values of real
+    layers have a few large channels: every 16th channel is four times as wide."""
+    hkv, bs, dim = c["hkv"], c["bs"], c["dim"]
+    spread = torch.ones(dim, device=dev)
+    spread[5::16] = 4.0 if c["kv"] == "fp4" else 1.0
+    out = []
+    per = max(1, (1 << 25) // (bs * hkv * dim))
+    for at in range(0, nb, per):
+        n = min(per, nb - at)
+        x = _normal((n * bs, hkv, dim), g, dev, spread)
+        if c["kv"] == "fp4":
+            out.append(_pack(*_quantise(x, s), n, hkv, bs, dim))
+        else:
+            x = x.view(n, bs, hkv, dim).transpose(1, 2).contiguous()
+            if c["kv"] == "fp8":
+                x = (x.float() / s.view(-1, 1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+                x = x.view(torch.uint8)
+            out.append(x)
+    return torch.cat(out)
+
+
+def prepare(c, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    lens = _lens(c)
+    batch, hq, hkv, dim, bs, q = (c[k] for k in ("batch", "hq", "hkv", "dim", "bs", "q"))
+    blocks = [-(-n // bs) for n in lens]
+    kept = [-(-min(n, c["budget"]) // bs) for n in lens]  # the blocks that eviction fills
+    need = sum(blocks) + sum(kept)
+    nb = int(math.ceil(1.25 * need)) if c["op"] != "evict" else need
+    order = torch.randperm(nb, generator=g, device=dev).to(torch.int32)
+
+    def tables(counts, first):
+        t = torch.full((batch, max(max(counts), 1)), -1, dtype=torch.int32, device=dev)
+        for b, n in enumerate(counts):
+            t[b, :n] = order[first:first + n]
+            first += n
+        return t
+
+    def scales(base):
+        return base * torch.exp(torch.rand(hkv, generator=g, device=dev) - 0.5)
+
+    s = dict(c, hi_len=max(lens), ks=scales(0.05), vs=scales(0.03), tables=tables(blocks, 0),
+             lens=torch.tensor(lens, dtype=torch.int32, device=dev), scale=1.0 / math.sqrt(dim),
+             max_blocks=max(blocks))
+    if c["op"] == "write":
+        tok = sum(lens)
+        spread = torch.ones(dim, device=dev)
+        spread[5::16] = 4.0
+        s["k_new"], s["v_new"] = (_normal((tok, hkv, dim), g, dev, spread) for _ in range(2))
+        at = torch.cat([torch.arange(n, device=dev) + b * s["max_blocks"] * bs
+                        for b, n in enumerate(lens)])
+        s["slots"] = s["tables"].flatten()[at // bs].long() * bs + at % bs
+        tile = (nb, hkv, bs, dim * 9 // 16)
+        s["k_cache"], s["v_cache"] = (torch.zeros(tile, dtype=torch.uint8, device=dev)
+                                      for _ in range(2))
+        return s
+    s["q_rows"] = _normal((batch, q, hq, dim) if q > 1 else (batch, hq, dim), g, dev)
+    s["k_cache"] = _cache(c, nb, s["ks"], g, dev)
+    if c["op"] != "weights":
+        s["v_cache"] = _cache(c, nb, s["vs"], g, dev)
+    if c["op"] == "weights":
+        # what earlier steps left there: about as much as one step adds
+        s["token_weights"] = torch.rand((batch, s["hi_len"] + 3), generator=g, device=dev)
+        s["token_weights"] *= 2.0 * hq * q / s["hi_len"]
+    if c["op"] == "evict":
+        s["dst"] = tables(kept, sum(blocks))
+        # accumulated weights fall off steeply and repeat: many tokens share the lowest values
+        w = torch.rand((batch, s["hi_len"] + 3), generator=g, device=dev).pow_(6)
+        s["token_weights"] = torch.where(w < 0.01, (w * 1000).round() / 1000, w)
+    if own:
+        import paged_kv_cache_92_gb300 as pk
+        pk.load()
+        s["pk"] = pk
+        hold = c["op"] == "decode" or c["then_decode"]
+        tab = s["dst"] if c["op"] == "evict" else s["tables"]
+        most = min(s["hi_len"], c["budget"]) if c["op"] == "evict" else s["hi_len"]
+        if hold:
+            s["out"] = torch.empty_like(s["q_rows"])
+            p = pk.make_decode_params(s["q_rows"], s["out"], s["k_cache"], s["v_cache"], tab,
+                                      s["lens"], most, s["scale"], k_scale=s["ks"],
+                                      v_scale=s["vs"])
+            n = pk.pa_decode_workspace_size(p)
+            s["workspace"] = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        if c["op"] == "weights":
+            n = pk.pa_token_weights_workspace_size(
+                s["q_rows"], s["k_cache"], s["tables"], s["lens"], s["hi_len"],
+                s["token_weights"], k_scale=s["ks"] if c["kv"] != "bf16" else None)
+            s["workspace"] = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+
+
+def _values(tiles, s, bs, dim):
+    """4-bit tiles [..., heads, bs, dim * 9/16] -> float32 values [..., heads, bs, dim]."""
+    flat = tiles.flatten(-2)
+    codes, f = flat.split([bs * dim // 2, bs * dim // 16], -1)
+    codes = codes.unflatten(-1, (bs, dim // 2))
+    f = f.contiguous().view(torch.float8_e4m3fn).float().unflatten(-1, (bs, dim // 16, 1))
+    v = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
+    v = _lut(tiles.device)[v.int()].unflatten(-1, (-1, 16)) * f
+    return v.flatten(-2) * s.view(-1, 1, 1)
+
+
+def _rows(s, which, tables):
+    """The cached rows of every sequence: float32 [batch, heads, tokens, dim]."""
+    cache, sc = s[which + "_cache"], s["ks" if which == "k" else "vs"]
+    tiles = cache[tables.clamp(min=0).long()]  # [batch, blocks, heads, bs, ...]
+    if s["kv"] == "fp4":
+        v = _values(tiles, sc, s["bs"], s["dim"])
+    elif s["kv"] == "fp8":
+        v = tiles.view(torch.float8_e4m3fn).float() * sc.view(-1, 1, 1)
+    else:
+        v = tiles.float()
+    return v.transpose(1, 2).flatten(2, 3)
+
+
+def _softmax_rows(s, k, lens):
+    """exp(score - max) and their sums: [batch, kv heads, group * q, tokens]."""
+    batch, hq, hkv, q = s["batch"], s["hq"], s["hkv"], s["q"]
+    rows = s["q_rows"].view(batch, q, hkv, hq // hkv, -1).permute(0, 2, 3, 1, 4).flatten(2, 3)
+    sc = (rows.float() * s["scale"]) @ k.transpose(-1, -2)
+    t = torch.arange(k.shape[2], device=k.device)
+    last = lens.long().view(-1, 1, 1) - q + torch.arange(q, device=k.device).view(1, -1, 1)
+    seen = (t.view(1, 1, -1) <= last).repeat(1, hq // hkv, 1).unsqueeze(1)
+    sc = torch.where(seen, sc, torch.full_like(sc, -math.inf))
+    p = torch.exp(sc - sc.amax(-1, keepdim=True).clamp(min=-1e30))
+    p = torch.where(seen, p, torch.zeros_like(p))
+    return p, p.sum(-1, keepdim=True)
+
+
+def _plain_decode(s, tables, lens):
+    p, l = _softmax_rows(s, _rows(s, "k", tables), lens)
+    v = _rows(s, "v", tables)
+    inside = torch.arange(v.shape[2], device=v.device) < lens.long().view(-1, 1, 1)
+    v = torch.where(inside.unsqueeze(-1), v, torch.zeros_like(v))
+    o = (p @ v) / l.clamp(min=1e-30)
+    o = o.unflatten(2, (-1, s["q"])).permute(0, 3, 1, 2, 4).flatten(2, 3)
+    return o.to(torch.bfloat16).view(s["q_rows"].shape)
+
+
+def _plain_select(s):
+    w, lens = s["token_weights"], s["lens"].long().view(-1, 1)
+    t = torch.arange(w.shape[1], device=w.device).view(1, -1)
+    key = torch.where(t >= lens - s["recent"], torch.full_like(w, math.inf), w)
+    key = torch.where(t < lens, key, torch.full_like(w, -math.inf))
+    best = torch.sort(key, dim=1, descending=True, stable=True)[1]
+    room = min(s["budget"], w.shape[1])
+    n = lens.clamp(max=s["budget"])
+    rank = torch.arange(room, device=w.device).view(1, -1)
+    kept = torch.where(rank < n, best[:, :room], torch.full_like(best[:, :room], 1 << 30))
+    kept = torch.sort(kept, dim=1)[0]
+    keep = torch.full((w.shape[0], s["budget"]), -1, dtype=torch.int32, device=w.device)
+    keep[:, :room] = torch.where(rank < n, kept, torch.full_like(kept, -1)).int()
+    return keep, n.flatten().int()
+
+
+def _plain_move(s, keep):
+    bs, dim = s["bs"], s["dim"]
+    b, j = (keep >= 0).nonzero(as_tuple=True)
+    t = keep[b, j].long()
+    src, dst = s["tables"][b, t // bs].long(), s["dst"][b, j // bs].long()
+    a, z = t % bs, j % bs
+    k, v = s["k_cache"], s["v_cache"]
+    if s["kv"] == "bf16":
+        k[dst, :, z], v[dst, :, z] = k[src, :, a], v[src, :, a]
+        return
+    cut = bs * dim // 2
+    parts = [x.flatten(2)[..., i:e].unflatten(-1, (bs, -1)) for x in (k, v)
+             for i, e in ((0, cut), (cut, None))]
+    for x in parts:
+        x[dst, :, z] = x[src, :, a]
+
+
+def run(s):
+    op = s["op"]
+    if own:
+        pk = s["pk"]
+        if op == "write":
+            pk.pa_reshape_and_cache_fp4(s["k_new"], s["v_new"], s["k_cache"], s["v_cache"],
+                                        s["slots"], s["ks"], s["vs"])
+            return pk.pa_gather_fp4(s["k_cache"], s["v_cache"], s["slots"], s["ks"], s["vs"])
+        if op == "decode":
+            return pk.pa_decode(s["q_rows"], s["k_cache"], s["v_cache"], s["tables"], s["lens"],
+                                s["hi_len"], s["scale"], out=s["out"], workspace=s["workspace"],
+                                k_scale=s["ks"], v_scale=s["vs"])
+        if op == "weights":
+            w = s["token_weights"].clone() if s["accumulate"] else s["token_weights"]
+            return pk.pa_token_weights(s["q_rows"], s["k_cache"], s["tables"], s["lens"],
+                                       s["hi_len"], w, accumulate=s["accumulate"],
+                                       scale=s["scale"], workspace=s["workspace"],
+                                       k_scale=s["ks"] if s["kv"] != "bf16" else None)
+        keep, n = pk.pa_evict_select(s["token_weights"], s["lens"], s["budget"], s["recent"])
+        pk.pa_evict_compact(s["k_cache"], s["v_cache"], s["tables"], s["dst"], keep, n)
+        if not s["then_decode"]:
+            return keep, n, s["k_cache"], s["v_cache"]
+        out = pk.pa_decode(s["q_rows"], s["k_cache"], s["v_cache"], s["dst"], n,
+                           min(s["hi_len"], s["budget"]), s["scale"], out=s["out"],
+                           workspace=s["workspace"], k_scale=s["ks"], v_scale=s["vs"])
+        return keep, n, out
+    if op == "write":
+        got = []
+        lut = _lut(s["k_new"].device)
+        for x, sc in ((s["k_new"], s["ks"]), (s["v_new"], s["vs"])):
+            code, sf = _quantise(x, sc)
+            v = lut[code.int()].unflatten(-1, (-1, 16)) * sf.unsqueeze(-1)
+            got.append((v.flatten(-2) * sc.view(-1, 1)).to(torch.bfloat16))
+        return tuple(got)
+    if op == "decode":
+        return _plain_decode(s, s["tables"], s["lens"])
+    if op == "weights":
+        k = _rows(s, "k", s["tables"])
+        p, l = _softmax_rows(s, k, s["lens"])
+        w = (p / l.clamp(min=1e-30)).sum((1, 2))
+        old = s["token_weights"].clone() if s["accumulate"] else s["token_weights"]
+        room = min(old.shape[1], w.shape[1])
+        inside = torch.arange(room, device=w.device) < s["lens"].view(-1, 1)
+        part = old[:, :room]
+        part.copy_(torch.where(inside, w[:, :room] + (part if s["accumulate"] else 0), part))
+        return old
+    keep, n = _plain_select(s)
+    _plain_move(s, keep)
+    if not s["then_decode"]:
+        return keep, n, s["k_cache"], s["v_cache"]
+    return keep, n, _plain_decode(s, s["dst"], n)
+
+
+# ---------------------------------------------------------------- 64 bits
+
+
+def _exact_row(s, which, b, table, h, n):
+    """Cached rows [0, n) of one sequence and KV head in 64 bits, block by block."""
+    bs, dim = s["bs"], s["dim"]
+    at = table[b, : -(-n // bs)].long()
+    x = s[which + "_cache"][at, h]
+    sc = s["ks" if which == "k" else "vs"][h].double()
+    if s["kv"] == "bf16":
+        return x.double().reshape(-1, dim)[:n]
+    if s["kv"] == "fp8":
+        return x.view(torch.float8_e4m3fn).double().reshape(-1, dim)[:n] * sc
+    flat = x.reshape(len(at), -1)
+    nib = flat[:, : bs * dim // 2].reshape(-1, 1)
+    nib = torch.cat([nib % 16, torch.div(nib, 16, rounding_mode="floor")], 1).long()
+    mag, neg = nib % 8, nib >= 8
+    ex, man = torch.div(mag, 2, rounding_mode="floor"), (mag % 2).double()
+    val = torch.where(ex == 0, man / 2, (1 + man / 2) * torch.pow(2.0, (ex - 1).double()))
+    val = torch.where(neg, -val, val).reshape(len(at) * bs, dim // 16, 16)
+    f = flat[:, bs * dim // 2:].contiguous().view(torch.float8_e4m3fn).double()
+    return (val * f.reshape(len(at) * bs, dim // 16, 1)).reshape(-1, dim)[:n] * sc
+
+
+def _exact_attention(s, table, lens, want):
+    """out [batch, q, hq, dim], or the weights summed over heads and new tokens."""
+    q, hq, hkv, dim = s["q"], s["hq"], s["hkv"], s["dim"]
+    rows = s["q_rows"].double().reshape(s["batch"], q, hkv, hq // hkv, dim)
+    out = torch.zeros_like(rows)
+    total = torch.zeros(s["token_weights"].shape if want == "weights" else (s["batch"], 1),
+                        dtype=torch.float64, device=rows.device)
+    for b in range(s["batch"]):
+        n = int(lens[b])
+        for h in range(hkv):
+            k = _exact_row(s, "k", b, table, h, n)
+            sc = torch.einsum("igd,td->igt", rows[b, :, h], k) * s["scale"]
+            for i in range(q):
+                p = torch.softmax(sc[i, :, : n - q + i + 1], -1)
+                if want == "weights":
+                    total[b, : n - q + i + 1] += p.sum(0)
+                else:
+                    v = _exact_row(s, "v", b, table, h, n) if i == 0 else v
+                    out[b, i, h] = p @ v[: n - q + i + 1]
+    return total if want == "weights" else out.reshape(s["q_rows"].shape)
+
+
+def exact(c, seed):
+    s = prepare(c, seed)
+    op, dev = c["op"], torch.device("cuda")
+    if c["batch"] * c["hkv"] * c["q"] > 16384:
+        return None
+    if op == "write":
+        got = []
+        grid = torch.tensor(E2M1, dtype=torch.float64, device=dev)
+        for x, sc in ((s["k_new"], s["ks"]), (s["v_new"], s["vs"])):
+            # the format's own roundings: float32 group maximum over 6 scales, to E4M3; the
+            # element over the float32 step to the nearest grid value, ties to the even code
+            x = x.float().reshape(x.shape[0], c["hkv"], -1, 16)
+            sf = torch.amax(torch.abs(x), 3) / (sc * 6.0).reshape(1, -1, 1)
+            sf = torch.minimum(sf, torch.tensor(448.0, device=dev)).to(torch.float8_e4m3fn).float()
+            step = sf * sc.reshape(1, -1, 1)
+            safe = torch.where(step > 0, step, torch.ones_like(step))
+            y = (x / safe[..., None]).double()
+            hi = torch.searchsorted(grid, y.abs().contiguous()).clamp(1, 7)
+            below, above = grid[hi - 1], grid[hi]
+            d = (y.abs() - below) - (above - y.abs())
+            pick = torch.where((d > 0) | ((d == 0) & (hi % 2 == 0)), above, below)
+            v = pick * torch.sign(y) * sf[..., None].double() * sc.double().reshape(1, -1, 1, 1)
+            got.append(torch.where(step[..., None] > 0, v, torch.zeros_like(v)).flatten(2))
+        return tuple(got)
+    if op == "decode":
+        return _exact_attention(s, s["tables"], s["lens"], "out")
+    if op == "weights":
+        w = _exact_attention(s, s["tables"], s["lens"], "weights")
+        old = s["token_weights"].double()
+        t = torch.arange(old.shape[1], device=dev)
+        inside = t < s["lens"].view(-1, 1)
+        return torch.where(inside, w + (old if c["accumulate"] else 0), old)
+    keep = torch.full((c["batch"], c["budget"]), -1, dtype=torch.int32)
+    n = torch.minimum(s["lens"].cpu(), torch.tensor(c["budget"], dtype=torch.int32))
+    for b, length in enumerate(s["lens"].tolist()):
+        w = s["token_weights"][b, :length].tolist()
+        old = max(0, length - c["recent"])
+        order = sorted(range(old), key=lambda t: (-w[t], t))
+        got = list(range(old, length)) + order
+        got = sorted((got if length > c["budget"] else range(length))[: c["budget"]])
+        keep[b, : len(got)] = torch.tensor(got, dtype=torch.int32)
+    keep, n = keep.to(dev), n.to(dev)
+    if not c["then_decode"]:  # a move computes nothing: only its choice is told here
+        return keep, n, None, None
+    spots = [[int(s["tables"][b, t // c["bs"]]) * c["bs"] + t % c["bs"] for t in row if t >= 0]
+             for b, row in enumerate(keep.tolist())]
+    out = torch.zeros(s["q_rows"].shape, dtype=torch.float64, device=dev)
+    every = torch.arange(s["k_cache"].shape[0], device=dev).view(1, -1)
+    size = s["k_cache"].shape[0] * c["bs"]
+    for h in range(c["hkv"]):
+        k, v = (_exact_row(s, w, 0, every, h, size) for w in "kv")
+        for b, at in enumerate(spots):
+            a = torch.tensor(at, dtype=torch.long, device=dev)
+            g = slice(h * (c["hq"] // c["hkv"]), (h + 1) * (c["hq"] // c["hkv"]))
+            p = torch.softmax(s["q_rows"][b, g].double() @ k[a].T * s["scale"], -1)
+            out[b, g] = p @ v[a]
+    return keep, n, out
