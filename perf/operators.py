@@ -208,6 +208,10 @@ def prepare(c, seed):
     s = dict(c, hi_len=max(lens), ks=scales(0.05), vs=scales(0.03), tables=tables(blocks, 0),
              lens=torch.tensor(lens, dtype=torch.int32, device=dev), scale=1.0 / math.sqrt(dim),
              max_blocks=max(blocks))
+    if own:
+        import paged_kv_cache_92_gb300 as pk
+        pk.load()
+        s["pk"] = pk
     if c["op"] == "write":
         tok = sum(lens)
         spread = torch.ones(dim, device=dev)
@@ -234,9 +238,6 @@ def prepare(c, seed):
         w = torch.rand((batch, s["hi_len"] + 3), generator=g, device=dev).pow_(6)
         s["token_weights"] = torch.where(w < 0.01, (w * 1000).round() / 1000, w)
     if own:
-        import paged_kv_cache_92_gb300 as pk
-        pk.load()
-        s["pk"] = pk
         hold = c["op"] == "decode" or c["then_decode"]
         tab = s["dst"] if c["op"] == "evict" else s["tables"]
         most = min(s["hi_len"], c["budget"]) if c["op"] == "evict" else s["hi_len"]
