@@ -133,8 +133,9 @@ typedef struct {
   int32_t num_blocks;
   int32_t max_context_len;     /* host-known upper bound of every context_lens[b] (>= 1) */
   float scale;                 /* softmax scale, normally 1/sqrt(head_dim) */
-  int32_t partition_tokens;    /* split-K partition length; 0 = 512; else a multiple of 16 in
-                                  [16, 4096], and on the CUDA-core kernel of block_size too */
+  int32_t partition_tokens;    /* split-K partition length; 0 = 512 (the 4-bit cache: chosen from
+                                  the shapes); else a multiple of 16 in [16, 4096], and on the
+                                  CUDA-core and 4-bit kernels of block_size too */
   int32_t variant;             /* PA_DECODE_TENSOR_CORE (default) or PA_DECODE_CUDA_CORE */
   int32_t overlap_prologue;    /* nonzero: context_lens and block_tables were final before the
                                   previous kernel on `stream` began (e.g. uploaded once per step),
@@ -145,9 +146,11 @@ typedef struct {
                                   prefetches its first cache blocks into L2, which cannot change
                                   any result even if that kernel writes them. 0 = plain stream
                                   order. */
-  int32_t kv_dtype;            /* PA_KV_BF16 (0, default) or PA_KV_FP8_E4M3 (1) */
-  const float* k_scale;        /* PA_KV_FP8_E4M3 only: device float [num_kv_heads], the
-                                  dequantisation scale of each KV head's K (value = code * scale) */
+  int32_t kv_dtype;            /* PA_KV_BF16 (0, default), PA_KV_FP8_E4M3 (1) or PA_KV_FP4_E2M1
+                                  (2) */
+  const float* k_scale;        /* the 8-bit and 4-bit caches only: device float [num_kv_heads], the
+                                  dequantisation scale of each KV head's K (8-bit: value = code *
+                                  scale) */
   const float* v_scale;        /* the same for V */
   int32_t query_len;           /* new tokens per sequence: 0 or 1 = one (the layouts above).
                                   Q > 1 ("How Paged Attention and Continuous Batching Actually
@@ -210,6 +213,21 @@ typedef struct {
  * Other shapes return PA_ERR_UNSUPPORTED. */
 #define PA_KV_BF16 0
 #define PA_KV_FP8_E4M3 1
+/* PA_KV_FP4_E2M1 -- the 4-bit KV cache (same page and section; the format is
+ * this library's): E2M1 codes with an E4M3 scale for every 16 elements of a row
+ * and one float scale per KV head, 9/16 byte an element:
+ *   value = code * group scale * scale[h]
+ *   k_cache, v_cache  uint8 [num_blocks][num_kv_heads][tile], tile =
+ *            block_size * head_dim * 9 / 16 bytes: the codes of the block's
+ *            rows [block_size][head_dim / 2] (element 2i in the low nibble of
+ *            byte i), then their scales [block_size][head_dim / 16]
+ * Written by pa_reshape_and_cache_fp4, read back by pa_gather_fp4, copied by
+ * pa_copy_blocks_fp4. One kernel decodes it whatever `variant` says: head_dim
+ * 64 or 128, every block size, G in {1, 2, 4, 8}, any number of KV heads,
+ * num_seqs * query_len <= 65535 (else PA_ERR_UNSUPPORTED). The codes are
+ * multiplied exactly; the softmax weights are rounded to f16. With several new
+ * tokens, up to 16 / G of them share each load of the keys. */
+#define PA_KV_FP4_E2M1 2
 
 #define PA_DECODE_TENSOR_CORE 0 /* tcgen05 MMAs, TMEM accumulators, tensor-map TMA ring */
 #define PA_DECODE_CUDA_CORE 1   /* fp32 FMAs on CUDA cores, 1-D bulk-copy rings */
@@ -295,7 +313,8 @@ pa_status pa_reshape_and_cache(const void* k_new, const void* v_new, void* k_cac
  * a->k_cache / a->v_cache must equal p->k_cache / p->v_cache (the caches are
  * written through these). With the 8-bit cache (p->kv_dtype PA_KV_FP8_E4M3)
  * the write is that of pa_reshape_and_cache_fp8 with p->k_scale / p->v_scale
- * (bit-identical codes). Same workspace as pa_decode. The CUDA-core variant
+ * (bit-identical codes), with the 4-bit cache that of pa_reshape_and_cache_fp4,
+ * in a launch of its own. Same workspace as pa_decode. The CUDA-core variant
  * and shapes the tensor-core kernel does not cover run the KV-write kernel
  * and then the decode, with the same result.
  * ---------------------------------------------------------------------- */
@@ -372,11 +391,12 @@ typedef struct {
   int32_t num_cow_pairs;
   float scale;
   int32_t variant;            /* PA_DECODE_TENSOR_CORE or PA_DECODE_CUDA_CORE */
-  int32_t kv_dtype;           /* PA_KV_BF16 (0) or PA_KV_FP8_E4M3: the caches as in pa_decode;
-                                 the 8-bit cache takes the tensor-core variant, the quantising
-                                 KV write and pa_copy_blocks_fp8 */
-  const float* k_scale;       /* PA_KV_FP8_E4M3 only: device float [num_kv_heads], as in
-                                 pa_decode_params */
+  int32_t kv_dtype;           /* PA_KV_BF16 (0), PA_KV_FP8_E4M3 or PA_KV_FP4_E2M1: the caches as
+                                 in pa_decode; the 8-bit cache takes the tensor-core variant, the
+                                 quantising KV write and pa_copy_blocks_fp8, the 4-bit cache its
+                                 own decode, write and pa_copy_blocks_fp4 */
+  const float* k_scale;       /* the 8-bit and 4-bit caches only: device float [num_kv_heads], as
+                                 in pa_decode_params */
   const float* v_scale;
   int32_t query_len;          /* new tokens per sequence, Q (0 or 1 = one): q and host_out hold
                                  [num_seqs][Q][num_q_heads][head_dim], k_new / v_new
@@ -411,6 +431,46 @@ pa_status pa_reshape_and_cache_fp8(const void* k_new, const void* v_new, void* k
 /* pa_copy_blocks for an 8-bit cache: the same whole-block copy of both caches
  * (block_size * head_dim bytes per KV head); block_size 16 or 32. */
 pa_status pa_copy_blocks_fp8(void* k_cache, void* v_cache, const int32_t* pairs,
+                             int32_t num_pairs, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t num_blocks, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_reshape_and_cache_fp4 -- the KV write into a 4-bit (PA_KV_FP4_E2M1)
+ * cache. For token t, KV head h and every group of 16 elements of its row,
+ * with a the group's largest magnitude and fl() rounding to float:
+ *   group scale = E4M3(fl(a / fl(6 * scale[h])))   nearest even, at most 448
+ *   step        = fl(group scale * scale[h])
+ *   code        = E2M1(fl(x / step))               nearest even, at most +-6
+ * A group whose scale rounds to zero is stored as (signed) zeros; an infinity
+ * saturates; a group that holds a NaN gets the E4M3 NaN as its scale, so all
+ * 16 elements read back as NaN. k_scale, v_scale: device float [num_kv_heads],
+ * each in [2^-60, 2^60] (others: unspecified codes). head_dim 64 or 128;
+ * block_size 8, 16 or 32. Otherwise as pa_reshape_and_cache (negative slots
+ * skipped, out-of-range slots set PA_DEVERR_SLOT).
+ * ---------------------------------------------------------------------- */
+pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_cache,
+                                   void* v_cache, const int64_t* slot_mapping,
+                                   const float* k_scale, const float* v_scale,
+                                   int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_gather_fp4 -- rows of a 4-bit cache read back, for a caller that moves a
+ * sequence to a bf16 cache or feeds cached rows to another kernel: row t of
+ * k_out / v_out (bf16 [num_tokens][num_kv_heads][head_dim]) is the row at
+ * slot_mapping[t], each element fl(code * group scale * scale[h]) rounded to
+ * bf16. A negative slot gives a row of zeros; an out-of-range slot does too,
+ * and sets PA_DEVERR_SLOT. A slot may occur any number of times.
+ * ---------------------------------------------------------------------- */
+pa_status pa_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, void* v_out,
+                        const int64_t* slot_mapping, const float* k_scale, const float* v_scale,
+                        int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t block_size, int32_t num_blocks, pa_stream_t stream);
+
+/* pa_copy_blocks for a 4-bit cache: the same whole-block copy of both caches
+ * (block_size * head_dim * 9 / 16 bytes per KV head); head_dim 64 or 128,
+ * block_size 8, 16 or 32. */
+pa_status pa_copy_blocks_fp4(void* k_cache, void* v_cache, const int32_t* pairs,
                              int32_t num_pairs, int32_t num_kv_heads, int32_t head_dim,
                              int32_t block_size, int32_t num_blocks, pa_stream_t stream);
 

@@ -397,6 +397,112 @@ def copy_blocks_fp8(k_cache, v_cache, pairs) -> Tuple[np.ndarray, np.ndarray]:
 
 
 # --------------------------------------------------------------------------
+# 4-bit KV cache: per (block, head) tile, E2M1 codes [BS][D/2] (element 2i in
+# the low nibble of byte i), then E4M3 group scales [BS][D/16]
+# --------------------------------------------------------------------------
+
+E2M1_GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _e4m3_grid() -> np.ndarray:
+    """The 127 non-negative finite E4M3 values, by code (written out from the format)."""
+    c = np.arange(127)
+    e, m = c >> 3, (c & 7) / 8.0
+    return np.where(e == 0, m * 2.0 ** -6, (1 + m) * 2.0 ** (e - 7.0))
+
+
+def nearest_code(a, grid) -> np.ndarray:
+    """Index of the grid value nearest to each a >= 0 (a tie to the even index),
+    the last one for values beyond the grid."""
+    a = np.asarray(a, dtype=np.float64)
+    hi = np.clip(np.searchsorted(grid, a), 1, len(grid) - 1)
+    below, above = a - grid[hi - 1], grid[hi] - a
+    return np.where((above < below) | ((above == below) & (hi % 2 == 0)), hi, hi - 1)
+
+
+def fp4_quantise(rows, scale) -> Tuple[np.ndarray, np.ndarray]:
+    """Rows [..., Hkv, D] (float64 holding bf16 values) -> (codes [..., Hkv, D]
+    with the sign in bit 3, scale codes [..., Hkv, D/16]), both uint8."""
+    x = np.asarray(rows, dtype=np.float32)
+    x = x.reshape(*x.shape[:-1], -1, 16)
+    s = np.asarray(scale, dtype=np.float32)[:, None]
+    nan = np.isnan(x).any(-1)
+    with np.errstate(invalid="ignore", over="ignore"):
+        amax = np.where(np.isnan(x), np.float32(0), np.abs(x)).max(-1)
+        sf = nearest_code(np.minimum((amax / (np.float32(6) * s)).astype(np.float64), 1e30),
+                          _e4m3_grid())
+        step = (_e4m3_grid()[sf].astype(np.float32) * s)[..., None]
+        y = np.abs(x) / np.where(step > 0, step, np.float32(1))
+    code = nearest_code(np.where(np.isnan(y), 0, np.minimum(y, 1e30)), E2M1_GRID)
+    code = np.where((step > 0) & ~nan[..., None], code, 0) | (np.signbit(x) << 3)
+    sf = np.where(nan, 0x7F, sf)
+    return (code.astype(np.uint8).reshape(*x.shape[:-2], -1), sf.astype(np.uint8))
+
+
+def fp4_write(rows, cache, slots, scale, D: int) -> np.ndarray:
+    """The quantising write of rows [T][Hkv][D] into a copy of one 4-bit cache."""
+    cache = np.array(cache, dtype=np.uint8)
+    NB, Hkv, BS = cache.shape[:3]
+    flat = cache.reshape(NB, Hkv, -1)
+    codes, sf = fp4_quantise(rows, scale)
+    for t, slot in enumerate(np.asarray(slots).tolist()):
+        if slot < 0 or slot >= NB * BS:
+            continue
+        blk, off = slot // BS, slot % BS
+        for h in range(Hkv):
+            byte = codes[t, h, 0::2] | (codes[t, h, 1::2] << 4)
+            flat[blk, h, off * D // 2:(off + 1) * D // 2] = byte
+            at = BS * D // 2 + off * D // 16
+            flat[blk, h, at:at + D // 16] = sf[t, h]
+    return flat.reshape(cache.shape)
+
+
+def fp4_values(cache, scale, D: int) -> np.ndarray:
+    """Every row of a 4-bit cache in float64: [NB][Hkv][BS][D]."""
+    cache = np.asarray(cache, dtype=np.uint8)
+    NB, Hkv, BS = cache.shape[:3]
+    flat = cache.reshape(NB, Hkv, -1)
+    byte = flat[..., :BS * D // 2].reshape(NB, Hkv, BS, D // 2)
+    code = np.stack([byte & 15, byte >> 4], -1).reshape(NB, Hkv, BS, D)
+    val = E2M1_GRID[code & 7] * np.where(code & 8, -1.0, 1.0)
+    sfc = flat[..., BS * D // 2:].reshape(NB, Hkv, BS, D // 16)
+    sf = np.append(_e4m3_grid(), np.nan)[sfc & 0x7F] * np.where(sfc & 0x80, -1.0, 1.0)
+    val = val.reshape(NB, Hkv, BS, D // 16, 16) * sf[..., None]
+    return val.reshape(NB, Hkv, BS, D) * np.asarray(scale, np.float64)[:, None, None]
+
+
+def attention_rows(q, k_rows, v_rows, block_tables, context_lens, scale: Optional[float] = None):
+    """Causal attention of the last Q tokens of each sequence over cached rows
+    in float64 (q [B][Q][Hq][D]; k_rows, v_rows [NB][Hkv][BS][D]; v_rows may be
+    None). Returns (out [B][Q][Hq][D] or None, weights: per sequence the softmax
+    weights [Q][Hq][L], zero where a token is not seen). Sequences shorter than
+    Q give zeros."""
+    q = np.asarray(q, dtype=np.float64)
+    B, QL, Hq, D = q.shape
+    Hkv, BS = k_rows.shape[1:3]
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    out = None if v_rows is None else np.zeros(q.shape)
+    weights = []
+    for b in range(B):
+        L = int(context_lens[b])
+        w = np.zeros((QL, Hq, max(L, 0)))
+        if L >= QL:
+            blocks = np.asarray(block_tables[b][: -(-L // BS)])
+            for h in range(Hq):
+                g = h // (Hq // Hkv)
+                K = k_rows[blocks, g].reshape(-1, D)[:L]
+                for i in range(QL):
+                    n = L - QL + i + 1
+                    s = scale * (K[:n] @ q[b, i, h])
+                    p = np.exp(s - s.max())
+                    w[i, h, :n] = p / p.sum()
+                    if out is not None:
+                        out[b, i, h] = w[i, h, :n] @ v_rows[blocks, g].reshape(-1, D)[:n]
+        weights.append(w)
+    return out, weights
+
+
+# --------------------------------------------------------------------------
 # block manager reference model
 # --------------------------------------------------------------------------
 

@@ -33,12 +33,14 @@ DEVERR_APPEND_SLOT = 0x20
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+KV_FP4_E2M1 = 2
 
 EXPORTED_SYMBOLS = [
     "pa_status_string", "pa_last_error", "pa_version", "pa_device_errors",
     "pa_decode_workspace_size", "pa_decode", "pa_decode_noalloc", "pa_append_decode",
     "pa_step_host_layout", "pa_step_host_workspace_size", "pa_step_host",
     "pa_reshape_and_cache", "pa_reshape_and_cache_fp8", "pa_copy_blocks_fp8",
+    "pa_reshape_and_cache_fp4", "pa_gather_fp4", "pa_copy_blocks_fp4",
     "pa_copy_blocks",
     "pa_pool_create", "pa_pool_destroy", "pa_pool_alloc", "pa_pool_incref", "pa_pool_decref",
     "pa_pool_refcount", "pa_pool_stats", "pa_seq_create", "pa_seq_free", "pa_seq_fork",
@@ -147,6 +149,10 @@ def load():
         "pa_reshape_and_cache_fp8": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp],
                                      ctypes.c_int),
         "pa_copy_blocks_fp8": ([vp, vp, vp, i32, i32, i32, i32, i32, vp], ctypes.c_int),
+        "pa_reshape_and_cache_fp4": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp],
+                                     ctypes.c_int),
+        "pa_gather_fp4": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp], ctypes.c_int),
+        "pa_copy_blocks_fp4": ([vp, vp, vp, i32, i32, i32, i32, i32, vp], ctypes.c_int),
         "pa_pool_create": ([i32, i32, vp, P(vp)], ctypes.c_int),
         "pa_pool_destroy": ([vp], None),
         "pa_pool_alloc": ([vp, P(i32)], ctypes.c_int),
@@ -208,6 +214,34 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream or None
 
 
+def kv_cache_format(k_cache) -> Tuple[int, int]:
+    """(kv_dtype, head_dim) of a K cache tensor: bf16 [NB][Hkv][BS][D]; uint8
+    [NB][Hkv][BS][D] for the 8-bit cache, [NB][Hkv][BS][D * 9 / 16] for the
+    4-bit one (36 or 72 bytes a row: no 8-bit head_dim)."""
+    import torch
+
+    if k_cache.dim() != 4:
+        raise ValueError("a cache is [num_blocks][num_kv_heads][block_size][row]")
+    row = k_cache.shape[3]
+    if k_cache.dtype == torch.uint8:
+        return (KV_FP4_E2M1, row * 16 // 9) if row in (36, 72) else (KV_FP8_E4M3, row)
+    return KV_BF16, row
+
+
+def fp4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int):
+    """Shape of a 4-bit K or V cache (uint8). The last two dimensions are one
+    tile's bytes (codes of all its rows, then their scales), not its rows."""
+    if head_dim not in (64, 128):
+        raise ValueError("the 4-bit cache takes head_dim 64 or 128")
+    return (num_blocks, num_kv_heads, block_size, head_dim * 9 // 16)
+
+
+def _v_cache_ok(fmt: int, k_cache, v_cache) -> bool:
+    if fmt == KV_FP8_E4M3:
+        return tuple(v_cache.shape) in fp8_v_shapes(*k_cache.shape)
+    return tuple(v_cache.shape) == tuple(k_cache.shape)
+
+
 def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
                        max_context_len: int, scale: Optional[float] = None,
                        partition_tokens: int = 0, variant: int = DECODE_TENSOR_CORE,
@@ -216,7 +250,8 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
     """Marshal a pa_decode call. q and out are bf16 [B][Hq][D] (one new token
     per sequence) or [B][Q][Hq][D] (Q new tokens per sequence, causal among
     them). bf16 caches [NB][Hkv][BS][D]; uint8 caches are the 8-bit E4M3 cache
-    (K [NB][Hkv][BS][D], V^T in 16-key sub-tiles [NB][Hkv][BS/16][D][16]) and
+    (K [NB][Hkv][BS][D], V^T in 16-key sub-tiles [NB][Hkv][BS/16][D][16]) or,
+    with D * 9 / 16 bytes a row, the 4-bit cache (``fp4_cache_shape``); both
     need k_scale / v_scale, float32 CUDA tensors [Hkv]."""
     import torch
 
@@ -224,10 +259,9 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
         B, QL, Hq, D = q.shape
     else:
         (B, Hq, D), QL = q.shape, 0
-    fp8 = k_cache.dtype == torch.uint8
-    NB, Hkv, BS, D2 = k_cache.shape
-    v_ok = tuple(v_cache.shape) in fp8_v_shapes(NB, Hkv, BS, D2) if fp8 else \
-        tuple(v_cache.shape) == tuple(k_cache.shape)
+    fmt, D2 = kv_cache_format(k_cache)
+    NB, Hkv, BS, _ = k_cache.shape
+    v_ok = _v_cache_ok(fmt, k_cache, v_cache)
     if D2 != D or not v_ok or tuple(out.shape) != tuple(q.shape):
         raise ValueError("shape mismatch between q / out / k_cache / v_cache")
     if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
@@ -235,15 +269,17 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
     p = DecodeParams()
     p.q = _dev_ptr(q, torch.bfloat16, "q")
     p.out = _dev_ptr(out, torch.bfloat16, "out")
-    cache_dtype = torch.uint8 if fp8 else torch.bfloat16
+    cache_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
     p.k_cache = _dev_ptr(k_cache, cache_dtype, "k_cache")
     p.v_cache = _dev_ptr(v_cache, cache_dtype, "v_cache")
-    if fp8:
+    if fmt != KV_BF16:
         if k_scale is None or v_scale is None:
-            raise ValueError("the 8-bit cache needs k_scale and v_scale")
-        p.kv_dtype = KV_FP8_E4M3
+            raise ValueError("the 8-bit and 4-bit caches need k_scale and v_scale")
+        p.kv_dtype = fmt
         p.k_scale = _dev_ptr(k_scale, torch.float32, "k_scale")
         p.v_scale = _dev_ptr(v_scale, torch.float32, "v_scale")
+        if fmt == KV_FP4_E2M1 and (k_scale.numel() != Hkv or v_scale.numel() != Hkv):
+            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
     p.block_tables = _dev_ptr(block_tables, torch.int32, "block_tables")
     p.context_lens = _dev_ptr(context_lens, torch.int32, "context_lens")
     p.max_blocks_per_seq = block_tables.shape[1]
@@ -296,7 +332,7 @@ def make_append_params(k_new, v_new, slot_mapping, k_cache, v_cache) -> AppendPa
 
     T, Hkv, D = k_new.shape  # T = num_seqs * (new tokens per sequence)
     if tuple(v_new.shape) != (T, Hkv, D) or tuple(slot_mapping.shape) != (T,) \
-            or tuple(k_cache.shape[1:2]) != (Hkv,) or k_cache.shape[3] != D:
+            or tuple(k_cache.shape[1:2]) != (Hkv,) or kv_cache_format(k_cache)[1] != D:
         raise ValueError("k_new/v_new must be [num_seqs * Q][num_kv_heads][head_dim] matching "
                          "the cache, slot_mapping [num_seqs * Q]")
     a = AppendParams()
@@ -321,7 +357,8 @@ def pa_append_decode(q, k_cache, v_cache, block_tables, context_lens, max_contex
     ``pa_decode``; returns ``out``. With q [B][Q][Hq][d], row b*Q + i of
     ``k_new``/``v_new``/``slot_mapping`` is token ``context_lens[b] - Q + i``.
     For the 8-bit cache (uint8 caches, with ``k_scale``/``v_scale``) the write
-    is the quantising one of ``pa_reshape_and_cache_fp8``."""
+    is the quantising one of ``pa_reshape_and_cache_fp8``, for the 4-bit cache
+    that of ``pa_reshape_and_cache_fp4``."""
     import torch
 
     lib = load()
@@ -347,22 +384,24 @@ def make_step_host_params(k_cache, v_cache, num_seqs: int, num_q_heads: int,
                           variant: int = DECODE_TENSOR_CORE, k_scale=None,
                           v_scale=None, query_len: int = 0) -> StepHostParams:
     """Shape half of a host-driven step; host_in / host_out are set by the caller
-    (or by ``pa_step_host``). uint8 caches are the 8-bit (E4M3) cache and need
-    ``k_scale`` / ``v_scale`` (float32 CUDA tensors [num_kv_heads]). With
+    (or by ``pa_step_host``). uint8 caches are the 8-bit (E4M3) or 4-bit cache and
+    need ``k_scale`` / ``v_scale`` (float32 CUDA tensors [num_kv_heads]). With
     ``query_len`` Q > 1 every sequence brings Q new tokens (the layouts of
     ``pa_append_decode``)."""
     import torch
 
-    NB, Hkv, BS, D = k_cache.shape
+    NB, Hkv, BS, _ = k_cache.shape
     p = StepHostParams()
-    fp8 = k_cache.dtype == torch.uint8
-    cache_dtype = torch.uint8 if fp8 else torch.bfloat16
+    fmt, D = kv_cache_format(k_cache)
+    cache_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
     p.k_cache = _dev_ptr(k_cache, cache_dtype, "k_cache")
     p.v_cache = _dev_ptr(v_cache, cache_dtype, "v_cache")
-    if fp8:
+    if fmt == KV_FP4_E2M1 and not _v_cache_ok(fmt, k_cache, v_cache):
+        raise ValueError("shape mismatch between k_cache and v_cache")
+    if fmt != KV_BF16:
         if k_scale is None or v_scale is None:
-            raise ValueError("the 8-bit cache needs k_scale and v_scale")
-        p.kv_dtype = KV_FP8_E4M3
+            raise ValueError("the 8-bit and 4-bit caches need k_scale and v_scale")
+        p.kv_dtype = fmt
         p.k_scale = _dev_ptr(k_scale, torch.float32, "k_scale")
         p.v_scale = _dev_ptr(v_scale, torch.float32, "v_scale")
     p.num_seqs, p.num_q_heads, p.num_kv_heads, p.head_dim = num_seqs, num_q_heads, Hkv, D
@@ -428,7 +467,7 @@ def pa_step_host(params: StepHostParams, host_in, host_out, workspace, stream=No
 
 def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
                       scale: Optional[float] = None, partition_tokens: int = 0, out=None,
-                      stream=None, variant: int = DECODE_TENSOR_CORE):
+                      stream=None, variant: int = DECODE_TENSOR_CORE, k_scale=None, v_scale=None):
     """Same decode as ``pa_decode`` without any workspace: for callers that
     cannot allocate device memory at decode time (all free HBM already handed
     to the KV pool, or no room for cudaMalloc's synchronisation in the serving
@@ -442,7 +481,8 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_conte
     if out is None:
         out = torch.empty_like(q)
     p = make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
-                           max_context_len, scale, partition_tokens, variant)
+                           max_context_len, scale, partition_tokens, variant, k_scale=k_scale,
+                           v_scale=v_scale)
     _check(lib.pa_decode_noalloc(ctypes.byref(p), _stream_handle(stream)), "pa_decode_noalloc")
     return out
 
@@ -518,6 +558,76 @@ def pa_copy_blocks_fp8(k_cache, v_cache, pairs, stream=None) -> None:
         _dev_ptr(k_cache, torch.uint8, "k_cache"), _dev_ptr(v_cache, torch.uint8, "v_cache"),
         _dev_ptr(pairs, torch.int32, "pairs"), pairs.shape[0], Hkv, D, BS, NB,
         _stream_handle(stream)), "pa_copy_blocks_fp8")
+
+
+def _check_fp4_rows(k_rows, v_rows, k_cache, v_cache, slot_mapping, k_scale, v_scale, who: str):
+    T, Hkv, D = k_rows.shape
+    fmt, D2 = kv_cache_format(k_cache)
+    if fmt != KV_FP4_E2M1 or (k_cache.shape[1], D2) != (Hkv, D) \
+            or tuple(v_rows.shape) != tuple(k_rows.shape) \
+            or tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(slot_mapping.shape) != (T,) \
+            or k_scale.numel() != Hkv or v_scale.numel() != Hkv:
+        raise ValueError(f"shape mismatch in {who}")
+    return T, Hkv, D, k_cache.shape[2], k_cache.shape[0]
+
+
+def pa_reshape_and_cache_fp4(k_new, v_new, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                             stream=None) -> None:
+    """KV write into the 4-bit cache (uint8, ``fp4_cache_shape``): E2M1 codes with
+    an E4M3 scale per 16 elements and the float32 scale of each KV head."""
+    import torch
+
+    dims = _check_fp4_rows(k_new, v_new, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                           "pa_reshape_and_cache_fp4")
+    lib = load()
+    _check(lib.pa_reshape_and_cache_fp4(
+        _dev_ptr(k_new, torch.bfloat16, "k_new"), _dev_ptr(v_new, torch.bfloat16, "v_new"),
+        _dev_ptr(k_cache, torch.uint8, "k_cache"), _dev_ptr(v_cache, torch.uint8, "v_cache"),
+        _dev_ptr(slot_mapping, torch.int64, "slot_mapping"),
+        _dev_ptr(k_scale, torch.float32, "k_scale"), _dev_ptr(v_scale, torch.float32, "v_scale"),
+        *dims, _stream_handle(stream)), "pa_reshape_and_cache_fp4")
+
+
+def pa_gather_fp4(k_cache, v_cache, slot_mapping, k_scale, v_scale, k_out=None, v_out=None,
+                  stream=None):
+    """Rows of the 4-bit cache read back as bf16 [num_tokens][Hkv][D]; returns
+    (k_out, v_out). A negative slot gives a row of zeros."""
+    import torch
+
+    fmt, D = kv_cache_format(k_cache)
+    if fmt != KV_FP4_E2M1:
+        raise ValueError("pa_gather_fp4 reads a 4-bit cache")
+    shape = (slot_mapping.shape[0], k_cache.shape[1], D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+    dims = _check_fp4_rows(k_out, v_out, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                           "pa_gather_fp4")
+    lib = load()
+    _check(lib.pa_gather_fp4(
+        _dev_ptr(k_cache, torch.uint8, "k_cache"), _dev_ptr(v_cache, torch.uint8, "v_cache"),
+        _dev_ptr(k_out, torch.bfloat16, "k_out"), _dev_ptr(v_out, torch.bfloat16, "v_out"),
+        _dev_ptr(slot_mapping, torch.int64, "slot_mapping"),
+        _dev_ptr(k_scale, torch.float32, "k_scale"), _dev_ptr(v_scale, torch.float32, "v_scale"),
+        *dims, _stream_handle(stream)), "pa_gather_fp4")
+    return k_out, v_out
+
+
+def pa_copy_blocks_fp4(k_cache, v_cache, pairs, stream=None) -> None:
+    import torch
+
+    fmt, D = kv_cache_format(k_cache)
+    if fmt != KV_FP4_E2M1 or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("pa_copy_blocks_fp4 copies blocks of a 4-bit cache")
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be int32 [n][2]")
+    NB, Hkv, BS, _ = k_cache.shape
+    lib = load()
+    _check(lib.pa_copy_blocks_fp4(
+        _dev_ptr(k_cache, torch.uint8, "k_cache"), _dev_ptr(v_cache, torch.uint8, "v_cache"),
+        _dev_ptr(pairs, torch.int32, "pairs"), pairs.shape[0], Hkv, D, BS, NB,
+        _stream_handle(stream)), "pa_copy_blocks_fp4")
 
 
 def pa_device_errors(stream=None) -> int:

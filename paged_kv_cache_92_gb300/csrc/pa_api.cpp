@@ -19,8 +19,19 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// The 4-bit decode's own choice: partitions short enough for 16 CTAs an SM of
+// a 152-SM GPU, so that ragged lengths even out, within [128, 4096] tokens.
+int fp4_partition_tokens(const pa_decode_params* p) {
+  const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
+  const int64_t cap = p->max_context_len < table ? p->max_context_len : table;
+  const int64_t units = int64_t(p->num_seqs) * p->num_kv_heads * fp4_columns(p).n_groups;
+  int64_t pt = (cap * units / (152 * 16) + 127) / 128 * 128;
+  return pt < 128 ? 128 : (pt > kMaxPartitionTokens ? kMaxPartitionTokens : int(pt));
+}
+
 int resolve_partition_tokens(const pa_decode_params* p) {
-  return p->partition_tokens == 0 ? kDefaultPartitionTokens : p->partition_tokens;
+  if (p->partition_tokens != 0) return p->partition_tokens;
+  return p->kv_dtype == PA_KV_FP4_E2M1 ? fp4_partition_tokens(p) : kDefaultPartitionTokens;
 }
 
 // Full host validation of decode params. Returns PA_OK or an error (message set).
@@ -58,8 +69,9 @@ pa_status check_decode(const pa_decode_params* p, bool need_pointers) {
     return set_error(PA_ERR_INVALID_ARG, "pa_decode: cache or query rows exceed 2^31");
   if (!(p->scale > 0.0f) || p->scale != p->scale)
     return set_error(PA_ERR_INVALID_ARG, "pa_decode: scale must be a positive finite number");
-  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3)
-    return set_error(PA_ERR_INVALID_ARG, "pa_decode: kv_dtype must be PA_KV_BF16 or PA_KV_FP8_E4M3");
+  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4_E2M1)
+    return set_error(PA_ERR_INVALID_ARG,
+                     "pa_decode: kv_dtype must be PA_KV_BF16, PA_KV_FP8_E4M3 or PA_KV_FP4_E2M1");
   if (p->query_len < 0 || p->query_len > 1024)
     return set_error(PA_ERR_INVALID_ARG, "pa_decode: query_len must be in [0, 1024]");
   if (p->wait_timeout_us < 0)
@@ -77,12 +89,12 @@ pa_status check_decode(const pa_decode_params* p, bool need_pointers) {
                      "pa_decode: on the CUDA-core kernel num_seqs * query_len must be <= 65535 "
                      "(the tensor-core kernel takes num_kv_heads 1/2/4/8 and num_seqs * "
                      "(query_len split into column groups) <= 16384)");
-  if (p->kv_dtype == PA_KV_FP8_E4M3) {
+  if (p->kv_dtype != PA_KV_BF16) {
     if (need_pointers && p->num_seqs > 0 &&
         (!p->k_scale || !p->v_scale || (reinterpret_cast<uintptr_t>(p->k_scale) & 3u) ||
          (reinterpret_cast<uintptr_t>(p->v_scale) & 3u)))
       return set_error(PA_ERR_INVALID_ARG,
-                       "pa_decode: the 8-bit cache needs k_scale and v_scale (float arrays)");
+                       "pa_decode: the 8-bit and 4-bit caches need k_scale and v_scale (float arrays)");
   }
   if (need_pointers && p->num_seqs > 0) {
     if (!p->q || !p->out || !p->k_cache || !p->v_cache || !p->block_tables || !p->context_lens)
@@ -221,6 +233,7 @@ static pa_status run_decode(const pa_decode_params* p, unsigned char* ws,
     L.part_acc = reinterpret_cast<float*>(ws + w.tc_acc);
     e = launch_decode_tc(L, stream);
   } else {
+    const bool fp4 = p->kv_dtype == PA_KV_FP4_E2M1;
     if (append && p->kv_dtype == PA_KV_FP8_E4M3) {
       // the quantising write with the fused path's slot rule, then the decode
       e = launch_quantize_q(nullptr, nullptr, nullptr, query_map(p), p, append, stream);
@@ -232,10 +245,17 @@ static pa_status run_decode(const pa_decode_params* p, unsigned char* ws,
       chk.cap = p->max_blocks_per_seq * p->block_size < p->max_context_len
                     ? p->max_blocks_per_seq * p->block_size : p->max_context_len;
       chk.q_len = query_len_of(p);
-      e = launch_reshape_and_cache(append->k_new, append->v_new, append->k_cache,
-                                   append->v_cache, append->slot_mapping,
-                                   p->num_seqs * query_len_of(p), p->num_kv_heads, p->head_dim,
-                                   p->block_size, p->num_blocks, stream, chk);
+      if (fp4)
+        e = launch_reshape_and_cache_fp4(append->k_new, append->v_new, append->k_cache,
+                                         append->v_cache, append->slot_mapping, p->k_scale,
+                                         p->v_scale, p->num_seqs * query_len_of(p),
+                                         p->num_kv_heads, p->head_dim, p->block_size,
+                                         p->num_blocks, stream, chk);
+      else
+        e = launch_reshape_and_cache(append->k_new, append->v_new, append->k_cache,
+                                     append->v_cache, append->slot_mapping,
+                                     p->num_seqs * query_len_of(p), p->num_kv_heads, p->head_dim,
+                                     p->block_size, p->num_blocks, stream, chk);
     }
     if (e) {
       std::snprintf(where, sizeof(where), "%s: launch", who);
@@ -245,7 +265,7 @@ static pa_status run_decode(const pa_decode_params* p, unsigned char* ws,
     L.part_m = np > 1 ? reinterpret_cast<float*>(ws + w.simt_m) : nullptr;
     L.part_l = np > 1 ? reinterpret_cast<float*>(ws + w.simt_l) : nullptr;
     L.part_acc = np > 1 ? reinterpret_cast<float*>(ws + w.simt_acc) : nullptr;
-    e = launch_decode(L, stream);
+    e = fp4 ? launch_decode_fp4(L, stream) : launch_decode(L, stream);
     if (!e) e = launch_merge(L, stream);
   }
   if (e) {
@@ -279,8 +299,9 @@ static pa_status check_step(const pa_step_host_params* p) {
     return set_error(PA_ERR_INVALID_ARG, "pa_step_host: counts must be positive");
   if (p->num_cow_pairs < 0 || p->num_cow_pairs > 65535)
     return set_error(PA_ERR_INVALID_ARG, "pa_step_host: num_cow_pairs must be in [0, 65535]");
-  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3)
-    return set_error(PA_ERR_INVALID_ARG, "pa_step_host: kv_dtype must be PA_KV_BF16 or PA_KV_FP8_E4M3");
+  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4_E2M1)
+    return set_error(PA_ERR_INVALID_ARG,
+                     "pa_step_host: kv_dtype must be PA_KV_BF16, PA_KV_FP8_E4M3 or PA_KV_FP4_E2M1");
   if (p->query_len < 0 || p->query_len > 1024)
     return set_error(PA_ERR_INVALID_ARG, "pa_step_host: query_len must be in [0, 1024]");
   return PA_OK;
@@ -374,14 +395,16 @@ pa_status pa_device_errors(pa_stream_t stream, uint32_t* flags) {
   if (!flags) return pa::set_error(PA_ERR_INVALID_ARG, "pa_device_errors: flags is NULL");
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return pa::set_cuda_error("pa_device_errors: stream sync", int(e));
-  uint32_t a = 0, b = 0, c = 0, d = 0, qm = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, qm = 0, f4 = 0, d4 = 0;
   int r = pa::read_and_clear_decode_errors(&a);
   if (r == 0) r = pa::read_and_clear_decode_tc_errors(&c);
   if (r == 0) r = pa::read_and_clear_cache_errors(&b);
   if (r == 0) r = pa::read_and_clear_fp8_errors(&d);
   if (r == 0) r = pa::read_and_clear_query_major_errors(&qm);
+  if (r == 0) r = pa::read_and_clear_fp4_errors(&f4);
+  if (r == 0) r = pa::read_and_clear_decode_fp4_errors(&d4);
   if (r != 0) return pa::set_cuda_error("pa_device_errors: read", r);
-  *flags = a | b | c | d | qm;
+  *flags = a | b | c | d | qm | f4 | d4;
   return PA_OK;
 }
 
@@ -514,12 +537,14 @@ pa_status pa_step_host(const pa_step_host_params* p, void* workspace, size_t wor
     if (e != cudaSuccess) return pa::set_cuda_error("pa_step_host: input copy", int(e));
   }
   if (p->num_cow_pairs > 0) {
-    // the 8-bit cache's blocks are the bytes of a bf16 block of half the head_dim
+    // the 8-bit cache's blocks are the bytes of a bf16 block of half the head_dim, the 4-bit
+    // cache's those of one of 9/32
     const int r = pa::launch_copy_blocks(p->k_cache, p->v_cache,
                                          reinterpret_cast<const int32_t*>(ws + sp.in.cow_pairs),
                                          p->num_cow_pairs, p->num_kv_heads,
-                                         p->kv_dtype == PA_KV_FP8_E4M3 ? p->head_dim / 2
-                                                                       : p->head_dim,
+                                         p->kv_dtype == PA_KV_FP8_E4M3   ? p->head_dim / 2
+                                         : p->kv_dtype == PA_KV_FP4_E2M1 ? p->head_dim * 9 / 32
+                                                                         : p->head_dim,
                                          p->block_size, p->num_blocks, stream);
     if (r != 0) return pa::set_cuda_error("pa_step_host: copy_blocks launch", r);
   }
@@ -625,6 +650,91 @@ pa_status pa_copy_blocks_fp8(void* k_cache, void* v_cache, const int32_t* pairs,
   // one byte per element: the same bytes as a bf16 block of head_dim / 2
   return pa_copy_blocks(k_cache, v_cache, pairs, num_pairs, num_kv_heads, head_dim / 2, block_size,
                         num_blocks, stream);
+}
+
+// Shapes and pointers of the 4-bit write and read-back (rows: the bf16 side).
+static pa_status check_fp4_rows(const char* who, const void* k_rows, const void* v_rows,
+                                const void* k_cache, const void* v_cache,
+                                const int64_t* slot_mapping, const float* k_scale,
+                                const float* v_scale, int32_t num_tokens, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t block_size, int32_t num_blocks) {
+  char msg[160];
+  auto fail = [&](pa_status st, const char* what) {
+    std::snprintf(msg, sizeof(msg), "%s: %s", who, what);
+    return pa::set_error(st, msg);
+  };
+  if (num_tokens < 0 || num_kv_heads < 1 || num_blocks < 1)
+    return fail(PA_ERR_INVALID_ARG, "num_tokens >= 0, num_kv_heads >= 1, num_blocks >= 1");
+  if (!pa::block_size_ok(block_size))
+    return fail(PA_ERR_UNSUPPORTED, "block_size must be 8, 16 or 32");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (num_tokens == 0) return PA_OK;
+  if (!k_rows || !v_rows || !k_cache || !v_cache || !slot_mapping || !k_scale || !v_scale)
+    return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!pa::aligned16(k_rows) || !pa::aligned16(v_rows) || !pa::aligned16(k_cache) ||
+      !pa::aligned16(v_cache) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) ||
+      (reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u))
+    return fail(PA_ERR_INVALID_ARG, "misaligned pointer");
+  // one thread per 16 elements, 256 per CTA: keep the grid within gridDim.x
+  if (int64_t(num_tokens) * num_kv_heads * (head_dim / 16) > (int64_t(1) << 38))
+    return fail(PA_ERR_INVALID_ARG, "too many tokens");
+  return PA_OK;
+}
+
+pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_cache,
+                                   void* v_cache, const int64_t* slot_mapping,
+                                   const float* k_scale, const float* v_scale,
+                                   int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, pa_stream_t stream) {
+  const pa_status st = check_fp4_rows("pa_reshape_and_cache_fp4", k_new, v_new, k_cache, v_cache,
+                                      slot_mapping, k_scale, v_scale, num_tokens, num_kv_heads,
+                                      head_dim, block_size, num_blocks);
+  if (st != PA_OK || num_tokens == 0) return st;
+  const int e = pa::launch_reshape_and_cache_fp4(k_new, v_new, k_cache, v_cache, slot_mapping,
+                                                 k_scale, v_scale, num_tokens, num_kv_heads,
+                                                 head_dim, block_size, num_blocks, stream);
+  if (e != 0) return pa::set_cuda_error("pa_reshape_and_cache_fp4: launch", e);
+  return PA_OK;
+}
+
+pa_status pa_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, void* v_out,
+                        const int64_t* slot_mapping, const float* k_scale, const float* v_scale,
+                        int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t block_size, int32_t num_blocks, pa_stream_t stream) {
+  const pa_status st = check_fp4_rows("pa_gather_fp4", k_out, v_out, k_cache, v_cache,
+                                      slot_mapping, k_scale, v_scale, num_tokens, num_kv_heads,
+                                      head_dim, block_size, num_blocks);
+  if (st != PA_OK || num_tokens == 0) return st;
+  const int e = pa::launch_gather_fp4(k_cache, v_cache, k_out, v_out, slot_mapping, k_scale,
+                                      v_scale, num_tokens, num_kv_heads, head_dim, block_size,
+                                      num_blocks, stream);
+  if (e != 0) return pa::set_cuda_error("pa_gather_fp4: launch", e);
+  return PA_OK;
+}
+
+pa_status pa_copy_blocks_fp4(void* k_cache, void* v_cache, const int32_t* pairs,
+                             int32_t num_pairs, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t num_blocks, pa_stream_t stream) {
+  if (num_pairs < 0 || num_pairs > 65535 || num_kv_heads < 1 || num_blocks < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_copy_blocks_fp4: num_pairs in [0, 65535], num_kv_heads >= 1, "
+                         "num_blocks >= 1");
+  if (!pa::block_size_ok(block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_copy_blocks_fp4: block_size must be 8, 16 or 32");
+  if (head_dim != 64 && head_dim != 128)
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_copy_blocks_fp4: head_dim must be 64 or 128");
+  if (num_pairs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !pairs)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_copy_blocks_fp4: a required pointer is NULL");
+  if (!pa::aligned16(k_cache) || !pa::aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(pairs) & 3u))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_copy_blocks_fp4: misaligned pointer");
+  // 9/16 byte an element: the bytes of a bf16 block of 9/32 the head_dim
+  const int e = pa::launch_copy_blocks(k_cache, v_cache, pairs, num_pairs, num_kv_heads,
+                                       head_dim * 9 / 32, block_size, num_blocks, stream);
+  if (e != 0) return pa::set_cuda_error("pa_copy_blocks_fp4: launch", e);
+  return PA_OK;
 }
 
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int32_t num_pairs,

@@ -131,6 +131,21 @@ __device__ __forceinline__ int64_t query_source_row(const QueryMap& m, int v, in
 }
 #endif
 
+// Column layout of the 4-bit decode: the query rows of a KV head are the
+// columns of its products, token by token, in 8-column tiles (one or two); a
+// sequence with more new tokens than those hold is decoded as several groups.
+struct Fp4Columns {
+  int n_tiles, q_group, n_groups;
+};
+inline Fp4Columns fp4_columns(const pa_decode_params* p) {
+  const int g = p->num_q_heads / p->num_kv_heads, q = query_len_of(p);
+  Fp4Columns c;
+  c.n_tiles = g * q <= 8 ? 1 : 2;
+  c.q_group = q < 8 * c.n_tiles / g ? q : 8 * c.n_tiles / g;
+  c.n_groups = (q + c.q_group - 1) / c.q_group;
+  return c;
+}
+
 // Bytes at the start of every decode workspace (reserved).
 constexpr size_t kWorkspaceHeaderBytes = 256;
 
@@ -190,6 +205,19 @@ int launch_reshape_and_cache_fp8(const void* k_new, const void* v_new, void* k_c
                                  int32_t head_dim, int32_t block_size, int32_t num_blocks,
                                  void* stream);
 int read_and_clear_fp8_errors(uint32_t* flags);
+// 4-bit cache (pa_fp4.cu, pa_decode_fp4.cu)
+int launch_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_cache,
+                                 void* v_cache, const int64_t* slot_mapping, const float* k_scale,
+                                 const float* v_scale, int32_t num_tokens, int32_t num_kv_heads,
+                                 int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                 void* stream, const AppendCheck& check = AppendCheck());
+int launch_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, void* v_out,
+                      const int64_t* slot_mapping, const float* k_scale, const float* v_scale,
+                      int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                      int32_t block_size, int32_t num_blocks, void* stream);
+int launch_decode_fp4(const DecodeLaunch& L, void* stream);  // then launch_merge
+int read_and_clear_fp4_errors(uint32_t* flags);
+int read_and_clear_decode_fp4_errors(uint32_t* flags);
 // Query preparation for the bf16 tensor-core decode with several new tokens
 // per sequence (pa_query.cu): the rows of q ([B][query_len][Hq][D] bf16) in
 // the column layout, padded to n_pad rows with zeros ([B][n_pad][D]).
