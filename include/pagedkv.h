@@ -92,6 +92,8 @@ typedef enum {
 #define PA_DEVERR_APPEND_SLOT 0x20u  /* pa_append_decode: a slot_mapping entry is not the slot
                                         of its token (context_lens[b]-1 for one new token per
                                         sequence); that token is not written */
+#define PA_DEVERR_KEEP 0x40u         /* pa_evict_compact: a keep entry that does not ascend or is
+                                        past the source table; that row is not moved */
 
 const char* pa_status_string(pa_status s);
 const char* pa_last_error(void);
@@ -488,6 +490,115 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int
                          int32_t num_blocks, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Eviction: fewer cached tokens instead of smaller ones. The pages leave open
+ * which tokens a cache under pressure gives up; here the most recent ones
+ * stay, and of the others those that attention has looked at most. A step is
+ *   pa_token_weights   what this step's queries look at, accumulated
+ *   pa_evict_select    the tokens to keep under a budget
+ *   pa_pool_compact    (host pool) the blocks that hold them
+ *   pa_evict_compact   their rows moved there
+ * after which the sequence is an ordinary one of new_lens[b] tokens: its next
+ * token is appended behind them (keys keep the position encoding that they
+ * were written with).
+ *
+ * pa_token_weights -- for every sequence b and cached token t
+ *   token_weights[b][t] (+)= sum over new tokens i and query heads h of
+ *                            softmax(scale * q[b][i][h] . K_b)_t
+ * over the keys that new token i sees (the causal rule of pa_decode). fp32;
+ * summed in a fixed order. Entries t >= context_lens[b] are left as they were,
+ * and so is the whole row of a sequence of length 0 or with fewer keys than
+ * new tokens (the latter sets PA_DEVERR_CONTEXT_LEN). Reads K only, of any of
+ * the three caches, at every block size. num_seqs * ceil(query_len / (16 / G))
+ * <= 65535 (else PA_ERR_UNSUPPORTED).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* q;               /* bf16 [num_seqs][query_len][num_q_heads][head_dim] */
+  const void* k_cache;         /* as in pa_decode_params, of type kv_dtype */
+  const int32_t* block_tables; /* int32 [num_seqs][max_blocks_per_seq] */
+  const int32_t* context_lens; /* int32 [num_seqs], the new tokens included */
+  float* token_weights;        /* float [num_seqs][weights_stride], written */
+  int32_t weights_stride;      /* >= min(max_context_len, max_blocks_per_seq * block_size) */
+  int32_t max_blocks_per_seq;
+  int32_t num_seqs;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t max_context_len;     /* host-known upper bound of every context_lens[b] (>= 1) */
+  float scale;
+  int32_t kv_dtype;            /* PA_KV_BF16, PA_KV_FP8_E4M3 or PA_KV_FP4_E2M1 */
+  const float* k_scale;        /* the 8-bit and 4-bit caches only: float [num_kv_heads] */
+  int32_t query_len;           /* new tokens per sequence (0 or 1 = one), up to 1024 */
+  int32_t accumulate;          /* nonzero: add to token_weights; 0: overwrite entries
+                                  [0, context_lens[b]) */
+} pa_token_weights_params;
+
+/* The scores of every (new token, query head) pass through the workspace:
+ * 4 * num_seqs * query_len * num_q_heads * max_context_len bytes and a little
+ * more. Caller-owned, 256-byte aligned, contents on entry do not matter; two
+ * calls in flight at once must not share it. 0 if the params are invalid. */
+size_t pa_token_weights_workspace_size(const pa_token_weights_params* p);
+pa_status pa_token_weights(const pa_token_weights_params* p, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_evict_select -- the tokens each sequence keeps: all of them if it has at
+ * most `budget`, else its last `recent` ones and, of the others, the budget -
+ * recent with the largest token_weights (ties: the lower index; +0 and -0 are
+ * equal, a NaN ranks below every number).
+ *   keep      int32 [num_seqs][budget]: their indices, ascending; -1 behind
+ *   new_lens  int32 [num_seqs]: min(context_lens[b], budget)
+ * token_weights: float [num_seqs][weights_stride]; a length beyond
+ * weights_stride is cut to it and sets PA_DEVERR_CONTEXT_LEN. budget >= 1,
+ * recent in [0, budget]. No workspace.
+ * ---------------------------------------------------------------------- */
+pa_status pa_evict_select(const float* token_weights, const int32_t* context_lens, int32_t* keep,
+                          int32_t* new_lens, int32_t num_seqs, int32_t weights_stride,
+                          int32_t budget, int32_t recent, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_evict_compact -- the move: for every sequence b and j < new_lens[b], the
+ * K and V rows of token keep[b][j] (through block_tables) become those of
+ * token j (through dst_tables), bit for bit, for every KV head.
+ *  - dst_tables may be block_tables itself (in place), or name other blocks
+ *    at some indices: entry j must be a block that none of the call's source
+ *    tables holds, or the source's own entry j, held by no other sequence of
+ *    the call unless every row of the block stays where it is; no two
+ *    sequences may write the same block. pa_pool_compact produces such tables.
+ *    Rows that already are where they belong are not touched.
+ *  - keep must ascend strictly (what pa_evict_select produces); an entry below
+ *    its own index or past the source table is not moved and sets
+ *    PA_DEVERR_KEEP.
+ *  - new_lens beyond keep_stride or the destination table is cut and sets
+ *    PA_DEVERR_CONTEXT_LEN; a table entry outside [0, num_blocks) moves nothing
+ *    and sets PA_DEVERR_TABLE_ENTRY.
+ *  - token_weights, if not NULL, is compacted the same way in place, and its
+ *    rows are zeroed from new_lens[b] on. Other rows behind the kept tokens are
+ *    left as they were.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* k_cache;               /* of type kv_dtype, as in pa_decode_params; written */
+  void* v_cache;
+  const int32_t* block_tables; /* int32 [num_seqs][max_blocks_per_seq] */
+  const int32_t* dst_tables;   /* int32 [num_seqs][max_dst_blocks_per_seq] */
+  const int32_t* keep;         /* int32 [num_seqs][keep_stride] */
+  const int32_t* new_lens;     /* int32 [num_seqs] */
+  float* token_weights;        /* float [num_seqs][weights_stride] or NULL */
+  int32_t weights_stride;
+  int32_t max_blocks_per_seq;
+  int32_t max_dst_blocks_per_seq;
+  int32_t keep_stride;         /* the budget given to pa_evict_select */
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t head_dim;            /* 64 or 128 */
+  int32_t block_size;          /* 8, 16 or 32 */
+  int32_t num_blocks;
+  int32_t kv_dtype;
+} pa_evict_compact_params;
+pa_status pa_evict_compact(const pa_evict_compact_params* p, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Host block pool [P1 §Paged attention; P2 §Prefix Caching and Copy-on-Write;
  * P3 §The architecture]. All memory here is host memory owned by the pool.
  * Not thread-safe: one pool per thread, or external locking.
@@ -544,6 +655,18 @@ pa_status pa_seq_append_slot(pa_pool* pool, int32_t seq, int64_t* slot, int32_t 
  * nothing: on PA_ERR_OOM the pool is unchanged. */
 pa_status pa_seq_append_tokens(pa_pool* pool, int32_t seq, int32_t n, int64_t* slots,
                                int32_t* cow_pairs, int32_t* num_cow);
+/* Shorten the sequences seqs[0..n) (distinct) to new_lens[0..n) tokens, each at
+ * most the sequence's length, in blocks that they may write: the pool's half of
+ * pa_evict_compact for a batch. A sequence that keeps its length keeps its
+ * table. Of the others the first ceil(new_len/block_size) entries stay, except
+ * that one whose block is shared (refcount > 1 before the call) or in the prefix
+ * cache is replaced by a fresh block; the replaced and the remaining blocks are
+ * released, after every fresh one has been taken. Read the tables before
+ * (block_tables) and after (dst_tables). The rows still lie in the old blocks,
+ * released ones among them, until the move has run: enqueue it before any work
+ * that writes a block handed out after this call. All or nothing: PA_ERR_OOM
+ * leaves the pool unchanged. */
+pa_status pa_pool_compact(pa_pool* pool, const int32_t* seqs, const int32_t* new_lens, int32_t n);
 pa_status pa_seq_length(const pa_pool* pool, int32_t seq, int32_t* length);
 /* Copy the sequence's table into out[0..cap); *n_blocks = its block count. */
 pa_status pa_seq_table(const pa_pool* pool, int32_t seq, int32_t* out, int32_t cap,

@@ -30,6 +30,7 @@ DEVERR_SLOT = 0x4
 DEVERR_COPY_PAIR = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_APPEND_SLOT = 0x20
+DEVERR_KEEP = 0x40
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
@@ -42,6 +43,8 @@ EXPORTED_SYMBOLS = [
     "pa_reshape_and_cache", "pa_reshape_and_cache_fp8", "pa_copy_blocks_fp8",
     "pa_reshape_and_cache_fp4", "pa_gather_fp4", "pa_copy_blocks_fp4",
     "pa_copy_blocks",
+    "pa_token_weights_workspace_size", "pa_token_weights", "pa_evict_select",
+    "pa_evict_compact", "pa_pool_compact",
     "pa_pool_create", "pa_pool_destroy", "pa_pool_alloc", "pa_pool_incref", "pa_pool_decref",
     "pa_pool_refcount", "pa_pool_stats", "pa_seq_create", "pa_seq_free", "pa_seq_fork",
     "pa_seq_append_slot", "pa_seq_append_tokens", "pa_seq_length", "pa_seq_table",
@@ -84,6 +87,34 @@ class AppendParams(ctypes.Structure):
         ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
         ("slot_mapping", ctypes.c_void_p),
         ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+    ]
+
+
+class TokenWeightsParams(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_cache", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+        ("token_weights", ctypes.c_void_p), ("weights_stride", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32), ("max_context_len", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("kv_dtype", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
+        ("query_len", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+    ]
+
+
+class EvictCompactParams(ctypes.Structure):
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p), ("dst_tables", ctypes.c_void_p),
+        ("keep", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+        ("token_weights", ctypes.c_void_p), ("weights_stride", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32), ("max_dst_blocks_per_seq", ctypes.c_int32),
+        ("keep_stride", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
     ]
 
 
@@ -153,6 +184,11 @@ def load():
                                      ctypes.c_int),
         "pa_gather_fp4": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp], ctypes.c_int),
         "pa_copy_blocks_fp4": ([vp, vp, vp, i32, i32, i32, i32, i32, vp], ctypes.c_int),
+        "pa_token_weights_workspace_size": ([P(TokenWeightsParams)], sz),
+        "pa_token_weights": ([P(TokenWeightsParams), vp, sz, vp], ctypes.c_int),
+        "pa_evict_select": ([vp, vp, vp, vp, i32, i32, i32, i32, vp], ctypes.c_int),
+        "pa_evict_compact": ([P(EvictCompactParams), vp], ctypes.c_int),
+        "pa_pool_compact": ([vp, vp, vp, i32], ctypes.c_int),
         "pa_pool_create": ([i32, i32, vp, P(vp)], ctypes.c_int),
         "pa_pool_destroy": ([vp], None),
         "pa_pool_alloc": ([vp, P(i32)], ctypes.c_int),
@@ -630,6 +666,135 @@ def pa_copy_blocks_fp4(k_cache, v_cache, pairs, stream=None) -> None:
         _stream_handle(stream)), "pa_copy_blocks_fp4")
 
 
+def make_token_weights_params(q, k_cache, block_tables, context_lens, max_context_len: int,
+                              token_weights, accumulate: bool = True,
+                              scale: Optional[float] = None, k_scale=None) -> TokenWeightsParams:
+    """Marshal a pa_token_weights call: q bf16 [B][Hq][D] or [B][Q][Hq][D], a K
+    cache of any type (``kv_cache_format``; uint8 ones need k_scale), token_weights
+    float32 [B][stride]."""
+    import torch
+
+    if q.dim() == 4:
+        B, QL, Hq, D = q.shape
+    else:
+        (B, Hq, D), QL = q.shape, 0
+    fmt, D2 = kv_cache_format(k_cache)
+    NB, Hkv, BS, _ = k_cache.shape
+    if D2 != D:
+        raise ValueError("q and k_cache differ in head_dim")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
+    if token_weights.dim() != 2 or token_weights.shape[0] != B:
+        raise ValueError("token_weights must be [num_seqs][stride]")
+    p = TokenWeightsParams()
+    p.q = _dev_ptr(q, torch.bfloat16, "q")
+    p.k_cache = _dev_ptr(k_cache, torch.bfloat16 if fmt == KV_BF16 else torch.uint8, "k_cache")
+    p.block_tables = _dev_ptr(block_tables, torch.int32, "block_tables")
+    p.context_lens = _dev_ptr(context_lens, torch.int32, "context_lens")
+    p.token_weights = _dev_ptr(token_weights, torch.float32, "token_weights")
+    p.weights_stride = token_weights.shape[1]
+    p.max_blocks_per_seq = block_tables.shape[1]
+    p.num_seqs, p.num_q_heads, p.num_kv_heads = B, Hq, Hkv
+    p.head_dim, p.block_size, p.num_blocks = D, BS, NB
+    p.max_context_len = int(max_context_len)
+    p.scale = float(1.0 / math.sqrt(D) if scale is None else scale)
+    p.kv_dtype = fmt
+    if fmt != KV_BF16:
+        if k_scale is None or k_scale.numel() != Hkv:
+            raise ValueError("the 8-bit and 4-bit caches need k_scale [num_kv_heads]")
+        p.k_scale = _dev_ptr(k_scale, torch.float32, "k_scale")
+    p.query_len = int(QL)
+    p.accumulate = int(bool(accumulate))
+    return p
+
+
+def pa_token_weights_workspace_size(q, k_cache, block_tables, context_lens, max_context_len: int,
+                                    token_weights, k_scale=None) -> int:
+    """Workspace bytes of ``pa_token_weights`` for these arguments."""
+    p = make_token_weights_params(q, k_cache, block_tables, context_lens, max_context_len,
+                                  token_weights, k_scale=k_scale)
+    return int(load().pa_token_weights_workspace_size(ctypes.byref(p)))
+
+
+def pa_token_weights(q, k_cache, block_tables, context_lens, max_context_len: int, token_weights,
+                     accumulate: bool = True, scale: Optional[float] = None, workspace=None,
+                     stream=None, k_scale=None):
+    """The attention weight that the new tokens give to every cached token, summed
+    over query heads and new tokens, added to (or, without ``accumulate``,
+    written over) ``token_weights`` [B][stride] for t < context_lens[b]; returns
+    it. Reads K only."""
+    import torch
+
+    lib = load()
+    p = make_token_weights_params(q, k_cache, block_tables, context_lens, max_context_len,
+                                  token_weights, accumulate, scale, k_scale)
+    if workspace is None:
+        need = int(lib.pa_token_weights_workspace_size(ctypes.byref(p)))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _check(lib.pa_token_weights(ctypes.byref(p), _dev_ptr(workspace, torch.uint8, "workspace"),
+                                workspace.numel(), _stream_handle(stream)), "pa_token_weights")
+    return token_weights
+
+
+def pa_evict_select(token_weights, context_lens, budget: int, recent: int = 0, keep=None,
+                    new_lens=None, stream=None):
+    """The tokens every sequence keeps under ``budget``: the last ``recent`` ones
+    and those with the largest weights. Returns (keep int32 [B][budget], ascending,
+    -1 behind; new_lens int32 [B])."""
+    import torch
+
+    if token_weights.dim() != 2 or tuple(context_lens.shape) != (token_weights.shape[0],):
+        raise ValueError("token_weights must be [num_seqs][stride], context_lens [num_seqs]")
+    B = token_weights.shape[0]
+    if keep is None:
+        keep = torch.empty((B, max(int(budget), 0)), dtype=torch.int32, device=token_weights.device)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=token_weights.device)
+    if tuple(keep.shape) != (B, budget) or tuple(new_lens.shape) != (B,):
+        raise ValueError("keep must be [num_seqs][budget], new_lens [num_seqs]")
+    _check(load().pa_evict_select(
+        _dev_ptr(token_weights, torch.float32, "token_weights"),
+        _dev_ptr(context_lens, torch.int32, "context_lens"), _dev_ptr(keep, torch.int32, "keep"),
+        _dev_ptr(new_lens, torch.int32, "new_lens"), B, token_weights.shape[1], int(budget),
+        int(recent), _stream_handle(stream)), "pa_evict_select")
+    return keep, new_lens
+
+
+def pa_evict_compact(k_cache, v_cache, block_tables, dst_tables, keep, new_lens,
+                     token_weights=None, stream=None) -> None:
+    """Move the kept tokens' rows: token keep[b][j] of ``block_tables`` becomes
+    token j of ``dst_tables`` (which may be ``block_tables``), for j <
+    new_lens[b]. ``token_weights`` is compacted along, zeroed behind."""
+    import torch
+
+    fmt, D = kv_cache_format(k_cache)
+    NB, Hkv, BS, _ = k_cache.shape
+    B = new_lens.shape[0]
+    if not _v_cache_ok(fmt, k_cache, v_cache):
+        raise ValueError("shape mismatch between k_cache and v_cache")
+    if block_tables.dim() != 2 or dst_tables.dim() != 2 or keep.dim() != 2 \
+            or block_tables.shape[0] != B or dst_tables.shape[0] != B or keep.shape[0] != B \
+            or (token_weights is not None
+                and (token_weights.dim() != 2 or token_weights.shape[0] != B)):
+        raise ValueError("block_tables, dst_tables, keep and token_weights must be [num_seqs][...]")
+    cache_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
+    p = EvictCompactParams()
+    p.k_cache = _dev_ptr(k_cache, cache_dtype, "k_cache")
+    p.v_cache = _dev_ptr(v_cache, cache_dtype, "v_cache")
+    p.block_tables = _dev_ptr(block_tables, torch.int32, "block_tables")
+    p.dst_tables = _dev_ptr(dst_tables, torch.int32, "dst_tables")
+    p.keep = _dev_ptr(keep, torch.int32, "keep")
+    p.new_lens = _dev_ptr(new_lens, torch.int32, "new_lens")
+    if token_weights is not None:
+        p.token_weights = _dev_ptr(token_weights, torch.float32, "token_weights")
+        p.weights_stride = token_weights.shape[1]
+    p.max_blocks_per_seq, p.max_dst_blocks_per_seq = block_tables.shape[1], dst_tables.shape[1]
+    p.keep_stride = keep.shape[1]
+    p.num_seqs, p.num_kv_heads, p.head_dim, p.block_size, p.num_blocks = B, Hkv, D, BS, NB
+    p.kv_dtype = fmt
+    _check(load().pa_evict_compact(ctypes.byref(p), _stream_handle(stream)), "pa_evict_compact")
+
+
 def pa_device_errors(stream=None) -> int:
     flags = ctypes.c_uint32(0)
     _check(load().pa_device_errors(_stream_handle(stream), ctypes.byref(flags)), "pa_device_errors")
@@ -730,6 +895,16 @@ class Pool:
         _check(self._lib.pa_seq_table(self._h, seq, buf.ctypes.data, buf.shape[0],
                                       ctypes.byref(n)), "pa_seq_table")
         return buf[:n.value].tolist()
+
+    def compact(self, seqs: Sequence[int], new_lens: Sequence[int]) -> None:
+        """Shorten the sequences in blocks they may write (for ``pa_evict_compact``:
+        export the tables before and after)."""
+        s = np.ascontiguousarray(np.asarray(seqs, dtype=np.int32))
+        n = np.ascontiguousarray(np.asarray(new_lens, dtype=np.int32))
+        if s.shape != n.shape or s.ndim != 1:
+            raise ValueError("seqs and new_lens must be lists of the same length")
+        _check(self._lib.pa_pool_compact(self._h, s.ctypes.data, n.ctypes.data, len(s)),
+               "pa_pool_compact")
 
     def export(self, seqs: Sequence[int], max_blocks: int):
         s = np.ascontiguousarray(np.asarray(seqs, dtype=np.int32))

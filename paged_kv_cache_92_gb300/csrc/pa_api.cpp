@@ -19,14 +19,19 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// The 4-bit decode's own choice: partitions short enough for 16 CTAs an SM of
-// a 152-SM GPU, so that ragged lengths even out, within [128, 4096] tokens.
+// Keys per CTA of the 4-bit decode and of the token weights: short enough for
+// 16 CTAs an SM of a 152-SM GPU, so that ragged lengths even out, within
+// [128, 4096] tokens. `units`: (sequence, KV head, column group)s.
+int auto_partition_tokens(int64_t cap, int64_t units) {
+  const int64_t pt = (cap * units / (152 * 16) + 127) / 128 * 128;
+  return pt < 128 ? 128 : (pt > kMaxPartitionTokens ? kMaxPartitionTokens : int(pt));
+}
+
 int fp4_partition_tokens(const pa_decode_params* p) {
   const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
   const int64_t cap = p->max_context_len < table ? p->max_context_len : table;
-  const int64_t units = int64_t(p->num_seqs) * p->num_kv_heads * fp4_columns(p).n_groups;
-  int64_t pt = (cap * units / (152 * 16) + 127) / 128 * 128;
-  return pt < 128 ? 128 : (pt > kMaxPartitionTokens ? kMaxPartitionTokens : int(pt));
+  const MmaColumns c = mma_columns(p->num_q_heads / p->num_kv_heads, query_len_of(p));
+  return auto_partition_tokens(cap, int64_t(p->num_seqs) * p->num_kv_heads * c.n_groups);
 }
 
 int resolve_partition_tokens(const pa_decode_params* p) {
@@ -395,7 +400,7 @@ pa_status pa_device_errors(pa_stream_t stream, uint32_t* flags) {
   if (!flags) return pa::set_error(PA_ERR_INVALID_ARG, "pa_device_errors: flags is NULL");
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return pa::set_cuda_error("pa_device_errors: stream sync", int(e));
-  uint32_t a = 0, b = 0, c = 0, d = 0, qm = 0, f4 = 0, d4 = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, qm = 0, f4 = 0, d4 = 0, tw = 0, ev = 0;
   int r = pa::read_and_clear_decode_errors(&a);
   if (r == 0) r = pa::read_and_clear_decode_tc_errors(&c);
   if (r == 0) r = pa::read_and_clear_cache_errors(&b);
@@ -403,8 +408,10 @@ pa_status pa_device_errors(pa_stream_t stream, uint32_t* flags) {
   if (r == 0) r = pa::read_and_clear_query_major_errors(&qm);
   if (r == 0) r = pa::read_and_clear_fp4_errors(&f4);
   if (r == 0) r = pa::read_and_clear_decode_fp4_errors(&d4);
+  if (r == 0) r = pa::read_and_clear_weights_errors(&tw);
+  if (r == 0) r = pa::read_and_clear_evict_errors(&ev);
   if (r != 0) return pa::set_cuda_error("pa_device_errors: read", r);
-  *flags = a | b | c | d | qm | f4 | d4;
+  *flags = a | b | c | d | qm | f4 | d4 | tw | ev;
   return PA_OK;
 }
 
@@ -757,6 +764,162 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int
   const int e = pa::launch_copy_blocks(k_cache, v_cache, pairs, num_pairs, num_kv_heads, head_dim,
                                        block_size, num_blocks, stream);
   if (e != 0) return pa::set_cuda_error("pa_copy_blocks: launch", e);
+  return PA_OK;
+}
+
+// ---- token weights and eviction
+
+static pa_status check_token_weights(const pa_token_weights_params* p, bool need_pointers) {
+  if (!p) return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: params is NULL");
+  const int q = p->query_len > 1 ? p->query_len : 1;
+  if (p->num_seqs < 0 || p->num_seqs > 65535)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: num_seqs must be in [0, 65535]");
+  if (p->num_q_heads < 1 || p->num_kv_heads < 1 || p->num_kv_heads > 65535 ||
+      p->num_q_heads % p->num_kv_heads != 0)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: num_q_heads must be a positive multiple of "
+                         "num_kv_heads (<= 65535)");
+  if (!pa::block_size_ok(p->block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_token_weights: block_size must be 8, 16 or 32");
+  if (p->head_dim != 64 && p->head_dim != 128)
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_token_weights: head_dim must be 64 or 128");
+  const int g = p->num_q_heads / p->num_kv_heads;
+  if (g != 1 && g != 2 && g != 4 && g != 8)
+    return pa::set_error(PA_ERR_UNSUPPORTED,
+                         "pa_token_weights: query heads per KV head must be 1, 2, 4 or 8");
+  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4_E2M1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: kv_dtype must be PA_KV_BF16, PA_KV_FP8_E4M3 or "
+                         "PA_KV_FP4_E2M1");
+  if (p->query_len < 0 || p->query_len > 1024)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: query_len must be in [0, 1024]");
+  if (int64_t(p->num_seqs) * pa::mma_columns(g, q).n_groups > 65535)
+    return pa::set_error(PA_ERR_UNSUPPORTED,
+                         "pa_token_weights: num_seqs * ceil(query_len / (16 / G)) must be <= 65535");
+  if (p->num_blocks < 1 || p->max_blocks_per_seq < 1 || p->max_context_len < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: num_blocks, max_blocks_per_seq and max_context_len "
+                         "must be positive");
+  if (int64_t(p->max_blocks_per_seq) * p->block_size > INT32_MAX - 64)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: max_blocks_per_seq too large");
+  if (!(p->scale > 0.0f))
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: scale must be a positive finite number");
+  const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
+  if (p->weights_stride < (p->max_context_len < table ? p->max_context_len : table))
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: weights_stride must cover min(max_context_len, "
+                         "max_blocks_per_seq * block_size) tokens");
+  if (need_pointers && p->num_seqs > 0) {
+    if (!p->q || !p->k_cache || !p->block_tables || !p->context_lens || !p->token_weights ||
+        (p->kv_dtype != PA_KV_BF16 && !p->k_scale))
+      return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: a required pointer is NULL");
+    if (!pa::aligned16(p->q) || !pa::aligned16(p->k_cache))
+      return pa::set_error(PA_ERR_INVALID_ARG,
+                           "pa_token_weights: q and k_cache must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(p->block_tables) & 3u) ||
+        (reinterpret_cast<uintptr_t>(p->context_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(p->token_weights) & 3u) ||
+        (p->kv_dtype != PA_KV_BF16 && (reinterpret_cast<uintptr_t>(p->k_scale) & 3u)))
+      return pa::set_error(PA_ERR_INVALID_ARG,
+                           "pa_token_weights: 4-byte arrays must be 4-byte aligned");
+  }
+  return PA_OK;
+}
+
+static pa::TokenWeightsSpace token_weights_space(const pa_token_weights_params* p) {
+  pa::TokenWeightsSpace s{};
+  const int q = p->query_len > 1 ? p->query_len : 1;
+  const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
+  s.cap = int(p->max_context_len < table ? p->max_context_len : table);
+  s.score_stride = (int64_t(s.cap) + 31) / 32 * 32;
+  const pa::MmaColumns c = pa::mma_columns(p->num_q_heads / p->num_kv_heads, q);
+  s.partition_tokens =
+      pa::auto_partition_tokens(s.cap, int64_t(p->num_seqs) * p->num_kv_heads * c.n_groups);
+  s.num_partitions = (s.cap + s.partition_tokens - 1) / s.partition_tokens;
+  const size_t rows = size_t(p->num_seqs) * q * p->num_q_heads;
+  s.part = pa::kWorkspaceHeaderBytes;
+  s.scores = s.part + pa::round_up(rows * s.num_partitions * 2 * sizeof(float), 256);
+  s.total = s.scores + pa::round_up(rows * s.score_stride * sizeof(float), 256);
+  return s;
+}
+
+size_t pa_token_weights_workspace_size(const pa_token_weights_params* p) {
+  if (check_token_weights(p, false) != PA_OK) return 0;
+  return token_weights_space(p).total;
+}
+
+pa_status pa_token_weights(const pa_token_weights_params* p, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream) {
+  const pa_status st = check_token_weights(p, true);
+  if (st != PA_OK) return st;
+  if (p->num_seqs == 0) return PA_OK;
+  const pa::TokenWeightsSpace s = token_weights_space(p);
+  if (!workspace || workspace_bytes < s.total)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: workspace smaller than "
+                         "pa_token_weights_workspace_size()");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: workspace must be 256-byte aligned");
+  const int e = pa::launch_token_weights(p, s, static_cast<unsigned char*>(workspace), stream);
+  if (e != 0) return pa::set_cuda_error("pa_token_weights: launch", e);
+  return PA_OK;
+}
+
+pa_status pa_evict_select(const float* token_weights, const int32_t* context_lens, int32_t* keep,
+                          int32_t* new_lens, int32_t num_seqs, int32_t weights_stride,
+                          int32_t budget, int32_t recent, pa_stream_t stream) {
+  if (num_seqs < 0 || weights_stride < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_evict_select: num_seqs >= 0 and weights_stride >= 1");
+  if (budget < 1 || recent < 0 || recent > budget)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_evict_select: budget >= 1 and recent in [0, budget]");
+  if (num_seqs == 0) return PA_OK;
+  if (!token_weights || !context_lens || !keep || !new_lens)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_select: a required pointer is NULL");
+  if ((reinterpret_cast<uintptr_t>(token_weights) & 3u) ||
+      (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(keep) & 3u) || (reinterpret_cast<uintptr_t>(new_lens) & 3u))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_select: misaligned pointer");
+  const int e = pa::launch_evict_select(token_weights, context_lens, keep, new_lens, num_seqs,
+                                        weights_stride, budget, recent, stream);
+  if (e != 0) return pa::set_cuda_error("pa_evict_select: launch", e);
+  return PA_OK;
+}
+
+pa_status pa_evict_compact(const pa_evict_compact_params* p, pa_stream_t stream) {
+  if (!p) return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: params is NULL");
+  if (p->num_seqs < 0 || p->num_seqs > 65535 || p->num_kv_heads < 1 || p->num_blocks < 1 ||
+      p->max_blocks_per_seq < 1 || p->max_dst_blocks_per_seq < 1 || p->keep_stride < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_evict_compact: num_seqs in [0, 65535], the other counts positive");
+  if (!pa::block_size_ok(p->block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_evict_compact: block_size must be 8, 16 or 32");
+  if (p->head_dim != 64 && p->head_dim != 128)
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_evict_compact: head_dim must be 64 or 128");
+  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4_E2M1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_evict_compact: kv_dtype must be PA_KV_BF16, PA_KV_FP8_E4M3 or "
+                         "PA_KV_FP4_E2M1");
+  if (int64_t(p->max_blocks_per_seq) * p->block_size > INT32_MAX ||
+      int64_t(p->max_dst_blocks_per_seq) * p->block_size > INT32_MAX)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: table rows too long");
+  if (p->token_weights && p->weights_stride < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: weights_stride must be positive");
+  if (p->num_seqs == 0) return PA_OK;
+  if (!p->k_cache || !p->v_cache || !p->block_tables || !p->dst_tables || !p->keep || !p->new_lens)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: a required pointer is NULL");
+  if (!pa::aligned16(p->k_cache) || !pa::aligned16(p->v_cache) ||
+      (reinterpret_cast<uintptr_t>(p->block_tables) & 3u) ||
+      (reinterpret_cast<uintptr_t>(p->dst_tables) & 3u) ||
+      (reinterpret_cast<uintptr_t>(p->keep) & 3u) ||
+      (reinterpret_cast<uintptr_t>(p->new_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(p->token_weights) & 3u))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: misaligned pointer");
+  const int e = pa::launch_evict_compact(p, stream);
+  if (e != 0) return pa::set_cuda_error("pa_evict_compact: launch", e);
   return PA_OK;
 }
 

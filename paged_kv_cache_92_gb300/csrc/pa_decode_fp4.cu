@@ -94,7 +94,6 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
     paged_decode_fp4_kernel(const Fp4Decode P) {
   using C = Cfg<D, NT, BS>;
   constexpr int ST = C::ST, NBK = C::NBK, TILE = C::TILE;
-  constexpr int KW = D / 32;  // code words of a lane's share of a K row (D / 4 elements)
   constexpr int VW = D / 64;  // code words of a lane's share of a V row (D / 8 elements)
   const int part = blockIdx.x, head = blockIdx.y;
   const int b = blockIdx.z / P.n_groups, grp = blockIdx.z - b * P.n_groups;
@@ -175,43 +174,16 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
   if (lane == 0)
     for (int i = 0; i < ST && i < n_my; ++i) issue(i);
 
-  // Queries as the B operand: column nt * 8 + g, elements [t * D/4, + D/4) of
-  // its row, scaled by a power of two so that the largest lies in [2^12, 2^13).
-  uint32_t qf[NT][2 * KW][2];
-  float factor[NT][2];  // of columns 2t and 2t+1: softmax scale * K scale / that power
+  // Queries as the B operand (columns nt * 8 + g), scaled into f16's range.
+  uint32_t qf[NT][D / 16][2];
+  float factor[NT][2];  // of columns 2t and 2t+1: softmax scale * K scale / the row's scaling
   int see[NT][2];       // keys that columns 2t and 2t+1 see
   const float kfac = P.scale_log2 * P.k_scale[head];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int n = nt * 8 + g;
-    float x[8 * KW];
-#pragma unroll
-    for (int i = 0; i < 8 * KW; ++i) x[i] = 0.0f;
-    if (n < n_cols) {
-      const uint4* src = reinterpret_cast<const uint4*>(P.q + q_row(n) * D + t * (D / 4));
-#pragma unroll
-      for (int c = 0; c < KW; ++c) {
-        float f[8];
-        dev::unpack8(src[c], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[c * 8 + i] = f[i];
-      }
-    }
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8 * KW; ++i) amax = fmaxf(amax, fabsf(x[i]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    int e = 0;
-    if (amax > 0.0f && amax <= 3.4e38f) (void)frexpf(amax, &e);  // amax < 2^e
-    e = max(e, -100);
-    const float a = ldexpf(1.0f, 13 - e);  // e in [-100, 128]: a normal power of two
-#pragma unroll
-    for (int s = 0; s < 2 * KW; ++s) {
-      qf[nt][s][0] = dev::pack_f16(x[4 * s] * a, x[4 * s + 1] * a);
-      qf[nt][s][1] = dev::pack_f16(x[4 * s + 2] * a, x[4 * s + 3] * a);
-    }
-    const float f = kfac * ldexpf(1.0f, e - 13);
+    const float f = kfac * dev::query_fragment<PA_KV_FP4_E2M1, D>(
+                               n < n_cols ? P.q + q_row(n) * D : nullptr, t, qf[nt]);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       factor[nt][c] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + c));
@@ -257,42 +229,13 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[h][nt][j] = 0.0f;
-      uint32_t w[2][KW], sc[2][VW];
+      dev::KeyRow<PA_KV_FP4_E2M1, D> rows[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = h * 16 + r * 8 + row_g;
-        const unsigned char* tile = kt + (row / BS) * TILE;
-        const unsigned char* codes = tile + (row % BS) * (D / 2) + t * (D / 8);
-        const unsigned char* scl = tile + BS * (D / 2) + (row % BS) * (D / 16) + t * VW;
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(codes);
-          w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
-          const uint32_t y = dev::e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(scl));
-          sc[r][0] = __byte_perm(y, 0, 0x1010);
-          sc[r][1] = __byte_perm(y, 0, 0x3232);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(codes);
-          w[r][0] = x.x; w[r][1] = x.y;
-          sc[r][0] = __byte_perm(dev::e4m3x2_to_f16(*scl), 0, 0x1010);
-        }
+        rows[r].load(kt + (row / BS) * TILE, row % BS, BS, t);
       }
-#pragma unroll
-      for (int c = 0; c < KW; ++c) {
-        uint32_t x[4], y[4];
-        dev::e2m1x8_to_f16(w[0][c], x);
-        dev::e2m1x8_to_f16(w[1][c], y);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = dev::mul_f16x2(x[j], sc[0][c / 2]);
-          y[j] = dev::mul_f16x2(y[j], sc[1][c / 2]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          dev::mma_f16(s[h][nt], x[0], y[0], x[1], y[1], qf[nt][2 * c][0], qf[nt][2 * c][1]);
-          dev::mma_f16(s[h][nt], x[2], y[2], x[3], y[3], qf[nt][2 * c + 1][0],
-                       qf[nt][2 * c + 1][1]);
-        }
-      }
+      dev::key_product<PA_KV_FP4_E2M1, D, NT>(s[h], rows[0], rows[1], qf);
     }
     // ---- softmax in the log2 domain; keys past a column's last are -inf
     const bool edge = key0 + KEYS > see_first;
@@ -526,7 +469,7 @@ int launch_bs(const Fp4Decode& P, const pa_decode_params* p, cudaStream_t s) {
 
 int launch_decode_fp4(const DecodeLaunch& L, void* stream) {
   const pa_decode_params* p = L.p;
-  const Fp4Columns cols = fp4_columns(p);
+  const MmaColumns cols = mma_columns(p->num_q_heads / p->num_kv_heads, query_len_of(p));
   Fp4Decode P;
   P.q = static_cast<const __nv_bfloat16*>(p->q);
   P.out = static_cast<__nv_bfloat16*>(p->out);

@@ -131,15 +131,15 @@ __device__ __forceinline__ int64_t query_source_row(const QueryMap& m, int v, in
 }
 #endif
 
-// Column layout of the 4-bit decode: the query rows of a KV head are the
-// columns of its products, token by token, in 8-column tiles (one or two); a
-// sequence with more new tokens than those hold is decoded as several groups.
-struct Fp4Columns {
+// Column layout of the 4-bit decode and of the token weights: the query rows
+// of a KV head are the columns of its products, token by token, in 8-column
+// tiles (one or two); a sequence with more new tokens than those hold is
+// worked off as several groups, each reading the keys.
+struct MmaColumns {
   int n_tiles, q_group, n_groups;
 };
-inline Fp4Columns fp4_columns(const pa_decode_params* p) {
-  const int g = p->num_q_heads / p->num_kv_heads, q = query_len_of(p);
-  Fp4Columns c;
+inline MmaColumns mma_columns(int g, int q) {
+  MmaColumns c;
   c.n_tiles = g * q <= 8 ? 1 : 2;
   c.q_group = q < 8 * c.n_tiles / g ? q : 8 * c.n_tiles / g;
   c.n_groups = (q + c.q_group - 1) / c.q_group;
@@ -218,6 +218,23 @@ int launch_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, voi
 int launch_decode_fp4(const DecodeLaunch& L, void* stream);  // then launch_merge
 int read_and_clear_fp4_errors(uint32_t* flags);
 int read_and_clear_decode_fp4_errors(uint32_t* flags);
+
+// Token weights (pa_weights.cu): the workspace and how the keys are split.
+struct TokenWeightsSpace {
+  size_t part, scores, total;  // byte offsets; the partitions' (max, sum), the scores
+  int64_t score_stride;        // floats of a score row
+  int cap;                     // keys a sequence may have
+  int partition_tokens, num_partitions;
+};
+int launch_token_weights(const pa_token_weights_params* p, const TokenWeightsSpace& sp,
+                         unsigned char* ws, void* stream);
+int read_and_clear_weights_errors(uint32_t* flags);
+// Eviction (pa_evict.cu)
+int launch_evict_select(const float* token_weights, const int32_t* context_lens, int32_t* keep,
+                        int32_t* new_lens, int32_t num_seqs, int64_t weights_stride,
+                        int32_t budget, int32_t recent, void* stream);
+int launch_evict_compact(const pa_evict_compact_params* p, void* stream);
+int read_and_clear_evict_errors(uint32_t* flags);
 // Query preparation for the bf16 tensor-core decode with several new tokens
 // per sequence (pa_query.cu): the rows of q ([B][query_len][Hq][D] bf16) in
 // the column layout, padded to n_pad rows with zeros ([B][n_pad][D]).

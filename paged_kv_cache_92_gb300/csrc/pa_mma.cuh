@@ -90,3 +90,146 @@ __device__ __forceinline__ int key_row(int g) { return g ^ (g >> 2); }
 
 }  // namespace dev
 }  // namespace pa
+
+// ---------------------------------------------------------------------------
+// Cached key rows times query rows. FMT is the cache's type (PA_KV_BF16,
+// PA_KV_FP8_E4M3, PA_KV_FP4_E2M1). The order of elements in the contraction is
+// free as long as both operands share it: a lane (t = lane % 4) takes every
+// fourth run of KeyRow::E elements of a row, one 16-byte read of the cache (8
+// bytes of a 4-bit row of 64), and the queries follow.
+// ---------------------------------------------------------------------------
+namespace pa {
+namespace dev {
+
+template <int FMT, int D>
+struct KeyRow {
+  static constexpr int E = FMT == 0 ? 8 : (FMT == 1 ? 16 : D / 4);  // elements of a run
+  static constexpr int BYTES = FMT == 0 ? 2 * D : (FMT == 1 ? D : D / 2);  // of a row (its codes)
+  static constexpr int RUN = BYTES * E / D;           // bytes of a run: 16, or 8
+  static constexpr int RUNS = D / (4 * E);            // runs of a lane
+  static constexpr int STEPS = D / 16;                // products of 16 elements
+  static constexpr int SCALES = FMT == 2 ? D / 16 : 0;  // scale bytes of a row
+  // bytes of one (block, KV head) tile, by block size
+  __host__ __device__ static constexpr int tile(int bs) { return bs * (BYTES + SCALES); }
+
+  uint32_t w[RUNS * RUN / 4];
+  uint32_t sc[D / 64];  // 4-bit: the group scales as f16 pairs
+
+  // row r of the tile at `p`, for the lane with t = lane % 4
+  __device__ __forceinline__ void load(const unsigned char* p, int r, int bs, int t) {
+    const unsigned char* row = p + r * BYTES;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const unsigned char* at = row + (4 * j + t) * RUN;
+      if constexpr (RUN == 16) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at);
+        w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        w[2 * j] = x.x; w[2 * j + 1] = x.y;
+      }
+    }
+    if constexpr (FMT == 2) {
+      const unsigned char* s = p + bs * BYTES + r * SCALES + t * (D / 64);
+      if constexpr (D == 128) {
+        const uint32_t y = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(s));
+        sc[0] = __byte_perm(y, 0, 0x1010);
+        sc[1] = __byte_perm(y, 0, 0x3232);
+      } else {
+        sc[0] = __byte_perm(e4m3x2_to_f16(*s), 0, 0x1010);
+      }
+    }
+  }
+  // elements [8 c, 8 c + 8) of the lane's list as pairs (two products' worth)
+  __device__ __forceinline__ void pairs(int c, uint32_t (&x)[4]) const {
+    if constexpr (FMT == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = w[4 * c + j];
+    } else if constexpr (FMT == 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = e4m3x2_to_f16((w[2 * c + j / 2] >> (16 * (j & 1))) & 0xffffu);
+    } else {
+      e2m1x8_to_f16(w[c], x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = mul_f16x2(x[j], sc[c / 2]);
+    }
+  }
+};
+
+// s[nt] (16 keys x 8 columns) += keys * queries^T; `lo` holds the lane's rows
+// for fragment rows 0..7, `hi` those for 8..15.
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void key_product(float (&s)[NT][4], const KeyRow<FMT, D>& lo,
+                                            const KeyRow<FMT, D>& hi,
+                                            const uint32_t (&qf)[NT][D / 16][2]) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t x[4], y[4];
+    lo.pairs(c, x);
+    hi.pairs(c, y);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t(&b)[2] = qf[nt][2 * c + k];
+        if constexpr (FMT == 0)
+          mma_bf16_regs(s[nt], x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1], b[0], b[1]);
+        else
+          mma_f16(s[nt], x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1], b[0], b[1]);
+      }
+  }
+}
+
+// One query row as the products' B operand (nullptr: a row of zeros), for the
+// lane with t = lane % 4; the four lanes of a row call together. bf16 rows stay
+// as they are and the result is 1. The others are scaled to f16 by a power of
+// two that brings the row's largest magnitude into [2^12, 2^13), exactly for
+// every element within 2^-30 of it, and its inverse is returned.
+template <int FMT, int D>
+__device__ __forceinline__ float query_fragment(const __nv_bfloat16* row, int t,
+                                                uint32_t (&qf)[D / 16][2]) {
+  using R = KeyRow<FMT, D>;
+  uint4 raw[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {  // 8 elements of the lane's list
+    const int e = 8 * c;
+    raw[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (row != nullptr)
+      raw[c] = *reinterpret_cast<const uint4*>(row + (4 * (e / R::E) + t) * R::E + e % R::E);
+  }
+  if constexpr (FMT == 0) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      qf[2 * c][0] = raw[c].x; qf[2 * c][1] = raw[c].y;
+      qf[2 * c + 1][0] = raw[c].z; qf[2 * c + 1][1] = raw[c].w;
+    }
+    return 1.0f;
+  } else {
+    float amax = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      float f[8];
+      unpack8(raw[c], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    int e = 0;
+    if (amax > 0.0f && amax <= 3.4e38f) (void)frexpf(amax, &e);  // amax < 2^e
+    e = max(e, -100);
+    const float a = ldexpf(1.0f, 13 - e);  // e in [-100, 128]: a normal power of two
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      float f[8];
+      unpack8(raw[c], f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        qf[2 * c + i / 2][i & 1] = pack_f16(f[2 * i] * a, f[2 * i + 1] * a);
+    }
+    return ldexpf(1.0f, e - 13);
+  }
+}
+
+}  // namespace dev
+}  // namespace pa

@@ -284,6 +284,50 @@ pa_status pa_seq_fork(pa_pool* p, int32_t parent, int32_t num_tokens, int32_t* c
   return PA_OK;
 }
 
+// The data still lies in the old blocks when this returns, so every fresh
+// block is taken before any block is released, and whether a block is shared
+// is judged by the refcounts before the call: of two sequences of the batch
+// that share a block, neither may write it.
+pa_status pa_pool_compact(pa_pool* p, const int32_t* seqs, const int32_t* new_lens, int32_t n) {
+  if (!p || n < 0 || (n > 0 && (!seqs || !new_lens)))
+    return fail(PA_ERR_INVALID_ARG, "pa_pool_compact: NULL argument or n < 0");
+  try {
+    std::vector<uint8_t> seen(p->seqs.size(), 0);
+    std::vector<std::vector<int32_t>> tables(n);
+    size_t fresh = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      if (!p->valid_seq(seqs[i])) return fail(PA_ERR_BOUNDS, "pa_pool_compact: unknown sequence");
+      if (seen[seqs[i]]++) return fail(PA_ERR_INVALID_ARG, "pa_pool_compact: a sequence twice");
+      const pa_pool::Seq& q = p->seqs[seqs[i]];
+      if (new_lens[i] < 0 || new_lens[i] > q.len)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_compact: new length outside [0, length]");
+      if (new_lens[i] == q.len) continue;
+      const int32_t nb = (new_lens[i] + p->block_size - 1) / p->block_size;
+      tables[i].assign(q.table.begin(), q.table.begin() + nb);
+      for (int32_t& b : tables[i])
+        if (p->ref[b] > 1 || p->cached[b]) {
+          b = -1;  // to be replaced
+          ++fresh;
+        }
+    }
+    if (fresh > p->available()) return fail(PA_ERR_OOM, "pa_pool_compact: pool exhausted");
+    for (std::vector<int32_t>& t : tables)
+      for (int32_t& b : t)
+        if (b < 0) b = p->pop();
+    for (int32_t i = 0; i < n; ++i) {
+      pa_pool::Seq& q = p->seqs[seqs[i]];
+      if (new_lens[i] == q.len) continue;
+      for (size_t j = 0; j < q.table.size(); ++j)
+        if (j >= tables[i].size() || tables[i][j] != q.table[j]) p->release(q.table[j]);
+      q.table.swap(tables[i]);
+      q.len = new_lens[i];
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(PA_ERR_OOM, "pa_pool_compact: host memory");
+  }
+  return PA_OK;
+}
+
 pa_status pa_seq_append_slot(pa_pool* p, int32_t seq, int64_t* slot, int32_t cow_pair[2],
                              int32_t* has_cow) {
   if (!p || !slot) return fail(PA_ERR_INVALID_ARG, "pa_seq_append_slot: NULL argument");
