@@ -159,20 +159,21 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
   const int n_steps = (nblk + NBK - 1) / NBK;
   const int n_my = n_steps > warp ? (n_steps - warp + NWARPS - 1) / NWARPS : 0;
   const uint64_t policy = dev::l2_evict_first_policy();
-  auto issue = [&](int i) {
+  // lane j copies the j-th tile of the step: its K tiles, then its V tiles
+  const int my_copy = lane % NBK;
+  const unsigned char* my_cache = (lane < NBK ? P.k_cache : P.v_cache) + int64_t(head) * TILE;
+  const int64_t block_bytes = int64_t(P.num_kv_heads) * TILE;
+  auto issue = [&](int i, int stage) {
     const int blk0 = NBK * (warp + NWARPS * i);
     const int n = min(NBK, nblk - blk0);
-    uint64_t* bar = &my_bars[i % ST];
-    unsigned char* dst = ring + (i % ST) * C::STAGE;
-    dev::mbar_arrive_expect_tx(bar, 2 * n * TILE);
-    for (int j = 0; j < n; ++j) {
-      const int64_t off = (int64_t(table[blk0 + j]) * P.num_kv_heads + head) * TILE;
-      dev::bulk_load(dst + j * TILE, P.k_cache + off, TILE, bar, policy);
-      dev::bulk_load(dst + (NBK + j) * TILE, P.v_cache + off, TILE, bar, policy);
-    }
+    uint64_t* bar = &my_bars[stage];
+    if (lane == 0) dev::mbar_arrive_expect_tx(bar, 2 * n * TILE);
+    __syncwarp();
+    if (lane < 2 * NBK && my_copy < n)
+      dev::bulk_load(ring + stage * C::STAGE + lane * TILE,
+                     my_cache + table[blk0 + my_copy] * block_bytes, TILE, bar, policy);
   };
-  if (lane == 0)
-    for (int i = 0; i < ST && i < n_my; ++i) issue(i);
+  for (int i = 0; i < ST && i < n_my; ++i) issue(i, i);
 
   // Queries as the B operand (columns nt * 8 + g), scaled into f16's range.
   uint32_t qf[NT][D / 16][2];
@@ -193,13 +194,16 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
   const int see_first = min(tok1, see0);  // no column sees fewer keys
 
   float o[D / 16][NT][4];  // O^T: D / 16 tiles of 16 rows
-  float m[NT][2], l[NT][2];
+  // Softmax state of columns 2t and 2t+1, in the log2 domain: a score is
+  // s * factor (s the raw product), ref the reference maximum (0 before the
+  // first key that the column sees), limit the raw product beyond which ref moves.
+  float ref[NT][2], limit[NT][2], l[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      m[nt][c] = -INFINITY;
-      l[nt][c] = 0.0f;
+      ref[nt][c] = l[nt][c] = 0.0f;
+      limit[nt][c] = -INFINITY;
     }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
@@ -208,20 +212,25 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
 
+  using KRow = dev::KeyRow<PA_KV_FP4_E2M1, D>;
   const int row_g = dev::key_row(g);                            // this lane's K rows
   const int row_a = dev::key_row(2 * t), row_b = dev::key_row(2 * t + 1);  // its V rows
+  // where they lie in a tile, apart from what is the same for every lane
+  const int lane_k = row_g * (D / 2) + t * KRow::RUN;
+  const int lane_ks = BS * (D / 2) + row_g * (D / 16) + t * (D / 64);
+  const int lane_va = row_a * (D / 2) + g * (D / 16), lane_vb = row_b * (D / 2) + g * (D / 16);
+  const int lane_vsa = BS * (D / 2) + row_a * (D / 16) + (g * VW) / 2;
+  const int lane_vsb = BS * (D / 2) + row_b * (D / 16) + (g * VW) / 2;
   int stalled_at = -1;
 
-  for (int i = 0; i < n_my; ++i) {
-    if (!__all_sync(0xffffffffu, dev::mbar_wait(&my_bars[i % ST], (i / ST) & 1))) {
-      stalled_at = i;
-      break;
-    }
-    const unsigned char* kt = ring + (i % ST) * C::STAGE;
+  // One step; with EDGE the one that holds keys which some column does not see.
+  auto step = [&](int i, int stage, auto edge_t) {
+    constexpr bool EDGE = decltype(edge_t)::value;
+    const unsigned char* kt = ring + stage * C::STAGE;
     const unsigned char* vt = kt + NBK * TILE;
     const int key0 = tok0 + KEYS * (warp + NWARPS * i);
 
-    // ---- scores: two tiles of 16 keys
+    // ---- raw scores: two tiles of 16 keys
     float s[2][NT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -229,28 +238,32 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[h][nt][j] = 0.0f;
-      dev::KeyRow<PA_KV_FP4_E2M1, D> rows[2];
+      KRow rows[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = h * 16 + r * 8 + row_g;
-        rows[r].load(kt + (row / BS) * TILE, row % BS, BS, t);
+        const int row = h * 16 + r * 8;  // of a lane with row_g 0 (which is below 8)
+        const unsigned char* tile = kt + (row / BS) * TILE;
+        rows[r].load(tile + (row % BS) * (D / 2) + lane_k, tile + (row % BS) * (D / 16) + lane_ks);
       }
       dev::key_product<PA_KV_FP4_E2M1, D, NT>(s[h], rows[0], rows[1], qf);
     }
-    // ---- softmax in the log2 domain; keys past a column's last are -inf
-    const bool edge = key0 + KEYS > see_first;
+    // ---- softmax; keys past a column's last are -inf
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (key0 + h * 16 + (j >> 1) * 8 + row_g >= see[nt][j & 1]) s[h][nt][j] = -INFINITY;
+    }
     bool over = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v = s[h][nt][j] * factor[nt][j & 1];
-          if (edge && key0 + h * 16 + (j >> 1) * 8 + row_g >= see[nt][j & 1]) v = -INFINITY;
-          s[h][nt][j] = v;
-          over |= v > m[nt][j & 1] + 8.0f;
-        }
+        for (int j = 0; j < 4; ++j) over |= s[h][nt][j] > limit[nt][j & 1];
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -259,15 +272,18 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
           float x = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(x, m[nt][c]);
-          const float a = x == -INFINITY ? 1.0f : dev::fast_exp2(m[nt][c] - x);
-          m[nt][c] = x;
-          l[nt][c] *= a;
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * factor[nt][c];
+          const bool first = limit[nt][c] == -INFINITY;
+          if (x != -INFINITY && (first || x > ref[nt][c])) {
+            const float a = first ? 0.0f : dev::fast_exp2(ref[nt][c] - x);
+            ref[nt][c] = x;
+            limit[nt][c] = (x + 8.0f) / factor[nt][c];
+            l[nt][c] *= a;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            o[k][nt][c] *= a;
-            o[k][nt][c + 2] *= a;
+            for (int k = 0; k < D / 16; ++k) {
+              o[k][nt][c] *= a;
+              o[k][nt][c + 2] *= a;
+            }
           }
         }
     }
@@ -279,8 +295,7 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
         float p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float ref = m[nt][j & 1];
-          p[j] = dev::fast_exp2(s[h][nt][j] - (ref == -INFINITY ? 0.0f : ref));
+          p[j] = dev::fast_exp2(fmaf(s[h][nt][j], factor[nt][j & 1], -ref[nt][j & 1]));
           l[nt][j & 1] += p[j];
         }
         pf[h][nt][0] = dev::transpose_8x8(dev::pack_f16(p[0], p[1]));
@@ -293,17 +308,18 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
       uint32_t w[4][VW], sb[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = h * 16 + (r >> 1) * 8 + ((r & 1) ? row_b : row_a);
+        const int row = h * 16 + (r >> 1) * 8;  // as above
         const unsigned char* tile = vt + (row / BS) * TILE;
-        const unsigned char* codes = tile + (row % BS) * (D / 2) + g * (D / 16);
+        const unsigned char* codes = tile + (row % BS) * (D / 2) + ((r & 1) ? lane_vb : lane_va);
         if constexpr (D == 128) {
           const uint2 x = *reinterpret_cast<const uint2*>(codes);
           w[r][0] = x.x; w[r][1] = x.y;
         } else {
           w[r][0] = *reinterpret_cast<const uint32_t*>(codes);
         }
-        sb[r] = tile[BS * (D / 2) + (row % BS) * (D / 16) + (g * VW) / 2];
-        if (key0 + row >= end) sb[r] = 0;  // a key that is not there: finite codes times zero
+        sb[r] = tile[(row % BS) * (D / 16) + ((r & 1) ? lane_vsb : lane_vsa)];
+        // a key that is not there: finite codes times zero
+        if (EDGE && key0 + row + ((r & 1) ? row_b : row_a) >= end) sb[r] = 0;
       }
       const uint32_t s01 = dev::e4m3x2_to_f16(sb[0] | sb[1] << 8);
       const uint32_t s23 = dev::e4m3x2_to_f16(sb[2] | sb[3] << 8);
@@ -333,8 +349,7 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
         }
       }
     };
-    bool split_tokens = false;
-    if (edge && P.q_len > 1) {
+    if constexpr (EDGE) {
       // a NaN in a key that only later new tokens see must not reach the
       // earlier ones as 0 * NaN: such steps run token by token
       uint32_t bad = 0;
@@ -345,18 +360,36 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
             vt + (row / BS) * TILE + BS * (D / 2) + (row % BS) * (D / 16) + (g * VW) / 2;
         bad |= uint32_t(key0 + row < tok1 && (*scl & 0x7F) == 0x7F);
       }
-      split_tokens = __any_sync(0xffffffffu, bad != 0);
-    }
-    if (!split_tokens) {
+      if (P.q_len > 1 && __any_sync(0xffffffffu, bad != 0)) {
+        for (int x = 0; x < n_tok; ++x)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) value_product(h, edge ? tok1 : INT32_MAX, -1, std::false_type{});
-    } else {
-      for (int x = 0; x < n_tok; ++x)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) value_product(h, min(tok1, see0 + x), x, std::true_type{});
+          for (int h = 0; h < 2; ++h) value_product(h, min(tok1, see0 + x), x, std::true_type{});
+        return;
+      }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) value_product(h, tok1, -1, std::false_type{});
+  };
+
+  // the steps before the first that is an edge; key0 + KEYS > see_first there
+  const int n_full = see_first <= tok0 ? 0 : (see_first - tok0) / KEYS;  // whole steps of the CTA
+  const int n_inner = n_full > warp ? (n_full - warp + NWARPS - 1) / NWARPS : 0;
+  uint32_t parity = 0;
+  for (int i = 0, stage = 0; i < n_my; ++i) {
+    if (!__all_sync(0xffffffffu, dev::mbar_wait(&my_bars[stage], parity))) {
+      stalled_at = i;
+      break;
+    }
+    if (i < n_inner)
+      step(i, stage, std::false_type{});
+    else
+      step(i, stage, std::true_type{});
     __syncwarp();
-    if (lane == 0 && i + ST < n_my) issue(i + ST);
+    if (i + ST < n_my) issue(i + ST, stage);
+    if (++stage == ST) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
 
   if (stalled_at >= 0) {
@@ -384,7 +417,7 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
     for (int c = 0; c < 2; ++c) {
       const int n = warp * C::COLS + nt * 8 + 2 * t + c;
       if (g == 0) {
-        sm_m[n] = m[nt][c];
+        sm_m[n] = limit[nt][c] == -INFINITY ? -INFINITY : ref[nt][c];
         sm_l[n] = l[nt][c];
       }
 #pragma unroll

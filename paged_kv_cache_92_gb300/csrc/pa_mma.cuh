@@ -115,12 +115,12 @@ struct KeyRow {
   uint32_t w[RUNS * RUN / 4];
   uint32_t sc[D / 64];  // 4-bit: the group scales as f16 pairs
 
-  // row r of the tile at `p`, for the lane with t = lane % 4
-  __device__ __forceinline__ void load(const unsigned char* p, int r, int bs, int t) {
-    const unsigned char* row = p + r * BYTES;
+  // The row whose first byte for this lane is `row` (RUN * (lane % 4) into the
+  // row), its scales for this lane at `s` (D / 64 * (lane % 4) into its scales).
+  __device__ __forceinline__ void load(const unsigned char* row, const unsigned char* s) {
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      const unsigned char* at = row + (4 * j + t) * RUN;
+      const unsigned char* at = row + 4 * j * RUN;
       if constexpr (RUN == 16) {
         const uint4 x = *reinterpret_cast<const uint4*>(at);
         w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
@@ -130,7 +130,6 @@ struct KeyRow {
       }
     }
     if constexpr (FMT == 2) {
-      const unsigned char* s = p + bs * BYTES + r * SCALES + t * (D / 64);
       if constexpr (D == 128) {
         const uint32_t y = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(s));
         sc[0] = __byte_perm(y, 0, 0x1010);

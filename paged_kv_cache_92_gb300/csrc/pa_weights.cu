@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(NTHREADS)
       l[nt][c] = 0.0f;
     }
   const int row_g = dev::key_row(g);
+  const int lane_k = row_g * Row::BYTES + t * Row::RUN;
+  const int lane_ks = row_g * Row::SCALES + t * (D / 64);
   int stalled_at = -1;
 
   for (int i = 0; i < n_my; ++i) {
@@ -191,8 +193,10 @@ __global__ void __launch_bounds__(NTHREADS)
       Row rows[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = h * 16 + r * 8 + row_g;
-        rows[r].load(kt + (row >> P.bs_log2) * tile_bytes, row & (BS - 1), BS, t);
+        const int row = h * 16 + r * 8;  // of a lane with row_g 0 (which is below 8)
+        const unsigned char* tile = kt + (row >> P.bs_log2) * tile_bytes;
+        rows[r].load(tile + (row & (BS - 1)) * Row::BYTES + lane_k,
+                     tile + BS * Row::BYTES + (row & (BS - 1)) * Row::SCALES + lane_ks);
       }
       dev::key_product<FMT, D, NT>(s[h], rows[0], rows[1], qf);
     }
