@@ -10,9 +10,10 @@
 // What bounds it: the cache's bytes, 9/16 an element, once. That leaves an SM
 // about three instruction lanes an element, so the design is about few
 // instructions and no shared-memory round trip:
-//  * A warp takes 32 keys a step. Lane 0 copies their K and V tiles (each
-//    contiguous: codes, then scales) into the warp's own ring with 1-D bulk
-//    copies; no CTA-wide barrier until the end.
+//  * A warp takes 32 keys a step. Its lanes copy the K and V tiles (each
+//    contiguous: codes, then scales) into the warp's own ring with 16-byte
+//    asynchronous copies; no CTA-wide barrier until the end. (1-D bulk copies
+//    of the 1152-byte tiles cost more instructions, which are what is scarce.)
 //  * S^T = K Q^T and O^T += V^T P^T are m16n8k16 products whose A operand is
 //    the cache: codes go from shared memory to registers, are converted to
 //    f16 pairs and multiplied by their group scale there (exact: a 2-bit and
@@ -66,7 +67,7 @@ struct Cfg {
   static constexpr int MERGE = NWARPS * COLS * (OROW + 2) * 4;
   static constexpr int RING = NWARPS * ST * STAGE;
   static constexpr int TILES = RING > MERGE ? RING : MERGE;
-  static_assert(TILE % 16 == 0, "bulk copies move multiples of 16 bytes");
+  static_assert(TILE % 16 == 0, "copies move 16 bytes");
 };
 
 struct Fp4Decode {
@@ -136,8 +137,7 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
   const int nblk = (tok1 - tok0 + BS - 1) / BS;
 
   extern __shared__ __align__(128) unsigned char smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::TILES);
-  int32_t* table = reinterpret_cast<int32_t*>(bars + NWARPS * ST);
+  int32_t* table = reinterpret_cast<int32_t*>(smem + C::TILES);
   const int32_t* trow = P.block_tables + int64_t(b) * P.max_blocks_per_seq + tok0 / BS;
   for (int i = tid; i < nblk; i += NTHREADS) {
     int32_t e = trow[i];
@@ -147,33 +147,34 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
     }
     table[i] = e;
   }
-  uint64_t* my_bars = bars + warp * ST;
-  unsigned char* ring = smem + warp * ST * C::STAGE;
-  if (lane == 0) {
-    for (int s = 0; s < ST; ++s) dev::mbar_init(&my_bars[s], 1);
-    dev::fence_barrier_init();
-  }
   __syncthreads();
 
   // step i of this warp: the partition's blocks [NBK * (warp + NWARPS * i), + NBK)
   const int n_steps = (nblk + NBK - 1) / NBK;
   const int n_my = n_steps > warp ? (n_steps - warp + NWARPS - 1) / NWARPS : 0;
+  unsigned char* ring = smem + warp * ST * C::STAGE;
   const uint64_t policy = dev::l2_evict_first_policy();
-  // lane j copies the j-th tile of the step: its K tiles, then its V tiles
-  const int my_copy = lane % NBK;
-  const unsigned char* my_cache = (lane < NBK ? P.k_cache : P.v_cache) + int64_t(head) * TILE;
+  const unsigned char* k_head = P.k_cache + int64_t(head) * TILE + lane * 16;
+  const unsigned char* v_head = P.v_cache + int64_t(head) * TILE + lane * 16;
   const int64_t block_bytes = int64_t(P.num_kv_heads) * TILE;
-  auto issue = [&](int i, int stage) {
+  auto issue = [&](int i, int stage) {  // one group, empty past the last step
+    unsigned char* dst = ring + stage * C::STAGE + lane * 16;
     const int blk0 = NBK * (warp + NWARPS * i);
-    const int n = min(NBK, nblk - blk0);
-    uint64_t* bar = &my_bars[stage];
-    if (lane == 0) dev::mbar_arrive_expect_tx(bar, 2 * n * TILE);
-    __syncwarp();
-    if (lane < 2 * NBK && my_copy < n)
-      dev::bulk_load(ring + stage * C::STAGE + lane * TILE,
-                     my_cache + table[blk0 + my_copy] * block_bytes, TILE, bar, policy);
+#pragma unroll
+    for (int j = 0; j < NBK; ++j)
+      if (blk0 + j < nblk) {
+        const int64_t off = table[blk0 + j] * block_bytes;
+#pragma unroll
+        for (int c = 0; c < TILE; c += 512)
+          if (c + 512 <= TILE || lane * 16 < TILE - c) {
+            dev::cp_async16(dst + j * TILE + c, k_head + off + c, policy);
+            dev::cp_async16(dst + (NBK + j) * TILE + c, v_head + off + c, policy);
+          }
+      }
+    dev::cp_async_commit();
   };
-  for (int i = 0; i < ST && i < n_my; ++i) issue(i, i);
+#pragma unroll
+  for (int i = 0; i < ST; ++i) issue(i, i);
 
   // Queries as the B operand (columns nt * 8 + g), scaled into f16's range.
   uint32_t qf[NT][D / 16][2];
@@ -221,7 +222,6 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
   const int lane_va = row_a * (D / 2) + g * (D / 16), lane_vb = row_b * (D / 2) + g * (D / 16);
   const int lane_vsa = BS * (D / 2) + row_a * (D / 16) + (g * VW) / 2;
   const int lane_vsb = BS * (D / 2) + row_b * (D / 16) + (g * VW) / 2;
-  int stalled_at = -1;
 
   // One step; with EDGE the one that holds keys which some column does not see.
   auto step = [&](int i, int stage, auto edge_t) {
@@ -374,30 +374,16 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
   // the steps before the first that is an edge; key0 + KEYS > see_first there
   const int n_full = see_first <= tok0 ? 0 : (see_first - tok0) / KEYS;  // whole steps of the CTA
   const int n_inner = n_full > warp ? (n_full - warp + NWARPS - 1) / NWARPS : 0;
-  uint32_t parity = 0;
   for (int i = 0, stage = 0; i < n_my; ++i) {
-    if (!__all_sync(0xffffffffu, dev::mbar_wait(&my_bars[stage], parity))) {
-      stalled_at = i;
-      break;
-    }
+    dev::cp_async_wait<ST - 1>();
+    __syncwarp();
     if (i < n_inner)
       step(i, stage, std::false_type{});
     else
       step(i, stage, std::true_type{});
     __syncwarp();
-    if (i + ST < n_my) issue(i + ST, stage);
-    if (++stage == ST) {
-      stage = 0;
-      parity ^= 1;
-    }
-  }
-
-  if (stalled_at >= 0) {
-    // record the stall, then wait (bounded) for this warp's copies in flight,
-    // so that none lands after the CTA has exited; the output is unspecified
-    if (lane == 0) atomicOr(&g_decode_fp4_errors, PA_DEVERR_TIMEOUT);
-    for (int j = stalled_at; j < n_my && j < stalled_at + ST; ++j)
-      (void)dev::mbar_wait(&my_bars[j % ST], (j / ST) & 1);
+    issue(i + ST, stage);
+    stage = stage + 1 == ST ? 0 : stage + 1;
   }
 
   // ---- merge the warps through shared memory (reusing the rings)
@@ -465,8 +451,7 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
 template <int D, int NT, int BS>
 int launch_t(const Fp4Decode& P, const pa_decode_params* p, cudaStream_t stream) {
   using C = Cfg<D, NT, BS>;
-  const size_t smem = C::TILES + NWARPS * C::ST * sizeof(uint64_t) +
-                      size_t(P.partition_tokens / BS + 1) * sizeof(int32_t);
+  const size_t smem = C::TILES + size_t(P.partition_tokens / BS + 1) * sizeof(int32_t);
   // the opt-in to large shared memory is per device: asked for the most that
   // a partition may need, once each
   static std::atomic<uint64_t> configured{0};
@@ -475,8 +460,7 @@ int launch_t(const Fp4Decode& P, const pa_decode_params* p, cudaStream_t stream)
   if (e != cudaSuccess) return int(e);
   const uint64_t bit = uint64_t(1) << (device & 63);
   if (!(configured.load(std::memory_order_relaxed) & bit)) {
-    const size_t most = C::TILES + NWARPS * C::ST * sizeof(uint64_t) +
-                        size_t(kMaxPartitionTokens / BS + 1) * sizeof(int32_t);
+    const size_t most = C::TILES + size_t(kMaxPartitionTokens / BS + 1) * sizeof(int32_t);
     e = cudaFuncSetAttribute(paged_decode_fp4_kernel<D, NT, BS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
     if (e != cudaSuccess) return int(e);

@@ -181,6 +181,22 @@ __device__ __forceinline__ void bulk_load(void* dst_smem, const void* src_gmem, 
       : "memory");
 }
 
+// 16 bytes global -> shared, past L1 (completion: cp_async_commit / cp_async_wait).
+__device__ __forceinline__ void cp_async16(void* dst_smem, const void* src_gmem, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
+                   smem_addr(dst_smem)),
+               "l"(src_gmem), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// until at most N of this thread's newest groups are in flight
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 2^x with the hardware approximation (MUFU.EX2): 2^0 is exactly 1 and
 // 2^-inf is 0, which the running softmax relies on.
 __device__ __forceinline__ float fast_exp2(float x) {
