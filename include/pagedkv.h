@@ -135,9 +135,9 @@ typedef struct {
   int32_t num_blocks;
   int32_t max_context_len;     /* host-known upper bound of every context_lens[b] (>= 1) */
   float scale;                 /* softmax scale, normally 1/sqrt(head_dim) */
-  int32_t partition_tokens;    /* split-K partition length; 0 = 512 (the 4-bit cache: chosen from
-                                  the shapes); else a multiple of 16 in [16, 4096], and on the
-                                  CUDA-core and 4-bit kernels of block_size too */
+  int32_t partition_tokens;    /* split-K partition length; 0 = 512; else a multiple of 16 in
+                                  [16, 4096], and on the CUDA-core kernel of block_size too (the
+                                  4-bit cache: checked like that, not used) */
   int32_t variant;             /* PA_DECODE_TENSOR_CORE (default) or PA_DECODE_CUDA_CORE */
   int32_t overlap_prologue;    /* nonzero: context_lens and block_tables were final before the
                                   previous kernel on `stream` began (e.g. uploaded once per step),
@@ -226,9 +226,10 @@ typedef struct {
  * Written by pa_reshape_and_cache_fp4, read back by pa_gather_fp4, copied by
  * pa_copy_blocks_fp4. One kernel decodes it whatever `variant` says: head_dim
  * 64 or 128, every block size, G in {1, 2, 4, 8}, any number of KV heads,
- * num_seqs * query_len <= 65535 (else PA_ERR_UNSUPPORTED). The codes are
- * multiplied exactly; the softmax weights are rounded to f16. With several new
- * tokens, up to 16 / G of them share each load of the keys. */
+ * num_seqs * query_len <= 65535 and num_seqs * num_kv_heads * (query_len + 1)
+ * < 2^27 (else PA_ERR_UNSUPPORTED). The codes are multiplied exactly; the
+ * softmax weights are rounded to f16. With several new tokens, up to 8 / G of
+ * them share each load of the keys. */
 #define PA_KV_FP4_E2M1 2
 
 #define PA_DECODE_TENSOR_CORE 0 /* tcgen05 MMAs, TMEM accumulators, tensor-map TMA ring */

@@ -19,7 +19,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Keys per CTA of the 4-bit decode and of the token weights: short enough for
+// Keys per CTA of the token weights: short enough for
 // 16 CTAs an SM of a 152-SM GPU, so that ragged lengths even out, within
 // [128, 4096] tokens. `units`: (sequence, KV head, column group)s.
 int auto_partition_tokens(int64_t cap, int64_t units) {
@@ -27,16 +27,8 @@ int auto_partition_tokens(int64_t cap, int64_t units) {
   return pt < 128 ? 128 : (pt > kMaxPartitionTokens ? kMaxPartitionTokens : int(pt));
 }
 
-int fp4_partition_tokens(const pa_decode_params* p) {
-  const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
-  const int64_t cap = p->max_context_len < table ? p->max_context_len : table;
-  const MmaColumns c = mma_columns(p->num_q_heads / p->num_kv_heads, query_len_of(p));
-  return auto_partition_tokens(cap, int64_t(p->num_seqs) * p->num_kv_heads * c.n_groups);
-}
-
 int resolve_partition_tokens(const pa_decode_params* p) {
-  if (p->partition_tokens != 0) return p->partition_tokens;
-  return p->kv_dtype == PA_KV_FP4_E2M1 ? fp4_partition_tokens(p) : kDefaultPartitionTokens;
+  return p->partition_tokens == 0 ? kDefaultPartitionTokens : p->partition_tokens;
 }
 
 // Full host validation of decode params. Returns PA_OK or an error (message set).
@@ -94,6 +86,11 @@ pa_status check_decode(const pa_decode_params* p, bool need_pointers) {
                      "pa_decode: on the CUDA-core kernel num_seqs * query_len must be <= 65535 "
                      "(the tensor-core kernel takes num_kv_heads 1/2/4/8 and num_seqs * "
                      "(query_len split into column groups) <= 16384)");
+  if (p->kv_dtype == PA_KV_FP4_E2M1 &&
+      int64_t(p->num_seqs) * p->num_kv_heads * (query_len_of(p) + 1) * 16 >= (int64_t(1) << 31))
+    return set_error(PA_ERR_UNSUPPORTED,
+                     "pa_decode: the 4-bit cache takes num_seqs * num_kv_heads * (query_len + 1) "
+                     "below 2^27");
   if (p->kv_dtype != PA_KV_BF16) {
     if (need_pointers && p->num_seqs > 0 &&
         (!p->k_scale || !p->v_scale || (reinterpret_cast<uintptr_t>(p->k_scale) & 3u) ||
@@ -149,6 +146,20 @@ WorkspaceLayout decode_workspace_layout(const pa_decode_params* p, int num_parti
     if (ns > 1) {
       const size_t rows = size_t(p->num_seqs) * query_len_of(p) * p->num_q_heads * ns;
       w.tc_m = H;
+      w.tc_acc = w.tc_m + round_up(rows * 2 * sizeof(float), 256);
+      w.total = w.tc_acc + round_up(rows * p->head_dim * sizeof(float), 256);
+    }
+    return w;
+  }
+  if (p->kv_dtype == PA_KV_FP4_E2M1) {
+    // the 4-bit kernel: the stream's plan and two partials per CTA
+    const Fp4Plan f = fp4_plan(p, grid);
+    w.total = H;
+    if (!f.whole) {
+      const size_t rows = size_t(2) * f.grid * f.cols;
+      const size_t v = size_t(p->num_seqs) * fp4_columns(p).n_groups;
+      w.tc_plan = H;
+      w.tc_m = w.tc_plan + round_up((v + 1) * sizeof(int64_t), 256);
       w.tc_acc = w.tc_m + round_up(rows * 2 * sizeof(float), 256);
       w.total = w.tc_acc + round_up(rows * p->head_dim * sizeof(float), 256);
     }
@@ -266,11 +277,24 @@ static pa_status run_decode(const pa_decode_params* p, unsigned char* ws,
       std::snprintf(where, sizeof(where), "%s: launch", who);
       return set_cuda_error(where, e);
     }
+    if (fp4) {
+      if (grid <= 0)
+        return set_cuda_error("the SM count of the current device", int(cudaErrorNoDevice));
+      L.plan = reinterpret_cast<int*>(ws + w.tc_plan);
+      L.part_m = reinterpret_cast<float*>(ws + w.tc_m);
+      L.part_acc = reinterpret_cast<float*>(ws + w.tc_acc);
+      e = launch_decode_fp4(L, fp4_plan(p, grid), stream);
+      if (e) {
+        std::snprintf(where, sizeof(where), "%s: launch", who);
+        return set_cuda_error(where, e);
+      }
+      return PA_OK;
+    }
     L.plan = nullptr;
     L.part_m = np > 1 ? reinterpret_cast<float*>(ws + w.simt_m) : nullptr;
     L.part_l = np > 1 ? reinterpret_cast<float*>(ws + w.simt_l) : nullptr;
     L.part_acc = np > 1 ? reinterpret_cast<float*>(ws + w.simt_acc) : nullptr;
-    e = fp4 ? launch_decode_fp4(L, stream) : launch_decode(L, stream);
+    e = launch_decode(L, stream);
     if (!e) e = launch_merge(L, stream);
   }
   if (e) {
@@ -793,7 +817,7 @@ static pa_status check_token_weights(const pa_token_weights_params* p, bool need
                          "PA_KV_FP4_E2M1");
   if (p->query_len < 0 || p->query_len > 1024)
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: query_len must be in [0, 1024]");
-  if (int64_t(p->num_seqs) * pa::mma_columns(g, q).n_groups > 65535)
+  if (int64_t(p->num_seqs) * pa::mma_columns(g, q, 2).n_groups > 65535)
     return pa::set_error(PA_ERR_UNSUPPORTED,
                          "pa_token_weights: num_seqs * ceil(query_len / (16 / G)) must be <= 65535");
   if (p->num_blocks < 1 || p->max_blocks_per_seq < 1 || p->max_context_len < 1)
@@ -833,7 +857,7 @@ static pa::TokenWeightsSpace token_weights_space(const pa_token_weights_params* 
   const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
   s.cap = int(p->max_context_len < table ? p->max_context_len : table);
   s.score_stride = (int64_t(s.cap) + 31) / 32 * 32;
-  const pa::MmaColumns c = pa::mma_columns(p->num_q_heads / p->num_kv_heads, q);
+  const pa::MmaColumns c = pa::mma_columns(p->num_q_heads / p->num_kv_heads, q, 2);
   s.partition_tokens =
       pa::auto_partition_tokens(s.cap, int64_t(p->num_seqs) * p->num_kv_heads * c.n_groups);
   s.num_partitions = (s.cap + s.partition_tokens - 1) / s.partition_tokens;

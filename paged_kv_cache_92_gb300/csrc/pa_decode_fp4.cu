@@ -18,7 +18,8 @@
 //    the cache: codes go from shared memory to registers, are converted to
 //    f16 pairs and multiplied by their group scale there (exact: a 2-bit and
 //    a 4-bit significand), and never return. The query rows of a KV head, G
-//    heads of up to 8 NT / G new tokens, are the 8 NT columns.
+//    heads of up to 8 / G new tokens, are the products' 8 columns; more new
+//    tokens are worked off in groups, whose re-read keys mostly come from L2.
 //  * The order of elements inside a product is free as long as both operands
 //    share it, so a lane reads its K elements as one run of head_dim / 4 codes.
 //    For V the contraction runs over keys: the nibbles of two keys are merged
@@ -33,8 +34,12 @@
 //    sums and the output stay in fp32.
 //  * The reference maximum moves only when a score exceeds it by 2^8, so O is
 //    rescaled rarely; f16 holds the weights up to 2^8 that this allows.
-// A sequence longer than a partition is split over CTAs; the partials are
-// merged by log-sum-exp.
+//  * Work is dealt out as a stream: every (sequence, column group, KV head) is
+//    an item of so many 32-key steps plus a start cost, and each of the
+//    persistent CTAs takes an equal stretch of the stream's cost, so ragged
+//    lengths leave no tail. An item cut by a stretch's end leaves partials,
+//    at most two a CTA, which a second launch joins by log-sum-exp. Batches
+//    whose contexts are all short take one CTA an item and no second launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,17 +61,17 @@ constexpr int NTHREADS = NWARPS * 32;
 constexpr int KEYS = 32;  // keys of a warp's step
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D, int NT, int BS>
+template <int D, int BS>
 struct Cfg {
   static constexpr int NBK = KEYS / BS;              // blocks of a step
   static constexpr int TILE = BS * D * 9 / 16;       // bytes of one (block, KV head) tile
   static constexpr int STAGE = 2 * NBK * TILE;       // K tiles, then V tiles
-  static constexpr int ST = D == 128 ? 3 : 4;        // ring stages per warp
-  static constexpr int COLS = 8 * NT;
+  static constexpr int ST = D == 128 ? 2 : 4;        // ring stages per warp
+  static constexpr int COLS = 8;
   static constexpr int OROW = D + 4;                 // padded row of the warps' merge
-  static constexpr int MERGE = NWARPS * COLS * (OROW + 2) * 4;
   static constexpr int RING = NWARPS * ST * STAGE;
-  static constexpr int TILES = RING > MERGE ? RING : MERGE;
+  static constexpr int SMEM = RING + NWARPS * COLS * (OROW + 2) * 4;
+  static constexpr int WINDOW = 32 / NBK;            // steps whose table entries a warp holds
   static_assert(TILE % 16 == 0, "copies move 16 bytes");
 };
 
@@ -79,139 +84,270 @@ struct Fp4Decode {
   const float* v_scale;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  float* part_m;
-  float* part_l;
-  float* part_acc;
+  int64_t* plan;    // [virtual sequences + 1]: cost before each, then the total
+  float* part_ml;   // [2 * grid][COLS][2]: max, sum
+  float* part_acc;  // [2 * grid][COLS][D]
   float scale_log2;
-  int max_blocks_per_seq, num_kv_heads, num_blocks, max_context_len;
+  int max_blocks_per_seq, num_kv_heads, num_blocks, cap;
   int g_log2;  // log2 of the query heads per KV head
   int q_len, q_group, n_groups;  // new tokens; of a column group; column groups
-  int partition_tokens, num_partitions;
+  int num_virtual;               // sequences * n_groups
+  int whole;                     // one CTA per item, nothing is cut
 };
 
-// grid (partition, KV head, sequence * n_groups + column group)
-template <int D, int NT, int BS>
-__global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
+// A virtual sequence: column group `grp` of sequence b.
+struct Virtual {
+  int see0;   // keys that the group's first token sees
+  int n_tok;  // its tokens; the last one sees see0 + n_tok - 1 keys
+  int steps;  // 0: an empty sequence, or one without room for the new tokens
+};
+__device__ __forceinline__ Virtual virtual_of(const Fp4Decode& P, int v) {
+  const int b = v / P.n_groups, first = (v - b * P.n_groups) * P.q_group;
+  const int L = min(P.context_lens[b], P.cap);
+  Virtual x;
+  x.n_tok = min(P.q_group, P.q_len - first);
+  x.see0 = L - P.q_len + first + 1;
+  x.steps = L < P.q_len || L <= 0 ? 0 : (x.see0 + x.n_tok - 1 + KEYS - 1) / KEYS;
+  return x;
+}
+// The stream: an item (virtual sequence, KV head) costs its steps and a start
+// (queries, pipeline fill, merge of the warps: about 990 instructions a warp,
+// against 570 for one of its steps, four of which run at a time).
+constexpr int START_COST = 8;
+__device__ __forceinline__ int item_cost(const Virtual& x) {
+  return x.steps > 0 ? x.steps + START_COST : 0;
+}
+// Stretches: at most one per position of the stream, so that none is empty.
+__device__ __forceinline__ int stretches(int64_t T, int grid) { return T < grid ? int(T) : grid; }
+// The stretch [c T / G, (c + 1) T / G) of G that holds stream position x.
+__device__ __forceinline__ int owner(int64_t x, int64_t T, int G) {
+  return int(((x + 1) * G - 1) / T);
+}
+
+// Where this CTA's stretch begins: the virtual sequence that holds position x0
+// and the cost before it. CTA 0 also writes the plan for the merge.
+struct Start {
+  int64_t x0, x1, before;
+  int v;
+};
+__device__ __forceinline__ void find_start(const Fp4Decode& P, Start* out, int64_t* warp_tot) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (P.num_virtual + NTHREADS - 1) / NTHREADS;
+  const int v0 = tid * per, v1 = min(P.num_virtual, v0 + per);
+  int64_t sum = 0;
+  for (int v = v0; v < v1; ++v) sum += int64_t(item_cost(virtual_of(P, v))) * P.num_kv_heads;
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) warp_tot[warp] = inc;
+  __syncthreads();
+  int64_t before = inc - sum, T = 0;
+#pragma unroll
+  for (int w = 0; w < NWARPS; ++w) {
+    if (w < warp) before += warp_tot[w];
+    T += warp_tot[w];
+  }
+  const int64_t G = stretches(T, gridDim.x), c = blockIdx.x;
+  const int64_t x0 = c < G ? c * T / G : T, x1 = c < G ? (c + 1) * T / G : T;
+  if (tid == 0) *out = Start{x0, x0, 0, 0};  // an empty stretch
+  __syncthreads();
+  const bool mine = x0 < x1 && before <= x0 && x0 < before + sum;
+  if (mine || blockIdx.x == 0) {
+    int64_t at = before;
+    for (int v = v0; v < v1; ++v) {
+      const int64_t cost = int64_t(item_cost(virtual_of(P, v))) * P.num_kv_heads;
+      if (blockIdx.x == 0) P.plan[v] = at;
+      if (mine && at <= x0 && x0 < at + cost) *out = Start{x0, x1, at, v};
+      at += cost;
+    }
+    if (blockIdx.x == 0 && tid == 0) P.plan[P.num_virtual] = T;
+  }
+  __syncthreads();
+}
+
+// A piece of an item: steps [first, last) of (virtual sequence v, KV head).
+struct Piece {
+  int v, head, first, last, steps;  // steps: of the whole item
+  int see0, n_tok;                  // of the virtual sequence
+  bool valid;                       // false: the stretch is done
+};
+// Walks a stretch piece by piece.
+struct Walk {
+  int64_t x, x1, before;  // position, end, cost before virtual sequence v
+  int v;
+  __device__ __forceinline__ Piece next(const Fp4Decode& P) {
+    Piece p{};
+    while (x < x1) {
+      const Virtual q = virtual_of(P, v);
+      const int cost = item_cost(q);
+      const int64_t all = int64_t(cost) * P.num_kv_heads;
+      if (x >= before + all) {
+        before += all;
+        ++v;
+        continue;
+      }
+      const int64_t in = x - before;
+      p.v = v;
+      p.head = int(in / cost);
+      const int64_t base = before + int64_t(p.head) * cost;
+      const int64_t end = min(x1, base + cost);
+      p.first = max(0, int(x - base) - START_COST);
+      p.last = int(end - base) - START_COST;
+      p.steps = q.steps;
+      p.see0 = q.see0;
+      p.n_tok = q.n_tok;
+      x = end;
+      p.valid = p.first < p.last;
+      if (p.valid) break;
+    }
+    return p;
+  }
+};
+
+template <int D, int BS>
+__global__ void __launch_bounds__(NTHREADS, 4)
     paged_decode_fp4_kernel(const Fp4Decode P) {
-  using C = Cfg<D, NT, BS>;
-  constexpr int ST = C::ST, NBK = C::NBK, TILE = C::TILE;
+  using C = Cfg<D, BS>;
+  constexpr int ST = C::ST, NBK = C::NBK, TILE = C::TILE, WINDOW = C::WINDOW;
   constexpr int VW = D / 64;  // code words of a lane's share of a V row (D / 8 elements)
-  const int part = blockIdx.x, head = blockIdx.y;
-  const int b = blockIdx.z / P.n_groups, grp = blockIdx.z - b * P.n_groups;
+  dev::griddep_launch_dependents();  // the merge may be dispatched as CTAs end; it waits for all
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = 1 << P.g_log2;
   const int num_q_heads = P.num_kv_heads << P.g_log2;
-  const int tok_i0 = grp * P.q_group;                       // first new token of the group
-  const int n_tok = min(P.q_group, P.q_len - tok_i0);       // its tokens
-  const int n_cols = n_tok << P.g_log2;                     // its columns
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* ring = smem + warp * ST * C::STAGE;
+  float* sm_o = reinterpret_cast<float*>(smem + C::RING);    // [NWARPS][COLS][OROW]
+  float* sm_m = sm_o + NWARPS * C::COLS * C::OROW;           // [NWARPS][COLS]
+  float* sm_l = sm_m + NWARPS * C::COLS;                     // [NWARPS][COLS]
+  __shared__ Start start;
+  __shared__ int64_t warp_tot[NWARPS];
+  __shared__ Walk walk;
+  __shared__ Piece pieces[2];  // the one being worked on, and the next
+
+  // bad lengths are flagged, and rows of sequences without keys zeroed, by the CTAs in turn
+  for (int v = blockIdx.x; v < P.num_virtual; v += gridDim.x) {
+    const int b = v / P.n_groups, first = (v - b * P.n_groups) * P.q_group;
+    const int L = P.context_lens[b];
+    if (L > 0 && L >= P.q_len && L <= P.cap) continue;
+    if (tid == 0 && first == 0 && L > 0) atomicOr(&g_decode_fp4_errors, PA_DEVERR_CONTEXT_LEN);
+    if (L > 0 && min(L, P.cap) >= P.q_len) continue;
+    const int n = min(P.q_group, P.q_len - first) * num_q_heads * D;
+    __nv_bfloat16* row = P.out + (int64_t(b) * P.q_len + first) * num_q_heads * D;
+    for (int i = tid; i < n; i += NTHREADS) row[i] = __float2bfloat16_rn(0.0f);
+  }
+
+  // thread 0 walks the stretch one piece ahead of the CTA
+  if (P.whole) {
+    if (tid == 0) {
+      Piece p{};
+      p.v = blockIdx.x / P.num_kv_heads;
+      p.head = blockIdx.x - p.v * P.num_kv_heads;
+      const Virtual q = virtual_of(P, p.v);
+      p.last = p.steps = q.steps;
+      p.see0 = q.see0;
+      p.n_tok = q.n_tok;
+      p.valid = q.steps > 0;
+      pieces[0] = p;
+      walk.x = walk.x1 = 0;
+    }
+  } else {
+    find_start(P, &start, warp_tot);
+    if (tid == 0) {
+      walk = Walk{start.x0, start.x1, start.before, start.v};
+      pieces[0] = walk.next(P);
+    }
+  }
+  __syncthreads();
+
+  const int64_t block_bytes = int64_t(P.num_kv_heads) * TILE;
+  // Table entries of this warp's steps [w0, w0 + WINDOW) of the piece, one a
+  // lane: step w0 + lane / NBK, block lane % NBK of it. Those past the piece
+  // are read within the table row, and not used.
+  auto load_window = [&](const Piece& p, int w0) {
+    const int step = p.first + warp + NWARPS * (w0 + lane / NBK);
+    const int j = min(step * NBK + lane % NBK, P.max_blocks_per_seq - 1);
+    return P.block_tables[int64_t(p.v / P.n_groups) * P.max_blocks_per_seq + j];
+  };
+  bool bad_entry = false;  // a table entry outside the pool (block 0 is read in its place)
+  // One copy group: step i of the warp (table entries in `window`), empty past the last.
+  auto issue = [&](const Piece& p, int i, int n_my, int window, int stage) {
+    if (i < n_my) {
+      unsigned char* dst = ring + stage * C::STAGE + lane * 16;
+      const int blk0 = (p.first + warp + NWARPS * i) * NBK;
+      const int nblk = (p.see0 + p.n_tok - 1 + BS - 1) / BS;
+      const unsigned char* k = P.k_cache + int64_t(p.head) * TILE + lane * 16;
+      const unsigned char* v = P.v_cache + int64_t(p.head) * TILE + lane * 16;
+#pragma unroll
+      for (int j = 0; j < NBK; ++j) {
+        int e = __shfl_sync(0xffffffffu, window, (i % WINDOW) * NBK + j);
+        if (blk0 + j < nblk) {
+          bad_entry |= e < 0 || e >= P.num_blocks;
+          e = e < 0 || e >= P.num_blocks ? 0 : e;
+          const int64_t off = e * block_bytes;
+#pragma unroll
+          for (int c = 0; c < TILE; c += 512) {
+            const bool on = c + 512 <= TILE || lane * 16 < TILE - c;
+            dev::cp_async16(dst + j * TILE + c, k + off + c, on);
+            dev::cp_async16(dst + (NBK + j) * TILE + c, v + off + c, on);
+          }
+        }
+      }
+    }
+    dev::cp_async_commit();
+  };
+  auto steps_of = [&](const Piece& p) {
+    const int n = p.last - p.first;
+    return n > warp ? (n - warp + NWARPS - 1) / NWARPS : 0;
+  };
+
+  int window = 0, n_my = 0, cur = 0;
+  auto begin = [&](const Piece& p) {
+    window = load_window(p, 0);
+    n_my = steps_of(p);
+#pragma unroll
+    for (int i = 0; i < ST; ++i) issue(p, i, n_my, window, i);
+  };
+  if (pieces[0].valid) begin(pieces[0]);
+  __syncwarp();
+  for (; pieces[cur].valid; cur ^= 1) {
+  const Piece& piece = pieces[cur];
+  const int head = piece.head;
+  const int b = piece.v / P.n_groups;
+  const int tok_i0 = (piece.v - b * P.n_groups) * P.q_group;  // first new token of the group
+  const int n_tok = piece.n_tok, see0 = piece.see0, see_last = see0 + n_tok - 1;
+  const int n_cols = n_tok << P.g_log2;
   // row of q / out of column n: token tok_i0 + n / G, query head head * G + n % G
   auto q_row = [&](int n) {
     return (int64_t(b) * P.q_len + tok_i0 + (n >> P.g_log2)) * num_q_heads + head * G +
            (n & (G - 1));
   };
 
-  int L = P.context_lens[b];
-  const int cap = min(P.max_blocks_per_seq * BS, P.max_context_len);
-  const bool report = tid == 0 && part == 0 && head == 0 && grp == 0;
-  if (L > cap) {
-    if (report) atomicOr(&g_decode_fp4_errors, PA_DEVERR_CONTEXT_LEN);
-    L = cap;
-  }
-  if (L > 0 && L < P.q_len) {  // no room for the new tokens: an empty sequence
-    if (report) atomicOr(&g_decode_fp4_errors, PA_DEVERR_CONTEXT_LEN);
-    L = 0;
-  }
-  if (L <= 0) {
-    if (part == 0)
-      for (int i = tid; i < n_cols * D; i += NTHREADS)
-        P.out[q_row(i / D) * D + i % D] = __float2bfloat16_rn(0.0f);
-    return;
-  }
-  // token i of the sequence's new ones sees L - q_len + i + 1 keys
-  const int see0 = L - P.q_len + tok_i0 + 1;
-  const int see_last = see0 + n_tok - 1;
-  const int tok0 = part * P.partition_tokens;
-  if (tok0 >= see_last) return;
-  const int tok1 = min(see_last, tok0 + P.partition_tokens);
-  const int nblk = (tok1 - tok0 + BS - 1) / BS;
-
-  extern __shared__ __align__(128) unsigned char smem[];
-  int32_t* table = reinterpret_cast<int32_t*>(smem + C::TILES);
-  const int32_t* trow = P.block_tables + int64_t(b) * P.max_blocks_per_seq + tok0 / BS;
-  for (int i = tid; i < nblk; i += NTHREADS) {
-    int32_t e = trow[i];
-    if (e < 0 || e >= P.num_blocks) {
-      atomicOr(&g_decode_fp4_errors, PA_DEVERR_TABLE_ENTRY);
-      e = 0;
-    }
-    table[i] = e;
-  }
-  __syncthreads();
-
-  // step i of this warp: the partition's blocks [NBK * (warp + NWARPS * i), + NBK)
-  const int n_steps = (nblk + NBK - 1) / NBK;
-  const int n_my = n_steps > warp ? (n_steps - warp + NWARPS - 1) / NWARPS : 0;
-  unsigned char* ring = smem + warp * ST * C::STAGE;
-  const uint64_t policy = dev::l2_evict_first_policy();
-  const unsigned char* k_head = P.k_cache + int64_t(head) * TILE + lane * 16;
-  const unsigned char* v_head = P.v_cache + int64_t(head) * TILE + lane * 16;
-  const int64_t block_bytes = int64_t(P.num_kv_heads) * TILE;
-  auto issue = [&](int i, int stage) {  // one group, empty past the last step
-    unsigned char* dst = ring + stage * C::STAGE + lane * 16;
-    const int blk0 = NBK * (warp + NWARPS * i);
-#pragma unroll
-    for (int j = 0; j < NBK; ++j)
-      if (blk0 + j < nblk) {
-        const int64_t off = table[blk0 + j] * block_bytes;
-#pragma unroll
-        for (int c = 0; c < TILE; c += 512)
-          if (c + 512 <= TILE || lane * 16 < TILE - c) {
-            dev::cp_async16(dst + j * TILE + c, k_head + off + c, policy);
-            dev::cp_async16(dst + (NBK + j) * TILE + c, v_head + off + c, policy);
-          }
-      }
-    dev::cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < ST; ++i) issue(i, i);
-
-  // Queries as the B operand (columns nt * 8 + g), scaled into f16's range.
-  uint32_t qf[NT][D / 16][2];
-  float factor[NT][2];  // of columns 2t and 2t+1: softmax scale * K scale / the row's scaling
-  int see[NT][2];       // keys that columns 2t and 2t+1 see
+  // Queries as the B operand (column g), scaled into f16's range.
+  uint32_t qf[1][D / 16][2];
+  float factor[2];  // of columns 2t and 2t+1: softmax scale * K scale / the row's scaling
+  int see[2];       // keys that columns 2t and 2t+1 see
   const float kfac = P.scale_log2 * P.k_scale[head];
+  const float row_factor = kfac * dev::query_fragment<PA_KV_FP4_E2M1, D>(
+                                      P.q + q_row(min(g, n_cols - 1)) * D, g < n_cols, t, qf[0]);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int n = nt * 8 + g;
-    const float f = kfac * dev::query_fragment<PA_KV_FP4_E2M1, D>(
-                               n < n_cols ? P.q + q_row(n) * D : nullptr, t, qf[nt]);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      factor[nt][c] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + c));
-      see[nt][c] = min(tok1, see0 + ((nt * 8 + 2 * t + c) >> P.g_log2));
-    }
+  for (int c = 0; c < 2; ++c) {
+    factor[c] = __shfl_sync(0xffffffffu, row_factor, 4 * (2 * t + c));
+    see[c] = min(see_last, see0 + ((2 * t + c) >> P.g_log2));
   }
-  const int see_first = min(tok1, see0);  // no column sees fewer keys
 
-  float o[D / 16][NT][4];  // O^T: D / 16 tiles of 16 rows
+  float o[D / 16][4];  // O^T: D / 16 tiles of 16 rows
   // Softmax state of columns 2t and 2t+1, in the log2 domain: a score is
   // s * factor (s the raw product), ref the reference maximum (0 before the
   // first key that the column sees), limit the raw product beyond which ref moves.
-  float ref[NT][2], limit[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      ref[nt][c] = l[nt][c] = 0.0f;
-      limit[nt][c] = -INFINITY;
-    }
+  float ref[2] = {0.0f, 0.0f}, limit[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
 
   using KRow = dev::KeyRow<PA_KV_FP4_E2M1, D>;
   const int row_g = dev::key_row(g);                            // this lane's K rows
@@ -223,21 +359,20 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
   const int lane_vsa = BS * (D / 2) + row_a * (D / 16) + (g * VW) / 2;
   const int lane_vsb = BS * (D / 2) + row_b * (D / 16) + (g * VW) / 2;
 
+  int nan_from = INT32_MAX;  // first key of an edge step with a NaN among this lane's elements
   // One step; with EDGE the one that holds keys which some column does not see.
   auto step = [&](int i, int stage, auto edge_t) {
     constexpr bool EDGE = decltype(edge_t)::value;
     const unsigned char* kt = ring + stage * C::STAGE;
     const unsigned char* vt = kt + NBK * TILE;
-    const int key0 = tok0 + KEYS * (warp + NWARPS * i);
+    const int key0 = KEYS * (piece.first + warp + NWARPS * i);
 
     // ---- raw scores: two tiles of 16 keys
-    float s[2][NT][4];
+    float s[2][1][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[h][nt][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) s[h][0][j] = 0.0f;
       KRow rows[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -245,66 +380,58 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
         const unsigned char* tile = kt + (row / BS) * TILE;
         rows[r].load(tile + (row % BS) * (D / 2) + lane_k, tile + (row % BS) * (D / 16) + lane_ks);
       }
-      dev::key_product<PA_KV_FP4_E2M1, D, NT>(s[h], rows[0], rows[1], qf);
+      dev::key_product<PA_KV_FP4_E2M1, D, 1>(s[h], rows[0], rows[1], qf);
     }
     // ---- softmax; keys past a column's last are -inf
-    if constexpr (EDGE) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (key0 + h * 16 + (j >> 1) * 8 + row_g >= see[nt][j & 1]) s[h][nt][j] = -INFINITY;
-    }
     bool over = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) over |= s[h][nt][j] > limit[nt][j & 1];
+      for (int j = 0; j < 4; ++j) {
+        if (EDGE && key0 + h * 16 + (j >> 1) * 8 + row_g >= see[j & 1]) s[h][0][j] = -INFINITY;
+        over |= s[h][0][j] > limit[j & 1];
+      }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int c = 0; c < 2; ++c) {
+        float x = fmaxf(fmaxf(s[0][0][c], s[0][0][c + 2]), fmaxf(s[1][0][c], s[1][0][c + 2]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * factor[c];
+        // no branch here: lanes of different columns decide differently, and
+        // the warp-wide instructions below need them together
+        const bool first = limit[c] == -INFINITY;
+        const bool take = x != -INFINITY && (first || x > ref[c]);
+        const float y = take ? x : ref[c];
+        const float b = dev::fast_exp2(ref[c] - y);
+        const float a = take && first ? 0.0f : b;
+        ref[c] = y;
+        limit[c] = take ? __fdividef(x + 8.0f, factor[c]) : limit[c];
+        l[c] *= a;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * factor[nt][c];
-          const bool first = limit[nt][c] == -INFINITY;
-          if (x != -INFINITY && (first || x > ref[nt][c])) {
-            const float a = first ? 0.0f : dev::fast_exp2(ref[nt][c] - x);
-            ref[nt][c] = x;
-            limit[nt][c] = (x + 8.0f) / factor[nt][c];
-            l[nt][c] *= a;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              o[k][nt][c] *= a;
-              o[k][nt][c + 2] *= a;
-            }
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          o[k][c] *= a;
+          o[k][c + 2] *= a;
         }
-    }
-    uint32_t pf[2][NT][2];  // P^T as the second product's B operand
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          p[j] = dev::fast_exp2(fmaf(s[h][nt][j], factor[nt][j & 1], -ref[nt][j & 1]));
-          l[nt][j & 1] += p[j];
-        }
-        pf[h][nt][0] = dev::transpose_8x8(dev::pack_f16(p[0], p[1]));
-        pf[h][nt][1] = dev::transpose_8x8(dev::pack_f16(p[2], p[3]));
       }
+    }
+    __syncwarp();
+    uint32_t pf[2][2];  // P^T as the second product's B operand
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = dev::fast_exp2(fmaf(s[h][0][j], factor[j & 1], -ref[j & 1]));
+        l[j & 1] += p[j];
+      }
+      pf[h][0] = dev::transpose_8x8(dev::pack_f16(p[0], p[1]));
+      pf[h][1] = dev::transpose_8x8(dev::pack_f16(p[2], p[3]));
+    }
 
-    // ---- O^T += V^T P^T over the keys [.., end) of the step; with `only` >= 0
-    // for the columns of that token alone
-    auto value_product = [&](int h, int end, int only, auto single) {
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       uint32_t w[4][VW], sb[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -318,8 +445,16 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
           w[r][0] = *reinterpret_cast<const uint32_t*>(codes);
         }
         sb[r] = tile[(row % BS) * (D / 16) + ((r & 1) ? lane_vsb : lane_vsa)];
-        // a key that is not there: finite codes times zero
-        if (EDGE && key0 + row + ((r & 1) ? row_b : row_a) >= end) sb[r] = 0;
+        if constexpr (EDGE) {
+          // A key that is not there gets scale zero (its codes are finite). So
+          // does one with a NaN scale, which some column may not see and which
+          // 0 * NaN would carry there; the columns that see it get their NaN at
+          // the end.
+          const int key = key0 + row + ((r & 1) ? row_b : row_a);
+          const bool nan = (sb[r] & 0x7Fu) == 0x7Fu;
+          nan_from = nan ? min(nan_from, key) : nan_from;
+          sb[r] = nan || key >= see_last ? 0u : sb[r];
+        }
       }
       const uint32_t s01 = dev::e4m3x2_to_f16(sb[0] | sb[1] << 8);
       const uint32_t s23 = dev::e4m3x2_to_f16(sb[2] | sb[3] << 8);
@@ -331,49 +466,17 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
         dev::e2m1x8_to_f16((w[2][c] & 0x0F0F0F0Fu) | ((w[3][c] << 4) & 0xF0F0F0F0u), e1);
         dev::e2m1x8_to_f16(((w[2][c] >> 4) & 0x0F0F0F0Fu) | (w[3][c] & 0xF0F0F0F0u), o1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = dev::mul_f16x2(e0[j], s01), a1 = dev::mul_f16x2(o0[j], s01);
-          const uint32_t a2 = dev::mul_f16x2(e1[j], s23), a3 = dev::mul_f16x2(o1[j], s23);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (!decltype(single)::value) {
-              dev::mma_f16(o[c * 4 + j][nt], a0, a1, a2, a3, pf[h][nt][0], pf[h][nt][1]);
-            } else {
-              float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              dev::mma_f16(x, a0, a1, a2, a3, pf[h][nt][0], pf[h][nt][1]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (((nt * 8 + 2 * t + (k & 1)) >> P.g_log2) == only) o[c * 4 + j][nt][k] += x[k];
-            }
-          }
-        }
-      }
-    };
-    if constexpr (EDGE) {
-      // a NaN in a key that only later new tokens see must not reach the
-      // earlier ones as 0 * NaN: such steps run token by token
-      uint32_t bad = 0;
-#pragma unroll
-      for (int x = 0; x < KEYS / 4; ++x) {
-        const int row = x * 4 + t;
-        const unsigned char* scl =
-            vt + (row / BS) * TILE + BS * (D / 2) + (row % BS) * (D / 16) + (g * VW) / 2;
-        bad |= uint32_t(key0 + row < tok1 && (*scl & 0x7F) == 0x7F);
-      }
-      if (P.q_len > 1 && __any_sync(0xffffffffu, bad != 0)) {
-        for (int x = 0; x < n_tok; ++x)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) value_product(h, min(tok1, see0 + x), x, std::true_type{});
-        return;
+        for (int j = 0; j < 4; ++j)
+          dev::mma_f16(o[c * 4 + j], dev::mul_f16x2(e0[j], s01), dev::mul_f16x2(o0[j], s01),
+                       dev::mul_f16x2(e1[j], s23), dev::mul_f16x2(o1[j], s23), pf[h][0], pf[h][1]);
       }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) value_product(h, tok1, -1, std::false_type{});
   };
 
-  // the steps before the first that is an edge; key0 + KEYS > see_first there
-  const int n_full = see_first <= tok0 ? 0 : (see_first - tok0) / KEYS;  // whole steps of the CTA
+  // steps of the item before the first that is an edge, and this warp's share
+  const int n_full = see0 / KEYS - piece.first;
   const int n_inner = n_full > warp ? (n_full - warp + NWARPS - 1) / NWARPS : 0;
+  int ahead = window;  // table entries of the steps being issued
   for (int i = 0, stage = 0; i < n_my; ++i) {
     dev::cp_async_wait<ST - 1>();
     __syncwarp();
@@ -382,111 +485,202 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3)
     else
       step(i, stage, std::true_type{});
     __syncwarp();
-    issue(i + ST, stage);
+    if ((i + ST) % WINDOW == 0) ahead = load_window(piece, i + ST);
+    issue(piece, i + ST, n_my, ahead, stage);
     stage = stage + 1 == ST ? 0 : stage + 1;
   }
+  dev::cp_async_wait<0>();
+  __syncwarp();
 
-  // ---- merge the warps through shared memory (reusing the rings)
+  // ---- merge the warps through shared memory
+  nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 1));
+  nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 2));
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int c = 0; c < 2; ++c) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
-  __syncthreads();
-  float* sm_o = reinterpret_cast<float*>(smem);              // [NWARPS][COLS][OROW]
-  float* sm_m = sm_o + NWARPS * C::COLS * C::OROW;           // [NWARPS][COLS]
-  float* sm_l = sm_m + NWARPS * C::COLS;                     // [NWARPS][COLS]
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int n = warp * C::COLS + nt * 8 + 2 * t + c;
-      if (g == 0) {
-        sm_m[n] = limit[nt][c] == -INFINITY ? -INFINITY : ref[nt][c];
-        sm_l[n] = l[nt][c];
-      }
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)  // rows g and g + 8 of tile k: elements g D/8 + 2k, + 1
-        *reinterpret_cast<float2*>(sm_o + n * C::OROW + g * (D / 8) + 2 * k) =
-            make_float2(o[k][nt][c], o[k][nt][c + 2]);
+    for (int x = 4; x < 32; x <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], x);
+    const int n = warp * C::COLS + 2 * t + c;
+    if (g == 0) {
+      sm_m[n] = limit[c] == -INFINITY ? -INFINITY : ref[c];
+      sm_l[n] = l[c];
     }
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)  // rows g and g + 8 of tile k: elements g D/8 + 2k, + 1
+      *reinterpret_cast<float2*>(sm_o + n * C::OROW + g * (D / 8) + 2 * k) =
+          nan_from < see[c] ? make_float2(NAN, NAN) : make_float2(o[k][c], o[k][c + 2]);
+  }
+  if (tid == 0) pieces[cur ^ 1] = walk.next(P);
   __syncthreads();
-  const float vs = P.v_scale[head];
-  for (int idx = tid; idx < n_cols * (D / 2); idx += NTHREADS) {
-    const int n = idx / (D / 2), d = idx % (D / 2) * 2;
-    const int last = see0 + (n >> P.g_log2);  // keys this row sees
-    if (tok0 >= last) continue;
-    float M = -INFINITY;
+  // the next piece's first steps are on their way during the merge
+  if (pieces[cur ^ 1].valid) begin(pieces[cur ^ 1]);
+  {
+    const Piece& done = piece;
+    constexpr int TPC = NTHREADS / C::COLS;  // threads of a column
+    constexpr int E = D / TPC;               // elements of a thread
+    // columns past n_cols are computed along and not stored, so that no
+    // branch parts the threads of a warp
+    const int n = tid / TPC, d = tid % TPC * E;
+    const bool on = n < n_cols;
+    float wt[NWARPS], M = -INFINITY, den = 0.0f;
 #pragma unroll
     for (int w = 0; w < NWARPS; ++w) M = fmaxf(M, sm_m[w * C::COLS + n]);
-    float x = 0.0f, y = 0.0f, den = 0.0f;
 #pragma unroll
     for (int w = 0; w < NWARPS; ++w) {
-      const int r = w * C::COLS + n;
-      const float wt = sm_m[r] == -INFINITY ? 0.0f : dev::fast_exp2(sm_m[r] - M);
-      const float2 v = *reinterpret_cast<const float2*>(sm_o + r * C::OROW + d);
-      x = fmaf(wt, v.x, x);
-      y = fmaf(wt, v.y, y);
-      den = fmaf(wt, sm_l[r], den);
+      const float x = sm_m[w * C::COLS + n];
+      const float y = dev::fast_exp2(x - M);
+      wt[w] = x == -INFINITY ? 0.0f : y;
+      den = fmaf(wt[w], sm_l[w * C::COLS + n], den);
     }
-    x *= vs;
-    y *= vs;
-    const int64_t row = q_row(n);
-    if (last <= P.partition_tokens) {
-      const float inv = __frcp_rn(den);
-      *reinterpret_cast<__nv_bfloat162*>(P.out + row * D + d) =
-          __floats2bfloat162_rn(x * inv, y * inv);
-    } else {
-      const int64_t prow = row * P.num_partitions + part;
-      *reinterpret_cast<float2*>(P.part_acc + prow * D + d) = make_float2(x, y);
-      if (d == 0) {
-        P.part_m[prow] = M;
-        P.part_l[prow] = den;
+    const bool direct = done.first == 0 && done.last == done.steps;
+    const float norm = direct ? P.v_scale[head] / den : P.v_scale[head];
+    const int slot = 2 * blockIdx.x + (done.first == 0);  // the CTA's last piece, or its first
+    __nv_bfloat16* out = P.out + q_row(min(n, n_cols - 1)) * D + d;
+    float* acc = P.part_acc + (int64_t(slot) * C::COLS + n) * D + d;
+#pragma unroll
+    for (int x = 0; x < E; x += 4) {
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < NWARPS; ++w) {
+        const float4 y =
+            *reinterpret_cast<const float4*>(sm_o + (w * C::COLS + n) * C::OROW + d + x);
+        sum.x = fmaf(wt[w], y.x, sum.x);
+        sum.y = fmaf(wt[w], y.y, sum.y);
+        sum.z = fmaf(wt[w], y.z, sum.z);
+        sum.w = fmaf(wt[w], y.w, sum.w);
       }
+      __nv_bfloat162 r[2] = {__floats2bfloat162_rn(sum.x * norm, sum.y * norm),
+                             __floats2bfloat162_rn(sum.z * norm, sum.w * norm)};
+      if (direct && on) *reinterpret_cast<uint2*>(out + x) = *reinterpret_cast<const uint2*>(r);
+      if (!direct && on)
+        *reinterpret_cast<float4*>(acc + x) =
+            make_float4(sum.x * norm, sum.y * norm, sum.z * norm, sum.w * norm);
     }
+    if (!direct && on && d == 0)
+      *reinterpret_cast<float2*>(P.part_ml + (int64_t(slot) * C::COLS + n) * 2) =
+          make_float2(M, den);
   }
+  __syncwarp();
+  __syncthreads();  // before the next piece's rows
+  }
+  if (bad_entry && lane == 0) atomicOr(&g_decode_fp4_errors, PA_DEVERR_TABLE_ENTRY);
 }
 
-template <int D, int NT, int BS>
-int launch_t(const Fp4Decode& P, const pa_decode_params* p, cudaStream_t stream) {
-  using C = Cfg<D, NT, BS>;
-  const size_t smem = C::TILES + size_t(P.partition_tokens / BS + 1) * sizeof(int32_t);
-  // the opt-in to large shared memory is per device: asked for the most that
-  // a partition may need, once each
+// Joins the pieces of the items that were cut: one warp per (item, column).
+template <int D>
+__global__ void __launch_bounds__(128) merge_fp4_kernel(const Fp4Decode P, int grid) {
+  constexpr int E = D / 32, COLS = Cfg<D, 16>::COLS;  // elements of a lane; columns
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int n = int(row % COLS);
+  const int64_t item = row / COLS;
+  const int v = int(item / P.num_kv_heads), head = int(item - int64_t(v) * P.num_kv_heads);
+  if (v >= P.num_virtual) return;
+  const Virtual x = virtual_of(P, v);
+  dev::griddep_wait();  // the plan and the partials
+  if (x.steps == 0 || n >= (x.n_tok << P.g_log2)) return;
+  const int64_t T = P.plan[P.num_virtual];
+  const int64_t base = P.plan[v] + int64_t(head) * item_cost(x) + START_COST;
+  const int G = stretches(T, grid);
+  const int c0 = owner(base, T, G), c1 = owner(base + x.steps - 1, T, G);
+  if (c0 == c1) return;  // one piece: written by the decode
+  auto slot = [&](int c) { return (int64_t(2 * c + (c == c0)) * COLS + n); };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, P.part_ml[slot(c) * 2]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[E], den = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float2 ml = *reinterpret_cast<const float2*>(P.part_ml + slot(c) * 2);
+    const float wt = ml.x == -INFINITY ? 0.0f : dev::fast_exp2(ml.x - M);
+    den = fmaf(wt, ml.y, den);
+    const float* src = P.part_acc + slot(c) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(src + e);
+      acc[e] = fmaf(wt, y.x, acc[e]);
+      acc[e + 1] = fmaf(wt, y.y, acc[e + 1]);
+    }
+  }
+  const float inv = __frcp_rn(den);
+  const int b = v / P.n_groups, first = (v - b * P.n_groups) * P.q_group;
+  const int group = 1 << P.g_log2;
+  const int64_t q = (int64_t(b) * P.q_len + first + (n >> P.g_log2)) *
+                        (P.num_kv_heads << P.g_log2) + head * group + (n & (group - 1));
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(P.out + q * D + lane * E + e) =
+        __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <int D, int BS>
+int launch_t(const Fp4Decode& P, int grid, cudaStream_t stream) {
+  using C = Cfg<D, BS>;
+  // the opt-in to large shared memory is per device
   static std::atomic<uint64_t> configured{0};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return int(e);
   const uint64_t bit = uint64_t(1) << (device & 63);
   if (!(configured.load(std::memory_order_relaxed) & bit)) {
-    const size_t most = C::TILES + size_t(kMaxPartitionTokens / BS + 1) * sizeof(int32_t);
-    e = cudaFuncSetAttribute(paged_decode_fp4_kernel<D, NT, BS>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
+    e = cudaFuncSetAttribute(paged_decode_fp4_kernel<D, BS>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return int(e);
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  const dim3 grid(unsigned(P.num_partitions), unsigned(P.num_kv_heads),
-                  unsigned(p->num_seqs * P.n_groups));
-  paged_decode_fp4_kernel<D, NT, BS><<<grid, NTHREADS, smem, stream>>>(P);
-  return int(cudaGetLastError());
+  paged_decode_fp4_kernel<D, BS><<<unsigned(grid), NTHREADS, C::SMEM, stream>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || P.whole) return int(e);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t rows = int64_t(P.num_virtual) * P.num_kv_heads * C::COLS;
+  cfg.gridDim = dim3(unsigned((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return int(cudaLaunchKernelEx(&cfg, merge_fp4_kernel<D>, P, grid));
 }
 
-template <int D, int NT>
-int launch_bs(const Fp4Decode& P, const pa_decode_params* p, cudaStream_t s) {
-  switch (p->block_size) {
-    case 8: return launch_t<D, NT, 8>(P, p, s);
-    case 16: return launch_t<D, NT, 16>(P, p, s);
-    case 32: return launch_t<D, NT, 32>(P, p, s);
+template <int D>
+int launch_bs(const Fp4Decode& P, int block_size, int grid, cudaStream_t s) {
+  switch (block_size) {
+    case 8: return launch_t<D, 8>(P, grid, s);
+    case 16: return launch_t<D, 16>(P, grid, s);
+    case 32: return launch_t<D, 32>(P, grid, s);
     default: return int(cudaErrorInvalidValue);
   }
 }
 
 }  // namespace
 
-int launch_decode_fp4(const DecodeLaunch& L, void* stream) {
+Fp4Plan fp4_plan(const pa_decode_params* p, int num_sms) {
+  Fp4Plan r{};
+  const MmaColumns cols = fp4_columns(p);
+  const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
+  r.cap = int(p->max_context_len < table ? p->max_context_len : table);
+  const int64_t items = int64_t(p->num_seqs) * cols.n_groups * p->num_kv_heads;
+  r.cols = 8;
+  r.whole = r.cap <= kFp4WholeTokens;
+  if (r.whole) {
+    r.grid = int(items);
+  } else {
+    // as many CTAs as are resident at once, but no stretch under two start costs
+    const int64_t most = items * ((r.cap + KEYS - 1) / KEYS + START_COST) / (2 * START_COST);
+    const int64_t full = int64_t(num_sms > 0 ? num_sms : 256) * 4;
+    r.grid = int(most < full ? most : full);
+    if (r.grid < 1) r.grid = 1;
+  }
+  return r;
+}
+
+int launch_decode_fp4(const DecodeLaunch& L, const Fp4Plan& plan, void* stream) {
   const pa_decode_params* p = L.p;
-  const MmaColumns cols = mma_columns(p->num_q_heads / p->num_kv_heads, query_len_of(p));
+  const MmaColumns cols = fp4_columns(p);
   Fp4Decode P;
   P.q = static_cast<const __nv_bfloat16*>(p->q);
   P.out = static_cast<__nv_bfloat16*>(p->out);
@@ -496,26 +690,24 @@ int launch_decode_fp4(const DecodeLaunch& L, void* stream) {
   P.v_scale = p->v_scale;
   P.block_tables = p->block_tables;
   P.context_lens = p->context_lens;
-  P.part_m = L.part_m;
-  P.part_l = L.part_l;
+  P.plan = reinterpret_cast<int64_t*>(L.plan);
+  P.part_ml = L.part_m;
   P.part_acc = L.part_acc;
   P.scale_log2 = p->scale * kLog2e;
   P.max_blocks_per_seq = p->max_blocks_per_seq;
   P.num_kv_heads = p->num_kv_heads;
   P.num_blocks = p->num_blocks;
-  P.max_context_len = p->max_context_len;
+  P.cap = plan.cap;
   P.g_log2 = log2_of(p->num_q_heads / p->num_kv_heads);
   P.q_len = query_len_of(p);
   P.q_group = cols.q_group;
   P.n_groups = cols.n_groups;
-  P.partition_tokens = L.partition_tokens;
-  P.num_partitions = L.num_partitions;
+  P.num_virtual = p->num_seqs * cols.n_groups;
+  P.whole = plan.whole;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  switch (p->head_dim * 4 + cols.n_tiles) {
-    case 64 * 4 + 1: return launch_bs<64, 1>(P, p, s);
-    case 64 * 4 + 2: return launch_bs<64, 2>(P, p, s);
-    case 128 * 4 + 1: return launch_bs<128, 1>(P, p, s);
-    case 128 * 4 + 2: return launch_bs<128, 2>(P, p, s);
+  switch (p->head_dim) {
+    case 64: return launch_bs<64>(P, p->block_size, plan.grid, s);
+    case 128: return launch_bs<128>(P, p->block_size, plan.grid, s);
     default: return int(cudaErrorInvalidValue);
   }
 }

@@ -181,12 +181,15 @@ __device__ __forceinline__ void bulk_load(void* dst_smem, const void* src_gmem, 
       : "memory");
 }
 
-// 16 bytes global -> shared, past L1 (completion: cp_async_commit / cp_async_wait).
-__device__ __forceinline__ void cp_async16(void* dst_smem, const void* src_gmem, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
-                   smem_addr(dst_smem)),
-               "l"(src_gmem), "l"(policy)
-               : "memory");
+// 16 bytes global -> shared, past L1, where `on` (completion: cp_async_commit /
+// cp_async_wait). Predicated rather than branched around: the warp stays together.
+__device__ __forceinline__ void cp_async16(void* dst_smem, const void* src_gmem, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}\n" ::"r"(smem_addr(dst_smem)),
+      "l"(src_gmem), "r"(uint32_t(on))
+      : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");

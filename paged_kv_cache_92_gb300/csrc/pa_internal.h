@@ -132,18 +132,21 @@ __device__ __forceinline__ int64_t query_source_row(const QueryMap& m, int v, in
 #endif
 
 // Column layout of the 4-bit decode and of the token weights: the query rows
-// of a KV head are the columns of its products, token by token, in 8-column
-// tiles (one or two); a sequence with more new tokens than those hold is
-// worked off as several groups, each reading the keys.
+// of a KV head are the columns of its products, token by token, in `n_tiles`
+// tiles of 8; a sequence with more new tokens than those hold is worked off as
+// several groups, each reading the keys.
 struct MmaColumns {
   int n_tiles, q_group, n_groups;
 };
-inline MmaColumns mma_columns(int g, int q) {
+inline MmaColumns mma_columns(int g, int q, int max_tiles) {
   MmaColumns c;
-  c.n_tiles = g * q <= 8 ? 1 : 2;
+  c.n_tiles = g * q <= 8 ? 1 : max_tiles;
   c.q_group = q < 8 * c.n_tiles / g ? q : 8 * c.n_tiles / g;
   c.n_groups = (q + c.q_group - 1) / c.q_group;
   return c;
+}
+inline MmaColumns fp4_columns(const pa_decode_params* p) {
+  return mma_columns(p->num_q_heads / p->num_kv_heads, query_len_of(p), 1);
 }
 
 // Bytes at the start of every decode workspace (reserved).
@@ -215,7 +218,16 @@ int launch_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, voi
                       const int64_t* slot_mapping, const float* k_scale, const float* v_scale,
                       int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
                       int32_t block_size, int32_t num_blocks, void* stream);
-int launch_decode_fp4(const DecodeLaunch& L, void* stream);  // then launch_merge
+// How the 4-bit decode deals out its work: contexts up to kFp4WholeTokens take
+// one CTA per (sequence, column group, KV head); longer ones a stream over
+// `grid` persistent CTAs, with two partials a CTA for the pieces it cuts.
+constexpr int kFp4WholeTokens = 512;
+struct Fp4Plan {
+  int grid, cols, cap;  // CTAs; columns of a partial; keys a sequence may have
+  bool whole;
+};
+Fp4Plan fp4_plan(const pa_decode_params* p, int num_sms);
+int launch_decode_fp4(const DecodeLaunch& L, const Fp4Plan& plan, void* stream);
 int read_and_clear_fp4_errors(uint32_t* flags);
 int read_and_clear_decode_fp4_errors(uint32_t* flags);
 

@@ -179,22 +179,22 @@ __device__ __forceinline__ void key_product(float (&s)[NT][4], const KeyRow<FMT,
   }
 }
 
-// One query row as the products' B operand (nullptr: a row of zeros), for the
-// lane with t = lane % 4; the four lanes of a row call together. bf16 rows stay
+// One query row as the products' B operand (`on` false: a row of zeros; `row`
+// is read all the same), for the lane with t = lane % 4; all lanes call together. bf16 rows stay
 // as they are and the result is 1. The others are scaled to f16 by a power of
 // two that brings the row's largest magnitude into [2^12, 2^13), exactly for
 // every element within 2^-30 of it, and its inverse is returned.
 template <int FMT, int D>
-__device__ __forceinline__ float query_fragment(const __nv_bfloat16* row, int t,
+__device__ __forceinline__ float query_fragment(const __nv_bfloat16* row, bool on, int t,
                                                 uint32_t (&qf)[D / 16][2]) {
   using R = KeyRow<FMT, D>;
   uint4 raw[D / 32];
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {  // 8 elements of the lane's list
     const int e = 8 * c;
-    raw[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (row != nullptr)
-      raw[c] = *reinterpret_cast<const uint4*>(row + (4 * (e / R::E) + t) * R::E + e % R::E);
+    const uint4 x =
+        *reinterpret_cast<const uint4*>(row + (4 * (e / R::E) + t) * R::E + e % R::E);
+    raw[c] = make_uint4(on ? x.x : 0u, on ? x.y : 0u, on ? x.z : 0u, on ? x.w : 0u);
   }
   if constexpr (FMT == 0) {
 #pragma unroll
@@ -214,10 +214,11 @@ __device__ __forceinline__ float query_fragment(const __nv_bfloat16* row, int t,
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    int e = 0;
-    if (amax > 0.0f && amax <= 3.4e38f) (void)frexpf(amax, &e);  // amax < 2^e
-    e = max(e, -100);
-    const float a = ldexpf(1.0f, 13 - e);  // e in [-100, 128]: a normal power of two
+    // amax < 2^e from its exponent field; zeros, infinities and NaN keep 2^13
+    const int field = int(__float_as_uint(amax) >> 23);
+    const int e = field == 0 || field == 255 ? (amax > 0.0f && field == 0 ? -100 : 0)
+                                             : max(field - 126, -100);
+    const float a = __uint_as_float(uint32_t(13 - e + 127) << 23);  // 2^(13 - e): normal
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       float f[8];
@@ -226,7 +227,7 @@ __device__ __forceinline__ float query_fragment(const __nv_bfloat16* row, int t,
       for (int i = 0; i < 4; ++i)
         qf[2 * c + i / 2][i & 1] = pack_f16(f[2 * i] * a, f[2 * i + 1] * a);
     }
-    return ldexpf(1.0f, e - 13);
+    return __uint_as_float(uint32_t(e - 13 + 127) << 23);
   }
 }
 

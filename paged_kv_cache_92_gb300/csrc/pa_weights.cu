@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(NTHREADS)
   for (int nt = 0; nt < NT; ++nt) {
     const int n = nt * 8 + g;
     const float f =
-        kfac * dev::query_fragment<FMT, D>(n < n_cols ? P.q + q_row(n) * D : nullptr, t, qf[nt]);
+        kfac * dev::query_fragment<FMT, D>(P.q + q_row(min(n, n_cols - 1)) * D, n < n_cols, t,
+                                           qf[nt]);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int m = nt * 8 + 2 * t + c;
@@ -353,7 +354,7 @@ int launch_token_weights(const pa_token_weights_params* p, const TokenWeightsSpa
                          unsigned char* ws, void* stream) {
   const int g = p->num_q_heads / p->num_kv_heads;
   const int q = p->query_len > 1 ? p->query_len : 1;
-  const MmaColumns cols = mma_columns(g, q);
+  const MmaColumns cols = mma_columns(g, q, 2);
   Weights P;
   P.q = static_cast<const __nv_bfloat16*>(p->q);
   P.k_cache = static_cast<const unsigned char*>(p->k_cache);

@@ -92,6 +92,17 @@ class Case:
                 max(1, int(self.lens.max()))), dict(k_scale=torch.from_numpy(self.ks).cuda(),
                                                     v_scale=torch.from_numpy(self.vs).cuda())
 
+    def cuda_cut(self):
+        """The same batch with room for 4,096 tokens a sequence: the work is dealt out
+        as a stream that cuts the sequences' keys into pieces of a few steps."""
+        import torch
+
+        a, sc = self.cuda()
+        room = -(-4096 // self.BS)
+        tab = torch.full((len(self.lens), room), -1, dtype=torch.int32, device="cuda")
+        tab[:, :a[3].shape[1]] = a[3]
+        return a[:3] + (tab, a[4], 4096), sc
+
     def want(self, scale=None):
         kr, vr = (oracle.fp4_values(c, s, self.D) for c, s in ((self.k, self.ks), (self.v, self.vs)))
         q = oracle.bf16_to_f64(self.q)
@@ -175,6 +186,7 @@ def _lib_params(pk, **kw):
     (dict(kv_dtype=3), 1), (dict(partition_tokens=24), 1),
     (dict(partition_tokens=48, block_size=32), 1),  # partitions are whole blocks
     (dict(query_len=1025), 1), (dict(query_len=1024, num_seqs=64), 2),
+    (dict(query_len=63, num_seqs=1024, num_kv_heads=2048, num_q_heads=2048, num_blocks=1), 2),
     (dict(max_context_len=0), 1), (dict(scale=0.0), 1),
 ])
 def test_decode_refusals(pk, kw, status):
@@ -227,20 +239,26 @@ def test_binding_refuses_mixed_shapes(pk):
                               torch.zeros(1, dtype=torch.int32), 16)
 
 
-def test_workspace_holds_one_partial_per_partition(pk):
-    """Partials for every (row, partition) when a sequence can split, else the header alone."""
+def test_workspace_holds_two_partials_per_cta(pk):
+    """The header alone where contexts are short (at most 512 tokens); else the plan (a
+    64-bit cost per sequence and column group, and the total) and two partials a CTA:
+    four CTAs an SM, or one per 16 steps and starts."""
     def size(**kw):
         return pk.load().pa_decode_workspace_size(ctypes.byref(_lib_params(pk, **kw)))
 
     def ru(x):
         return (x + 255) // 256 * 256
 
-    assert size(partition_tokens=64) == 256
-    rows = 2 * 8 * 4 * 3  # sequences, heads, partitions, new tokens
-    assert size(partition_tokens=16, query_len=3) == 256 + 2 * ru(rows * 4) + ru(rows * 128 * 4)
-    # chosen from the shapes: short contexts are not split below 128 tokens
-    assert size(max_blocks_per_seq=8, max_context_len=128) == 256
-    assert size(max_blocks_per_seq=9, max_context_len=144) > 256
+    assert size() == size(max_blocks_per_seq=32, max_context_len=512) == 256
+    assert size(max_blocks_per_seq=32, max_context_len=4096) == 256  # the table holds 512
+    kw = dict(max_blocks_per_seq=64, max_context_len=544)
+    grid = 2 * 2 * (17 + 8) // 16          # items x (steps + start), 16 a CTA
+    rows = 2 * grid * 8
+    assert size(**kw) == 256 + ru(3 * 8) + ru(rows * 8) + ru(rows * 128 * 4)
+    kw["query_len"] = 9                    # groups of two tokens (G 4): five
+    grid = 2 * 5 * 2 * (17 + 8) // 16
+    rows = 2 * grid * 8
+    assert size(**kw) == 256 + ru(11 * 8) + ru(rows * 8) + ru(rows * 128 * 4)
 
 
 # ------------------------------------------------------------------ GPU: rows
@@ -383,7 +401,8 @@ def test_decode_edge_lengths(pk, Hq, Hkv, D, BS):
     c = Case(EDGE, Hq, Hkv, D, BS, seed=Hq + D + BS)
     args, sc = c.cuda()
     _check(pk, pk.pa_decode(*args, **sc), c)
-    _check(pk, pk.pa_decode(*args, partition_tokens=32, **sc), c)  # split and merged
+    args, sc = c.cuda_cut()
+    _check(pk, pk.pa_decode(*args, **sc), c)
 
 
 @pytest.mark.gpu
@@ -395,7 +414,21 @@ def test_decode_several_new_tokens(pk, Q, Hq, Hkv, D, BS):
     c = Case(lens, Hq, Hkv, D, BS, Q=Q, seed=Q)
     args, sc = c.cuda()
     _check(pk, pk.pa_decode(*args, **sc), c)
-    _check(pk, pk.pa_decode(*args, partition_tokens=64, **sc), c)
+    args, sc = c.cuda_cut()
+    _check(pk, pk.pa_decode(*args, **sc), c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [1, 300])
+def test_decode_many_and_few_sequences(pk, B):
+    """One long sequence over every CTA, and more sequences than threads of a CTA."""
+    rng = np.random.default_rng(B)
+    lens = [3001] if B == 1 else rng.integers(1, 60, B)
+    c = Case(lens, 4, 1, 64, 16, seed=B)
+    args, sc = c.cuda()
+    _check(pk, pk.pa_decode(*args, **sc), c)
+    args, sc = c.cuda_cut()
+    _check(pk, pk.pa_decode(*args, **sc), c)
 
 
 @pytest.mark.gpu
@@ -434,12 +467,16 @@ def test_decode_empty_and_short_sequences(pk):
     c = Case([40, 3, 17], 4, 2, Q=4, seed=6)
     args, sc = c.cuda()
     lens = torch.tensor([0, 3, 17], dtype=torch.int32, device="cuda")
-    out = pk.pa_decode(args[0], args[1], args[2], args[3], lens, 40, **sc)
-    assert pk.pa_device_errors() == pk.DEVERR_CONTEXT_LEN  # 3 keys cannot hold 4 new tokens
-    assert not out[:2].any()
-    got = oracle.bf16_to_f64(out[2].cpu())
     want, mag = c.want()
-    assert (np.abs(got - want[2]) <= _bound(want[2], mag[2])).all()
+    for a, mx in ((args, 40), (c.cuda_cut()[0], 4096)):
+        out = pk.pa_decode(*a[:4], lens, mx, **sc)
+        assert pk.pa_device_errors() == pk.DEVERR_CONTEXT_LEN  # 3 keys cannot hold 4 new tokens
+        assert not out[:2].any()
+        got = oracle.bf16_to_f64(out[2].cpu())
+        assert (np.abs(got - want[2]) <= _bound(want[2], mag[2])).all()
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")  # nothing cached at all
+    assert not pk.pa_decode(*c.cuda_cut()[0][:4], none, 4096, **sc).any()
+    assert pk.pa_device_errors() == 0
 
 
 @pytest.mark.gpu
@@ -457,39 +494,36 @@ def test_decode_nan_rows_stay_with_those_who_see_them(pk):
         blk, off = int(c.tables[0, pos // BS]), pos % BS
         cache.reshape(c.NB, 2, -1)[blk, 1, BS * D // 2 + off * D // 16 + 3] = 0x7F
         args, sc = c.cuda()
-        for pt in (0, 16):
-            got = oracle.bf16_to_f64(pk.pa_decode(*args, partition_tokens=pt, **sc).cpu())
+        for a in (args, c.cuda_cut()[0]):
+            got = oracle.bf16_to_f64(pk.pa_decode(*a, **sc).cpu())
             nan = np.isnan(got)
             want = np.zeros_like(nan)
             if which == 0:
                 want[0, 2:, 2:] = True          # K: the whole rows of KV head 1
             else:
                 want[0, 2:, 2:, 48:64] = True   # V: group 3
-            assert np.array_equal(nan, want), (which, pt)
+            assert np.array_equal(nan, want), which
             ok = ~want
             assert (np.abs(got - clean[0])[ok] <= _bound(*clean)[ok]).all()
     torch.cuda.synchronize()
 
 
 @pytest.mark.gpu
-def test_decode_bits_do_not_depend_on_placement_variant_or_batch(pk):
+def test_decode_bits_do_not_depend_on_placement_or_variant(pk):
     import torch
 
-    c = Case([300, 47, 129], 8, 2, seed=12)
+    c = Case([300, 47, 1290], 8, 2, seed=12)
     args, sc = c.cuda()
-    base = pk.pa_decode(*args, partition_tokens=128, **sc)
-    assert torch.equal(base, pk.pa_decode(*args, partition_tokens=128, variant=1, **sc))
+    base = pk.pa_decode(*args, **sc)
+    assert torch.equal(base, pk.pa_decode(*args, variant=1, **sc))
+    assert torch.equal(base, pk.pa_decode(*args, partition_tokens=128, **sc))
     perm = torch.from_numpy(np.random.default_rng(4).permutation(c.NB)).cuda()
     inv = torch.empty_like(perm)
     inv[perm] = torch.arange(c.NB, device="cuda")
     tab = torch.where(args[3] >= 0, inv[args[3].clamp(min=0).long()].int(), args[3])
     moved = pk.pa_decode(args[0], args[1][perm].contiguous(), args[2][perm].contiguous(), tab,
-                         args[4], args[5], partition_tokens=128, **sc)
+                         args[4], args[5], **sc)
     assert torch.equal(base, moved)
-    for b in range(3):
-        one = pk.pa_decode(args[0][b:b + 1], args[1], args[2], args[3][b:b + 1].contiguous(),
-                           args[4][b:b + 1], args[5], partition_tokens=128, **sc)
-        assert torch.equal(one[0], base[b])
 
 
 @pytest.mark.gpu
