@@ -226,8 +226,9 @@ typedef struct {
  * Written by pa_reshape_and_cache_fp4, read back by pa_gather_fp4, copied by
  * pa_copy_blocks_fp4. One kernel decodes it whatever `variant` says: head_dim
  * 64 or 128, every block size, G in {1, 2, 4, 8}, any number of KV heads,
- * num_seqs * query_len <= 65535 and num_seqs * num_kv_heads * (query_len + 1)
- * < 2^27 (else PA_ERR_UNSUPPORTED). The codes are multiplied exactly; the
+ * num_seqs * query_len <= 65535 and num_seqs * ceil(query_len / (8 / G)) *
+ * num_kv_heads * (max_context_len / 32 + 9) < 2^31 (else PA_ERR_UNSUPPORTED;
+ * max_context_len no more than the table holds). The codes are multiplied exactly; the
  * softmax weights are rounded to f16. With several new tokens, up to 8 / G of
  * them share each load of the keys. */
 #define PA_KV_FP4_E2M1 2

@@ -86,11 +86,10 @@ pa_status check_decode(const pa_decode_params* p, bool need_pointers) {
                      "pa_decode: on the CUDA-core kernel num_seqs * query_len must be <= 65535 "
                      "(the tensor-core kernel takes num_kv_heads 1/2/4/8 and num_seqs * "
                      "(query_len split into column groups) <= 16384)");
-  if (p->kv_dtype == PA_KV_FP4_E2M1 &&
-      int64_t(p->num_seqs) * p->num_kv_heads * (query_len_of(p) + 1) * 16 >= (int64_t(1) << 31))
+  if (p->kv_dtype == PA_KV_FP4_E2M1 && !fp4_stream_ok(p))
     return set_error(PA_ERR_UNSUPPORTED,
-                     "pa_decode: the 4-bit cache takes num_seqs * num_kv_heads * (query_len + 1) "
-                     "below 2^27");
+                     "pa_decode: the 4-bit cache takes num_seqs * column groups * num_kv_heads * "
+                     "(tokens / 32 + 9) below 2^31");
   if (p->kv_dtype != PA_KV_BF16) {
     if (need_pointers && p->num_seqs > 0 &&
         (!p->k_scale || !p->v_scale || (reinterpret_cast<uintptr_t>(p->k_scale) & 3u) ||
@@ -159,7 +158,7 @@ WorkspaceLayout decode_workspace_layout(const pa_decode_params* p, int num_parti
       const size_t rows = size_t(2) * f.grid * f.cols;
       const size_t v = size_t(p->num_seqs) * fp4_columns(p).n_groups;
       w.tc_plan = H;
-      w.tc_m = w.tc_plan + round_up((v + 1) * sizeof(int64_t), 256);
+      w.tc_m = w.tc_plan + round_up((v + 1) * sizeof(int32_t), 256);
       w.tc_acc = w.tc_m + round_up(rows * 2 * sizeof(float), 256);
       w.total = w.tc_acc + round_up(rows * p->head_dim * sizeof(float), 256);
     }

@@ -59,6 +59,7 @@ __device__ unsigned int g_decode_fp4_errors;
 constexpr int NWARPS = 4;
 constexpr int NTHREADS = NWARPS * 32;
 constexpr int KEYS = 32;  // keys of a warp's step
+constexpr int CTAS = 4;   // resident on an SM
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int BS>
@@ -70,7 +71,11 @@ struct Cfg {
   static constexpr int COLS = 8;
   static constexpr int OROW = D + 4;                 // padded row of the warps' merge
   static constexpr int RING = NWARPS * ST * STAGE;
-  static constexpr int SMEM = RING + NWARPS * COLS * (OROW + 2) * 4;
+  // after the rings: the queries, then the warps' (maximum, sum) per column; a
+  // warp's rows of the merge lie in the second stage of its ring
+  static constexpr int QUERIES = D * 16;
+  static constexpr int SMEM = RING + QUERIES + NWARPS * COLS * 2 * 4;
+  static_assert(COLS * OROW * 4 <= STAGE, "the merge rows fit a stage");
   static constexpr int WINDOW = 32 / NBK;            // steps whose table entries a warp holds
   static_assert(TILE % 16 == 0, "copies move 16 bytes");
 };
@@ -84,7 +89,7 @@ struct Fp4Decode {
   const float* v_scale;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int64_t* plan;    // [virtual sequences + 1]: cost before each, then the total
+  int32_t* plan;    // [virtual sequences + 1]: cost before each, then the total
   float* part_ml;   // [2 * grid][COLS][2]: max, sum
   float* part_acc;  // [2 * grid][COLS][D]
   float scale_log2;
@@ -117,53 +122,61 @@ constexpr int START_COST = 8;
 __device__ __forceinline__ int item_cost(const Virtual& x) {
   return x.steps > 0 ? x.steps + START_COST : 0;
 }
-// Stretches: at most one per position of the stream, so that none is empty.
-__device__ __forceinline__ int stretches(int64_t T, int grid) { return T < grid ? int(T) : grid; }
-// The stretch [c T / G, (c + 1) T / G) of G that holds stream position x.
-__device__ __forceinline__ int owner(int64_t x, int64_t T, int G) {
-  return int(((x + 1) * G - 1) / T);
-}
+// The stream's T positions (T below 2^31, checked on the host) in stretches of
+// T / n or one more, at most one stretch per position, so that none is empty.
+struct Deal {
+  int n, base, longer;  // stretches; positions of one; how many hold one more
+  __device__ __forceinline__ Deal(int T, int grid) {
+    n = T < grid ? T : grid;
+    base = n > 0 ? T / n : 0;
+    longer = T - base * n;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * base + min(c, longer); }
+  __device__ __forceinline__ int owner(int x) const {  // the stretch that holds position x
+    const int cut = longer * (base + 1);
+    return x < cut ? x / (base + 1) : longer + (x - cut) / base;
+  }
+};
 
 // Where this CTA's stretch begins: the virtual sequence that holds position x0
 // and the cost before it. CTA 0 also writes the plan for the merge.
 struct Start {
-  int64_t x0, x1, before;
-  int v;
+  int x0, x1, before, v;
 };
-__device__ __forceinline__ void find_start(const Fp4Decode& P, Start* out, int64_t* warp_tot) {
+__device__ __forceinline__ void find_start(const Fp4Decode& P, Start* out, int* warp_tot) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (P.num_virtual + NTHREADS - 1) / NTHREADS;
   const int v0 = tid * per, v1 = min(P.num_virtual, v0 + per);
-  int64_t sum = 0;
-  for (int v = v0; v < v1; ++v) sum += int64_t(item_cost(virtual_of(P, v))) * P.num_kv_heads;
-  int64_t inc = sum;
+  if (tid == 0) *out = Start{0, 0, 0, 0};  // an empty stretch
+  int sum = 0;
+  for (int v = v0; v < v1; ++v) sum += item_cost(virtual_of(P, v)) * P.num_kv_heads;
+  int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   if (lane == 31) warp_tot[warp] = inc;
   __syncthreads();
-  int64_t before = inc - sum, T = 0;
+  int before = inc - sum, T = 0;
 #pragma unroll
   for (int w = 0; w < NWARPS; ++w) {
     if (w < warp) before += warp_tot[w];
     T += warp_tot[w];
   }
-  const int64_t G = stretches(T, gridDim.x), c = blockIdx.x;
-  const int64_t x0 = c < G ? c * T / G : T, x1 = c < G ? (c + 1) * T / G : T;
-  if (tid == 0) *out = Start{x0, x0, 0, 0};  // an empty stretch
-  __syncthreads();
+  const Deal deal(T, gridDim.x);
+  const int c = blockIdx.x;
+  const int x0 = c < deal.n ? deal.start(c) : T, x1 = c < deal.n ? deal.start(c + 1) : T;
   const bool mine = x0 < x1 && before <= x0 && x0 < before + sum;
-  if (mine || blockIdx.x == 0) {
-    int64_t at = before;
+  if (mine || c == 0) {
+    int at = before;
     for (int v = v0; v < v1; ++v) {
-      const int64_t cost = int64_t(item_cost(virtual_of(P, v))) * P.num_kv_heads;
-      if (blockIdx.x == 0) P.plan[v] = at;
+      const int cost = item_cost(virtual_of(P, v)) * P.num_kv_heads;
+      if (c == 0) P.plan[v] = at;
       if (mine && at <= x0 && x0 < at + cost) *out = Start{x0, x1, at, v};
       at += cost;
     }
-    if (blockIdx.x == 0 && tid == 0) P.plan[P.num_virtual] = T;
+    if (c == 0 && tid == 0) P.plan[P.num_virtual] = T;
   }
   __syncthreads();
 }
@@ -172,30 +185,27 @@ __device__ __forceinline__ void find_start(const Fp4Decode& P, Start* out, int64
 struct Piece {
   int v, head, first, last, steps;  // steps: of the whole item
   int see0, n_tok;                  // of the virtual sequence
-  bool valid;                       // false: the stretch is done
+  int valid;                        // 0: the stretch is done
 };
 // Walks a stretch piece by piece.
 struct Walk {
-  int64_t x, x1, before;  // position, end, cost before virtual sequence v
-  int v;
+  int x, x1, before, v;  // position, end, cost before virtual sequence v
   __device__ __forceinline__ Piece next(const Fp4Decode& P) {
     Piece p{};
     while (x < x1) {
       const Virtual q = virtual_of(P, v);
-      const int cost = item_cost(q);
-      const int64_t all = int64_t(cost) * P.num_kv_heads;
+      const int cost = item_cost(q), all = cost * P.num_kv_heads;
       if (x >= before + all) {
         before += all;
         ++v;
         continue;
       }
-      const int64_t in = x - before;
       p.v = v;
-      p.head = int(in / cost);
-      const int64_t base = before + int64_t(p.head) * cost;
-      const int64_t end = min(x1, base + cost);
-      p.first = max(0, int(x - base) - START_COST);
-      p.last = int(end - base) - START_COST;
+      p.head = (x - before) / cost;
+      const int base = before + p.head * cost;
+      const int end = min(x1, base + cost);
+      p.first = max(0, x - base - START_COST);
+      p.last = end - base - START_COST;
       p.steps = q.steps;
       p.see0 = q.see0;
       p.n_tok = q.n_tok;
@@ -208,7 +218,7 @@ struct Walk {
 };
 
 template <int D, int BS>
-__global__ void __launch_bounds__(NTHREADS, 4)
+__global__ void __launch_bounds__(NTHREADS, CTAS)
     paged_decode_fp4_kernel(const Fp4Decode P) {
   using C = Cfg<D, BS>;
   constexpr int ST = C::ST, NBK = C::NBK, TILE = C::TILE, WINDOW = C::WINDOW;
@@ -220,27 +230,15 @@ __global__ void __launch_bounds__(NTHREADS, 4)
   const int num_q_heads = P.num_kv_heads << P.g_log2;
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem + warp * ST * C::STAGE;
-  float* sm_o = reinterpret_cast<float*>(smem + C::RING);    // [NWARPS][COLS][OROW]
-  float* sm_m = sm_o + NWARPS * C::COLS * C::OROW;           // [NWARPS][COLS]
+  uint4* sm_q = reinterpret_cast<uint4*>(smem + C::RING);    // [D / 32][32 lanes]
+  float* sm_m = reinterpret_cast<float*>(smem + C::RING + C::QUERIES);  // [NWARPS][COLS]
   float* sm_l = sm_m + NWARPS * C::COLS;                     // [NWARPS][COLS]
   __shared__ Start start;
-  __shared__ int64_t warp_tot[NWARPS];
+  __shared__ int warp_tot[NWARPS];
   __shared__ Walk walk;
-  __shared__ Piece pieces[2];  // the one being worked on, and the next
+  __shared__ Piece pieces[3];  // the one being worked on, the next, and the one after
 
-  // bad lengths are flagged, and rows of sequences without keys zeroed, by the CTAs in turn
-  for (int v = blockIdx.x; v < P.num_virtual; v += gridDim.x) {
-    const int b = v / P.n_groups, first = (v - b * P.n_groups) * P.q_group;
-    const int L = P.context_lens[b];
-    if (L > 0 && L >= P.q_len && L <= P.cap) continue;
-    if (tid == 0 && first == 0 && L > 0) atomicOr(&g_decode_fp4_errors, PA_DEVERR_CONTEXT_LEN);
-    if (L > 0 && min(L, P.cap) >= P.q_len) continue;
-    const int n = min(P.q_group, P.q_len - first) * num_q_heads * D;
-    __nv_bfloat16* row = P.out + (int64_t(b) * P.q_len + first) * num_q_heads * D;
-    for (int i = tid; i < n; i += NTHREADS) row[i] = __float2bfloat16_rn(0.0f);
-  }
-
-  // thread 0 walks the stretch one piece ahead of the CTA
+  // thread 0 walks the stretch, two pieces ahead of the CTA
   if (P.whole) {
     if (tid == 0) {
       Piece p{};
@@ -252,6 +250,7 @@ __global__ void __launch_bounds__(NTHREADS, 4)
       p.n_tok = q.n_tok;
       p.valid = q.steps > 0;
       pieces[0] = p;
+      pieces[1] = Piece{};
       walk.x = walk.x1 = 0;
     }
   } else {
@@ -259,6 +258,7 @@ __global__ void __launch_bounds__(NTHREADS, 4)
     if (tid == 0) {
       walk = Walk{start.x0, start.x1, start.before, start.v};
       pieces[0] = walk.next(P);
+      pieces[1] = walk.next(P);
     }
   }
   __syncthreads();
@@ -304,35 +304,55 @@ __global__ void __launch_bounds__(NTHREADS, 4)
     return n > warp ? (n - warp + NWARPS - 1) / NWARPS : 0;
   };
 
-  int window = 0, n_my = 0, cur = 0;
+  // row of q / out of column n of a piece: new token n / G of the group, query
+  // head head * G + n % G
+  auto q_row = [&](const Piece& p, int n) {
+    const int b = p.v / P.n_groups;
+    return (int64_t(b) * P.q_len + (p.v - b * P.n_groups) * P.q_group + (n >> P.g_log2)) *
+               num_q_heads + p.head * G + (n & (G - 1));
+  };
+  // What a warp has in hand when it turns to a piece; the loads start together,
+  // then the first copies, into the ring's first stage.
+  int window = 0;            // table entries of its first steps
+  int n_my = 0;              // its steps
+  float k_scale = 0.0f, v_scale = 0.0f;
+  uint32_t qf[D / 16][2];    // the queries as the B operand (column g), in f16's range
+  float inv_scaling = 1.0f;  // of this lane's query row
   auto begin = [&](const Piece& p) {
+    const int n_cols = p.n_tok << P.g_log2;
     window = load_window(p, 0);
     n_my = steps_of(p);
+    k_scale = P.k_scale[p.head];
+    v_scale = P.v_scale[p.head];
+    uint4 raw[D / 32];
+    dev::query_load<PA_KV_FP4_E2M1, D>(P.q + q_row(p, min(g, n_cols - 1)) * D, g < n_cols, t, raw);
+    issue(p, 0, n_my, window, 0);
+    inv_scaling = dev::query_fragment<PA_KV_FP4_E2M1, D>(raw, qf);
+  };
+  auto share_queries = [&]() {  // every warp has them; each writes a part
 #pragma unroll
-    for (int i = 0; i < ST; ++i) issue(p, i, n_my, window, i);
+    for (int c = 0; c < D / 32; ++c)
+      if (c == warp)
+        sm_q[c * 32 + lane] = make_uint4(qf[2 * c][0], qf[2 * c][1], qf[2 * c + 1][0],
+                                         qf[2 * c + 1][1]);
   };
-  if (pieces[0].valid) begin(pieces[0]);
-  __syncwarp();
-  for (; pieces[cur].valid; cur ^= 1) {
+  if (pieces[0].valid) {
+    begin(pieces[0]);
+    share_queries();
+  }
+  __syncthreads();
+  int cur = 0;
+  for (; pieces[cur].valid; cur = cur == 2 ? 0 : cur + 1) {
   const Piece& piece = pieces[cur];
-  const int head = piece.head;
-  const int b = piece.v / P.n_groups;
-  const int tok_i0 = (piece.v - b * P.n_groups) * P.q_group;  // first new token of the group
-  const int n_tok = piece.n_tok, see0 = piece.see0, see_last = see0 + n_tok - 1;
-  const int n_cols = n_tok << P.g_log2;
-  // row of q / out of column n: token tok_i0 + n / G, query head head * G + n % G
-  auto q_row = [&](int n) {
-    return (int64_t(b) * P.q_len + tok_i0 + (n >> P.g_log2)) * num_q_heads + head * G +
-           (n & (G - 1));
-  };
+  const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1;
+  const int see0 = piece.see0, see_last = see0 + piece.n_tok - 1;
+  const int n_cols = piece.n_tok << P.g_log2;
+#pragma unroll
+  for (int i = 1; i < ST; ++i) issue(piece, i, n_my, window, i);
 
-  // Queries as the B operand (column g), scaled into f16's range.
-  uint32_t qf[1][D / 16][2];
   float factor[2];  // of columns 2t and 2t+1: softmax scale * K scale / the row's scaling
   int see[2];       // keys that columns 2t and 2t+1 see
-  const float kfac = P.scale_log2 * P.k_scale[head];
-  const float row_factor = kfac * dev::query_fragment<PA_KV_FP4_E2M1, D>(
-                                      P.q + q_row(min(g, n_cols - 1)) * D, g < n_cols, t, qf[0]);
+  const float row_factor = P.scale_log2 * k_scale * inv_scaling;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     factor[c] = __shfl_sync(0xffffffffu, row_factor, 4 * (2 * t + c));
@@ -368,11 +388,11 @@ __global__ void __launch_bounds__(NTHREADS, 4)
     const int key0 = KEYS * (piece.first + warp + NWARPS * i);
 
     // ---- raw scores: two tiles of 16 keys
-    float s[2][1][4];
+    float s[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[h][0][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) s[h][j] = 0.0f;
       KRow rows[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -380,7 +400,7 @@ __global__ void __launch_bounds__(NTHREADS, 4)
         const unsigned char* tile = kt + (row / BS) * TILE;
         rows[r].load(tile + (row % BS) * (D / 2) + lane_k, tile + (row % BS) * (D / 16) + lane_ks);
       }
-      dev::key_product<PA_KV_FP4_E2M1, D, 1>(s[h], rows[0], rows[1], qf);
+      dev::key_product_shared<PA_KV_FP4_E2M1, D>(s[h], rows[0], rows[1], sm_q + lane);
     }
     // ---- softmax; keys past a column's last are -inf
     bool over = false;
@@ -388,13 +408,13 @@ __global__ void __launch_bounds__(NTHREADS, 4)
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (EDGE && key0 + h * 16 + (j >> 1) * 8 + row_g >= see[j & 1]) s[h][0][j] = -INFINITY;
-        over |= s[h][0][j] > limit[j & 1];
+        if (EDGE && key0 + h * 16 + (j >> 1) * 8 + row_g >= see[j & 1]) s[h][j] = -INFINITY;
+        over |= s[h][j] > limit[j & 1];
       }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float x = fmaxf(fmaxf(s[0][0][c], s[0][0][c + 2]), fmaxf(s[1][0][c], s[1][0][c + 2]));
+        float x = fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2]));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * factor[c];
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(NTHREADS, 4)
       float p[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        p[j] = dev::fast_exp2(fmaf(s[h][0][j], factor[j & 1], -ref[j & 1]));
+        p[j] = dev::fast_exp2(fmaf(s[h][j], factor[j & 1], -ref[j & 1]));
         l[j & 1] += p[j];
       }
       pf[h][0] = dev::transpose_8x8(dev::pack_f16(p[0], p[1]));
@@ -493,6 +513,7 @@ __global__ void __launch_bounds__(NTHREADS, 4)
   __syncwarp();
 
   // ---- merge the warps through shared memory
+  float* my_o = reinterpret_cast<float*>(ring + C::STAGE);  // [COLS][OROW]
   nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 1));
   nan_from = min(nan_from, __shfl_xor_sync(0xffffffffu, nan_from, 2));
 #pragma unroll
@@ -506,13 +527,15 @@ __global__ void __launch_bounds__(NTHREADS, 4)
     }
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)  // rows g and g + 8 of tile k: elements g D/8 + 2k, + 1
-      *reinterpret_cast<float2*>(sm_o + n * C::OROW + g * (D / 8) + 2 * k) =
+      *reinterpret_cast<float2*>(my_o + (2 * t + c) * C::OROW + g * (D / 8) + 2 * k) =
           nan_from < see[c] ? make_float2(NAN, NAN) : make_float2(o[k][c], o[k][c + 2]);
   }
-  if (tid == 0) pieces[cur ^ 1] = walk.next(P);
-  __syncthreads();
   // the next piece's first steps are on their way during the merge
-  if (pieces[cur ^ 1].valid) begin(pieces[cur ^ 1]);
+  const float scale_v = v_scale;
+  if (pieces[next].valid) begin(pieces[next]);
+  __syncthreads();
+  if (pieces[next].valid) share_queries();
+  if (tid == 0) pieces[after] = walk.next(P);
   {
     const Piece& done = piece;
     constexpr int TPC = NTHREADS / C::COLS;  // threads of a column
@@ -532,9 +555,9 @@ __global__ void __launch_bounds__(NTHREADS, 4)
       den = fmaf(wt[w], sm_l[w * C::COLS + n], den);
     }
     const bool direct = done.first == 0 && done.last == done.steps;
-    const float norm = direct ? P.v_scale[head] / den : P.v_scale[head];
+    const float norm = direct ? scale_v / den : scale_v;
     const int slot = 2 * blockIdx.x + (done.first == 0);  // the CTA's last piece, or its first
-    __nv_bfloat16* out = P.out + q_row(min(n, n_cols - 1)) * D + d;
+    __nv_bfloat16* out = P.out + q_row(done, min(n, n_cols - 1)) * D + d;
     float* acc = P.part_acc + (int64_t(slot) * C::COLS + n) * D + d;
 #pragma unroll
     for (int x = 0; x < E; x += 4) {
@@ -542,7 +565,8 @@ __global__ void __launch_bounds__(NTHREADS, 4)
 #pragma unroll
       for (int w = 0; w < NWARPS; ++w) {
         const float4 y =
-            *reinterpret_cast<const float4*>(sm_o + (w * C::COLS + n) * C::OROW + d + x);
+            *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(
+                smem + (w * ST + 1) * C::STAGE) + n * C::OROW + d + x);
         sum.x = fmaf(wt[w], y.x, sum.x);
         sum.y = fmaf(wt[w], y.y, sum.y);
         sum.z = fmaf(wt[w], y.z, sum.z);
@@ -560,9 +584,21 @@ __global__ void __launch_bounds__(NTHREADS, 4)
           make_float2(M, den);
   }
   __syncwarp();
-  __syncthreads();  // before the next piece's rows
+  __syncthreads();  // before the next piece's copies
   }
   if (bad_entry && lane == 0) atomicOr(&g_decode_fp4_errors, PA_DEVERR_TABLE_ENTRY);
+
+  // bad lengths are flagged, and rows of sequences without keys zeroed, by the CTAs in turn
+  for (int v = blockIdx.x; v < P.num_virtual; v += gridDim.x) {
+    const int b = v / P.n_groups, first = (v - b * P.n_groups) * P.q_group;
+    const int L = P.context_lens[b];
+    if (L > 0 && L >= P.q_len && L <= P.cap) continue;
+    if (tid == 0 && first == 0 && L > 0) atomicOr(&g_decode_fp4_errors, PA_DEVERR_CONTEXT_LEN);
+    if (L > 0 && min(L, P.cap) >= P.q_len) continue;
+    const int n = min(P.q_group, P.q_len - first) * num_q_heads * D;
+    __nv_bfloat16* row = P.out + (int64_t(b) * P.q_len + first) * num_q_heads * D;
+    for (int i = tid; i < n; i += NTHREADS) row[i] = __float2bfloat16_rn(0.0f);
+  }
 }
 
 // Joins the pieces of the items that were cut: one warp per (item, column).
@@ -578,30 +614,45 @@ __global__ void __launch_bounds__(128) merge_fp4_kernel(const Fp4Decode P, int g
   const Virtual x = virtual_of(P, v);
   dev::griddep_wait();  // the plan and the partials
   if (x.steps == 0 || n >= (x.n_tok << P.g_log2)) return;
-  const int64_t T = P.plan[P.num_virtual];
-  const int64_t base = P.plan[v] + int64_t(head) * item_cost(x) + START_COST;
-  const int G = stretches(T, grid);
-  const int c0 = owner(base, T, G), c1 = owner(base + x.steps - 1, T, G);
+  const int T = P.plan[P.num_virtual];
+  const int base = P.plan[v] + head * item_cost(x) + START_COST;
+  const Deal deal(T, grid);
+  const int c0 = deal.owner(base), c1 = deal.owner(base + x.steps - 1);
   if (c0 == c1) return;  // one piece: written by the decode
-  auto slot = [&](int c) { return (int64_t(2 * c + (c == c0)) * COLS + n); };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, P.part_ml[slot(c) * 2]);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[E], den = 0.0f;
+  // four pieces at a time, their loads in flight together
+  constexpr int BATCH = 4;
+  float M = -INFINITY, den = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = *reinterpret_cast<const float2*>(P.part_ml + slot(c) * 2);
-    const float wt = ml.x == -INFINITY ? 0.0f : dev::fast_exp2(ml.x - M);
-    den = fmaf(wt, ml.y, den);
-    const float* src = P.part_acc + slot(c) * D + lane * E;
+  for (int c = c0; c <= c1; c += BATCH) {
+    float2 ml[BATCH], row[BATCH][E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src + e);
-      acc[e] = fmaf(wt, y.x, acc[e]);
-      acc[e + 1] = fmaf(wt, y.y, acc[e + 1]);
+    for (int k = 0; k < BATCH; ++k) {
+      const int64_t slot = int64_t(2 * min(c + k, c1) + (c + k == c0)) * COLS + n;
+      ml[k] = *reinterpret_cast<const float2*>(P.part_ml + slot * 2);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e)
+        row[k][e] = *reinterpret_cast<const float2*>(P.part_acc + slot * D + lane * E + 2 * e);
+      if (c + k > c1) ml[k].x = -INFINITY;
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+    const float a = M == -INFINITY ? 0.0f : dev::fast_exp2(M - top);
+    M = top;
+    den *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (ml[k].x == -INFINITY) continue;  // no keys of this column in the piece
+      const float wt = dev::fast_exp2(ml[k].x - M);
+      den = fmaf(wt, ml[k].y, den);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        acc[2 * e] = fmaf(wt, row[k][e].x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(wt, row[k][e].y, acc[2 * e + 1]);
+      }
     }
   }
   const float inv = __frcp_rn(den);
@@ -671,7 +722,7 @@ Fp4Plan fp4_plan(const pa_decode_params* p, int num_sms) {
   } else {
     // as many CTAs as are resident at once, but no stretch under two start costs
     const int64_t most = items * ((r.cap + KEYS - 1) / KEYS + START_COST) / (2 * START_COST);
-    const int64_t full = int64_t(num_sms > 0 ? num_sms : 256) * 4;
+    const int64_t full = int64_t(num_sms > 0 ? num_sms : 256) * CTAS;
     r.grid = int(most < full ? most : full);
     if (r.grid < 1) r.grid = 1;
   }
@@ -690,7 +741,7 @@ int launch_decode_fp4(const DecodeLaunch& L, const Fp4Plan& plan, void* stream) 
   P.v_scale = p->v_scale;
   P.block_tables = p->block_tables;
   P.context_lens = p->context_lens;
-  P.plan = reinterpret_cast<int64_t*>(L.plan);
+  P.plan = L.plan;
   P.part_ml = L.part_m;
   P.part_acc = L.part_acc;
   P.scale_log2 = p->scale * kLog2e;

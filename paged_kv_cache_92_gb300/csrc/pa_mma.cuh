@@ -179,16 +179,28 @@ __device__ __forceinline__ void key_product(float (&s)[NT][4], const KeyRow<FMT,
   }
 }
 
-// One query row as the products' B operand (`on` false: a row of zeros; `row`
-// is read all the same), for the lane with t = lane % 4; all lanes call together. bf16 rows stay
-// as they are and the result is 1. The others are scaled to f16 by a power of
-// two that brings the row's largest magnitude into [2^12, 2^13), exactly for
-// every element within 2^-30 of it, and its inverse is returned.
+// The same for one column tile whose queries lie in shared memory: entry
+// [c][lane] of `qs` holds the lane's pairs of products 2c and 2c + 1.
 template <int FMT, int D>
-__device__ __forceinline__ float query_fragment(const __nv_bfloat16* row, bool on, int t,
-                                                uint32_t (&qf)[D / 16][2]) {
+__device__ __forceinline__ void key_product_shared(float (&s)[4], const KeyRow<FMT, D>& lo,
+                                                   const KeyRow<FMT, D>& hi, const uint4* qs) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t x[4], y[4];
+    lo.pairs(c, x);
+    hi.pairs(c, y);
+    const uint4 b = qs[c * 32];
+    mma_f16(s, x[0], y[0], x[1], y[1], b.x, b.y);
+    mma_f16(s, x[2], y[2], x[3], y[3], b.z, b.w);
+  }
+}
+
+// The lane's part of a query row (t = lane % 4), in the order of its key
+// elements; `on` false: a row of zeros (`row` is read all the same).
+template <int FMT, int D>
+__device__ __forceinline__ void query_load(const __nv_bfloat16* row, bool on, int t,
+                                           uint4 (&raw)[D / 32]) {
   using R = KeyRow<FMT, D>;
-  uint4 raw[D / 32];
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {  // 8 elements of the lane's list
     const int e = 8 * c;
@@ -196,6 +208,15 @@ __device__ __forceinline__ float query_fragment(const __nv_bfloat16* row, bool o
         *reinterpret_cast<const uint4*>(row + (4 * (e / R::E) + t) * R::E + e % R::E);
     raw[c] = make_uint4(on ? x.x : 0u, on ? x.y : 0u, on ? x.z : 0u, on ? x.w : 0u);
   }
+}
+
+// A query row as the products' B operand; all lanes call together. bf16 rows
+// stay as they are and the result is 1. The others are scaled to f16 by a power
+// of two that brings the row's largest magnitude into [2^12, 2^13), exactly for
+// every element within 2^-30 of it, and its inverse is returned.
+template <int FMT, int D>
+__device__ __forceinline__ float query_fragment(const uint4 (&raw)[D / 32],
+                                                uint32_t (&qf)[D / 16][2]) {
   if constexpr (FMT == 0) {
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {

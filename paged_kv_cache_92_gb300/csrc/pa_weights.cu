@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(NTHREADS)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int n = nt * 8 + g;
-    const float f =
-        kfac * dev::query_fragment<FMT, D>(P.q + q_row(min(n, n_cols - 1)) * D, n < n_cols, t,
-                                           qf[nt]);
+    uint4 raw[D / 32];
+    dev::query_load<FMT, D>(P.q + q_row(min(n, n_cols - 1)) * D, n < n_cols, t, raw);
+    const float f = kfac * dev::query_fragment<FMT, D>(raw, qf[nt]);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int m = nt * 8 + 2 * t + c;

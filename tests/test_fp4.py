@@ -186,7 +186,8 @@ def _lib_params(pk, **kw):
     (dict(kv_dtype=3), 1), (dict(partition_tokens=24), 1),
     (dict(partition_tokens=48, block_size=32), 1),  # partitions are whole blocks
     (dict(query_len=1025), 1), (dict(query_len=1024, num_seqs=64), 2),
-    (dict(query_len=63, num_seqs=1024, num_kv_heads=2048, num_q_heads=2048, num_blocks=1), 2),
+    (dict(num_seqs=512, num_kv_heads=16, num_q_heads=16, max_blocks_per_seq=1 << 20,
+          max_context_len=1 << 24), 2),  # more stream positions than 32 bits count
     (dict(max_context_len=0), 1), (dict(scale=0.0), 1),
 ])
 def test_decode_refusals(pk, kw, status):
@@ -241,7 +242,7 @@ def test_binding_refuses_mixed_shapes(pk):
 
 def test_workspace_holds_two_partials_per_cta(pk):
     """The header alone where contexts are short (at most 512 tokens); else the plan (a
-    64-bit cost per sequence and column group, and the total) and two partials a CTA:
+    cost per sequence and column group, and the total) and two partials a CTA:
     four CTAs an SM, or one per 16 steps and starts."""
     def size(**kw):
         return pk.load().pa_decode_workspace_size(ctypes.byref(_lib_params(pk, **kw)))
@@ -254,11 +255,11 @@ def test_workspace_holds_two_partials_per_cta(pk):
     kw = dict(max_blocks_per_seq=64, max_context_len=544)
     grid = 2 * 2 * (17 + 8) // 16          # items x (steps + start), 16 a CTA
     rows = 2 * grid * 8
-    assert size(**kw) == 256 + ru(3 * 8) + ru(rows * 8) + ru(rows * 128 * 4)
+    assert size(**kw) == 256 + ru(3 * 4) + ru(rows * 8) + ru(rows * 128 * 4)
     kw["query_len"] = 9                    # groups of two tokens (G 4): five
     grid = 2 * 5 * 2 * (17 + 8) // 16
     rows = 2 * grid * 8
-    assert size(**kw) == 256 + ru(11 * 8) + ru(rows * 8) + ru(rows * 128 * 4)
+    assert size(**kw) == 256 + ru(11 * 4) + ru(rows * 8) + ru(rows * 128 * 4)
 
 
 # ------------------------------------------------------------------ GPU: rows
