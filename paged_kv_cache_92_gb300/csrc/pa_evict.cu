@@ -7,12 +7,14 @@
 // with the largest accumulated attention weight (pa_weights.cu).
 //
 //  * evict_select_kernel: one CTA per sequence. The candidates' weights become
-//    ordered 32-bit keys in registers (32 a thread; longer sequences re-read
-//    them from L2), and the threshold is found bit by bit: a count of the keys
-//    at or above a trial value, 32 rounds at most and fewer when a trial
-//    splits the keys exactly. No histogram, so equal weights -- most tokens of
-//    a long context have nearly none -- cost nothing extra. Ties go to the
-//    lowest index through ranks, and the kept indices come out ascending.
+//    ordered 32-bit keys in registers (up to 32 a thread; longer sequences
+//    re-read them from L2), and the threshold is found by three rounds of a
+//    shared-memory histogram over 11, 11 and 10 bits of the keys that still
+//    tie with it. A warp whose lanes all hit one bin adds once, so equal
+//    weights -- most tokens of a long context have nearly none -- do not
+//    serialise. (A search bit by bit, 32 counts over the CTA, took 39 us
+//    where this takes 7 to 13.) Ties go to the lowest index through ranks, and
+//    the kept indices come out ascending.
 //  * compact_rows_kernel: row j of the destination <- row keep[j] of the
 //    source. keep ascends, so keep[j] >= j, and moving rows in order within
 //    one CTA is safe in place: a tile's rows are in registers before any of
@@ -37,7 +39,8 @@ __device__ unsigned int g_evict_errors;
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_KEYS = 32;  // keys a thread holds at a time
-constexpr int SEL_SPAN = SEL_THREADS * SEL_KEYS;
+constexpr int SEL_BINS = 2048;
+constexpr int SEL_COPIES = 4;
 
 // Order-preserving map of a weight to an unsigned key; NaN below everything,
 // both zeros alike.
@@ -56,50 +59,153 @@ struct Select {
   int num_seqs, budget, recent, max_len;
 };
 
-// Sum over the CTA, the same in every thread. `buf` alternates between two
-// rows of shared memory, so one barrier a call is enough.
-__device__ __forceinline__ int block_sum(int x, int (*sm)[SEL_WARPS], int& buf) {
-  x = __reduce_add_sync(0xffffffffu, x);
+// Inclusive prefix of x over the CTA's threads; `all` is the total.
+__device__ __forceinline__ int block_scan(int x, int* warp_tot, int& all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) sm[buf][warp] = x;
-  __syncthreads();
-  const int total = __reduce_add_sync(0xffffffffu, sm[buf][lane]);
-  buf ^= 1;
-  return total;
-}
-
-// Exclusive prefix over cnt[SEL_KEYS][SEL_WARPS] (in place), + base; returns the total.
-__device__ __forceinline__ int scan_counts(int* cnt, int base, int* warp_tot) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __syncthreads();
-  const int x = cnt[tid];
   int inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
+  __syncthreads();  // the previous scan's totals have been read
   if (lane == 31) warp_tot[warp] = inc;
   __syncthreads();
-  int tot = warp_tot[lane], run = tot;
+  const int tot = warp_tot[lane];
+  int run = tot;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, run, o);
     if (lane >= o) run += y;
   }
-  const int before = __shfl_sync(0xffffffffu, run - tot, warp);
-  const int all = __shfl_sync(0xffffffffu, run, 31);
-  cnt[tid] = base + before + inc - x;
-  __syncthreads();
-  return all;
+  all = __shfl_sync(0xffffffffu, run, 31);
+  return inc + __shfl_sync(0xffffffffu, run - tot, warp);
 }
 
-// Key e of this thread in a span: token span * SEL_SPAN + e * SEL_THREADS + tid.
+struct SelectShared {
+  int hist[SEL_COPIES][SEL_BINS];
+  int cnt[SEL_KEYS * SEL_WARPS];
+  int warp_tot[SEL_WARPS];
+  int bin, left;
+};
+
+// The choice for one sequence of more than `budget` tokens: E keys a thread at
+// a time, key e of span s being token s * SEL_THREADS * E + e * SEL_THREADS + tid.
+template <int E>
+__device__ __forceinline__ void select_row(const Select& P, const float* w, int32_t* keep, int L,
+                                           SelectShared& sm) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_cand = L - P.recent;       // the others always stay
+  const int need = P.budget - P.recent;  // of the candidates, fewer than n_cand
+  const int span_len = SEL_THREADS * E;
+  const int spans = (n_cand + span_len - 1) / span_len;
+  uint32_t key[E];
+  auto token = [&](int span, int e) { return span * span_len + e * SEL_THREADS + tid; };
+  auto load = [&](int span) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = token(span, e);
+      key[e] = i < n_cand ? weight_key(w[i]) : 0u;
+    }
+  };
+  if (spans == 1) load(0);
+
+  // the key of rank `need`, digit by digit; `left`: how many of the keys that
+  // equal it are kept (the first ones)
+  uint32_t prefix = 0, mask = 0;
+  int left = need;
+  if (need > 0) {
+#pragma unroll 1
+    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : (shift == 10 ? 0 : -1)) {
+      const uint32_t digits = shift == 0 ? 1023u : 2047u;
+      for (int i = tid; i < SEL_COPIES * SEL_BINS; i += SEL_THREADS) (&sm.hist[0][0])[i] = 0;
+      __syncthreads();
+      for (int span = 0; span < spans; ++span) {
+        if (spans > 1) load(span);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const bool in = token(span, e) < n_cand && (key[e] & mask) == prefix;
+          if (in) atomicAdd(&sm.hist[lane % SEL_COPIES][(key[e] >> shift) & digits], 1);
+        }
+      }
+      __syncthreads();
+      // bins from the top, two a thread: where the count reaches `left`
+      const int b1 = SEL_BINS - 1 - 2 * tid, b0 = b1 - 1;
+      int n1 = 0, n0 = 0;
+#pragma unroll
+      for (int k = 0; k < SEL_COPIES; ++k) {
+        n1 += sm.hist[k][b1];
+        n0 += sm.hist[k][b0];
+      }
+      int all;
+      const int upto = block_scan(n1 + n0, sm.warp_tot, all), before = upto - n1 - n0;
+      if (before < left && left <= upto) {
+        const bool first = left <= before + n1;
+        sm.bin = first ? b1 : b0;
+        sm.left = left - before - (first ? 0 : n1);
+      }
+      __syncthreads();
+      prefix |= uint32_t(sm.bin) << shift;
+      mask |= digits << shift;
+      left = sm.left;
+      __syncthreads();
+    }
+  }
+
+  // ranks in token order: of the keys equal to the threshold, then of the kept
+  int eq_base = 0, keep_base = 0;
+  const uint32_t below = (1u << lane) - 1u;
+  // exclusive prefix of the warps' counts, in token order (entry e * SEL_WARPS + warp)
+  auto scan_counts = [&](int base) {
+    __syncthreads();
+    const int x = tid < E * SEL_WARPS ? sm.cnt[tid] : 0;
+    int all;
+    const int inc = block_scan(x, sm.warp_tot, all);
+    if (tid < E * SEL_WARPS) sm.cnt[tid] = base + inc - x;
+    __syncthreads();
+    return all;
+  };
+  for (int span = 0; span < spans; ++span) {
+    if (spans > 1) load(span);
+    uint32_t kept = 0, eq = 0;  // a bit per key
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool cand = token(span, e) < n_cand && need > 0;
+      const bool same = cand && key[e] == prefix;
+      kept |= uint32_t(cand && key[e] > prefix) << e;
+      eq |= uint32_t(same) << e;
+      const uint32_t v = __ballot_sync(0xffffffffu, same);
+      if (lane == 0) sm.cnt[e * SEL_WARPS + warp] = __popc(v);
+    }
+    const int eq_all = scan_counts(eq_base);
+    uint32_t in_kept[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool same = (eq >> e) & 1u;
+      const uint32_t v = __ballot_sync(0xffffffffu, same);
+      const int rank = sm.cnt[e * SEL_WARPS + warp] + __popc(v & below);
+      const bool on = ((kept >> e) & 1u) || (same && rank < left);
+      in_kept[e] = __ballot_sync(0xffffffffu, on);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (lane == 0) sm.cnt[e * SEL_WARPS + warp] = __popc(in_kept[e]);
+    const int keep_all = scan_counts(keep_base);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if ((in_kept[e] >> lane) & 1u)
+        keep[sm.cnt[e * SEL_WARPS + warp] + __popc(in_kept[e] & below)] = token(span, e);
+    eq_base += eq_all;
+    keep_base += keep_all;
+    __syncthreads();
+  }
+  for (int j = tid; j < P.recent; j += SEL_THREADS) keep[need + j] = n_cand + j;
+}
+
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Select P) {
-  __shared__ int sums[2][SEL_WARPS];
-  __shared__ int cnt_eq[SEL_KEYS * SEL_WARPS], cnt_keep[SEL_KEYS * SEL_WARPS];
-  __shared__ int warp_tot[SEL_WARPS];
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ SelectShared sm;
+  const int b = blockIdx.x, tid = threadIdx.x;
   int L = P.context_lens[b];
   if (L > P.max_len) {
     if (tid == 0) atomicOr(&g_evict_errors, PA_DEVERR_CONTEXT_LEN);
@@ -114,94 +220,23 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Select 
     for (int j = tid; j < L; j += SEL_THREADS) keep[j] = j;
     return;
   }
-  const int n_cand = L - P.recent;          // the others always stay
-  const int need = P.budget - P.recent;     // of the candidates, fewer than n_cand
   const float* w = P.weights + int64_t(b) * P.weights_stride;
-  const int spans = (n_cand + SEL_SPAN - 1) / SEL_SPAN;
-  uint32_t key[SEL_KEYS];  // candidates only; 0 elsewhere
-  auto load = [&](int span) {
-#pragma unroll
-    for (int e = 0; e < SEL_KEYS; ++e) {
-      const int64_t i = int64_t(span) * SEL_SPAN + e * SEL_THREADS + tid;
-      key[e] = i < n_cand ? weight_key(w[i]) : 0u;
-    }
-  };
-  if (spans == 1) load(0);
-
-  // the largest threshold that at least `need` keys reach
-  uint32_t T = 0;
-  bool exact = false;  // exactly `need` keys reach it
-  int buf = 0;
-  if (need > 0) {
-    for (int bit = 31; bit >= 0 && !exact; --bit) {
-      const uint32_t c = T | (1u << bit);
-      int n = 0;
-      for (int span = 0; span < spans; ++span) {
-        if (spans > 1) load(span);
-#pragma unroll
-        for (int e = 0; e < SEL_KEYS; ++e) n += key[e] >= c;
-      }
-      n = block_sum(n, sums, buf);
-      if (n >= need) T = c;
-      exact = n == need;
-    }
+  // no more keys a thread than the sequence needs
+  const int n_cand = L - P.recent;
+  if (n_cand <= 2 * SEL_THREADS) {
+    select_row<2>(P, w, keep, L, sm);
+  } else if (n_cand <= 8 * SEL_THREADS) {
+    select_row<8>(P, w, keep, L, sm);
+  } else {
+    select_row<SEL_KEYS>(P, w, keep, L, sm);
   }
-  int ties = 0;  // keys equal to T that are kept: the first ones
-  if (need > 0 && !exact) {
-    int n = 0;
-    for (int span = 0; span < spans; ++span) {
-      if (spans > 1) load(span);
-#pragma unroll
-      for (int e = 0; e < SEL_KEYS; ++e) n += key[e] > T;
-    }
-    ties = need - block_sum(n, sums, buf);
-  }
-
-  // ranks in token order: of the ties, then of the kept
-  int eq_base = 0, keep_base = 0;
-  for (int span = 0; span < spans; ++span) {
-    if (spans > 1) load(span);
-    uint32_t in_key = 0, eq = 0;
-#pragma unroll
-    for (int e = 0; e < SEL_KEYS; ++e) {
-      const int64_t i = int64_t(span) * SEL_SPAN + e * SEL_THREADS + tid;
-      const bool cand = i < n_cand && need > 0;
-      const bool same = cand && !exact && key[e] == T;
-      in_key |= uint32_t(cand && (exact ? key[e] >= T : key[e] > T)) << e;
-      eq |= uint32_t(same) << e;
-      const uint32_t v = __ballot_sync(0xffffffffu, same);
-      if (lane == 0) cnt_eq[e * SEL_WARPS + warp] = __popc(v);
-    }
-    const int eq_all = scan_counts(cnt_eq, eq_base, warp_tot);
-    const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-    for (int e = 0; e < SEL_KEYS; ++e) {
-      const bool same = (eq >> e) & 1u;
-      const uint32_t v = __ballot_sync(0xffffffffu, same);
-      if (same && cnt_eq[e * SEL_WARPS + warp] + __popc(v & below) < ties) in_key |= 1u << e;
-      const uint32_t k = __ballot_sync(0xffffffffu, (in_key >> e) & 1u);
-      if (lane == 0) cnt_keep[e * SEL_WARPS + warp] = __popc(k);
-    }
-    const int keep_all = scan_counts(cnt_keep, keep_base, warp_tot);
-#pragma unroll
-    for (int e = 0; e < SEL_KEYS; ++e) {
-      const bool on = (in_key >> e) & 1u;
-      const uint32_t k = __ballot_sync(0xffffffffu, on);
-      if (on)
-        keep[cnt_keep[e * SEL_WARPS + warp] + __popc(k & below)] =
-            span * SEL_SPAN + e * SEL_THREADS + tid;
-    }
-    eq_base += eq_all;
-    keep_base += keep_all;
-    __syncthreads();
-  }
-  for (int j = tid; j < P.recent; j += SEL_THREADS) keep[need + j] = n_cand + j;
 }
 
 // ---------------------------------------------------------------- compaction
 
 constexpr int MOVE_THREADS = 128;
-constexpr int MOVE_DEPTH = 8;  // rows a thread has in flight, twice
+constexpr int MOVE_DEPTH = 4;    // rows a thread has in flight, twice
+constexpr int MOVE_LIST = 512;   // rows whose places are looked up at a time
 
 // One set of rows of the caches: `base` + block * block_bytes + head *
 // tile_bytes + first + offset * row_bytes.
@@ -223,27 +258,28 @@ struct Compact {
   int keep_stride, num_kv_heads, num_blocks, bs_log2;
 };
 
-// Rows j of the destination and keep[j] of the source, as (block, offset)
-// pairs packed block * BS + offset; -1 where there is nothing to move.
-__device__ __forceinline__ bool move_of(const Compact& P, int b, int j, int n, bool report,
-                                        int64_t& src, int64_t& dst) {
-  src = dst = 0;
-  if (j >= n) return false;
-  const int BS = 1 << P.bs_log2;
-  const int t = P.keep[int64_t(b) * P.keep_stride + j];
+// Row j's source and destination as slots (block * block_size + offset);
+// src = -1 where there is nothing to move.
+struct Move {
+  int64_t src, dst;
+};
+__device__ __forceinline__ Move move_of(const Compact& P, int b, int j, int t, bool report) {
+  Move m{-1, 0};
   if (t < j || (t >> P.bs_log2) >= P.src_blocks) {  // not ascending, or no such row
     if (report) atomicOr(&g_evict_errors, PA_DEVERR_KEEP);
-    return false;
+    return m;
   }
   const int sb = P.src_tables[int64_t(b) * P.src_blocks + (t >> P.bs_log2)];
   const int db = P.dst_tables[int64_t(b) * P.dst_blocks + (j >> P.bs_log2)];
   if (sb < 0 || sb >= P.num_blocks || db < 0 || db >= P.num_blocks) {
     if (report) atomicOr(&g_evict_errors, PA_DEVERR_TABLE_ENTRY);
-    return false;
+    return m;
   }
-  src = int64_t(sb) * BS + (t & (BS - 1));
-  dst = int64_t(db) * BS + (j & (BS - 1));
-  return src != dst;  // a row that stays
+  const int mask = (1 << P.bs_log2) - 1;
+  m.src = (int64_t(sb) << P.bs_log2) + (t & mask);
+  m.dst = (int64_t(db) << P.bs_log2) + (j & mask);
+  if (m.src == m.dst) m.src = -1;  // a row that stays
+  return m;
 }
 
 __device__ __forceinline__ int rows_to_move(const Compact& P, int b, bool report) {
@@ -256,51 +292,82 @@ __device__ __forceinline__ int rows_to_move(const Compact& P, int b, bool report
   return n;
 }
 
+// The moves of rows [j0, j0 + MOVE_LIST) in shared memory. `t` holds this
+// thread's keep entries of those rows, and on return those of the next ones, so
+// that a list costs one dependent load (the tables) and not two.
+constexpr int MOVE_EACH = MOVE_LIST / MOVE_THREADS;
+__device__ __forceinline__ void load_keep(const Compact& P, int b, int j0, int n,
+                                          int (&t)[MOVE_EACH]) {
+#pragma unroll
+  for (int k = 0; k < MOVE_EACH; ++k) {
+    const int j = j0 + k * MOVE_THREADS + threadIdx.x;
+    t[k] = j < n ? P.keep[int64_t(b) * P.keep_stride + j] : 0;
+  }
+}
+__device__ __forceinline__ void fill_list(const Compact& P, int b, int j0, int n, bool report,
+                                          int (&t)[MOVE_EACH], Move* list) {
+  Move m[MOVE_EACH];
+#pragma unroll
+  for (int k = 0; k < MOVE_EACH; ++k) {
+    const int j = j0 + k * MOVE_THREADS + threadIdx.x;
+    m[k] = j < n ? move_of(P, b, j, t[k], report) : Move{-1, 0};
+  }
+  __syncthreads();  // the previous list is done with
+#pragma unroll
+  for (int k = 0; k < MOVE_EACH; ++k) list[k * MOVE_THREADS + threadIdx.x] = m[k];
+  load_keep(P, b, j0 + MOVE_LIST, n, t);
+  __syncthreads();
+}
+
+// One tile of rows is on its way while the previous one is written: its
+// sources lie behind the rows that are overwritten, so their order does not
+// matter.
 template <typename V>
 __device__ __forceinline__ void move_rows(const Compact& P, const Plane& pl, int b, int head,
-                                          int slice) {
+                                          int slice, Move* list) {
   const int per_row = pl.row_bytes / pl.slices / int(sizeof(V));  // threads of a row
   const int lane = threadIdx.x % per_row, r = threadIdx.x / per_row;
   const int rows = MOVE_THREADS / per_row;                        // rows of a pass
-  const int tile = rows * MOVE_DEPTH;
-  const bool report = lane == 0 && head == 0 && slice == 0;
-  const int n = rows_to_move(P, b, threadIdx.x == 0 && head == 0 && slice == 0);
+  const bool report = head == 0 && slice == 0;
+  const int n = rows_to_move(P, b, report && threadIdx.x == 0);
   const int BS = 1 << P.bs_log2;
-  const int64_t col = pl.first + (slice * per_row + lane) * int64_t(sizeof(V));
+  unsigned char* base = pl.base + int64_t(head) * pl.tile_bytes + pl.first +
+                        (slice * per_row + lane) * int(sizeof(V));
+  const int64_t block_bytes = int64_t(P.num_kv_heads) * pl.tile_bytes;
   auto at = [&](int64_t slot) {
-    return pl.base + ((slot >> P.bs_log2) * P.num_kv_heads + head) * pl.tile_bytes +
-           (slot & (BS - 1)) * pl.row_bytes + col;
+    return base + (slot >> P.bs_log2) * block_bytes + int(slot & (BS - 1)) * pl.row_bytes;
   };
-  struct Addr {
-    const unsigned char* src[MOVE_DEPTH];
-    unsigned char* dst[MOVE_DEPTH];
-  };
-  auto find = [&](int j0, Addr& a) {
+  int t[MOVE_EACH];
+  load_keep(P, b, 0, n, t);
+  for (int j0 = 0; j0 < n; j0 += MOVE_LIST) {
+    fill_list(P, b, j0, n, report, t, list);
+    const int m = min(MOVE_LIST, n - j0);
+    V data[MOVE_DEPTH], more[MOVE_DEPTH];
+    auto load = [&](int i0, V (&d)[MOVE_DEPTH]) {
 #pragma unroll
-    for (int u = 0; u < MOVE_DEPTH; ++u) {
-      int64_t s, d;
-      const bool go = move_of(P, b, j0 + u * rows + r, n, report, s, d);
-      a.src[u] = go ? at(s) : nullptr;
-      a.dst[u] = go ? at(d) : nullptr;
+      for (int u = 0; u < MOVE_DEPTH; ++u) {
+        const int i = i0 + u * rows + r;
+        if (i < m && list[i].src >= 0) d[u] = *reinterpret_cast<const V*>(at(list[i].src));
+      }
+    };
+    load(0, data);
+    for (int i0 = 0; i0 < m; i0 += rows * MOVE_DEPTH) {
+      load(i0 + rows * MOVE_DEPTH, more);
+      __syncthreads();  // the tile's rows are read before any of them is overwritten
+#pragma unroll
+      for (int u = 0; u < MOVE_DEPTH; ++u) {
+        const int i = i0 + u * rows + r;
+        if (i < m && list[i].src >= 0) *reinterpret_cast<V*>(at(list[i].dst)) = data[u];
+        data[u] = more[u];
+      }
     }
-  };
-  V data[MOVE_DEPTH];
-  for (int j0 = 0; j0 < n; j0 += tile) {
-    Addr a;
-    find(j0, a);
-#pragma unroll
-    for (int u = 0; u < MOVE_DEPTH; ++u)
-      if (a.src[u]) data[u] = *reinterpret_cast<const V*>(a.src[u]);
-    __syncthreads();  // the tile's rows are read before any of them is overwritten
-#pragma unroll
-    for (int u = 0; u < MOVE_DEPTH; ++u)
-      if (a.dst[u]) *reinterpret_cast<V*>(a.dst[u]) = data[u];
   }
 }
 
 // The 8-bit cache's V^T: a token is a column of its sub-tile, one byte in each
-// of head_dim rows of W bytes. A thread takes one row and W tokens at a time.
-__device__ __forceinline__ void move_columns(const Compact& P, const Plane& pl, int b, int head) {
+// of head_dim rows of W bytes. A thread takes one row and 16 tokens at a time.
+__device__ __forceinline__ void move_columns(const Compact& P, const Plane& pl, int b, int head,
+                                             Move* list) {
   const int BS = 1 << P.bs_log2, W = min(BS, 16), D = pl.row_bytes;
   const int n = rows_to_move(P, b, threadIdx.x == 0 && head == 0);
   const bool on = int(threadIdx.x) < D;
@@ -309,34 +376,36 @@ __device__ __forceinline__ void move_columns(const Compact& P, const Plane& pl, 
     return pl.base + ((slot >> P.bs_log2) * P.num_kv_heads + head) * pl.tile_bytes +
            (off / W) * (W * D) + int64_t(threadIdx.x) * W + off % W;
   };
-  for (int j0 = 0; j0 < n; j0 += 16) {
-    unsigned char x[16];
-    unsigned char* to[16];
+  int t[MOVE_EACH];
+  load_keep(P, b, 0, n, t);
+  for (int j0 = 0; j0 < n; j0 += MOVE_LIST) {
+    fill_list(P, b, j0, n, head == 0, t, list);
+    const int m = min(MOVE_LIST, n - j0);
+    for (int i0 = 0; i0 < m; i0 += 16) {
+      unsigned char x[16];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      int64_t s, d;
-      const bool go = move_of(P, b, j0 + u, n, threadIdx.x == 0 && head == 0, s, d) && on;
-      to[u] = go ? at(d) : nullptr;
-      if (go) x[u] = *at(s);
+      for (int u = 0; u < 16; ++u)
+        if (on && i0 + u < m && list[i0 + u].src >= 0) x[u] = *at(list[i0 + u].src);
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        if (on && i0 + u < m && list[i0 + u].src >= 0) *at(list[i0 + u].dst) = x[u];
     }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 16; ++u)
-      if (to[u]) *to[u] = x[u];
   }
 }
 
 // grid (KV head, sequence, slices of every plane)
 __global__ void __launch_bounds__(MOVE_THREADS) compact_rows_kernel(const Compact P) {
+  __shared__ Move list[MOVE_LIST];
   int z = blockIdx.z, p = 0;
   while (z >= P.plane[p].slices) z -= P.plane[p++].slices;
   const Plane& pl = P.plane[p];
   const int head = blockIdx.x, b = blockIdx.y;
   switch (pl.vec) {
-    case 16: move_rows<uint4>(P, pl, b, head, z); break;
-    case 8: move_rows<uint2>(P, pl, b, head, z); break;
-    case 4: move_rows<uint32_t>(P, pl, b, head, z); break;
-    default: move_columns(P, pl, b, head); break;
+    case 16: move_rows<uint4>(P, pl, b, head, z, list); break;
+    case 8: move_rows<uint2>(P, pl, b, head, z, list); break;
+    case 4: move_rows<uint32_t>(P, pl, b, head, z, list); break;
+    default: move_columns(P, pl, b, head, list); break;
   }
 }
 
@@ -389,11 +458,12 @@ int launch_evict_compact(const pa_evict_compact_params* p, void* stream) {
       P.plane[n++] = Plane{kv[i], BS * D * 9 / 16, BS * D / 2, D / 16, D / 16, 1};
     }
   }
-  // few sequences: several CTAs share a row, down to 32 bytes (a sector) each
-  int64_t ctas = int64_t(p->num_seqs) * p->num_kv_heads * n;
+  // few sequences: several CTAs share a row, down to 32 bytes (a sector) each,
+  // for about six CTAs an SM
+  const int64_t ctas = int64_t(p->num_seqs) * p->num_kv_heads * n;
   for (int i = 0; i < n; ++i)
     while (P.plane[i].vec == 16 && P.plane[i].row_bytes / P.plane[i].slices > 32 &&
-           ctas * P.plane[i].slices < 152 * 4)
+           ctas * P.plane[i].slices < 152 * 6)
       P.plane[i].slices *= 2;
   int z = 0;
   for (int i = 0; i < n; ++i) z += P.plane[i].slices;

@@ -10,8 +10,8 @@
 //    in the 4-bit decode), writes each score once (fp32, log2 domain, 4 G
 //    bytes a K row of 256, 128 or 72) and each partition's (max, sum);
 //  * sum_weights_kernel joins the partitions' sums and adds up exp2(score -
-//    max) / sum over the rows of a token. Rows are summed in a fixed order by
-//    one thread a token: no atomics, the same bits on every run.
+//    max) / sum over the rows of a token, in a fixed order: no atomics, the
+//    same bits on every run.
 // Reading K twice instead would cost 256 (128, 72) bytes a row against the
 // scores' 8 G, so the scores win for every type up to G = 8.
 // Scores, sums and weights are fp32; 8-bit and 4-bit rows enter the products
@@ -270,46 +270,94 @@ __global__ void __launch_bounds__(NTHREADS)
 }
 
 constexpr int SUM_THREADS = 256;
-constexpr int SUM_ROWS = 256;  // rows whose (max, 1/sum) are joined at a time
+constexpr int SUM_GROUPS = 4;   // threads that share a token's rows
+constexpr int SUM_TOKENS = SUM_THREADS / SUM_GROUPS * 4;  // of a CTA, four a thread
+constexpr int SUM_ROWS = 256;   // rows whose (max, 1/sum) are joined at a time
+constexpr int SUM_LANES = 8;    // lanes that join one row's partitions
+static_assert(SUM_TOKENS == SUM_THREADS, "the last step takes one token a thread");
 
-// One thread per token: grid (tokens / SUM_THREADS, sequence). Every block
-// joins the partitions of the sequence's rows for itself (8 bytes a row and
-// partition, against 4 a row and token that it reads).
+// grid (tokens / SUM_TOKENS, sequence). Every block joins the partitions of the
+// sequence's rows for itself (8 bytes a row and partition, against 4 a row and
+// token that it reads). A thread adds up every fourth row of four tokens, with
+// four 16-byte loads in flight; the four sums are added in a fixed order.
 __global__ void __launch_bounds__(SUM_THREADS) sum_weights_kernel(const Weights P) {
-  const int b = blockIdx.y;
+  const int b = blockIdx.y, tid = threadIdx.x;
   const int L = checked_len(P, b, false);
-  if (int(blockIdx.x) * SUM_THREADS >= L) return;
-  const int key = blockIdx.x * SUM_THREADS + threadIdx.x;
+  const int key0 = blockIdx.x * SUM_TOKENS;
+  if (key0 >= L) return;
+  const int quad = tid % (SUM_THREADS / SUM_GROUPS), group = tid / (SUM_THREADS / SUM_GROUPS);
+  const int key = key0 + quad * 4;
   const int num_q_heads = P.num_kv_heads << P.g_log2;
   const int rows = P.q_len * num_q_heads;
   const int64_t row0 = int64_t(b) * rows;
+  // keys that the first new token sees: below it nothing is masked
+  const int all_see = L - P.q_len + 1;
   __shared__ float2 norm[SUM_ROWS];
-  float w = 0.0f;
+  __shared__ float4 part_sum[SUM_GROUPS][SUM_THREADS / SUM_GROUPS];
+  float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int r0 = 0; r0 < rows; r0 += SUM_ROWS) {
     const int n = min(SUM_ROWS, rows - r0);
     __syncthreads();
-    for (int r = threadIdx.x; r < n; r += SUM_THREADS) {
-      const int see = L - P.q_len + (r0 + r) / num_q_heads + 1;
+    const int sub = tid % SUM_LANES;
+    for (int r1 = 0; r1 < n; r1 += SUM_THREADS / SUM_LANES) {
+      const int r = min(r1 + tid / SUM_LANES, n - 1);
+      const int see = all_see + (r0 + r) / num_q_heads;
       const int np = (see + P.partition_tokens - 1) / P.partition_tokens;
       const float2* part = P.part + (row0 + r0 + r) * P.num_partitions;
       float M = -INFINITY, S = 0.0f;
-      for (int p = 0; p < np; ++p) M = fmaxf(M, part[p].x);
-      const float ref = M == -INFINITY ? 0.0f : M;
-      for (int p = 0; p < np; ++p) S += part[p].y * dev::fast_exp2(part[p].x - ref);
-      norm[r] = make_float2(M, 1.0f / S);
+      for (int p = sub; p < np; p += SUM_LANES) {
+        const float2 x = part[p];
+        const float top = fmaxf(M, x.x), ref = top == -INFINITY ? 0.0f : top;
+        S = S * dev::fast_exp2(M - ref) + x.y * dev::fast_exp2(x.x - ref);
+        M = top;
+      }
+#pragma unroll
+      for (int o = 1; o < SUM_LANES; o <<= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, M, o), os = __shfl_xor_sync(0xffffffffu, S, o);
+        const float top = fmaxf(M, om), ref = top == -INFINITY ? 0.0f : top;
+        S = S * dev::fast_exp2(M - ref) + os * dev::fast_exp2(om - ref);
+        M = top;
+      }
+      if (sub == 0) norm[r] = make_float2(M, 1.0f / S);
     }
     __syncthreads();
     if (key < L) {
       const float* src = P.scores + (row0 + r0) * P.score_stride + key;
-      for (int r = 0; r < n; ++r) {
-        if (key < L - P.q_len + (r0 + r) / num_q_heads + 1)
-          w = fmaf(dev::fast_exp2(src[r * P.score_stride] - norm[r].x), norm[r].y, w);
+      if (key + 3 < all_see) {
+#pragma unroll 4
+        for (int r = group; r < n; r += SUM_GROUPS) {
+          const float4 s = *reinterpret_cast<const float4*>(src + r * P.score_stride);
+          const float2 z = norm[r];
+          w.x = fmaf(dev::fast_exp2(s.x - z.x), z.y, w.x);
+          w.y = fmaf(dev::fast_exp2(s.y - z.x), z.y, w.y);
+          w.z = fmaf(dev::fast_exp2(s.z - z.x), z.y, w.z);
+          w.w = fmaf(dev::fast_exp2(s.w - z.x), z.y, w.w);
+        }
+      } else {
+        // scores past a row's last key were never written
+        for (int r = group; r < n; r += SUM_GROUPS) {
+          const int see = all_see + (r0 + r) / num_q_heads;
+          const float2 z = norm[r];
+          const float* s = src + r * P.score_stride;
+          if (key < see) w.x = fmaf(dev::fast_exp2(s[0] - z.x), z.y, w.x);
+          if (key + 1 < see) w.y = fmaf(dev::fast_exp2(s[1] - z.x), z.y, w.y);
+          if (key + 2 < see) w.z = fmaf(dev::fast_exp2(s[2] - z.x), z.y, w.z);
+          if (key + 3 < see) w.w = fmaf(dev::fast_exp2(s[3] - z.x), z.y, w.w);
+        }
       }
     }
   }
-  if (key < L) {
-    float* dst = P.token_weights + int64_t(b) * P.weights_stride + key;
-    *dst = P.accumulate ? *dst + w : w;
+  part_sum[group][quad] = w;
+  __syncthreads();
+  // one thread a token now
+  const int at = key0 + tid;
+  if (at < L) {
+    const float* p = reinterpret_cast<const float*>(part_sum) + tid;
+    float x = 0.0f;
+#pragma unroll
+    for (int g = 0; g < SUM_GROUPS; ++g) x += p[g * SUM_TOKENS];
+    float* dst = P.token_weights + int64_t(b) * P.weights_stride + at;
+    *dst = P.accumulate ? *dst + x : x;
   }
 }
 
@@ -389,7 +437,7 @@ int launch_token_weights(const pa_token_weights_params* p, const TokenWeightsSpa
     default: return int(cudaErrorInvalidValue);
   }
   if (e) return e;
-  const dim3 grid(unsigned((sp.cap + SUM_THREADS - 1) / SUM_THREADS), unsigned(p->num_seqs));
+  const dim3 grid(unsigned((sp.cap + SUM_TOKENS - 1) / SUM_TOKENS), unsigned(p->num_seqs));
   sum_weights_kernel<<<grid, SUM_THREADS, 0, s>>>(P);
   return int(cudaGetLastError());
 }
