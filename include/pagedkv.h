@@ -552,8 +552,8 @@ pa_status pa_token_weights(const pa_token_weights_params* p, void* workspace,
  *   keep      int32 [num_seqs][budget]: their indices, ascending; -1 behind
  *   new_lens  int32 [num_seqs]: min(context_lens[b], budget)
  * token_weights: float [num_seqs][weights_stride]; a length beyond
- * weights_stride is cut to it and sets PA_DEVERR_CONTEXT_LEN. budget >= 1,
- * recent in [0, budget]. No workspace.
+ * weights_stride is cut to it and sets PA_DEVERR_CONTEXT_LEN. num_seqs up to
+ * 65535, budget >= 1, recent in [0, budget]. No workspace.
  * ---------------------------------------------------------------------- */
 pa_status pa_evict_select(const float* token_weights, const int32_t* context_lens, int32_t* keep,
                           int32_t* new_lens, int32_t num_seqs, int32_t weights_stride,

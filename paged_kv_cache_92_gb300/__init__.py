@@ -231,7 +231,7 @@ def _dev_ptr(t, dtype, name: str) -> int:
 
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
@@ -241,10 +241,11 @@ def _dev_ptr(t, dtype, name: str) -> int:
 
 
 def _stream_handle(stream) -> Optional[int]:
-    import torch
-
     if stream is None:
-        stream = torch.cuda.current_stream()
+        import torch
+
+        # the handle alone: a Stream object costs a call several microseconds
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -259,7 +260,7 @@ def kv_cache_format(k_cache) -> Tuple[int, int]:
     if k_cache.dim() != 4:
         raise ValueError("a cache is [num_blocks][num_kv_heads][block_size][row]")
     row = k_cache.shape[3]
-    if k_cache.dtype == torch.uint8:
+    if k_cache.dtype is torch.uint8:
         return (KV_FP4_E2M1, row * 16 // 9) if row in (36, 72) else (KV_FP8_E4M3, row)
     return KV_BF16, row
 
@@ -275,7 +276,7 @@ def fp4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_di
 def _v_cache_ok(fmt: int, k_cache, v_cache) -> bool:
     if fmt == KV_FP8_E4M3:
         return tuple(v_cache.shape) in fp8_v_shapes(*k_cache.shape)
-    return tuple(v_cache.shape) == tuple(k_cache.shape)
+    return v_cache.shape == k_cache.shape
 
 
 def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
@@ -297,38 +298,27 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
         (B, Hq, D), QL = q.shape, 0
     fmt, D2 = kv_cache_format(k_cache)
     NB, Hkv, BS, _ = k_cache.shape
-    v_ok = _v_cache_ok(fmt, k_cache, v_cache)
-    if D2 != D or not v_ok or tuple(out.shape) != tuple(q.shape):
+    if D2 != D or not _v_cache_ok(fmt, k_cache, v_cache) or out.shape != q.shape:
         raise ValueError("shape mismatch between q / out / k_cache / v_cache")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
-    p = DecodeParams()
-    p.q = _dev_ptr(q, torch.bfloat16, "q")
-    p.out = _dev_ptr(out, torch.bfloat16, "out")
-    cache_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
-    p.k_cache = _dev_ptr(k_cache, cache_dtype, "k_cache")
-    p.v_cache = _dev_ptr(v_cache, cache_dtype, "v_cache")
+    fmt_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
+    ks = vs = None
     if fmt != KV_BF16:
         if k_scale is None or v_scale is None:
             raise ValueError("the 8-bit and 4-bit caches need k_scale and v_scale")
-        p.kv_dtype = fmt
-        p.k_scale = _dev_ptr(k_scale, torch.float32, "k_scale")
-        p.v_scale = _dev_ptr(v_scale, torch.float32, "v_scale")
+        ks = _dev_ptr(k_scale, torch.float32, "k_scale")
+        vs = _dev_ptr(v_scale, torch.float32, "v_scale")
         if fmt == KV_FP4_E2M1 and (k_scale.numel() != Hkv or v_scale.numel() != Hkv):
             raise ValueError("k_scale and v_scale must be [num_kv_heads]")
-    p.block_tables = _dev_ptr(block_tables, torch.int32, "block_tables")
-    p.context_lens = _dev_ptr(context_lens, torch.int32, "context_lens")
-    p.max_blocks_per_seq = block_tables.shape[1]
-    p.num_seqs, p.num_q_heads, p.num_kv_heads = B, Hq, Hkv
-    p.head_dim, p.block_size, p.num_blocks = D, BS, NB
-    p.max_context_len = int(max_context_len)
-    p.scale = float(1.0 / math.sqrt(D) if scale is None else scale)
-    p.partition_tokens = int(partition_tokens)
-    p.variant = int(variant)
-    p.overlap_prologue = int(bool(overlap_prologue))
-    p.query_len = int(QL)
-    p.wait_timeout_us = int(wait_timeout_us)
-    return p
+    return DecodeParams(
+        _dev_ptr(q, torch.bfloat16, "q"), _dev_ptr(out, torch.bfloat16, "out"),
+        _dev_ptr(k_cache, fmt_dtype, "k_cache"), _dev_ptr(v_cache, fmt_dtype, "v_cache"),
+        _dev_ptr(block_tables, torch.int32, "block_tables"),
+        _dev_ptr(context_lens, torch.int32, "context_lens"),
+        block_tables.shape[1], B, Hq, Hkv, D, BS, NB, int(max_context_len),
+        float(1.0 / math.sqrt(D) if scale is None else scale), int(partition_tokens),
+        int(variant), int(bool(overlap_prologue)), fmt, ks, vs, int(QL), int(wait_timeout_us))
 
 
 def pa_decode_workspace_size(params: DecodeParams) -> int:
@@ -354,9 +344,10 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, max_context_len: 
     p = make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
                            max_context_len, scale, partition_tokens, variant, overlap_prologue,
                            k_scale, v_scale, wait_timeout_us)
-    need = int(lib.pa_decode_workspace_size(ctypes.byref(p)))
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        need = int(lib.pa_decode_workspace_size(ctypes.byref(p)))
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_ptr = _dev_ptr(workspace, torch.uint8, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() if workspace is not None else 0
     _check(lib.pa_decode(ctypes.byref(p), ws_ptr, ws_bytes, _stream_handle(stream)), "pa_decode")
@@ -599,12 +590,12 @@ def pa_copy_blocks_fp8(k_cache, v_cache, pairs, stream=None) -> None:
 def _check_fp4_rows(k_rows, v_rows, k_cache, v_cache, slot_mapping, k_scale, v_scale, who: str):
     T, Hkv, D = k_rows.shape
     fmt, D2 = kv_cache_format(k_cache)
-    if fmt != KV_FP4_E2M1 or (k_cache.shape[1], D2) != (Hkv, D) \
-            or tuple(v_rows.shape) != tuple(k_rows.shape) \
-            or tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(slot_mapping.shape) != (T,) \
+    NB, Hkv2, BS, _ = k_cache.shape
+    if fmt != KV_FP4_E2M1 or Hkv2 != Hkv or D2 != D or v_rows.shape != k_rows.shape \
+            or v_cache.shape != k_cache.shape or slot_mapping.shape != (T,) \
             or k_scale.numel() != Hkv or v_scale.numel() != Hkv:
         raise ValueError(f"shape mismatch in {who}")
-    return T, Hkv, D, k_cache.shape[2], k_cache.shape[0]
+    return T, Hkv, D, BS, NB
 
 
 def pa_reshape_and_cache_fp4(k_new, v_new, k_cache, v_cache, slot_mapping, k_scale, v_scale,
@@ -682,30 +673,24 @@ def make_token_weights_params(q, k_cache, block_tables, context_lens, max_contex
     NB, Hkv, BS, _ = k_cache.shape
     if D2 != D:
         raise ValueError("q and k_cache differ in head_dim")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
     if token_weights.dim() != 2 or token_weights.shape[0] != B:
         raise ValueError("token_weights must be [num_seqs][stride]")
-    p = TokenWeightsParams()
-    p.q = _dev_ptr(q, torch.bfloat16, "q")
-    p.k_cache = _dev_ptr(k_cache, torch.bfloat16 if fmt == KV_BF16 else torch.uint8, "k_cache")
-    p.block_tables = _dev_ptr(block_tables, torch.int32, "block_tables")
-    p.context_lens = _dev_ptr(context_lens, torch.int32, "context_lens")
-    p.token_weights = _dev_ptr(token_weights, torch.float32, "token_weights")
-    p.weights_stride = token_weights.shape[1]
-    p.max_blocks_per_seq = block_tables.shape[1]
-    p.num_seqs, p.num_q_heads, p.num_kv_heads = B, Hq, Hkv
-    p.head_dim, p.block_size, p.num_blocks = D, BS, NB
-    p.max_context_len = int(max_context_len)
-    p.scale = float(1.0 / math.sqrt(D) if scale is None else scale)
-    p.kv_dtype = fmt
+    ks = None
     if fmt != KV_BF16:
         if k_scale is None or k_scale.numel() != Hkv:
             raise ValueError("the 8-bit and 4-bit caches need k_scale [num_kv_heads]")
-        p.k_scale = _dev_ptr(k_scale, torch.float32, "k_scale")
-    p.query_len = int(QL)
-    p.accumulate = int(bool(accumulate))
-    return p
+        ks = _dev_ptr(k_scale, torch.float32, "k_scale")
+    return TokenWeightsParams(
+        _dev_ptr(q, torch.bfloat16, "q"),
+        _dev_ptr(k_cache, torch.bfloat16 if fmt == KV_BF16 else torch.uint8, "k_cache"),
+        _dev_ptr(block_tables, torch.int32, "block_tables"),
+        _dev_ptr(context_lens, torch.int32, "context_lens"),
+        _dev_ptr(token_weights, torch.float32, "token_weights"), token_weights.shape[1],
+        block_tables.shape[1], B, Hq, Hkv, D, BS, NB, int(max_context_len),
+        float(1.0 / math.sqrt(D) if scale is None else scale), fmt, ks, int(QL),
+        int(bool(accumulate)))
 
 
 def pa_token_weights_workspace_size(q, k_cache, block_tables, context_lens, max_context_len: int,
@@ -743,14 +728,14 @@ def pa_evict_select(token_weights, context_lens, budget: int, recent: int = 0, k
     -1 behind; new_lens int32 [B])."""
     import torch
 
-    if token_weights.dim() != 2 or tuple(context_lens.shape) != (token_weights.shape[0],):
+    if token_weights.dim() != 2 or context_lens.shape != (token_weights.shape[0],):
         raise ValueError("token_weights must be [num_seqs][stride], context_lens [num_seqs]")
     B = token_weights.shape[0]
     if keep is None:
         keep = torch.empty((B, max(int(budget), 0)), dtype=torch.int32, device=token_weights.device)
     if new_lens is None:
         new_lens = torch.empty(B, dtype=torch.int32, device=token_weights.device)
-    if tuple(keep.shape) != (B, budget) or tuple(new_lens.shape) != (B,):
+    if keep.shape != (B, budget) or new_lens.shape != (B,):
         raise ValueError("keep must be [num_seqs][budget], new_lens [num_seqs]")
     _check(load().pa_evict_select(
         _dev_ptr(token_weights, torch.float32, "token_weights"),
@@ -778,20 +763,14 @@ def pa_evict_compact(k_cache, v_cache, block_tables, dst_tables, keep, new_lens,
                 and (token_weights.dim() != 2 or token_weights.shape[0] != B)):
         raise ValueError("block_tables, dst_tables, keep and token_weights must be [num_seqs][...]")
     cache_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
-    p = EvictCompactParams()
-    p.k_cache = _dev_ptr(k_cache, cache_dtype, "k_cache")
-    p.v_cache = _dev_ptr(v_cache, cache_dtype, "v_cache")
-    p.block_tables = _dev_ptr(block_tables, torch.int32, "block_tables")
-    p.dst_tables = _dev_ptr(dst_tables, torch.int32, "dst_tables")
-    p.keep = _dev_ptr(keep, torch.int32, "keep")
-    p.new_lens = _dev_ptr(new_lens, torch.int32, "new_lens")
-    if token_weights is not None:
-        p.token_weights = _dev_ptr(token_weights, torch.float32, "token_weights")
-        p.weights_stride = token_weights.shape[1]
-    p.max_blocks_per_seq, p.max_dst_blocks_per_seq = block_tables.shape[1], dst_tables.shape[1]
-    p.keep_stride = keep.shape[1]
-    p.num_seqs, p.num_kv_heads, p.head_dim, p.block_size, p.num_blocks = B, Hkv, D, BS, NB
-    p.kv_dtype = fmt
+    p = EvictCompactParams(
+        _dev_ptr(k_cache, cache_dtype, "k_cache"), _dev_ptr(v_cache, cache_dtype, "v_cache"),
+        _dev_ptr(block_tables, torch.int32, "block_tables"),
+        _dev_ptr(dst_tables, torch.int32, "dst_tables"), _dev_ptr(keep, torch.int32, "keep"),
+        _dev_ptr(new_lens, torch.int32, "new_lens"),
+        None if token_weights is None else _dev_ptr(token_weights, torch.float32, "token_weights"),
+        0 if token_weights is None else token_weights.shape[1], block_tables.shape[1],
+        dst_tables.shape[1], keep.shape[1], B, Hkv, D, BS, NB, fmt)
     _check(load().pa_evict_compact(ctypes.byref(p), _stream_handle(stream)), "pa_evict_compact")
 
 

@@ -20,10 +20,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Keys per CTA of the token weights: short enough for
-// 16 CTAs an SM of a 152-SM GPU, so that ragged lengths even out, within
+// 10 CTAs an SM of a 152-SM GPU, so that ragged lengths even out, within
 // [128, 4096] tokens. `units`: (sequence, KV head, column group)s.
 int auto_partition_tokens(int64_t cap, int64_t units) {
-  const int64_t pt = (cap * units / (152 * 16) + 127) / 128 * 128;
+  const int64_t pt = (cap * units / (152 * 10) + 127) / 128 * 128;
   return pt < 128 ? 128 : (pt > kMaxPartitionTokens ? kMaxPartitionTokens : int(pt));
 }
 
@@ -893,9 +893,9 @@ pa_status pa_token_weights(const pa_token_weights_params* p, void* workspace,
 pa_status pa_evict_select(const float* token_weights, const int32_t* context_lens, int32_t* keep,
                           int32_t* new_lens, int32_t num_seqs, int32_t weights_stride,
                           int32_t budget, int32_t recent, pa_stream_t stream) {
-  if (num_seqs < 0 || weights_stride < 1)
+  if (num_seqs < 0 || num_seqs > 65535 || weights_stride < 1)
     return pa::set_error(PA_ERR_INVALID_ARG,
-                         "pa_evict_select: num_seqs >= 0 and weights_stride >= 1");
+                         "pa_evict_select: num_seqs in [0, 65535] and weights_stride >= 1");
   if (budget < 1 || recent < 0 || recent > budget)
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_evict_select: budget >= 1 and recent in [0, budget]");

@@ -6,15 +6,15 @@
 // go is left open. Here the most recent ones stay, and of the others those
 // with the largest accumulated attention weight (pa_weights.cu).
 //
-//  * evict_select_kernel: one CTA per sequence. The candidates' weights become
-//    ordered 32-bit keys in registers (up to 32 a thread; longer sequences
-//    re-read them from L2), and the threshold is found by three rounds of a
+//  * evict_select_kernel: one CTA per sequence, or a cluster of eight for long
+//    ones, each with an eighth of the tokens. The candidates' weights become
+//    ordered 32-bit keys in registers (up to 8 a thread; longer ranges re-read
+//    them from L2), and the threshold is found by three rounds of a
 //    shared-memory histogram over 11, 11 and 10 bits of the keys that still
-//    tie with it. A warp whose lanes all hit one bin adds once, so equal
-//    weights -- most tokens of a long context have nearly none -- do not
-//    serialise. (A search bit by bit, 32 counts over the CTA, took 39 us
-//    where this takes 7 to 13.) Ties go to the lowest index through ranks, and
-//    the kept indices come out ascending.
+//    tie with it; the CTAs of a cluster read each other's. Four copies of the
+//    histogram, by lane, keep equal weights -- most tokens of a long context
+//    have nearly none -- from serialising more than eight deep. Ties go to the
+//    lowest index through ranks, and the kept indices come out ascending.
 //  * compact_rows_kernel: row j of the destination <- row keep[j] of the
 //    source. keep ascends, so keep[j] >= j, and moving rows in order within
 //    one CTA is safe in place: a tile's rows are in registers before any of
@@ -22,6 +22,7 @@
 //    owns one (sequence, KV head) and a slice of the row's bytes, so CTAs never
 //    meet. Bound by memory traffic: every kept row is read and written once,
 //    and rows that stay where they are not at all.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -32,15 +33,19 @@
 namespace pa {
 namespace {
 
+namespace cg = cooperative_groups;
+
 __device__ unsigned int g_evict_errors;
 
 // ---------------------------------------------------------------- selection
 
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
-constexpr int SEL_KEYS = 32;  // keys a thread holds at a time
+constexpr int SEL_KEYS = 8;       // keys a thread holds at a time
 constexpr int SEL_BINS = 2048;
 constexpr int SEL_COPIES = 4;
+constexpr int SEL_CLUSTER = 8;    // CTAs of a long sequence
+constexpr int SEL_LONG = 4096;    // a row of weights longer than this takes a cluster
 
 // Order-preserving map of a weight to an unsigned key; NaN below everything,
 // both zeros alike.
@@ -84,28 +89,34 @@ __device__ __forceinline__ int block_scan(int x, int* warp_tot, int& all) {
 
 struct SelectShared {
   int hist[SEL_COPIES][SEL_BINS];
+  int bins[2][SEL_BINS];           // their sum, read by the cluster; alternates
   int cnt[SEL_KEYS * SEL_WARPS];
   int warp_tot[SEL_WARPS];
   int bin, left;
+  int above, equal;                // keys of the CTAs before this one
 };
 
-// The choice for one sequence of more than `budget` tokens: E keys a thread at
-// a time, key e of span s being token s * SEL_THREADS * E + e * SEL_THREADS + tid.
+// The choice for one sequence of more than `budget` tokens, E keys a thread at
+// a time. This CTA, rank `rank` of `ctas`, has the candidates [c0, c1); key e of
+// span s is token c0 + s * SEL_THREADS * E + e * SEL_THREADS + tid.
 template <int E>
 __device__ __forceinline__ void select_row(const Select& P, const float* w, int32_t* keep, int L,
-                                           SelectShared& sm) {
+                                           SelectShared& sm, cg::cluster_group& cluster) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
   const int n_cand = L - P.recent;       // the others always stay
   const int need = P.budget - P.recent;  // of the candidates, fewer than n_cand
+  const int share = (n_cand + ctas - 1) / ctas;
+  const int c0 = min(n_cand, rank * share), c1 = min(n_cand, c0 + share);
   const int span_len = SEL_THREADS * E;
-  const int spans = (n_cand + span_len - 1) / span_len;
+  const int spans = (c1 - c0 + span_len - 1) / span_len;
   uint32_t key[E];
-  auto token = [&](int span, int e) { return span * span_len + e * SEL_THREADS + tid; };
+  auto token = [&](int span, int e) { return c0 + span * span_len + e * SEL_THREADS + tid; };
   auto load = [&](int span) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int i = token(span, e);
-      key[e] = i < n_cand ? weight_key(w[i]) : 0u;
+      key[e] = i < c1 ? weight_key(w[i]) : 0u;
     }
   };
   if (spans == 1) load(0);
@@ -114,17 +125,19 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
   // equal it are kept (the first ones)
   uint32_t prefix = 0, mask = 0;
   int left = need;
+  if (tid == 0) sm.above = sm.equal = 0;
   if (need > 0) {
 #pragma unroll 1
-    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : (shift == 10 ? 0 : -1)) {
-      const uint32_t digits = shift == 0 ? 1023u : 2047u;
+    for (int round = 0; round < 3; ++round) {
+      const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
+      const uint32_t digits = round == 2 ? 1023u : 2047u;
       for (int i = tid; i < SEL_COPIES * SEL_BINS; i += SEL_THREADS) (&sm.hist[0][0])[i] = 0;
       __syncthreads();
       for (int span = 0; span < spans; ++span) {
         if (spans > 1) load(span);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const bool in = token(span, e) < n_cand && (key[e] & mask) == prefix;
+          const bool in = token(span, e) < c1 && (key[e] & mask) == prefix;
           if (in) atomicAdd(&sm.hist[lane % SEL_COPIES][(key[e] >> shift) & digits], 1);
         }
       }
@@ -137,6 +150,29 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
         n1 += sm.hist[k][b1];
         n0 += sm.hist[k][b0];
       }
+      int before1 = 0, before0 = 0;  // of the CTAs before this one
+      if (ctas > 1) {
+        int* mine = &sm.bins[round & 1][b0];
+        *reinterpret_cast<int2*>(mine) = make_int2(n0, n1);
+        cluster.sync();  // (the buffer's last readers passed the previous one)
+        n1 = n0 = 0;
+        int2 x[SEL_CLUSTER];
+#pragma unroll
+        for (int k = 0; k < SEL_CLUSTER; ++k)
+          x[k] = *reinterpret_cast<const int2*>(
+              cluster.map_shared_rank(mine, unsigned(min(k, ctas - 1))));
+#pragma unroll
+        for (int k = 0; k < SEL_CLUSTER; ++k) {
+          if (k < ctas) {
+            n0 += x[k].x;
+            n1 += x[k].y;
+          }
+          if (k < rank) {
+            before0 += x[k].x;
+            before1 += x[k].y;
+          }
+        }
+      }
       int all;
       const int upto = block_scan(n1 + n0, sm.warp_tot, all), before = upto - n1 - n0;
       if (before < left && left <= upto) {
@@ -145,15 +181,22 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
         sm.left = left - before - (first ? 0 : n1);
       }
       __syncthreads();
-      prefix |= uint32_t(sm.bin) << shift;
+      const int bin = sm.bin;
+      prefix |= uint32_t(bin) << shift;
       mask |= digits << shift;
       left = sm.left;
+      if (ctas > 1) {
+        const int above = __reduce_add_sync(0xffffffffu, (b1 > bin ? before1 : 0) +
+                                                             (b0 > bin ? before0 : 0));
+        if (lane == 0 && above) atomicAdd(&sm.above, above);
+        if (round == 2 && (b1 == bin || b0 == bin)) sm.equal = b1 == bin ? before1 : before0;
+      }
       __syncthreads();
     }
   }
-
+  // of the CTAs before this one: keys that equal the threshold, keys that are kept
+  int eq_base = sm.equal, keep_base = sm.above + min(sm.equal, left);
   // ranks in token order: of the keys equal to the threshold, then of the kept
-  int eq_base = 0, keep_base = 0;
   const uint32_t below = (1u << lane) - 1u;
   // exclusive prefix of the warps' counts, in token order (entry e * SEL_WARPS + warp)
   auto scan_counts = [&](int base) {
@@ -170,7 +213,7 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
     uint32_t kept = 0, eq = 0;  // a bit per key
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const bool cand = token(span, e) < n_cand && need > 0;
+      const bool cand = token(span, e) < c1 && need > 0;
       const bool same = cand && key[e] == prefix;
       kept |= uint32_t(cand && key[e] > prefix) << e;
       eq |= uint32_t(same) << e;
@@ -183,8 +226,8 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
     for (int e = 0; e < E; ++e) {
       const bool same = (eq >> e) & 1u;
       const uint32_t v = __ballot_sync(0xffffffffu, same);
-      const int rank = sm.cnt[e * SEL_WARPS + warp] + __popc(v & below);
-      const bool on = ((kept >> e) & 1u) || (same && rank < left);
+      const int at = sm.cnt[e * SEL_WARPS + warp] + __popc(v & below);
+      const bool on = ((kept >> e) & 1u) || (same && at < left);
       in_kept[e] = __ballot_sync(0xffffffffu, on);
     }
     __syncthreads();
@@ -200,41 +243,42 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
     keep_base += keep_all;
     __syncthreads();
   }
-  for (int j = tid; j < P.recent; j += SEL_THREADS) keep[need + j] = n_cand + j;
+  for (int j = rank * SEL_THREADS + tid; j < P.recent; j += ctas * SEL_THREADS)
+    keep[need + j] = n_cand + j;
+  if (ctas > 1 && need > 0) cluster.sync();  // no CTA leaves while another reads its bins
 }
 
+// grid (CTAs of a sequence, sequence), in clusters of gridDim.x
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Select P) {
   __shared__ SelectShared sm;
-  const int b = blockIdx.x, tid = threadIdx.x;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int first = blockIdx.x * SEL_THREADS + tid, stride = gridDim.x * SEL_THREADS;
   int L = P.context_lens[b];
   if (L > P.max_len) {
-    if (tid == 0) atomicOr(&g_evict_errors, PA_DEVERR_CONTEXT_LEN);
+    if (first == 0) atomicOr(&g_evict_errors, PA_DEVERR_CONTEXT_LEN);
     L = P.max_len;
   }
   L = max(L, 0);
   const int n_keep = min(L, P.budget);
   int32_t* keep = P.keep + int64_t(b) * P.budget;
-  if (tid == 0) P.new_lens[b] = n_keep;
-  for (int j = n_keep + tid; j < P.budget; j += SEL_THREADS) keep[j] = -1;
+  if (first == 0) P.new_lens[b] = n_keep;
+  for (int j = n_keep + first; j < P.budget; j += stride) keep[j] = -1;
   if (L <= P.budget) {
-    for (int j = tid; j < L; j += SEL_THREADS) keep[j] = j;
+    for (int j = first; j < L; j += stride) keep[j] = j;
     return;
   }
   const float* w = P.weights + int64_t(b) * P.weights_stride;
   // no more keys a thread than the sequence needs
-  const int n_cand = L - P.recent;
-  if (n_cand <= 2 * SEL_THREADS) {
-    select_row<2>(P, w, keep, L, sm);
-  } else if (n_cand <= 8 * SEL_THREADS) {
-    select_row<8>(P, w, keep, L, sm);
-  } else {
-    select_row<SEL_KEYS>(P, w, keep, L, sm);
-  }
+  if ((L - P.recent + int(gridDim.x) - 1) / int(gridDim.x) <= 2 * SEL_THREADS)
+    select_row<2>(P, w, keep, L, sm, cluster);
+  else
+    select_row<SEL_KEYS>(P, w, keep, L, sm, cluster);
 }
 
 // ---------------------------------------------------------------- compaction
 
-constexpr int MOVE_THREADS = 128;
+constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_DEPTH = 4;    // rows a thread has in flight, twice
 constexpr int MOVE_LIST = 512;   // rows whose places are looked up at a time
 
@@ -436,10 +480,21 @@ __global__ void __launch_bounds__(256)
 int launch_evict_select(const float* token_weights, const int32_t* context_lens, int32_t* keep,
                         int32_t* new_lens, int32_t num_seqs, int64_t weights_stride,
                         int32_t budget, int32_t recent, void* stream) {
-  Select P{token_weights, context_lens, keep, new_lens, weights_stride,
-           num_seqs, budget, recent, int(weights_stride)};
-  evict_select_kernel<<<unsigned(num_seqs), SEL_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(P);
-  return int(cudaGetLastError());
+  const Select P{token_weights, context_lens, keep, new_lens, weights_stride,
+                 num_seqs, budget, recent, int(weights_stride)};
+  const unsigned ctas = weights_stride > SEL_LONG ? SEL_CLUSTER : 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, unsigned(num_seqs));
+  cfg.blockDim = dim3(SEL_THREADS);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return int(cudaLaunchKernelEx(&cfg, evict_select_kernel, P));
 }
 
 int launch_evict_compact(const pa_evict_compact_params* p, void* stream) {
@@ -458,11 +513,11 @@ int launch_evict_compact(const pa_evict_compact_params* p, void* stream) {
       P.plane[n++] = Plane{kv[i], BS * D * 9 / 16, BS * D / 2, D / 16, D / 16, 1};
     }
   }
-  // few sequences: several CTAs share a row, down to 32 bytes (a sector) each,
+  // few sequences: several CTAs share a row, down to 64 bytes (an HBM access) each,
   // for about six CTAs an SM
   const int64_t ctas = int64_t(p->num_seqs) * p->num_kv_heads * n;
   for (int i = 0; i < n; ++i)
-    while (P.plane[i].vec == 16 && P.plane[i].row_bytes / P.plane[i].slices > 32 &&
+    while (P.plane[i].vec == 16 && P.plane[i].row_bytes / P.plane[i].slices > 64 &&
            ctas * P.plane[i].slices < 152 * 6)
       P.plane[i].slices *= 2;
   int z = 0;

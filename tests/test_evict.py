@@ -127,7 +127,7 @@ def test_token_weights_workspace(pk):
 
 @pytest.mark.parametrize("args,status", [
     ((2, 64, 0, 0), 1), ((2, 64, 8, -1), 1), ((2, 64, 8, 9), 1), ((-1, 64, 8, 0), 1),
-    ((2, 0, 8, 0), 1), ((2, 64, 8, 8), 1), ((0, 64, 8, 8), 0)])
+    ((2, 0, 8, 0), 1), ((65536, 64, 8, 0), 1), ((2, 64, 8, 8), 1), ((0, 64, 8, 8), 0)])
 def test_select_refusals(pk, args, status):
     assert pk.load().pa_evict_select(None, None, None, None, *args, None) == status
 
@@ -399,14 +399,16 @@ def test_select(pk, budget, recent):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("budget,recent", [(33000, 100), (9, 2), (69000, 0)])
+@pytest.mark.parametrize("budget,recent", [(33000, 100), (9, 2), (69000, 0), (12, 12)])
 def test_select_beyond_one_span(pk, budget, recent):
-    """Sequences of more tokens than one round of registers holds (32,768)."""
+    """Clusters of CTAs: sequences of a few tokens for each, of as many as one round of
+    registers holds (8,192 a CTA), and of more."""
     import torch
 
     rng = np.random.default_rng(5)
-    lens = np.array([70001, 32768, 32769 + recent, 40000], np.int32)
-    w = _weights_with_ties(rng, 4, 70001)
+    lens = np.array([70001, 32768, 32769 + recent, 40000, 65536 + recent, 13, 1, 9000], np.int32)
+    w = _weights_with_ties(rng, 8, 70001)
+    w[3, ::2] = 0.25                 # ties over every CTA of the cluster
     want = select(w, lens, budget, recent)
     keep, n = pk.pa_evict_select(torch.from_numpy(w).cuda(), torch.from_numpy(lens).cuda(), budget,
                                  recent)
