@@ -48,6 +48,28 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float* y) {
   return w;
 }
 
+// Largest magnitude of 16 bf16 values, NaN if one of them is.
+__device__ __forceinline__ float group_max(const uint4& lo, const uint4& hi) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i)
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
+  const float a = dev::bf16_lo(m), b = dev::bf16_hi(m);
+  return a != a ? a : (b != b ? b : fmaxf(a, b));
+}
+
+// fl(x / step) where it lies within the grid (below 8), with inv = fl(1 / step):
+// one correction by the remainder, which is exact in a fused multiply-add
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990). Beyond, the code saturates whatever the last place, and
+// an infinity stays one. The sign is that of x, zeros included.
+__device__ __forceinline__ float quotient(float x, float step, float inv) {
+  const float q0 = __fmul_rn(x, inv);
+  const float q = __fmaf_rn(__fmaf_rn(-q0, step, x), inv, q0);
+  return copysignf(fabsf(q0) < 8.0f ? q : q0, x);
+}
+
 struct Fp4Rows {
   int64_t num_groups;  // tokens * num_kv_heads * groups of a row
   int64_t num_slots;
@@ -65,7 +87,47 @@ __device__ __forceinline__ void fp4_place(const Fp4Rows& r, int64_t slot, int h,
   scale = tile + int64_t(BS) * r.groups * 8 + off * r.groups + c;
 }
 
-// One thread per group; blockIdx.y = 0 writes K, 1 writes V.
+// 16 bf16 values quantised with the head's scale: their codes and group scale.
+__device__ __forceinline__ uint2 quantise_group(const uint4& lo, const uint4& hi, float s,
+                                                uint8_t& sf) {
+  float x[16];
+  {
+    float a[8], b[8];
+    dev::unpack8(lo, a);
+    dev::unpack8(hi, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = a[i];
+      x[i + 8] = b[i];
+    }
+  }
+  // the largest magnitude, two elements at a time; a NaN stays one
+  const float amax = group_max(lo, hi);
+  const bool nan = amax != amax;
+  sf = nan ? 0x7F : dev::to_e4m3(__fdiv_rn(amax, __fmul_rn(6.0f, s)));
+  uint2 codes;
+  if (sf == 0 || nan) {
+    // no step to divide by: zeros that keep their sign
+    codes.x = codes.y = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      codes.x |= (__float_as_uint(x[i]) >> 31) << (4 * i + 3);
+      codes.y |= (__float_as_uint(x[i + 8]) >> 31) << (4 * i + 3);
+    }
+  } else {
+    const float step = __fmul_rn(dev::from_e4m3(sf), s);
+    const float inv = __frcp_rn(step);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = quotient(x[i], step, inv);
+    codes.x = to_e2m1x8(x);
+    codes.y = to_e2m1x8(x + 8);
+  }
+  return codes;
+}
+
+// One thread per group, of K and of V: their loads are in flight together
+// (7 k tokens of 8 heads, dim 128: 11.8 us, 3.6 TB/s; one thread for each
+// 13.4 us).
 __global__ void __launch_bounds__(256)
     reshape_and_cache_fp4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                                  uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
@@ -75,17 +137,16 @@ __global__ void __launch_bounds__(256)
   dev::griddep_launch_dependents();
   const int64_t idx = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= r.num_groups) return;
-  const bool is_v = blockIdx.y != 0;
   const int c = int(idx % r.groups);
   const int64_t row = idx / r.groups;  // t * num_kv_heads + h
   const int h = int(row % r.num_kv_heads);
   const int64_t t = row / r.num_kv_heads;
   const int64_t slot = slot_mapping[t];
-  const uint4* src = (is_v ? v_new : k_new) + idx * 2;
-  const uint4 lo = src[0], hi = src[1];
-  const float s = (is_v ? v_scale : k_scale)[h];
+  const uint4 k0 = k_new[idx * 2], k1 = k_new[idx * 2 + 1];
+  const uint4 v0 = v_new[idx * 2], v1 = v_new[idx * 2 + 1];
+  const float ks = k_scale[h], vs = v_scale[h];
   if (slot < 0) return;  // padding token: no write
-  const bool report = h == 0 && c == 0 && !is_v;
+  const bool report = h == 0 && c == 0;
   if (slot >= r.num_slots) {
     if (report) atomicOr(&g_fp4_errors, PA_DEVERR_SLOT);
     return;
@@ -104,52 +165,37 @@ __global__ void __launch_bounds__(256)
       return;
     }
   }
-  float x[16];
-  {
-    float a[8], b[8];
-    dev::unpack8(lo, a);
-    dev::unpack8(hi, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = a[i];
-      x[i + 8] = b[i];
-    }
-  }
-  float amax = 0.0f;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    amax = fmaxf(amax, fabsf(x[i]));
-    nan |= x[i] != x[i];
-  }
-  uint8_t sf = dev::to_e4m3(__fdiv_rn(amax, __fmul_rn(6.0f, s)));
-  if (nan) sf = 0x7F;
-  uint2 codes;
-  if (sf == 0 || nan) {
-    // no step to divide by: zeros that keep their sign
-    codes.x = codes.y = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      codes.x |= (__float_as_uint(x[i]) >> 31) << (4 * i + 3);
-      codes.y |= (__float_as_uint(x[i + 8]) >> 31) << (4 * i + 3);
-    }
-  } else {
-    const float step = __fmul_rn(dev::from_e4m3(sf), s);
-    const float inv = __frcp_rn(step);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = dev::div_rn_by(x[i], step, inv);
-    codes.x = to_e2m1x8(x);
-    codes.y = to_e2m1x8(x + 8);
-  }
-  uint8_t* cache = is_v ? v_cache : k_cache;
   int64_t at, at_scale;
   fp4_place(r, slot, h, c, at, at_scale);
-  *reinterpret_cast<uint2*>(cache + at) = codes;
-  cache[at_scale] = sf;
+  uint8_t sf;
+  *reinterpret_cast<uint2*>(k_cache + at) = quantise_group(k0, k1, ks, sf);
+  k_cache[at_scale] = sf;
+  *reinterpret_cast<uint2*>(v_cache + at) = quantise_group(v0, v1, vs, sf);
+  v_cache[at_scale] = sf;
 }
 
-// One thread per group of a row read back: value = fl(code * group scale *
-// scale[h]), rounded to bf16. The product of code and group scale is exact.
+// Codes of 16 elements to bf16: fl(code * group scale * scale[h]) rounded to
+// bf16. The product of code and group scale is exact.
+__device__ __forceinline__ void read_group(const uint2& codes, float sf, float s, uint4* dst) {
+  uint32_t out[8];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t p[4];
+    dev::e2m1x8_to_f16(half ? codes.y : codes.x, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x * sf, s), __fmul_rn(f.y * sf, s));
+      out[half * 4 + i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+// One thread per group of a row read back; blockIdx.y = 0 reads K, 1 reads V.
+// (A thread for both, as in the write, took 10.3 us on 7 k tokens of 8 heads
+// where this takes 9.2: here the stores are what is wide.)
 __global__ void __launch_bounds__(256)
     gather_fp4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                       uint4* __restrict__ k_out, uint4* __restrict__ v_out,
@@ -173,21 +219,7 @@ __global__ void __launch_bounds__(256)
   int64_t at, at_scale;
   fp4_place(r, slot, h, c, at, at_scale);
   const uint2 codes = *reinterpret_cast<const uint2*>(cache + at);
-  const float sf = dev::from_e4m3(cache[at_scale]);
-  uint32_t out[8];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t p[4];
-    dev::e2m1x8_to_f16(half ? codes.y : codes.x, p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x * sf, s), __fmul_rn(f.y * sf, s));
-      out[half * 4 + i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-  }
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  read_group(codes, dev::from_e4m3(cache[at_scale]), s, dst);
 }
 
 Fp4Rows fp4_rows(int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
@@ -211,7 +243,7 @@ int launch_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_c
   const Fp4Rows r = fp4_rows(num_tokens, num_kv_heads, head_dim, block_size, num_blocks);
   if (r.num_groups == 0) return int(cudaSuccess);
   const int threads = 256;
-  const dim3 grid(unsigned((r.num_groups + threads - 1) / threads), 2);
+  const unsigned grid = unsigned((r.num_groups + threads - 1) / threads);
   reshape_and_cache_fp4_kernel<<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(
       static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
       static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), slot_mapping, k_scale,
