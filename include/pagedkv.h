@@ -230,7 +230,8 @@ typedef struct {
  * num_kv_heads * (max_context_len / 32 + 9) < 2^31 (else PA_ERR_UNSUPPORTED;
  * max_context_len no more than the table holds). The codes are multiplied exactly; the
  * softmax weights are rounded to f16. With several new tokens, up to 8 / G of
- * them share each load of the keys. */
+ * them share each load of the keys. overlap_prologue and wait_timeout_us are
+ * accepted and not used (the kernel waits on no barrier of its own). */
 #define PA_KV_FP4_E2M1 2
 
 #define PA_DECODE_TENSOR_CORE 0 /* tcgen05 MMAs, TMEM accumulators, tensor-map TMA ring */
@@ -450,7 +451,8 @@ pa_status pa_copy_blocks_fp8(void* k_cache, void* v_cache, const int32_t* pairs,
  * 16 elements read back as NaN. k_scale, v_scale: device float [num_kv_heads],
  * each in [2^-60, 2^60] (others: unspecified codes). head_dim 64 or 128;
  * block_size 8, 16 or 32. Otherwise as pa_reshape_and_cache (negative slots
- * skipped, out-of-range slots set PA_DEVERR_SLOT).
+ * skipped, out-of-range slots set PA_DEVERR_SLOT; two tokens with the same slot
+ * race, and may leave codes of one with scales of the other).
  * ---------------------------------------------------------------------- */
 pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_cache,
                                    void* v_cache, const int64_t* slot_mapping,

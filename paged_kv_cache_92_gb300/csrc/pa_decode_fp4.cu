@@ -328,6 +328,14 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
     dev::query_load<PA_KV_FP4_E2M1, D>(P.q + q_row(p, min(g, n_cols - 1)) * D, g < n_cols, t, raw);
     issue(p, 0, n_my, window, 0);
     inv_scaling = dev::query_fragment<PA_KV_FP4_E2M1, D>(raw, qf);
+    // a negative scale turns the queries, so that a larger product stays a larger score
+    const uint32_t sign = k_scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      qf[s][0] ^= sign;
+      qf[s][1] ^= sign;
+    }
+    k_scale = fabsf(k_scale);
   };
   auto share_queries = [&]() {  // every warp has them; each writes a part
 #pragma unroll
@@ -356,6 +364,9 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     factor[c] = __shfl_sync(0xffffffffu, row_factor, 4 * (2 * t + c));
+    // A scale of zero makes all scores equal, but 0 * -inf is NaN: below 2^-100 the
+    // products (under 2^35) count as zero either way. The comparison keeps a NaN scale.
+    factor[c] = factor[c] < 0x1p-100f ? 0x1p-100f : factor[c];
     see[c] = min(see_last, see0 + ((2 * t + c) >> P.g_log2));
   }
 
