@@ -235,6 +235,8 @@ def _dev_ptr(t, dtype, name: str) -> int:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must live on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()

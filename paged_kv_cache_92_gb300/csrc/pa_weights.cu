@@ -274,7 +274,7 @@ constexpr int SUM_THREADS = 256;
 constexpr int SUM_GROUPS = 4;   // threads that share a token's rows
 constexpr int SUM_TOKENS = SUM_THREADS / SUM_GROUPS * 4;  // of a CTA, four a thread
 constexpr int SUM_ROWS = 256;   // rows whose (max, 1/sum) are joined at a time
-constexpr int SUM_LANES = 8;    // lanes that join one row's partitions
+constexpr int SUM_LANES = 4;    // lanes that join one row's partitions
 static_assert(SUM_TOKENS == SUM_THREADS, "the last step takes one token a thread");
 
 // grid (tokens / SUM_TOKENS, sequence). Every block joins the partitions of the

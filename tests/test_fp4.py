@@ -614,7 +614,84 @@ def test_decode_on_a_stream_and_in_a_graph(pk):
 
 
 @pytest.mark.gpu
-def test_bounded_wait_is_not_needed_for_an_empty_batch(pk):
+def test_decode_negative_and_zero_scales(pk):
+    """A head scale is a factor like any other: its sign turns the scores, zero makes them equal."""
+    c = Case([300, 47, 17], 8, 4, seed=16)
+    c.ks *= np.array([1, -1, 0, -40], np.float32)
+    c.vs *= np.array([-1, 1, 0, 1], np.float32)
+    args, sc = c.cuda()
+    _check(pk, pk.pa_decode(*args, **sc), c)
+    args, sc = c.cuda_cut()
+    _check(pk, pk.pa_decode(*args, **sc), c)
+
+
+@pytest.mark.gpu
+def test_tensors_of_another_device_are_refused(pk, monkeypatch):
+    import torch
+
+    c = Case([40], 8, 2, seed=20)
+    args, sc = c.cuda()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)  # as under torch.cuda.device(1)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        pk.pa_decode(*args, **sc)
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(pk):
+    """Two batches on two streams, each with its workspace."""
+    import torch
+
+    cases = [Case([3000, 700, 40], 8, 2, seed=17), Case([2500, 1, 1200, 90], 8, 2, seed=18)]
+    calls = [c.cuda() for c in cases]
+    want = [pk.pa_decode(*a, **sc) for a, sc in calls]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [torch.empty_like(w) for w in want]
+    spaces = [torch.empty(8 << 20, dtype=torch.uint8, device="cuda") for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (a, sc), s, o, ws in zip(calls, streams, outs, spaces):
+            pk.pa_decode(*a, out=o, workspace=ws, stream=s, **sc)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits(pk):
+    """A cache of more than 2^32 bytes: rows in its last blocks decode, copy, read back and
+    weigh as the same rows in a small one."""
+    import torch
+
+    c = Case([200, 77], 8, 2, seed=19)
+    args, sc = c.cuda()
+    shift = (1 << 32) // (2 * _tile(16, 128)) + 1000     # blocks before the small cache's copy
+    big = [torch.zeros(pk.fp4_cache_shape(shift + c.NB, 2, 16, 128), dtype=torch.uint8,
+                       device="cuda") for _ in range(2)]
+    for b, small in zip(big, args[1:3]):
+        b[shift:] = small
+    tab = torch.where(args[3] >= 0, args[3] + shift, args[3])
+    far = (args[0], big[0], big[1], tab, *args[4:])
+    assert torch.equal(pk.pa_decode(*far, **sc), pk.pa_decode(*args, **sc))
+    w = [torch.zeros(2, 200, device="cuda") for _ in range(2)]
+    for a, x in ((far, w[0]), (args, w[1])):
+        pk.pa_token_weights(a[0], a[1], a[3], a[4], 200, x, k_scale=sc["k_scale"])
+    assert torch.equal(*w)
+    slots = torch.arange(c.NB * 16, device="cuda")
+    for x, y in zip(pk.pa_gather_fp4(*big, slots + shift * 16, **sc),
+                    pk.pa_gather_fp4(args[1], args[2], slots, **sc)):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    keep, n = pk.pa_evict_select(w[0], args[4], 50, 3)
+    for a in (far, args):
+        pk.pa_evict_compact(a[1], a[2], a[3], a[3], keep, n)
+    pair = torch.tensor([[int(args[3][0, 0]), c.NB - 1]], dtype=torch.int32, device="cuda")
+    pk.pa_copy_blocks_fp4(big[0], big[1], pair + shift)
+    pk.pa_copy_blocks_fp4(args[1], args[2], pair)
+    for b, small in zip(big, args[1:3]):
+        assert torch.equal(b[shift:], small) and not b[:64].any()
+    assert pk.pa_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_empty_batch(pk):
     import torch
 
     c = Case([16], 8, 2, seed=15)
