@@ -7,7 +7,10 @@ been built, every call raises.
 
 Names follow the C ABI: ``pa_decode``, ``pa_decode_workspace_size``,
 ``pa_reshape_and_cache``, ``pa_copy_blocks``, ``pa_device_errors`` and the
-``pa_pool_*`` / ``pa_seq_*`` block-pool calls (wrapped by ``Pool``).
+``pa_pool_*`` / ``pa_seq_*`` block-pool calls (wrapped by ``Pool``). The cache
+calls have forms for the 8-bit (``_fp8``) and the 4-bit (``_fp4``) cache;
+``pa_token_weights``, ``pa_evict_select``, ``pa_evict_compact`` and
+``Pool.compact`` evict tokens.
 """
 from __future__ import annotations
 
@@ -253,6 +256,20 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream or None
 
 
+def _empty(stream, like, shape, dtype):
+    """Uninitialised memory for a call on ``stream``, from that stream's pool of the
+    caching allocator: what lies there then neither waits for other streams' work
+    nor, once dropped, is handed to them while the call still runs."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def kv_cache_format(k_cache) -> Tuple[int, int]:
     """(kv_dtype, head_dim) of a K cache tensor: bf16 [NB][Hkv][BS][D]; uint8
     [NB][Hkv][BS][D] for the 8-bit cache, [NB][Hkv][BS][D * 9 / 16] for the
@@ -342,14 +359,14 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, max_context_len: 
 
     lib = load()
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q, q.shape, q.dtype)
     p = make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
                            max_context_len, scale, partition_tokens, variant, overlap_prologue,
                            k_scale, v_scale, wait_timeout_us)
     if workspace is None:
         need = int(lib.pa_decode_workspace_size(ctypes.byref(p)))
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _empty(stream, q, need, torch.uint8)
     ws_ptr = _dev_ptr(workspace, torch.uint8, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() if workspace is not None else 0
     _check(lib.pa_decode(ctypes.byref(p), ws_ptr, ws_bytes, _stream_handle(stream)), "pa_decode")
@@ -392,14 +409,14 @@ def pa_append_decode(q, k_cache, v_cache, block_tables, context_lens, max_contex
 
     lib = load()
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q, q.shape, q.dtype)
     p = make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
                            max_context_len, scale, partition_tokens, variant, overlap_prologue,
                            k_scale, v_scale)
     a = make_append_params(k_new, v_new, slot_mapping, k_cache, v_cache)
     need = int(lib.pa_decode_workspace_size(ctypes.byref(p)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, q, need, torch.uint8)
     ws_ptr = _dev_ptr(workspace, torch.uint8, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() if workspace is not None else 0
     _check(lib.pa_append_decode(ctypes.byref(p), ctypes.byref(a), ws_ptr, ws_bytes,
@@ -430,6 +447,8 @@ def make_step_host_params(k_cache, v_cache, num_seqs: int, num_q_heads: int,
     if fmt != KV_BF16:
         if k_scale is None or v_scale is None:
             raise ValueError("the 8-bit and 4-bit caches need k_scale and v_scale")
+        if fmt == KV_FP4_E2M1 and (k_scale.numel() != Hkv or v_scale.numel() != Hkv):
+            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
         p.kv_dtype = fmt
         p.k_scale = _dev_ptr(k_scale, torch.float32, "k_scale")
         p.v_scale = _dev_ptr(v_scale, torch.float32, "v_scale")
@@ -504,11 +523,9 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_conte
     library; larger needs are rejected. ``out`` must be given by such callers;
     when omitted it is allocated here for convenience. Calls that overlap on
     the GPU share that array and race."""
-    import torch
-
     lib = load()
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q, q.shape, q.dtype)
     p = make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
                            max_context_len, scale, partition_tokens, variant, k_scale=k_scale,
                            v_scale=v_scale)
@@ -628,9 +645,9 @@ def pa_gather_fp4(k_cache, v_cache, slot_mapping, k_scale, v_scale, k_out=None, 
         raise ValueError("pa_gather_fp4 reads a 4-bit cache")
     shape = (slot_mapping.shape[0], k_cache.shape[1], D)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        k_out = _empty(stream, k_cache, shape, torch.bfloat16)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        v_out = _empty(stream, k_cache, shape, torch.bfloat16)
     dims = _check_fp4_rows(k_out, v_out, k_cache, v_cache, slot_mapping, k_scale, v_scale,
                            "pa_gather_fp4")
     lib = load()
@@ -717,7 +734,7 @@ def pa_token_weights(q, k_cache, block_tables, context_lens, max_context_len: in
                                   token_weights, accumulate, scale, k_scale)
     if workspace is None:
         need = int(lib.pa_token_weights_workspace_size(ctypes.byref(p)))
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, q, max(need, 256), torch.uint8)
     _check(lib.pa_token_weights(ctypes.byref(p), _dev_ptr(workspace, torch.uint8, "workspace"),
                                 workspace.numel(), _stream_handle(stream)), "pa_token_weights")
     return token_weights
@@ -734,9 +751,9 @@ def pa_evict_select(token_weights, context_lens, budget: int, recent: int = 0, k
         raise ValueError("token_weights must be [num_seqs][stride], context_lens [num_seqs]")
     B = token_weights.shape[0]
     if keep is None:
-        keep = torch.empty((B, max(int(budget), 0)), dtype=torch.int32, device=token_weights.device)
+        keep = _empty(stream, token_weights, (B, max(int(budget), 0)), torch.int32)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=token_weights.device)
+        new_lens = _empty(stream, token_weights, B, torch.int32)
     if keep.shape != (B, budget) or new_lens.shape != (B,):
         raise ValueError("keep must be [num_seqs][budget], new_lens [num_seqs]")
     _check(load().pa_evict_select(
