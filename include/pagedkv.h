@@ -513,7 +513,8 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int
  * and so is the whole row of a sequence of length 0 or with fewer keys than
  * new tokens (the latter sets PA_DEVERR_CONTEXT_LEN). Reads K only, of any of
  * the three caches, at every block size. num_seqs * ceil(query_len / (16 / G))
- * <= 65535 (else PA_ERR_UNSUPPORTED).
+ * <= 65535 (else PA_ERR_UNSUPPORTED); table rows hold up to 2^30 tokens, here
+ * and below.
  * ---------------------------------------------------------------------- */
 typedef struct {
   const void* q;               /* bf16 [num_seqs][query_len][num_q_heads][head_dim] */
@@ -555,7 +556,8 @@ pa_status pa_token_weights(const pa_token_weights_params* p, void* workspace,
  *   new_lens  int32 [num_seqs]: min(context_lens[b], budget)
  * token_weights: float [num_seqs][weights_stride]; a length beyond
  * weights_stride is cut to it and sets PA_DEVERR_CONTEXT_LEN. num_seqs up to
- * 65535, budget >= 1, recent in [0, budget]. No workspace.
+ * 65535, weights_stride and budget in [1, 2^30], recent in [0, budget]. No
+ * workspace.
  * ---------------------------------------------------------------------- */
 pa_status pa_evict_select(const float* token_weights, const int32_t* context_lens, int32_t* keep,
                           int32_t* new_lens, int32_t num_seqs, int32_t weights_stride,

@@ -3,6 +3,7 @@
 // Every check here runs before anything is launched.
 #include <cuda_runtime_api.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -792,6 +793,9 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int
 
 // ---- token weights and eviction
 
+// Longest sequence that the weights and the eviction take.
+constexpr int64_t kMaxEvictTokens = int64_t(1) << 30;
+
 static pa_status check_token_weights(const pa_token_weights_params* p, bool need_pointers) {
   if (!p) return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: params is NULL");
   const int q = p->query_len > 1 ? p->query_len : 1;
@@ -823,9 +827,13 @@ static pa_status check_token_weights(const pa_token_weights_params* p, bool need
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_token_weights: num_blocks, max_blocks_per_seq and max_context_len "
                          "must be positive");
-  if (int64_t(p->max_blocks_per_seq) * p->block_size > INT32_MAX - 64)
-    return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: max_blocks_per_seq too large");
-  if (!(p->scale > 0.0f))
+  // token indices stay within 32 bits beyond any tile's end, the workspace within 64
+  if (int64_t(p->max_blocks_per_seq) * p->block_size > kMaxEvictTokens)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_token_weights: table rows of more than 2^30 tokens");
+  if (int64_t(p->num_seqs) * q * p->num_q_heads > INT32_MAX)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: query rows exceed 2^31");
+  if (!(p->scale > 0.0f) || std::isinf(p->scale))
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_token_weights: scale must be a positive finite number");
   const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
@@ -896,6 +904,9 @@ pa_status pa_evict_select(const float* token_weights, const int32_t* context_len
   if (num_seqs < 0 || num_seqs > 65535 || weights_stride < 1)
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_evict_select: num_seqs in [0, 65535] and weights_stride >= 1");
+  if (weights_stride > kMaxEvictTokens || budget > kMaxEvictTokens)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_evict_select: weights_stride and budget at most 2^30");
   if (budget < 1 || recent < 0 || recent > budget)
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_evict_select: budget >= 1 and recent in [0, budget]");
@@ -926,9 +937,10 @@ pa_status pa_evict_compact(const pa_evict_compact_params* p, pa_stream_t stream)
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_evict_compact: kv_dtype must be PA_KV_BF16, PA_KV_FP8_E4M3 or "
                          "PA_KV_FP4_E2M1");
-  if (int64_t(p->max_blocks_per_seq) * p->block_size > INT32_MAX ||
-      int64_t(p->max_dst_blocks_per_seq) * p->block_size > INT32_MAX)
-    return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: table rows too long");
+  if (int64_t(p->max_blocks_per_seq) * p->block_size > kMaxEvictTokens ||
+      int64_t(p->max_dst_blocks_per_seq) * p->block_size > kMaxEvictTokens)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_evict_compact: table rows of more than 2^30 tokens");
   if (p->token_weights && p->weights_stride < 1)
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: weights_stride must be positive");
   if (p->num_seqs == 0) return PA_OK;

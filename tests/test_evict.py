@@ -110,6 +110,35 @@ def test_token_weights_refusals(pk, kw, status):
     assert lib.pa_token_weights(None, None, 0, None) == 1
 
 
+@pytest.mark.parametrize("kw", [
+    dict(max_blocks_per_seq=1 << 26, block_size=32), dict(scale=float("inf")),
+    dict(num_seqs=32768, query_len=2, num_q_heads=32768, num_kv_heads=32768)])  # 2^31 rows
+def test_token_weights_sizes_beyond_the_index_range(pk, kw):
+    p = _tw(pk, **kw)
+    assert pk.load().pa_token_weights(ctypes.byref(p), None, 0, None) == 1
+    assert pk.load().pa_token_weights_workspace_size(ctypes.byref(p)) == 0
+
+
+@pytest.mark.parametrize("stride,budget", [((1 << 30) + 1, 8), (64, (1 << 30) + 1),
+                                           (2**31 - 1, 2**31 - 1)])
+def test_select_sizes_beyond_the_index_range(pk, stride, budget):
+    lib = pk.load()
+    assert lib.pa_evict_select(256, 256, 256, 256, 1, stride, budget, 0, None) == 1
+    assert b"2^30" in lib.pa_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(max_blocks_per_seq=1 << 26), dict(max_dst_blocks_per_seq=1 << 26)])
+def test_compact_sizes_beyond_the_index_range(pk, kw):
+    p = pk.EvictCompactParams()
+    base = dict(num_seqs=1, num_kv_heads=1, num_blocks=1, max_blocks_per_seq=1,
+                max_dst_blocks_per_seq=1, keep_stride=1, head_dim=64, block_size=32)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(p, k, v)
+    lib = pk.load()
+    assert lib.pa_evict_compact(ctypes.byref(p), None) == 1 and b"2^30" in lib.pa_last_error()
+
+
 def test_token_weights_workspace(pk):
     """The header, a (max, sum) per row and partition, and every score."""
     p = _tw(pk, query_len=3)
@@ -676,3 +705,39 @@ def test_captured_and_on_another_stream(pk):
     step()
     want = state()
     assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(want, got))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_call_allocates_on_its_own_stream(pk, handle):
+    """Memory that a call on another stream borrows is not handed to the current one
+    while the call still waits there, and the result does not come from memory that
+    the current stream still writes."""
+    import torch
+
+    B, L, Hq, Hkv, D, BS = 2, 4000, 8, 2, 128, 16
+    torch.manual_seed(3)
+    nb = -(-L // BS)
+    q = torch.randn(B, Hq, D, device="cuda").bfloat16()
+    kc, vc = (torch.randn(B * nb, Hkv, BS, D, device="cuda").bfloat16() for _ in range(2))
+    tab = torch.arange(B * nb, dtype=torch.int32, device="cuda").reshape(B, nb)
+    lens = torch.tensor([L, 1234], dtype=torch.int32, device="cuda")
+    w = torch.zeros(B, L, device="cuda")
+    pk.pa_token_weights(q, kc, tab, lens, L, w)
+    out = pk.pa_decode(q, kc, vc, tab, lens, L)
+    keep, n = pk.pa_evict_select(w, lens, 300, 20)
+    side = torch.cuda.Stream()
+    on = side.cuda_stream if handle else side
+    w2 = torch.zeros_like(w)
+    size = pk.pa_token_weights_workspace_size(q, kc, tab, lens, L, w)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)           # some 10 ms
+    pk.pa_token_weights(q, kc, tab, lens, L, w2, stream=on)
+    out2 = pk.pa_decode(q, kc, vc, tab, lens, L, stream=on)
+    keep2, n2 = pk.pa_evict_select(w2, lens, 300, 20, stream=on)
+    mine = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in (size, size // 2, 4096, 512)]
+    torch.cuda.synchronize()
+    assert not any(m.any() for m in mine)
+    assert torch.equal(w, w2) and torch.equal(out, out2)
+    assert torch.equal(keep, keep2) and torch.equal(n, n2)
