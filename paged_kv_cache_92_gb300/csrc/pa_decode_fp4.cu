@@ -591,8 +591,9 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
             make_float4(sum.x * norm, sum.y * norm, sum.z * norm, sum.w * norm);
     }
     if (!direct && on && d == 0)
+      // (where every score is NaN there is no maximum, but the NaN has to reach the merge)
       *reinterpret_cast<float2*>(P.part_ml + (int64_t(slot) * C::COLS + n) * 2) =
-          make_float2(M, den);
+          make_float2(den != den ? 0.0f : M, den);
   }
   __syncwarp();
   __syncthreads();  // before the next piece's copies

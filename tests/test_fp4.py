@@ -637,6 +637,21 @@ def test_tensors_of_another_device_are_refused(pk, monkeypatch):
 
 
 @pytest.mark.gpu
+def test_decode_nan_keys_of_a_whole_piece(pk):
+    """NaN scales in all of a long run of K rows: their head's outputs are NaN, however the
+    run falls to the CTAs, and the others' are not."""
+    import torch
+
+    c = Case([6000, 6000], 8, 2, seed=21)
+    args, sc = c.cuda()
+    k = args[1].view(c.NB, 2, -1)
+    k[args[3][0, :300].long(), 1, 16 * 64:] = 0x7F      # keys 0 to 4799 of sequence 0, KV head 1
+    out = pk.pa_decode(*args, **sc).float()
+    assert out[0, 4:].isnan().all()
+    assert out[0, :4].isfinite().all() and out[1].isfinite().all()
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once(pk):
     """Two batches on two streams, each with its workspace."""
     import torch
