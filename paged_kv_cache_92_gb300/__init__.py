@@ -232,17 +232,19 @@ def _check(status: int, where: str) -> None:
 def _dev_ptr(t, dtype, name: str) -> int:
     import torch
 
+    # one condition for the tensor that passes (get_device() is -1 on the CPU)
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() \
+            and t.get_device() == torch._C._cuda_getDevice():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} must live on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must live on the current CUDA device")
 
 
 def _stream_handle(stream) -> Optional[int]:
@@ -250,7 +252,7 @@ def _stream_handle(stream) -> Optional[int]:
         import torch
 
         # the handle alone: a Stream object costs a call several microseconds
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
