@@ -837,7 +837,11 @@ static pa_status check_token_weights(const pa_token_weights_params* p, bool need
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_token_weights: scale must be a positive finite number");
   const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
-  if (p->weights_stride < (p->max_context_len < table ? p->max_context_len : table))
+  const int64_t cap = p->max_context_len < table ? p->max_context_len : table;
+  // 1 TB of scores; below it both launches' grids fit 31 bits
+  if (int64_t(p->num_seqs) * q * p->num_q_heads * cap > (int64_t(1) << 38))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_token_weights: more than 2^38 scores");
+  if (p->weights_stride < cap)
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_token_weights: weights_stride must cover min(max_context_len, "
                          "max_blocks_per_seq * block_size) tokens");

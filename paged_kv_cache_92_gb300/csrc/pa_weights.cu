@@ -97,11 +97,20 @@ __global__ void __launch_bounds__(NTHREADS)
     return (int64_t(b) * P.q_len + tok_i0 + (n >> P.g_log2)) * num_q_heads + head * G +
            (n & (G - 1));
   };
+  const int tok0 = part * P.partition_tokens;
+  // the partition's table entries, on their way while the length is
+  constexpr int ENTRIES = kMaxPartitionTokens / 8 / NTHREADS;
+  int32_t entry[ENTRIES];
+#pragma unroll
+  for (int k = 0; k < ENTRIES; ++k) {
+    const int i = tid + k * NTHREADS, j = (tok0 >> P.bs_log2) + i;
+    const bool on = i < P.partition_tokens >> P.bs_log2 && j < P.max_blocks_per_seq;
+    entry[k] = on ? P.block_tables[int64_t(b) * P.max_blocks_per_seq + j] : 0;
+  }
   const int L = checked_len(P, b, tid == 0 && part == 0 && head == 0 && grp == 0);
   if (L == 0) return;
   const int see0 = L - P.q_len + tok_i0 + 1;  // keys of the group's first token
   const int see_last = see0 + n_tok - 1;
-  const int tok0 = part * P.partition_tokens;
   if (tok0 >= see_last) return;
   const int tok1 = min(see_last, tok0 + P.partition_tokens);
   const int nblk = (tok1 - tok0 + BS - 1) >> P.bs_log2;
@@ -110,15 +119,14 @@ __global__ void __launch_bounds__(NTHREADS)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NWARPS * ST * STAGE);
   float2* sm_ml = reinterpret_cast<float2*>(bars + NWARPS * ST);  // [NWARPS][COLS]
   int32_t* table = reinterpret_cast<int32_t*>(sm_ml + NWARPS * COLS);
-  const int32_t* trow =
-      P.block_tables + int64_t(b) * P.max_blocks_per_seq + (tok0 >> P.bs_log2);
-  for (int i = tid; i < nblk; i += NTHREADS) {
-    int32_t e = trow[i];
-    if (e < 0 || e >= P.num_blocks) {
-      atomicOr(&g_weights_errors, PA_DEVERR_TABLE_ENTRY);
-      e = 0;
+#pragma unroll
+  for (int k = 0; k < ENTRIES; ++k) {
+    const int i = tid + k * NTHREADS;
+    if (i < nblk) {
+      const bool bad = entry[k] < 0 || entry[k] >= P.num_blocks;
+      if (bad) atomicOr(&g_weights_errors, PA_DEVERR_TABLE_ENTRY);
+      table[i] = bad ? 0 : entry[k];
     }
-    table[i] = e;
   }
   uint64_t* my_bars = bars + warp * ST;
   unsigned char* ring = smem + warp * ST * STAGE;

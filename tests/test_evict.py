@@ -112,6 +112,7 @@ def test_token_weights_refusals(pk, kw, status):
 
 @pytest.mark.parametrize("kw", [
     dict(max_blocks_per_seq=1 << 26, block_size=32), dict(scale=float("inf")),
+    dict(num_seqs=512, max_blocks_per_seq=1 << 25, max_context_len=1 << 27, weights_stride=1 << 27),
     dict(num_seqs=32768, query_len=2, num_q_heads=32768, num_kv_heads=32768)])  # 2^31 rows
 def test_token_weights_sizes_beyond_the_index_range(pk, kw):
     p = _tw(pk, **kw)
