@@ -229,14 +229,27 @@ def _check(status: int, where: str) -> None:
 # device calls (torch tensors in, marshalled to raw pointers)
 # --------------------------------------------------------------------------
 
-def _dev_ptr(t, dtype, name: str) -> int:
+# torch's tensor class and its calls for the current device, looked up once: the
+# checks below run for every tensor of every call, and a step is a few microseconds
+_Tensor = _device = _raw_stream = None
+
+
+def _bind_torch() -> None:
+    global _Tensor, _device, _raw_stream
     import torch
 
+    _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _Tensor = torch.Tensor
+
+
+def _dev_ptr(t, dtype, name: str) -> int:
+    if _Tensor is None:
+        _bind_torch()
     # one condition for the tensor that passes (get_device() is -1 on the CPU)
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() \
-            and t.get_device() == torch._C._cuda_getDevice():
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous() \
+            and t.get_device() == _device():
         return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -249,10 +262,10 @@ def _dev_ptr(t, dtype, name: str) -> int:
 
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        import torch
-
+        if _Tensor is None:
+            _bind_torch()
         # the handle alone: a Stream object costs a call several microseconds
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
+        return _raw_stream(_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
   using C = Cfg<D, BS>;
   constexpr int ST = C::ST, NBK = C::NBK, TILE = C::TILE, WINDOW = C::WINDOW;
   constexpr int VW = D / 64;  // code words of a lane's share of a V row (D / 8 elements)
-  dev::griddep_launch_dependents();  // the merge may be dispatched as CTAs end; it waits for all
+  dev::griddep_enter();  // the merge may be dispatched as CTAs end; it waits for all
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = 1 << P.g_log2;
@@ -624,7 +624,9 @@ __global__ void __launch_bounds__(128) merge_fp4_kernel(const Fp4Decode P, int g
   const int v = int(item / P.num_kv_heads), head = int(item - int64_t(v) * P.num_kv_heads);
   if (v >= P.num_virtual) return;
   const Virtual x = virtual_of(P, v);
-  dev::griddep_wait();  // the plan and the partials
+  // The plan and the partials. (No early dispatch of what follows: its CTAs would
+  // find the SMs unevenly taken; the next decode of a 26 us batch took 29.)
+  dev::griddep_wait();
   if (x.steps == 0 || n >= (x.n_tok << P.g_log2)) return;
   const int T = P.plan[P.num_virtual];
   const int base = P.plan[v] + head * item_cost(x) + START_COST;
@@ -693,20 +695,12 @@ int launch_t(const Fp4Decode& P, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return int(e);
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  paged_decode_fp4_kernel<D, BS><<<unsigned(grid), NTHREADS, C::SMEM, stream>>>(P);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || P.whole) return int(e);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
+  const int err = launch_ordered(paged_decode_fp4_kernel<D, BS>, dim3(unsigned(grid)), NTHREADS,
+                                 C::SMEM, stream, 1, P);
+  if (err || P.whole) return err;
   const int64_t rows = int64_t(P.num_virtual) * P.num_kv_heads * C::COLS;
-  cfg.gridDim = dim3(unsigned((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return int(cudaLaunchKernelEx(&cfg, merge_fp4_kernel<D>, P, grid));
+  return launch_ordered(merge_fp4_kernel<D>, dim3(unsigned((rows + 3) / 4)), 128, 0, stream, 1, P,
+                        grid);
 }
 
 template <int D>

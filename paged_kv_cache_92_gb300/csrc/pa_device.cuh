@@ -162,6 +162,13 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Start of a kernel launched by launch_ordered: plain stream order, and the next
+// kernel may be dispatched from here on. The wait comes first, so that what was
+// complete before this kernel is also complete before a dependent's own prologue.
+__device__ __forceinline__ void griddep_enter() {
+  griddep_wait();
+  griddep_launch_dependents();
+}
 
 // L2 policy for data that is streamed once (K/V tiles).
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
@@ -480,4 +487,29 @@ __device__ __forceinline__ void fence_async_global() {
 }
 
 }  // namespace dev
+
+// Launch of a kernel whose every CTA waits for the preceding kernel
+// (griddep_wait, griddep_enter) before it touches memory: its CTAs are
+// dispatched while that kernel's last ones still run, which hides the launch
+// (about 1.5 us in a chain of small kernels). `cluster`: CTAs of a cluster.
+template <typename... Params, typename... Args>
+int launch_ordered(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
+                   cudaStream_t stream, unsigned cluster, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return int(cudaLaunchKernelEx(&cfg, kernel, Params(args)...));
+}
+
 }  // namespace pa

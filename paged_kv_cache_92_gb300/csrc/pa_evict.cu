@@ -251,6 +251,7 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
 // grid (CTAs of a sequence, sequence), in clusters of gridDim.x
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Select P) {
   __shared__ SelectShared sm;
+  dev::griddep_enter();
   cg::cluster_group cluster = cg::this_cluster();
   const int b = blockIdx.y, tid = threadIdx.x;
   const int first = blockIdx.x * SEL_THREADS + tid, stride = gridDim.x * SEL_THREADS;
@@ -441,6 +442,7 @@ __device__ __forceinline__ void move_columns(const Compact& P, const Plane& pl, 
 // grid (KV head, sequence, slices of every plane)
 __global__ void __launch_bounds__(MOVE_THREADS) compact_rows_kernel(const Compact P) {
   __shared__ Move list[MOVE_LIST];
+  dev::griddep_enter();
   int z = blockIdx.z, p = 0;
   while (z >= P.plane[p].slices) z -= P.plane[p++].slices;
   const Plane& pl = P.plane[p];
@@ -456,6 +458,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) compact_rows_kernel(const Compac
 // The weights of the kept tokens, moved in place; the rest of the row is zeroed.
 __global__ void __launch_bounds__(256)
     compact_weights_kernel(const Compact P, float* weights, int64_t stride) {
+  dev::griddep_enter();
   const int b = blockIdx.x;
   float* row = weights + b * stride;
   const int n = int(min(int64_t(rows_to_move(P, b, false)), stride));
@@ -483,18 +486,8 @@ int launch_evict_select(const float* token_weights, const int32_t* context_lens,
   const Select P{token_weights, context_lens, keep, new_lens, weights_stride,
                  num_seqs, budget, recent, int(weights_stride)};
   const unsigned ctas = weights_stride > SEL_LONG ? SEL_CLUSTER : 1;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, unsigned(num_seqs));
-  cfg.blockDim = dim3(SEL_THREADS);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return int(cudaLaunchKernelEx(&cfg, evict_select_kernel, P));
+  return launch_ordered(evict_select_kernel, dim3(ctas, unsigned(num_seqs)), SEL_THREADS, 0,
+                        static_cast<cudaStream_t>(stream), ctas, P);
 }
 
 int launch_evict_compact(const pa_evict_compact_params* p, void* stream) {
@@ -534,14 +527,11 @@ int launch_evict_compact(const pa_evict_compact_params* p, void* stream) {
   P.bs_log2 = log2_of(BS);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(unsigned(p->num_kv_heads), unsigned(p->num_seqs), unsigned(z));
-  compact_rows_kernel<<<grid, MOVE_THREADS, 0, s>>>(P);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && p->token_weights) {
-    compact_weights_kernel<<<unsigned(p->num_seqs), 256, 0, s>>>(P, p->token_weights,
-                                                                 p->weights_stride);
-    e = cudaGetLastError();
-  }
-  return int(e);
+  int e = launch_ordered(compact_rows_kernel, grid, MOVE_THREADS, 0, s, 1, P);
+  if (e == 0 && p->token_weights)
+    e = launch_ordered(compact_weights_kernel, dim3(unsigned(p->num_seqs)), 256, 0, s, 1, P,
+                       p->token_weights, int64_t(p->weights_stride));
+  return e;
 }
 
 int read_and_clear_evict_errors(uint32_t* flags) {

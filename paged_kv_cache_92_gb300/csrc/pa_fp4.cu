@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256)
                                  const int64_t* __restrict__ slot_mapping,
                                  const float* __restrict__ k_scale,
                                  const float* __restrict__ v_scale, Fp4Rows r, AppendCheck check) {
-  dev::griddep_launch_dependents();
+  dev::griddep_enter();
   const int64_t idx = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= r.num_groups) return;
   const int c = int(idx % r.groups);
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(256)
                       uint4* __restrict__ k_out, uint4* __restrict__ v_out,
                       const int64_t* __restrict__ slot_mapping, const float* __restrict__ k_scale,
                       const float* __restrict__ v_scale, Fp4Rows r) {
+  dev::griddep_enter();
   const int64_t idx = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= r.num_groups) return;
   const bool is_v = blockIdx.y != 0;
@@ -244,11 +245,10 @@ int launch_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_c
   if (r.num_groups == 0) return int(cudaSuccess);
   const int threads = 256;
   const unsigned grid = unsigned((r.num_groups + threads - 1) / threads);
-  reshape_and_cache_fp4_kernel<<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
-      static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), slot_mapping, k_scale,
-      v_scale, r, check);
-  return int(cudaGetLastError());
+  return launch_ordered(reshape_and_cache_fp4_kernel, dim3(grid), threads, 0,
+                        static_cast<cudaStream_t>(stream), 1, static_cast<const uint4*>(k_new),
+                        static_cast<const uint4*>(v_new), static_cast<uint8_t*>(k_cache),
+                        static_cast<uint8_t*>(v_cache), slot_mapping, k_scale, v_scale, r, check);
 }
 
 int launch_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, void* v_out,
@@ -259,10 +259,10 @@ int launch_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, voi
   if (r.num_groups == 0) return int(cudaSuccess);
   const int threads = 256;
   const dim3 grid(unsigned((r.num_groups + threads - 1) / threads), 2);
-  gather_fp4_kernel<<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
-      static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), slot_mapping, k_scale, v_scale, r);
-  return int(cudaGetLastError());
+  return launch_ordered(gather_fp4_kernel, grid, threads, 0, static_cast<cudaStream_t>(stream), 1,
+                        static_cast<const uint8_t*>(k_cache),
+                        static_cast<const uint8_t*>(v_cache), static_cast<uint4*>(k_out),
+                        static_cast<uint4*>(v_out), slot_mapping, k_scale, v_scale, r);
 }
 
 int read_and_clear_fp4_errors(uint32_t* flags) {

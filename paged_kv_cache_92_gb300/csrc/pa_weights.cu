@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(NTHREADS)
   using Row = dev::KeyRow<FMT, D>;
   constexpr int ST = Ring<FMT, D>::ST, STAGE = Ring<FMT, D>::STAGE;
   constexpr int COLS = 8 * NT;
-  dev::griddep_launch_dependents();  // the sums' blocks wait for all of this kernel
+  dev::griddep_enter();  // the sums' blocks wait for all of this kernel
   const int part = blockIdx.x, head = blockIdx.y;
   const int b = blockIdx.z / P.n_groups, grp = blockIdx.z - b * P.n_groups;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -292,7 +292,7 @@ static_assert(SUM_TOKENS == SUM_THREADS, "the last step takes one token a thread
 __global__ void __launch_bounds__(SUM_THREADS) sum_weights_kernel(const Weights P) {
   const int b = blockIdx.y, tid = threadIdx.x;
   const int L = checked_len(P, b, false);
-  dev::griddep_wait();  // the scores
+  dev::griddep_wait();  // the scores (no early dispatch of what follows, which costs it 1 us)
   const int key0 = blockIdx.x * SUM_TOKENS;
   if (key0 >= L) return;
   const int quad = tid % (SUM_THREADS / SUM_GROUPS), group = tid / (SUM_THREADS / SUM_GROUPS);
@@ -392,8 +392,7 @@ int launch_scores(const Weights& P, cudaStream_t stream) {
   }
   const dim3 grid(unsigned(P.num_partitions), unsigned(P.num_kv_heads),
                   unsigned(P.num_seqs * P.n_groups));
-  kernel<<<grid, NTHREADS, smem, stream>>>(P);
-  return int(cudaGetLastError());
+  return launch_ordered(kernel, grid, NTHREADS, smem, stream, 1, P);
 }
 
 template <int FMT>
@@ -449,16 +448,7 @@ int launch_token_weights(const pa_token_weights_params* p, const TokenWeightsSpa
   }
   if (e) return e;
   const dim3 grid(unsigned((sp.cap + SUM_TOKENS - 1) / SUM_TOKENS), unsigned(p->num_seqs));
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(SUM_THREADS);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return int(cudaLaunchKernelEx(&cfg, sum_weights_kernel, P));
+  return launch_ordered(sum_weights_kernel, grid, SUM_THREADS, 0, s, 1, P);
 }
 
 int read_and_clear_weights_errors(uint32_t* flags) {

@@ -627,11 +627,10 @@ def test_decode_negative_and_zero_scales(pk):
 
 @pytest.mark.gpu
 def test_tensors_of_another_device_are_refused(pk, monkeypatch):
-    import torch
-
     c = Case([40], 8, 2, seed=20)
     args, sc = c.cuda()
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)  # as under torch.cuda.device(1)
+    pk.pa_decode(*args, **sc)
+    monkeypatch.setattr(pk, "_device", lambda: 1)  # as under torch.cuda.device(1)
     with pytest.raises(ValueError, match="current CUDA device"):
         pk.pa_decode(*args, **sc)
 
