@@ -6,12 +6,13 @@
 // go is left open. Here the most recent ones stay, and of the others those
 // with the largest accumulated attention weight (pa_weights.cu).
 //
-//  * evict_select_kernel: one CTA per sequence, or a cluster of eight for long
-//    ones, each with an eighth of the tokens. The candidates' weights become
+//  * evict_select_kernel: one CTA per sequence, or a cluster of up to eight for
+//    long ones, each with its share of the tokens. The candidates' weights become
 //    ordered 32-bit keys in registers (up to 8 a thread; longer ranges re-read
 //    them from L2), and the threshold is found by three rounds of a
 //    shared-memory histogram over 11, 11 and 10 bits of the keys that still
-//    tie with it; the CTAs of a cluster read each other's. Four copies of the
+//    tie with it (fewer where a bin is kept whole, as one of a single key is);
+//    the CTAs of a cluster read each other's. Four copies of the
 //    histogram, by lane, keep equal weights -- most tokens of a long context
 //    have nearly none -- from serialising more than eight deep. Ties go to the
 //    lowest index through ranks, and the kept indices come out ascending.
@@ -44,8 +45,7 @@ constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_KEYS = 8;       // keys a thread holds at a time
 constexpr int SEL_BINS = 2048;
 constexpr int SEL_COPIES = 4;
-constexpr int SEL_CLUSTER = 8;    // CTAs of a long sequence
-constexpr int SEL_LONG = 4096;    // a row of weights longer than this takes a cluster
+constexpr int SEL_CLUSTER = 8;    // CTAs of a sequence, at most
 
 // Order-preserving map of a weight to an unsigned key; NaN below everything,
 // both zeros alike.
@@ -92,7 +92,7 @@ struct SelectShared {
   int bins[2][SEL_BINS];           // their sum, read by the cluster; alternates
   int cnt[SEL_KEYS * SEL_WARPS];
   int warp_tot[SEL_WARPS];
-  int bin, left;
+  int bin, left, done;
   int above, equal;                // keys of the CTAs before this one
 };
 
@@ -121,8 +121,8 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
   };
   if (spans == 1) load(0);
 
-  // the key of rank `need`, digit by digit; `left`: how many of the keys that
-  // equal it are kept (the first ones)
+  // the key of rank `need`, digit by digit, as far as it has to be known; `left`:
+  // how many of the keys that equal it in these digits are kept (the first ones)
   uint32_t prefix = 0, mask = 0;
   int left = need;
   if (tid == 0) sm.above = sm.equal = 0;
@@ -159,8 +159,8 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
         int2 x[SEL_CLUSTER];
 #pragma unroll
         for (int k = 0; k < SEL_CLUSTER; ++k)
-          x[k] = *reinterpret_cast<const int2*>(
-              cluster.map_shared_rank(mine, unsigned(min(k, ctas - 1))));
+          if (k < ctas)
+            x[k] = *reinterpret_cast<const int2*>(cluster.map_shared_rank(mine, unsigned(k)));
 #pragma unroll
         for (int k = 0; k < SEL_CLUSTER; ++k) {
           if (k < ctas) {
@@ -178,20 +178,24 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
       if (before < left && left <= upto) {
         const bool first = left <= before + n1;
         sm.bin = first ? b1 : b0;
-        sm.left = left - before - (first ? 0 : n1);
+        const int rest = left - before - (first ? 0 : n1);
+        sm.left = rest;
+        sm.done = rest == (first ? n1 : n0);  // the whole bin is kept: no need to look further
       }
       __syncthreads();
       const int bin = sm.bin;
       prefix |= uint32_t(bin) << shift;
       mask |= digits << shift;
       left = sm.left;
+      const bool done = sm.done || round == 2;
       if (ctas > 1) {
         const int above = __reduce_add_sync(0xffffffffu, (b1 > bin ? before1 : 0) +
                                                              (b0 > bin ? before0 : 0));
         if (lane == 0 && above) atomicAdd(&sm.above, above);
-        if (round == 2 && (b1 == bin || b0 == bin)) sm.equal = b1 == bin ? before1 : before0;
+        if (done && (b1 == bin || b0 == bin)) sm.equal = b1 == bin ? before1 : before0;
       }
       __syncthreads();
+      if (done) break;
     }
   }
   // of the CTAs before this one: keys that equal the threshold, keys that are kept
@@ -214,8 +218,8 @@ __device__ __forceinline__ void select_row(const Select& P, const float* w, int3
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const bool cand = token(span, e) < c1 && need > 0;
-      const bool same = cand && key[e] == prefix;
-      kept |= uint32_t(cand && key[e] > prefix) << e;
+      const bool same = cand && (key[e] & mask) == prefix;
+      kept |= uint32_t(cand && (key[e] & mask) > prefix) << e;
       eq |= uint32_t(same) << e;
       const uint32_t v = __ballot_sync(0xffffffffu, same);
       if (lane == 0) sm.cnt[e * SEL_WARPS + warp] = __popc(v);
@@ -485,7 +489,12 @@ int launch_evict_select(const float* token_weights, const int32_t* context_lens,
                         int32_t budget, int32_t recent, void* stream) {
   const Select P{token_weights, context_lens, keep, new_lens, weights_stride,
                  num_seqs, budget, recent, int(weights_stride)};
-  const unsigned ctas = weights_stride > SEL_LONG ? SEL_CLUSTER : 1;
+  // As many CTAs as hold a row's candidates in registers, by the longest row there
+  // may be (8 sequences of 8 k tokens: 10.9 us with one CTA or four; of 10 k: 17.6
+  // with one, 14.1 with four; of 32 k: 32 and 15.2, 18.0 with eight; one of 40 k:
+  // 25.6 with four, 17.6 with eight; two are no faster than four).
+  const int64_t most = weights_stride - recent, one = SEL_THREADS * SEL_KEYS;
+  const unsigned ctas = most > 4 * one ? 8 : (most > one ? 4 : 1);
   return launch_ordered(evict_select_kernel, dim3(ctas, unsigned(num_seqs)), SEL_THREADS, 0,
                         static_cast<cudaStream_t>(stream), ctas, P);
 }

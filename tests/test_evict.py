@@ -446,6 +446,21 @@ def test_select_beyond_one_span(pk, budget, recent):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("stride", [8192 + 5, 8193 + 5, 4 * 8192 + 5, 4 * 8192 + 6])
+def test_select_at_the_change_of_ctas(pk, stride):
+    """Rows of candidates that one CTA, four and eight hold: the last of each and the first."""
+    import torch
+
+    rng = np.random.default_rng(stride)
+    lens = np.array([stride, stride - 1, 2048 * 4 + 5, 2049, 700, 600, 0], np.int32)
+    w = _weights_with_ties(rng, 7, stride)
+    w[1, 1::3] = 0.5
+    want = select(w, lens, 600, 5)
+    keep, n = pk.pa_evict_select(torch.from_numpy(w).cuda(), torch.from_numpy(lens).cuda(), 600, 5)
+    assert np.array_equal(keep.cpu().numpy(), want[0]) and np.array_equal(n.cpu().numpy(), want[1])
+
+
+@pytest.mark.gpu
 def test_select_cuts_lengths_beyond_the_weights(pk):
     import torch
 
