@@ -229,27 +229,30 @@ def _check(status: int, where: str) -> None:
 # device calls (torch tensors in, marshalled to raw pointers)
 # --------------------------------------------------------------------------
 
-# torch's tensor class and its calls for the current device, looked up once: the
-# checks below run for every tensor of every call, and a step is a few microseconds
-_Tensor = _device = _raw_stream = None
+# torch's calls for the current device, looked up once: the checks below run for
+# every tensor of every call, and a step is a few microseconds
+_device = _raw_stream = None
 
 
 def _bind_torch() -> None:
-    global _Tensor, _device, _raw_stream
+    global _device, _raw_stream
     import torch
 
-    _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _Tensor = torch.Tensor
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _device = torch._C._cuda_getDevice
 
 
 def _dev_ptr(t, dtype, name: str) -> int:
-    if _Tensor is None:
+    if _device is None:
         _bind_torch()
-    # one condition for the tensor that passes (get_device() is -1 on the CPU)
-    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous() \
-            and t.get_device() == _device():
-        return t.data_ptr()
-    if not isinstance(t, _Tensor):
+    try:  # one condition for the tensor that passes (get_device() is -1 on the CPU)
+        if t.dtype is dtype and t.is_contiguous() and t.get_device() == _device():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    import torch
+
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -262,7 +265,7 @@ def _dev_ptr(t, dtype, name: str) -> int:
 
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        if _Tensor is None:
+        if _device is None:
             _bind_torch()
         # the handle alone: a Stream object costs a call several microseconds
         return _raw_stream(_device()) or None
@@ -291,9 +294,10 @@ def kv_cache_format(k_cache) -> Tuple[int, int]:
     4-bit one (36 or 72 bytes a row: no 8-bit head_dim)."""
     import torch
 
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("a cache is [num_blocks][num_kv_heads][block_size][row]")
-    row = k_cache.shape[3]
+    row = shape[3]
     if k_cache.dtype is torch.uint8:
         return (KV_FP4_E2M1, row * 16 // 9) if row in (36, 72) else (KV_FP8_E4M3, row)
     return KV_BF16, row
@@ -326,15 +330,17 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
     need k_scale / v_scale, float32 CUDA tensors [Hkv]."""
     import torch
 
-    if q.dim() == 4:
-        B, QL, Hq, D = q.shape
+    shape = q.shape
+    if len(shape) == 4:
+        B, QL, Hq, D = shape
     else:
-        (B, Hq, D), QL = q.shape, 0
+        (B, Hq, D), QL = shape, 0
     fmt, D2 = kv_cache_format(k_cache)
     NB, Hkv, BS, _ = k_cache.shape
-    if D2 != D or not _v_cache_ok(fmt, k_cache, v_cache) or out.shape != q.shape:
+    if D2 != D or not _v_cache_ok(fmt, k_cache, v_cache) or out.shape != shape:
         raise ValueError("shape mismatch between q / out / k_cache / v_cache")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
     fmt_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
     ks = vs = None
@@ -350,7 +356,7 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
         _dev_ptr(k_cache, fmt_dtype, "k_cache"), _dev_ptr(v_cache, fmt_dtype, "v_cache"),
         _dev_ptr(block_tables, torch.int32, "block_tables"),
         _dev_ptr(context_lens, torch.int32, "context_lens"),
-        block_tables.shape[1], B, Hq, Hkv, D, BS, NB, int(max_context_len),
+        tables[1], B, Hq, Hkv, D, BS, NB, int(max_context_len),
         float(1.0 / math.sqrt(D) if scale is None else scale), int(partition_tokens),
         int(variant), int(bool(overlap_prologue)), fmt, ks, vs, int(QL), int(wait_timeout_us))
 
@@ -622,11 +628,11 @@ def pa_copy_blocks_fp8(k_cache, v_cache, pairs, stream=None) -> None:
 
 
 def _check_fp4_rows(k_rows, v_rows, k_cache, v_cache, slot_mapping, k_scale, v_scale, who: str):
-    T, Hkv, D = k_rows.shape
-    fmt, D2 = kv_cache_format(k_cache)
-    NB, Hkv2, BS, _ = k_cache.shape
-    if fmt != KV_FP4_E2M1 or Hkv2 != Hkv or D2 != D or v_rows.shape != k_rows.shape \
-            or v_cache.shape != k_cache.shape or slot_mapping.shape != (T,) \
+    rows, cache = k_rows.shape, k_cache.shape
+    T, Hkv, D = rows
+    NB, Hkv2, BS, bytes_ = cache
+    if D not in (64, 128) or bytes_ * 16 != D * 9 or Hkv2 != Hkv or v_rows.shape != rows \
+            or v_cache.shape != cache or slot_mapping.shape != (T,) \
             or k_scale.numel() != Hkv or v_scale.numel() != Hkv:
         raise ValueError(f"shape mismatch in {who}")
     return T, Hkv, D, BS, NB
