@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "pa_fp4.h"
 #include "pa_internal.h"
 #include "pa_query_major.h"
 
@@ -132,7 +133,7 @@ pa_status set_cuda_error(const char* where, int err) {
 }
 
 bool decode_uses_tc(const pa_decode_params* p) {
-  return p->variant == PA_DECODE_TENSOR_CORE && tc_supports(p);
+  return p->variant == PA_DECODE_TENSOR_CORE && p->kv_dtype != PA_KV_FP4_E2M1 && tc_supports(p);
 }
 
 WorkspaceLayout decode_workspace_layout(const pa_decode_params* p, int num_partitions,
@@ -588,7 +589,8 @@ pa_status pa_step_host(const pa_step_host_params* p, void* workspace, size_t wor
     a.v_cache = p->v_cache;
     const pa::WorkspaceLayout w = pa::decode_workspace_layout(&d, np, grid);
     if (out_dev) d.out = out_dev;
-    if (in_dev && d.variant == PA_DECODE_TENSOR_CORE && pa::tc_supports(&d)) {
+    if (in_dev && d.variant == PA_DECODE_TENSOR_CORE && d.kv_dtype != PA_KV_FP4_E2M1 &&
+        pa::tc_supports(&d)) {
       // The lengths and tables in host_in are final before this call, so the
       // tensor-core decode reads them there and plans its work while the
       // staging kernel still runs (programmatic dependent launch); it reads

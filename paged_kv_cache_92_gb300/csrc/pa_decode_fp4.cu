@@ -48,8 +48,9 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
-#include "pa_internal.h"
+#include "pa_fp4.h"
 #include "pa_mma.cuh"
+#include "pa_ordered.cuh"
 
 namespace pa {
 namespace {

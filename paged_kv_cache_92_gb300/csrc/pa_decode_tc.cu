@@ -11,7 +11,6 @@ bool tc_supports(const pa_decode_params* p) {
   const int G = p->num_q_heads / H;
   if (!(H == 1 || H == 2 || H == 4 || H == 8) || !(G == 1 || G == 2 || G == 4 || G == 8))
     return false;
-  if (p->kv_dtype == PA_KV_FP4_E2M1) return false;  // its own kernel
   const bool fp8 = p->kv_dtype == PA_KV_FP8_E4M3;
   if (fp8 && p->head_dim != 128) return false;  // (the CUDA-core kernel takes head_dim 64)
   if (p->block_size != 16) {  // block sizes 8 and 32: bf16 head_dim 64 or 128, the

@@ -29,7 +29,8 @@
 #include <cstdint>
 
 #include "pa_device.cuh"
-#include "pa_internal.h"
+#include "pa_fp4.h"
+#include "pa_ordered.cuh"
 
 namespace pa {
 namespace {

@@ -23,8 +23,9 @@
 #include <cstdint>
 
 #include "pa_device.cuh"
-#include "pa_internal.h"
+#include "pa_fp4.h"
 #include "pa_mma.cuh"
+#include "pa_ordered.cuh"
 
 namespace pa {
 namespace {
