@@ -36,8 +36,11 @@ int launch_gather_fp4(const void* k_cache, const void* v_cache, void* k_out, voi
                       int32_t block_size, int32_t num_blocks, void* stream);
 // How the 4-bit decode deals out its work: contexts up to kFp4WholeTokens take
 // one CTA per (sequence, column group, KV head); longer ones a stream over
-// `grid` persistent CTAs, with two partials a CTA for the pieces it cuts.
-constexpr int kFp4WholeTokens = 512;
+// `grid` persistent CTAs, with two partials a CTA for the pieces it cuts. (32 / 8
+// heads, d 128, whole against stream: one sequence of 512 tokens 6.2 and 9.2 us, of
+// 1,024 8.8 and 9.4, of 2,048 14.6 and 10.0; 64 of up to 1,024 16.8 and 17.9, of up
+// to 2,048 28.9 and 24.5.)
+constexpr int kFp4WholeTokens = 1024;
 struct Fp4Plan {
   int grid, cols, cap;  // CTAs; columns of a partial; keys a sequence may have
   bool whole;

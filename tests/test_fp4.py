@@ -241,7 +241,7 @@ def test_binding_refuses_mixed_shapes(pk):
 
 
 def test_workspace_holds_two_partials_per_cta(pk):
-    """The header alone where contexts are short (at most 512 tokens); else the plan (a
+    """The header alone where contexts are short (at most 1,024 tokens); else the plan (a
     cost per sequence and column group, and the total) and two partials a CTA:
     four CTAs an SM, or one per 16 steps and starts."""
     def size(**kw):
@@ -250,14 +250,14 @@ def test_workspace_holds_two_partials_per_cta(pk):
     def ru(x):
         return (x + 255) // 256 * 256
 
-    assert size() == size(max_blocks_per_seq=32, max_context_len=512) == 256
-    assert size(max_blocks_per_seq=32, max_context_len=4096) == 256  # the table holds 512
-    kw = dict(max_blocks_per_seq=64, max_context_len=544)
-    grid = 2 * 2 * (17 + 8) // 16          # items x (steps + start), 16 a CTA
+    assert size() == size(max_blocks_per_seq=64, max_context_len=1024) == 256
+    assert size(max_blocks_per_seq=64, max_context_len=4096) == 256  # the table holds 1,024
+    kw = dict(max_blocks_per_seq=128, max_context_len=1056)
+    grid = 2 * 2 * (33 + 8) // 16          # items x (steps + start), 16 a CTA
     rows = 2 * grid * 8
     assert size(**kw) == 256 + ru(3 * 4) + ru(rows * 8) + ru(rows * 128 * 4)
     kw["query_len"] = 9                    # groups of two tokens (G 4): five
-    grid = 2 * 5 * 2 * (17 + 8) // 16
+    grid = 2 * 5 * 2 * (33 + 8) // 16
     rows = 2 * grid * 8
     assert size(**kw) == 256 + ru(11 * 4) + ru(rows * 8) + ru(rows * 128 * 4)
 
