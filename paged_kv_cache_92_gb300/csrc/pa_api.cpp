@@ -21,9 +21,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Keys per CTA of the token weights: short enough for
-// 8 CTAs an SM of a 152-SM GPU, so that ragged lengths even out, within
-// [128, 4096] tokens. `units`: (sequence, KV head, column group)s.
+// Keys per CTA of the token weights: for 8 CTAs an SM of a 152-SM GPU, so that
+// ragged lengths even out (the figures are with the kernel), within [128, 4096]
+// tokens. `units`: (sequence, KV head, column group)s.
 int auto_partition_tokens(int64_t cap, int64_t units) {
   const int64_t pt = (cap * units / (152 * 8) + 127) / 128 * 128;
   return pt < 128 ? 128 : (pt > kMaxPartitionTokens ? kMaxPartitionTokens : int(pt));

@@ -40,6 +40,17 @@
 //    lengths leave no tail. An item cut by a stretch's end leaves partials,
 //    at most two a CTA, which a second launch joins by log-sum-exp. Batches
 //    whose contexts are all short take one CTA an item and no second launch.
+//
+// Measured (GB300, whose copy rate is 6.79 TB/s): 32 sequences of 8 to 32 k
+// tokens, 64 / 8 heads, d 128: 144.8 us, 5.83 TB/s of cache, 86 % of the copy
+// rate; issuing the same instructions without waiting for memory takes 124 us,
+// about what the bytes take, so neither hides the other entirely (52 % of issue
+// slots, 50 % of the ALU, 24 % of the matrix unit busy on 8 such sequences).
+// 64 sequences of up to 2 k tokens, 32 / 8 heads: 26.4 us, of which the bytes
+// are 12.2 and some 10 are fixed: two launches, the plan, the first loads, the
+// pieces' starts and the merge. Dropped: 5 or 6 CTAs an SM (spills: 175 us), a
+// third ring stage (three CTAs an SM), one CTA per fixed partition (164 us), 1-D
+// bulk copies (174 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -118,7 +129,8 @@ __device__ __forceinline__ Virtual virtual_of(const Fp4Decode& P, int v) {
 }
 // The stream: an item (virtual sequence, KV head) costs its steps and a start
 // (queries, pipeline fill, merge of the warps: about 990 instructions a warp,
-// against 570 for one of its steps, four of which run at a time).
+// against 570 for one of its steps, four of which run at a time; 4 to 16 measure
+// the same).
 constexpr int START_COST = 8;
 __device__ __forceinline__ int item_cost(const Virtual& x) {
   return x.steps > 0 ? x.steps + START_COST : 0;

@@ -23,6 +23,12 @@
 //    owns one (sequence, KV head) and a slice of the row's bytes, so CTAs never
 //    meet. Bound by memory traffic: every kept row is read and written once,
 //    and rows that stay where they are not at all.
+// Measured (GB300, copy rate 6.79 TB/s): 64 sequences of up to 2 k tokens cut to
+// 512, bf16, 8 KV heads, d 128: 51.0 us, of which the choice takes 7 and the move
+// 44 (its bytes: 37.9 us); 8 of 8 to 32 k cut to 4 k: 67.4 us, 16 and 51 (39.7).
+// The move of few sequences has 512 CTAs for 152 SMs and rows in 64-byte slices;
+// slices of 128 or 32 bytes take 10 and 16 us more, tiles of twice or half the
+// rows 24 and 6.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -19,7 +19,9 @@
 //
 // Both kernels are bound by memory traffic: one thread per group of 16
 // elements reads or writes 32 bytes of bf16 and 9 bytes of cache. The codes of
-// a row are written by head_dim / 16 neighbouring threads, 8 bytes each.
+// a row are written by head_dim / 16 neighbouring threads, 8 bytes each. At a
+// decode step's sizes the launch is what they cost (64 tokens of 8 heads, d 128:
+// 4.6 us for the two of them, against 0.1 us of traffic).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
