@@ -553,7 +553,8 @@ pa_status pa_token_weights(const pa_token_weights_params* p, void* workspace,
  * recent with the largest token_weights (ties: the lower index; +0 and -0 are
  * equal, a NaN ranks below every number).
  *   keep      int32 [num_seqs][budget]: their indices, ascending; -1 behind
- *   new_lens  int32 [num_seqs]: min(context_lens[b], budget)
+ *   new_lens  int32 [num_seqs]: min(context_lens[b], budget); not context_lens
+ *             itself nor overlapping it (PA_ERR_INVALID_ARG)
  * token_weights: float [num_seqs][weights_stride]; a length beyond
  * weights_stride is cut to it and sets PA_DEVERR_CONTEXT_LEN. num_seqs up to
  * 65535, weights_stride and budget in [1, 2^30], recent in [0, budget]. No

@@ -923,6 +923,10 @@ pa_status pa_evict_select(const float* token_weights, const int32_t* context_len
       (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(keep) & 3u) || (reinterpret_cast<uintptr_t>(new_lens) & 3u))
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_select: misaligned pointer");
+  // a sequence's length is read by several warps and CTAs, with no order to the write
+  if (new_lens < context_lens + num_seqs && context_lens < new_lens + num_seqs)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_evict_select: new_lens must not overlap context_lens");
   const int e = pa::launch_evict_select(token_weights, context_lens, keep, new_lens, num_seqs,
                                         weights_stride, budget, recent, stream);
   if (e != 0) return pa::set_cuda_error("pa_evict_select: launch", e);

@@ -29,7 +29,7 @@
 //    wants; an 8x8 register transpose turns it.
 //  * Queries are scaled by a power of two per row into f16's range (exact for
 //    every element within 2^-30 of the row's largest) and the factor goes to
-//    the softmax scale. P is rounded to f16 (2^-12 of its value, eight times
+//    the softmax scale. P is rounded to f16 (at most 2^-11 of its value, eight times
 //    finer than bf16, and no cheaper form exists); the running maximum, the
 //    sums and the output stay in fp32.
 //  * The reference maximum moves only when a score exceeds it by 2^8, so O is

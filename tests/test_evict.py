@@ -128,6 +128,14 @@ def test_select_sizes_beyond_the_index_range(pk, stride, budget):
     assert b"2^30" in lib.pa_last_error()
 
 
+@pytest.mark.parametrize("at", [0, 4, -4])
+def test_select_refuses_lengths_in_place(pk, at):
+    """The kept lengths over the lengths that other CTAs may still have to read."""
+    lib = pk.load()
+    assert lib.pa_evict_select(256, 1024, 256, 1024 + at, 2, 64, 8, 0, None) == 1
+    assert b"overlap" in lib.pa_last_error()
+
+
 @pytest.mark.parametrize("kw", [dict(max_blocks_per_seq=1 << 26), dict(max_dst_blocks_per_seq=1 << 26)])
 def test_compact_sizes_beyond_the_index_range(pk, kw):
     p = pk.EvictCompactParams()
