@@ -765,3 +765,64 @@ def test_a_call_allocates_on_its_own_stream(pk, handle):
     assert not any(m.any() for m in mine)
     assert torch.equal(w, w2) and torch.equal(out, out2)
     assert torch.equal(keep, keep2) and torch.equal(n, n2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+def test_kernels_wait_for_the_one_before(pk, fmt):
+    """A kernel's CTAs may be dispatched while the preceding kernel runs, one that lets its
+    dependents start at its entry among them: what it writes is seen all the same. Every call
+    follows at once a kernel that changes what it reads."""
+    import torch
+
+    B, L, Hq, Hkv, D, BS = 16, 1200, 8, 8, 128, 16
+    torch.manual_seed(4)
+    nb = -(-L // BS)
+    T = B * nb * BS
+    shape = pk.fp4_cache_shape(B * nb, Hkv, BS, D) if fmt == "fp4" else (B * nb, Hkv, BS, D)
+    kc = torch.zeros(shape, dtype=torch.uint8 if fmt == "fp4" else torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    sc = dict(k_scale=torch.full((Hkv,), .05, device="cuda"),
+              v_scale=torch.full((Hkv,), .03, device="cuda")) if fmt == "fp4" else {}
+    tab = torch.arange(B * nb, dtype=torch.int32, device="cuda").reshape(B, nb)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    rows = [[torch.randn(T, Hkv, D, device="cuda").bfloat16() for _ in range(2)] for _ in range(2)]
+    qs = [torch.randn(B, Hq, D, device="cuda").bfloat16() for _ in range(2)]
+    ls = [torch.randint(600, L + 1, (B,), dtype=torch.int32, device="cuda") for _ in range(2)]
+    q, w = qs[0].clone(), torch.zeros(B, L, device="cuda")
+    ks = dict(k_scale=sc["k_scale"]) if sc else {}
+
+    def step(i, settle):
+        wait = torch.cuda.synchronize if settle else (lambda: None)
+        lens.copy_(ls[i])
+        wait()
+        if fmt == "fp4":
+            pk.pa_reshape_and_cache_fp4(*rows[i], kc, vc, slots, **sc)
+        else:
+            pk.pa_reshape_and_cache(*rows[i], kc, vc, slots)
+        wait()
+        pk.pa_token_weights(q, kc, tab, lens, L, w, accumulate=False, **ks)
+        wait()
+        q.copy_(qs[i])
+        wait()
+        out = pk.pa_decode(q, kc, vc, tab, lens, L, **sc)
+        w.mul_(1 + i)
+        wait()
+        keep, n = pk.pa_evict_select(w, lens, 500, 30)
+        wait()
+        pk.pa_evict_compact(kc, vc, tab, tab, keep, n, w)
+        wait()
+        after = pk.pa_decode(q, kc, vc, tab, n, 500, **sc)
+        got = [out, w.clone(), keep, n, after, kc.clone(), vc.clone()]
+        if fmt == "fp4":
+            got += pk.pa_gather_fp4(kc, vc, slots[:5000], **sc)
+        return got
+
+    step(0, True)
+    want = [step(i, True) for i in (1, 0)]
+    for _ in range(8):
+        for i, ref in zip((1, 0), want):
+            torch.cuda._sleep(200_000)
+            for x, y in zip(step(i, False), ref):
+                assert torch.equal(x, y)
