@@ -130,13 +130,14 @@ __device__ __forceinline__ uint2 quantise_group(const uint4& lo, const uint4& hi
 
 // One thread per group, of K and of V: their loads are in flight together
 // (7 k tokens of 8 heads, dim 128: 11.8 us, 3.6 TB/s; one thread for each
-// 13.4 us).
+// 13.4 us). No pointer is __restrict__ here: what a kernel reads through its
+// read-only path must not change from its start on, and this one may start
+// before the preceding kernel has written it.
 __global__ void __launch_bounds__(256)
-    reshape_and_cache_fp4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
-                                 uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
-                                 const int64_t* __restrict__ slot_mapping,
-                                 const float* __restrict__ k_scale,
-                                 const float* __restrict__ v_scale, Fp4Rows r, AppendCheck check) {
+    reshape_and_cache_fp4_kernel(const uint4* k_new, const uint4* v_new, uint8_t* k_cache,
+                                 uint8_t* v_cache, const int64_t* slot_mapping,
+                                 const float* k_scale, const float* v_scale, Fp4Rows r,
+                                 AppendCheck check) {
   dev::griddep_enter();
   const int64_t idx = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= r.num_groups) return;
@@ -200,10 +201,9 @@ __device__ __forceinline__ void read_group(const uint2& codes, float sf, float s
 // (A thread for both, as in the write, took 10.3 us on 7 k tokens of 8 heads
 // where this takes 9.2: here the stores are what is wide.)
 __global__ void __launch_bounds__(256)
-    gather_fp4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
-                      uint4* __restrict__ k_out, uint4* __restrict__ v_out,
-                      const int64_t* __restrict__ slot_mapping, const float* __restrict__ k_scale,
-                      const float* __restrict__ v_scale, Fp4Rows r) {
+    gather_fp4_kernel(const uint8_t* k_cache, const uint8_t* v_cache, uint4* k_out, uint4* v_out,
+                      const int64_t* slot_mapping, const float* k_scale, const float* v_scale,
+                      Fp4Rows r) {
   dev::griddep_enter();
   const int64_t idx = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= r.num_groups) return;
