@@ -739,7 +739,9 @@ Fp4Plan fp4_plan(const pa_decode_params* p, int num_sms) {
   if (r.whole) {
     r.grid = int(items);
   } else {
-    // as many CTAs as are resident at once, but no stretch under two start costs
+    // as many CTAs as are resident at once, but no stretch under two start costs (for 2,
+    // 3, 4, 8 CTAs an SM: 29.6, 26.6, 26.2, 30.7 us on 64 sequences of up to 2 k tokens,
+    // 161, 147, 145, 147 on 32 of up to 32 k)
     const int64_t most = items * ((r.cap + KEYS - 1) / KEYS + START_COST) / (2 * START_COST);
     const int64_t full = int64_t(num_sms > 0 ? num_sms : 256) * CTAS;
     r.grid = int(most < full ? most : full);
