@@ -826,3 +826,68 @@ def test_kernels_wait_for_the_one_before(pk, fmt):
             torch.cuda._sleep(200_000)
             for x, y in zip(step(i, False), ref):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_captured_behind_copies_fills_and_joined_streams(pk):
+    """Capture where a call does not follow one kernel on its stream: behind a copy, a fill, a
+    host-to-device copy, and behind two streams' work; and two branches of calls that join."""
+    import torch
+
+    B, L, Hq, Hkv, D, BS = 4, 3000, 8, 2, 128, 16
+    torch.manual_seed(6)
+    nb = -(-L // BS)
+    k, v = (torch.randint(0, 256, pk.fp4_cache_shape(B * nb, Hkv, BS, D), dtype=torch.uint8,
+                          device="cuda") for _ in range(2))
+    for c in (k, v):
+        c.view(B * nb, Hkv, -1)[..., BS * D // 2:] = 0x38        # group scales of one
+    sc = dict(k_scale=torch.full((Hkv,), .05, device="cuda"),
+              v_scale=torch.full((Hkv,), .03, device="cuda"))
+    tab = torch.arange(B * nb, dtype=torch.int32, device="cuda").reshape(B, nb)
+    host = torch.tensor([3000, 1, 1700, 2999], dtype=torch.int32).pin_memory()
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    q0 = torch.randn(B, Hq, D, device="cuda").bfloat16()
+    q, out, out2 = torch.zeros_like(q0), torch.zeros_like(q0), torch.zeros_like(q0)
+    w, junk = torch.ones(B, L, device="cuda"), torch.zeros(1 << 20, device="cuda")
+    ws = [torch.empty(32 << 20, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    slots = torch.arange(100, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def body():
+        lens.copy_(host, non_blocking=True)
+        q.copy_(q0)
+        pk.pa_decode(q, k, v, tab, lens, L, out=out, workspace=ws[0], **sc)
+        w.zero_()
+        pk.pa_token_weights(q, k, tab, lens, L, w, workspace=ws[0], k_scale=sc["k_scale"])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            junk.add_(1)
+            pk.pa_decode(q, k, v, tab, lens, L, out=out2, workspace=ws[1], **sc)
+        keep, n = pk.pa_evict_select(w, lens, 200, 9)
+        rows = pk.pa_gather_fp4(k, v, slots, **sc)
+        main.wait_stream(side)
+        pk.pa_evict_compact(k, v, tab, tab, keep, n)
+        after = pk.pa_decode(q, k, v, tab, n, 200, workspace=ws[0], **sc)
+        return keep, n, *rows, after
+
+    k0, v0 = k.clone(), v.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        want = body()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (*want, out, out2, w, k, v)]
+    k.copy_(k0)
+    v.copy_(v0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        got = body()
+    for _ in range(3):
+        k.copy_(k0)
+        v.copy_(v0)
+        lens.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((*got, out, out2, w, k, v), want):
+            assert torch.equal(x, y)
+    assert pk.pa_device_errors() == 0
