@@ -30,6 +30,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_fp4.h"
@@ -194,13 +195,21 @@ __global__ void __launch_bounds__(NTHREADS)
   const int row_g = dev::key_row(g);
   const int lane_k = row_g * Row::BYTES + t * Row::RUN;
   const int lane_ks = row_g * Row::SCALES + t * (D / 64);
+  int off_k[2][2], off_s[2][2];  // of a step's 8-row quarters: this lane's row and its scales
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = h * 16 + r * 8;  // of a lane with row_g 0 (which is below 8)
+      const int tile = (row >> P.bs_log2) * tile_bytes;
+      off_k[h][r] = tile + (row & (BS - 1)) * Row::BYTES + lane_k;
+      off_s[h][r] = tile + BS * Row::BYTES + (row & (BS - 1)) * Row::SCALES + lane_ks;
+    }
   int stalled_at = -1;
 
-  for (int i = 0; i < n_my; ++i) {
-    if (!__all_sync(0xffffffffu, dev::mbar_wait(&my_bars[i % ST], (i / ST) & 1))) {
-      stalled_at = i;
-      break;
-    }
+  // One step; with EDGE one that holds keys which some column does not see.
+  auto step = [&](int i, auto edge_t) {
+    constexpr bool EDGE = decltype(edge_t)::value;
     const unsigned char* kt = ring + (i % ST) * STAGE;
     const int key0 = tok0 + KEYS * (warp + NWARPS * i);
     float s[2][NT][4];
@@ -212,12 +221,7 @@ __global__ void __launch_bounds__(NTHREADS)
         for (int j = 0; j < 4; ++j) s[h][nt][j] = 0.0f;
       Row rows[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = h * 16 + r * 8;  // of a lane with row_g 0 (which is below 8)
-        const unsigned char* tile = kt + (row >> P.bs_log2) * tile_bytes;
-        rows[r].load(tile + (row & (BS - 1)) * Row::BYTES + lane_k,
-                     tile + BS * Row::BYTES + (row & (BS - 1)) * Row::SCALES + lane_ks);
-      }
+      for (int r = 0; r < 2; ++r) rows[r].load(kt + off_k[h][r], kt + off_s[h][r]);
       dev::key_product<FMT, D, NT>(s[h], rows[0], rows[1], qf);
     }
     __syncwarp();
@@ -235,11 +239,11 @@ __global__ void __launch_bounds__(NTHREADS)
             const int key = key0 + h * 16 + r * 8 + row_g;
             float& v = s[h][nt][2 * r + c];
             v *= factor[nt][c];
-            if (key < see[nt][c]) {
-              out[nt][c][key] = v;
-              top = fmaxf(top, v);
-            } else {
+            if (EDGE && key >= see[nt][c]) {
               v = -INFINITY;
+            } else {
+              if (see[nt][c] > 0) out[nt][c][key] = v;
+              top = fmaxf(top, v);
             }
           }
         // each lane keeps the running maximum of its own keys
@@ -253,6 +257,20 @@ __global__ void __launch_bounds__(NTHREADS)
         m[nt][c] = x;
         l[nt][c] = sum;
       }
+  };
+  // steps before the first that is an edge, and this warp's share (columns that no
+  // query row has see nothing, and store nothing)
+  const int n_full = (min(tok1, see0) - tok0) / KEYS;
+  const int n_inner = n_full > warp ? (n_full - warp + NWARPS - 1) / NWARPS : 0;
+  for (int i = 0; i < n_my; ++i) {
+    if (!__all_sync(0xffffffffu, dev::mbar_wait(&my_bars[i % ST], (i / ST) & 1))) {
+      stalled_at = i;
+      break;
+    }
+    if (i < n_inner)
+      step(i, std::false_type{});
+    else
+      step(i, std::true_type{});
   }
   if (stalled_at >= 0) {
     if (lane == 0) atomicOr(&g_weights_errors, PA_DEVERR_TIMEOUT);
