@@ -28,7 +28,9 @@
 // 44 (its bytes: 37.9 us); 8 of 8 to 32 k cut to 4 k: 67.4 us, 16 and 51 (39.7).
 // The move of few sequences has 512 CTAs for 152 SMs and rows in 64-byte slices;
 // slices of 128 or 32 bytes take 10 and 16 us more, tiles of twice or half the
-// rows 24 and 6.
+// rows 24 and 6 (64 registers let four CTAs share an SM, so that all 512 are
+// resident; larger tiles do not), and clusters that share a tile's rows instead of
+// their bytes 1 to 4.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -13,7 +13,7 @@
 //    max) / sum over the rows of a token, in a fixed order: no atomics, the
 //    same bits on every run.
 // Reading K twice instead would cost 256 (128, 72) bytes a row against the
-// scores' 8 G, so the scores win for every type up to G = 8.
+// scores' 8 G (of one new token), so the scores win for every type up to G = 8.
 // The keys of a (sequence, KV head) are split into partitions, a CTA each, for
 // about 8 CTAs an SM when every sequence is as long as the longest. Measured
 // (GB300, copy rate 6.79 TB/s): 64 sequences of up to 2 k tokens, bf16, 32 / 8
