@@ -29,11 +29,17 @@
 //    wants; an 8x8 register transpose turns it.
 //  * Queries are scaled by a power of two per row into f16's range (exact for
 //    every element within 2^-30 of the row's largest) and the factor goes to
-//    the softmax scale. P is rounded to f16 (at most 2^-11 of its value, eight times
-//    finer than bf16, and no cheaper form exists); the running maximum, the
-//    sums and the output stay in fp32.
-//  * The reference maximum moves only when a score exceeds it by 2^8, so O is
-//    rescaled rarely; f16 holds the weights up to 2^8 that this allows.
+//    the softmax scale. P is rounded to f16, eight times finer than bf16 (no
+//    cheaper form exists); the running maximum, the sums and the output stay in
+//    fp32.
+//  * P = exp2(score - reference), with the reference 2^7 below the largest weight
+//    that it was taken from, and moved only when a weight exceeds that one by 2^8,
+//    so O is rescaled rarely. P stays within 2^15, which f16 holds, and weights
+//    down to 2^-21 of the row's largest are rounded by at most 2^-11 of their
+//    value; lesser ones by at most 2^-32 of the largest (f16's subnormals, and zero
+//    below them). With the reference at the largest weight that would be 2^-25: a
+//    flat tail of a long context behind one large weight was lost, or half again as
+//    large as it is.
 //  * Work is dealt out as a stream: every (sequence, column group, KV head) is
 //    an item of so many 32-key steps plus a start cost, and each of the
 //    persistent CTAs takes an equal stretch of the stream's cost, so ragged
@@ -73,6 +79,7 @@ constexpr int NTHREADS = NWARPS * 32;
 constexpr int KEYS = 32;  // keys of a warp's step
 constexpr int CTAS = 4;   // resident on an SM
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float HEADROOM = 7.0f;  // of the softmax reference below the maximum, log2
 
 template <int D, int BS>
 struct Cfg {
@@ -385,8 +392,9 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
 
   float o[D / 16][4];  // O^T: D / 16 tiles of 16 rows
   // Softmax state of columns 2t and 2t+1, in the log2 domain: a score is
-  // s * factor (s the raw product), ref the reference maximum (0 before the
-  // first key that the column sees), limit the raw product beyond which ref moves.
+  // s * factor (s the raw product), ref the reference (0 before the first key that
+  // the column sees), HEADROOM below the score that it was taken from, limit the
+  // raw product beyond which ref moves: 8 above that score.
   float ref[2] = {0.0f, 0.0f}, limit[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
@@ -445,12 +453,15 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
         // no branch here: lanes of different columns decide differently, and
         // the warp-wide instructions below need them together
         const bool first = limit[c] == -INFINITY;
-        const bool take = x != -INFINITY && (first || x > ref[c]);
-        const float y = take ? x : ref[c];
+        // beyond 2^20 the roundings of x and of the limit count: that much less room
+        const float slack = fabsf(x) * 0x1p-20f;
+        const float low = x - fmaxf(HEADROOM - slack, 0.0f);
+        const bool take = x != -INFINITY && (first || low > ref[c]);
+        const float y = take ? low : ref[c];
         const float b = dev::fast_exp2(ref[c] - y);
         const float a = take && first ? 0.0f : b;
         ref[c] = y;
-        limit[c] = take ? __fdividef(x + 8.0f, factor[c]) : limit[c];
+        limit[c] = take ? __fdividef(x + 8.0f - slack, factor[c]) : limit[c];
         l[c] *= a;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {

@@ -716,3 +716,97 @@ def test_empty_batch(pk):
     pk.pa_reshape_and_cache_fp4(e, e, args[1], args[2],
                                 torch.empty(0, dtype=torch.int64, device="cuda"), **sc)
     assert pk.pa_device_errors() == 0
+
+
+# ------------------------------------------------------------------ GPU: the softmax weights' range
+#
+# Weights are held in f16 with the largest that a reference was taken from at 2^7 (and at most
+# 2^15): those down to 2^-14 are rounded by at most 2^-11 of their value, lesser ones by at most
+# half the subnormal step, 2^-25, which is 2^-32 of the row's largest weight. So beside the terms of
+# `_bound` an element is off by at most 2^-32 L max|V|.
+
+
+def _ones_case(pk, keys, values):
+    """One sequence, one KV head, d 64, block 16, head scales and group scales of one: K codes
+    `keys` [L][64], V codes `values` [L][64] (E2M1, the sign in bit 3)."""
+    import torch
+
+    L, D, BS = len(keys), 64, 16
+    nb = -(-L // BS)
+    caches = []
+    for codes in (keys, values):
+        full = np.zeros((nb * BS, D), np.uint8)
+        full[:L] = codes
+        flat = np.full((nb, 1, BS * D * 9 // 16), 0x38, np.uint8)
+        flat[:, 0, :BS * D // 2] = (full[:, 0::2] | full[:, 1::2] << 4).reshape(nb, -1)
+        caches.append(flat.reshape(nb, 1, BS, D * 9 // 16))
+    tab = np.random.default_rng(L).permutation(nb).astype(np.int32)[None]
+    for c in caches:
+        c[tab[0]] = c.copy()
+    return caches, tab
+
+
+def _check_weights_range(pk, caches, tab, L, q, scale):
+    import torch
+
+    one = np.ones(1, np.float32)
+    kr, vr = (oracle.fp4_values(c, one, 64) for c in caches)
+    qd = oracle.bf16_to_f64(q)
+    lens = np.array([L], np.int32)
+    want, _ = oracle.attention_rows(qd, kr, vr, tab, lens, scale)
+    mag, _ = oracle.attention_rows(qd, kr, np.abs(vr), tab, lens, scale)
+    bound = _bound(want, mag) + 2.0 ** -32 * L * np.abs(vr).max()
+    s = torch.ones(1, device="cuda")
+    dev = [torch.from_numpy(c).cuda() for c in caches]
+    for room in (tab.shape[1], 256):  # as it is, and with room for 4,096 tokens (the stream)
+        wide = np.full((1, max(room, tab.shape[1])), -1, np.int32)
+        wide[:, :tab.shape[1]] = tab
+        got = pk.pa_decode(q[:, 0].cuda(), *dev, torch.from_numpy(wide).cuda(),
+                           torch.from_numpy(lens).cuda(), max(L, room * 16), scale,
+                           k_scale=s, v_scale=s)
+        got = oracle.bf16_to_f64(got.cpu())[:, None]
+        assert np.isfinite(got).all()
+        over = np.abs(got - want) / bound
+        assert over.max() <= 1.0, (room, over.max())
+    assert pk.pa_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gap", [12.0, 20.0, 24.5, 25.5, 27.0, 30.0])
+@pytest.mark.parametrize("L", [300, 1000, 2000])
+def test_decode_flat_tail_behind_large_weights(pk, gap, L):
+    """A few keys whose weights are 2^gap times those of all others, with values of zero, so
+    that the output is the tail's alone. One of them in each warp's first step."""
+    import torch
+
+    rng = np.random.default_rng(L)
+    keys = np.zeros((L, 64), np.uint8)
+    values = rng.integers(0, 8, (L, 64)).astype(np.uint8)
+    keys[[0, 32, 64, 96]] = 2          # elements of one: a product of 64
+    values[[0, 32, 64, 96]] = 0
+    caches, tab = _ones_case(pk, keys, values)
+    q = torch.ones(1, 1, 2, 64, dtype=torch.bfloat16)
+    q[:, :, 1] = 0.5                   # the second head's gap is half as wide
+    scale = float(np.float32(gap * np.log(2.0) / 64))
+    _check_weights_range(pk, caches, tab, L, q, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("big", [2.0 ** -2, 2.0 ** 6, 2.0 ** 8])
+def test_decode_scores_of_millions(pk, big):
+    """Scores far beyond the softmax's range that differ by a few units, rising from step to
+    step of a warp by just under and just over what moves the reference. All products are exact
+    (21 bits), and so are the scores' differences up to the scale's last places."""
+    import torch
+
+    L = 1000
+    keys = np.zeros((L, 64), np.uint8)
+    keys[:, 0] = 7                                            # 6 * big
+    keys[:, 1] = np.minimum(np.arange(L) // 128, 7)           # 0 to 6, times big * 2^-17
+    values = np.random.default_rng(1).integers(0, 16, (L, 64)).astype(np.uint8)
+    caches, tab = _ones_case(pk, keys, values)
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    q[..., 0], q[..., 1] = big, big * 2.0 ** -17
+    for unit in np.linspace(2.4, 3.3, 19):  # of half a code in the log2 domain; 3 units are a jump
+        scale = float(np.float32(unit * np.log(2.0) / (big * 2.0 ** -18)))
+        _check_weights_range(pk, caches, tab, L, q, scale)
