@@ -93,7 +93,8 @@ typedef enum {
                                         of its token (context_lens[b]-1 for one new token per
                                         sequence); that token is not written */
 #define PA_DEVERR_KEEP 0x40u         /* pa_evict_compact: a keep entry that does not ascend or is
-                                        past the source table; that row is not moved */
+                                        past the source table (that row is not moved), or past the
+                                        token weights (that weight becomes 0) */
 
 const char* pa_status_string(pa_status s);
 const char* pa_last_error(void);
@@ -580,9 +581,10 @@ pa_status pa_evict_select(const float* token_weights, const int32_t* context_len
  *  - new_lens beyond keep_stride or the destination table is cut and sets
  *    PA_DEVERR_CONTEXT_LEN; a table entry outside [0, num_blocks) moves nothing
  *    and sets PA_DEVERR_TABLE_ENTRY.
- *  - token_weights, if not NULL, is compacted the same way in place, and its
- *    rows are zeroed from new_lens[b] on. Other rows behind the kept tokens are
- *    left as they were.
+ *  - token_weights, if not NULL, is compacted the same way in place (a weight
+ *    stays where its row is not moved; one of a token at or beyond weights_stride
+ *    becomes 0 and sets PA_DEVERR_KEEP), and its rows are zeroed from new_lens[b]
+ *    on. Other rows behind the kept tokens are left as they were.
  * ---------------------------------------------------------------------- */
 typedef struct {
   void* k_cache;               /* of type kv_dtype, as in pa_decode_params; written */

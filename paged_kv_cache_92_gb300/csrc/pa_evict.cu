@@ -317,11 +317,11 @@ struct Compact {
 };
 
 // Row j's source and destination as slots (block * block_size + offset);
-// src = -1 where there is nothing to move.
+// src = -1 where the row cannot be moved.
 struct Move {
   int64_t src, dst;
 };
-__device__ __forceinline__ Move move_of(const Compact& P, int b, int j, int t, bool report) {
+__device__ __forceinline__ Move places_of(const Compact& P, int b, int j, int t, bool report) {
   Move m{-1, 0};
   if (t < j || (t >> P.bs_log2) >= P.src_blocks) {  // not ascending, or no such row
     if (report) atomicOr(&g_evict_errors, PA_DEVERR_KEEP);
@@ -336,7 +336,12 @@ __device__ __forceinline__ Move move_of(const Compact& P, int b, int j, int t, b
   const int mask = (1 << P.bs_log2) - 1;
   m.src = (int64_t(sb) << P.bs_log2) + (t & mask);
   m.dst = (int64_t(db) << P.bs_log2) + (j & mask);
-  if (m.src == m.dst) m.src = -1;  // a row that stays
+  return m;
+}
+// The same, with src = -1 also for a row that stays where it is.
+__device__ __forceinline__ Move move_of(const Compact& P, int b, int j, int t, bool report) {
+  Move m = places_of(P, b, j, t, report);
+  if (m.src == m.dst) m.src = -1;
   return m;
 }
 
@@ -469,20 +474,25 @@ __global__ void __launch_bounds__(MOVE_THREADS) compact_rows_kernel(const Compac
 }
 
 // The weights of the kept tokens, moved in place; the rest of the row is zeroed.
+// A weight goes where its row goes: it stays where that is not moved. That of a
+// token past the end of the weights is unknown: zero, and flagged.
 __global__ void __launch_bounds__(256)
     compact_weights_kernel(const Compact P, float* weights, int64_t stride) {
   dev::griddep_enter();
   const int b = blockIdx.x;
   float* row = weights + b * stride;
   const int n = int(min(int64_t(rows_to_move(P, b, false)), stride));
-  for (int j0 = 0; j0 < n; j0 += 256) {
+  auto keep = [&](int j) { return j < n ? P.keep[int64_t(b) * P.keep_stride + j] : 0; };
+  int t = keep(threadIdx.x), next;
+  for (int j0 = 0; j0 < n; j0 += 256, t = next) {
     const int j = j0 + threadIdx.x;
     float x = 0.0f;
     bool go = false;
+    next = keep(j + 256);  // on its way while this one's weight and tables are looked up
     if (j < n) {
-      const int t = P.keep[int64_t(b) * P.keep_stride + j];
-      go = t >= j && t < stride;
-      if (go) x = row[t];
+      if (t >= 0 && t < stride) x = row[t];
+      go = places_of(P, b, j, t, false).src >= 0;
+      if (go && t >= stride) atomicOr(&g_evict_errors, PA_DEVERR_KEEP);
     }
     __syncthreads();
     if (go) row[j] = x;

@@ -891,3 +891,57 @@ def test_captured_behind_copies_fills_and_joined_streams(pk):
         for x, y in zip((*got, out, out2, w, k, v), want):
             assert torch.equal(x, y)
     assert pk.pa_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_compacted_weights_follow_their_rows(pk):
+    """Where a row is not moved its weight stays too; a weight that the row of weights does
+    not reach becomes zero and is flagged."""
+    import torch
+
+    c = Case("bf16", [64, 64], 2, 2, 64, seed=7)
+    tab = torch.from_numpy(c.tables).cuda()
+    w = torch.rand(2, 80, generator=torch.Generator().manual_seed(1)) + 0.5
+    keep = torch.tensor([[2, 0, 5, 64, 70], [1, 2, 3, 4, 20]], dtype=torch.int32, device="cuda")
+    n = torch.tensor([5, 5], dtype=torch.int32, device="cuda")
+    dst = tab.clone()
+    dst[1, 0] = c.NB                                   # no such block: nothing of sequence 1 moves
+    k0, got = c.k.cuda(), w.cuda()
+    k = k0.clone()
+    pk.pa_evict_compact(k, c.v.cuda(), tab, dst, keep, n, got)
+    assert pk.pa_device_errors() == pk.DEVERR_KEEP | pk.DEVERR_TABLE_ENTRY
+    want = torch.zeros(2, 80)
+    want[0, :5] = w[0, [2, 1, 5, 3, 4]]                # entries 0 < 1, 64 and 70: not moved
+    want[1, :5] = w[1, :5]
+    assert torch.equal(got.cpu(), want)
+    old = [k0[c.tables[0, t // 16], :, t % 16] for t in (2, 1, 5, 3, 4)]
+    assert all(torch.equal(k[c.tables[0, 0], :, j], x) for j, x in enumerate(old))
+
+    short = w[:, :40].contiguous().cuda()              # weights of 40 tokens, tables of 64
+    keep = torch.tensor([[3, 39, 40, 63], [0, 1, 2, 3]], dtype=torch.int32, device="cuda")
+    pk.pa_evict_compact(k0, c.v.cuda(), tab, tab, keep, n - 1, short)
+    assert pk.pa_device_errors() == pk.DEVERR_KEEP
+    want = torch.zeros(2, 40)
+    want[0, :2], want[1, :4] = w[0, [3, 39]], w[1, :4]
+    assert torch.equal(short.cpu(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("budget", [513, 1200, 4000])
+def test_compacted_weights_of_long_rows(pk, budget):
+    """Many tiles of weights in place, of sequences cut a little, much and not at all."""
+    import torch
+
+    c = Case("bf16", [5000, 1201, 700, budget, 0], 1, 1, 64, seed=8)
+    rng = np.random.default_rng(budget)
+    w = rng.random((5, 5001)).astype(np.float32)
+    w[1, :600] = 2.0
+    keep, n = select(w, c.lens, budget, 11)
+    tab, got = torch.from_numpy(c.tables).cuda(), torch.from_numpy(w).cuda()
+    pk.pa_evict_compact(c.k.cuda(), c.v.cuda(), tab, tab, torch.from_numpy(keep).cuda(),
+                        torch.from_numpy(n).cuda(), got)
+    want = np.zeros_like(w)
+    for b in range(5):
+        want[b, :n[b]] = w[b, keep[b, :n[b]]]
+    assert np.array_equal(got.cpu().numpy(), want)
+    assert pk.pa_device_errors() == 0
