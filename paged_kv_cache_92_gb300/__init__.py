@@ -245,8 +245,8 @@ def _bind_torch() -> None:
 def _dev_ptr(t, dtype, name: str) -> int:
     if _device is None:
         _bind_torch()
-    try:  # one condition for the tensor that passes (get_device() is -1 on the CPU)
-        if t.dtype is dtype and t.is_contiguous() and t.get_device() == _device():
+    try:  # one condition for the tensor that passes (without a driver _device() raises)
+        if t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.get_device() == _device():
             return t.data_ptr()
     except AttributeError:
         pass

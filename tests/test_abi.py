@@ -409,3 +409,16 @@ def test_step_host_layout_with_new_tokens_and_cache_type(pk):
         setattr(q, field, bad)
         assert lib.pa_step_host_layout(ctypes.byref(q), ctypes.byref(L)) == 1  # PA_ERR_INVALID_ARG
         assert lib.pa_step_host_workspace_size(ctypes.byref(q)) == 0
+
+
+def test_host_tensors_are_refused_by_name(pk):
+    """A tensor in host memory is named and refused, with or without a CUDA driver."""
+    import torch
+
+    k = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    pairs = torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="k_cache must live on a CUDA device"):
+        pk.pa_copy_blocks(k, k, pairs)
+    q, n = torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="q must live on a CUDA device"):
+        pk.make_decode_params(q, q, k, k, pairs[:, :1], n, 16)
