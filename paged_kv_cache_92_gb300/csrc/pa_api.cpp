@@ -77,18 +77,23 @@ pa_status check_decode(const pa_decode_params* p, bool need_pointers) {
     return set_error(PA_ERR_INVALID_ARG, "pa_decode: wait_timeout_us must be >= 0");
   if (int64_t(p->num_seqs) * query_len_of(p) * p->num_q_heads >= (int64_t(1) << 31) - 16)
     return set_error(PA_ERR_INVALID_ARG, "pa_decode: query rows exceed 2^31");
-  // the CUDA-core kernel's partitions are whole blocks
+  // the CUDA-core kernel's partitions are whole blocks (the 4-bit cache's kernel
+  // has none, and takes what that one takes)
+  const bool fp4 = p->kv_dtype == PA_KV_FP4_E2M1;
   if (!decode_uses_tc(p) && pt % p->block_size != 0)
     return set_error(PA_ERR_INVALID_ARG,
-                     "pa_decode: on the CUDA-core kernel partition_tokens must be a multiple of "
-                     "block_size");
+                     fp4 ? "pa_decode: with the 4-bit cache partition_tokens must be a multiple of "
+                           "block_size"
+                         : "pa_decode: on the CUDA-core kernel partition_tokens must be a multiple "
+                           "of block_size");
   // the CUDA-core kernel runs one CTA row per (sequence, new token) in grid z
   if (!decode_uses_tc(p) && int64_t(p->num_seqs) * query_len_of(p) > 65535)
     return set_error(PA_ERR_UNSUPPORTED,
-                     "pa_decode: on the CUDA-core kernel num_seqs * query_len must be <= 65535 "
-                     "(the tensor-core kernel takes num_kv_heads 1/2/4/8 and num_seqs * "
-                     "(query_len split into column groups) <= 16384)");
-  if (p->kv_dtype == PA_KV_FP4_E2M1 && !fp4_stream_ok(p))
+                     fp4 ? "pa_decode: the 4-bit cache takes num_seqs * query_len <= 65535"
+                         : "pa_decode: on the CUDA-core kernel num_seqs * query_len must be <= "
+                           "65535 (the tensor-core kernel takes num_kv_heads 1/2/4/8 and num_seqs "
+                           "* (query_len split into column groups) <= 16384)");
+  if (fp4 && !fp4_stream_ok(p))
     return set_error(PA_ERR_UNSUPPORTED,
                      "pa_decode: the 4-bit cache takes num_seqs * column groups * num_kv_heads * "
                      "(tokens / 32 + 9) below 2^31");

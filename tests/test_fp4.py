@@ -196,6 +196,20 @@ def test_decode_refusals(pk, kw, status):
     assert pk.load().pa_last_error()
 
 
+@pytest.mark.parametrize("kw,words", [
+    (dict(partition_tokens=48, block_size=32), b"partition_tokens must be a multiple of block_size"),
+    (dict(query_len=1024, num_seqs=64), b"num_seqs * query_len <= 65535"),
+    (dict(num_seqs=512, num_kv_heads=16, num_q_heads=16, max_blocks_per_seq=1 << 20,
+          max_context_len=1 << 24), b"below 2^31")])
+def test_decode_refusals_name_this_cache(pk, kw, words):
+    """What a refusal says is about the 4-bit cache, not about a kernel that it never takes."""
+    for variant in (0, 1):
+        p = _lib_params(pk, variant=variant, **kw)
+        assert pk.load().pa_decode(ctypes.byref(p), None, 0, None) in (1, 2)
+        got = pk.load().pa_last_error()
+        assert words in got and b"4-bit cache" in got and b"CUDA-core" not in got
+
+
 @pytest.mark.parametrize("name", ["pa_reshape_and_cache_fp4", "pa_gather_fp4"])
 @pytest.mark.parametrize("dims,status", [
     ((-1, 2, 64, 16, 4), 1), ((2, 0, 64, 16, 4), 1), ((2, 2, 96, 16, 4), 2),
