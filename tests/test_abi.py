@@ -422,3 +422,21 @@ def test_host_tensors_are_refused_by_name(pk):
     q, n = torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="q must live on a CUDA device"):
         pk.make_decode_params(q, q, k, k, pairs[:, :1], n, 16)
+
+
+@pytest.mark.parametrize("source", ["pa_weights.cu", "pa_decode_fp4.cu", "pa_fp4.cu", "pa_evict.cu"])
+def test_kernels_do_not_spill(source, tmp_path):
+    """ptxas keeps every kernel of the 4-bit cache, the token weights and the eviction in
+    registers: their variants and launch bounds were chosen so."""
+    import subprocess
+
+    from paged_kv_cache_92_gb300 import build
+
+    src = os.path.join(build.CSRC, source)
+    got = subprocess.run([build._nvcc(), *build.ARCH, "-O3", "-std=c++17", f"-I{build.INCLUDE}",
+                          "-lineinfo", "-Xptxas", "-v", "-cubin", "-o", str(tmp_path / "k.cubin"),
+                          src], capture_output=True, text=True, check=True)
+    lines = re.findall(r"function '(\w+)'.*?(\d+) bytes spill stores, (\d+) bytes spill loads",
+                       got.stderr, flags=re.S)
+    assert lines
+    assert [x for x in lines if x[1:] != ("0", "0")] == []
