@@ -945,3 +945,49 @@ def test_compacted_weights_of_long_rows(pk, budget):
         want[b, :n[b]] = w[b, keep[b, :n[b]]]
     assert np.array_equal(got.cpu().numpy(), want)
     assert pk.pa_device_errors() == 0
+
+
+def _check_weights(pk, c, stride, scale=None):
+    import torch
+
+    args, sc = c.args()
+    want, A = c.want(stride, scale)
+    tol = 2.0 ** -17 * (1 + A) * want + 1e-37
+    base = torch.rand(len(c.lens), stride, device="cuda")
+    w = pk.pa_token_weights(*args, base.clone(), accumulate=False, scale=scale, **sc)
+    got = w.cpu().double().numpy()
+    for b, L in enumerate(c.lens):
+        assert (np.abs(got[b, :L] - want[b, :L]) <= tol[b, :L]).all(), (b, A)
+        assert torch.equal(w[b, L:], base[b, L:])
+    assert pk.pa_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("Hq,Hkv,D,BS,Q", [(16, 4, 128, 16, 4), (8, 1, 128, 32, 2), (4, 4, 128, 8, 17),
+                                           (32, 8, 128, 16, 3), (2, 2, 64, 8, 9)])
+def test_token_weights_over_two_column_tiles(pk, fmt, Hq, Hkv, D, BS, Q):
+    """More than eight query rows a KV head, and partitions (128 tokens here) that end
+    among the new tokens, so that rows of one column group span different numbers of them."""
+    lens = [Q, 128, 128 + Q // 2, 127 + Q, 128 + Q, 255, 256 + Q // 2, 255 + Q, 300]
+    _check_weights(pk, Case(fmt, lens, Hq, Hkv, D, BS, Q, seed=Hq + BS + Q), 301)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,Q,lens", [(8, 2, 128, 130, [130, 131, 200, 333]),
+                                             (1, 1, 64, 1024, [1024, 1100])])
+def test_token_weights_of_prompt_chunks(pk, Hq, Hkv, D, Q, lens):
+    for fmt in ("bf16", "fp4"):
+        _check_weights(pk, Case(fmt, lens, Hq, Hkv, D, 16, Q, seed=Q), max(lens))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("Q", [1, 5])
+def test_token_weights_negative_and_zero_scales(pk, fmt, Q):
+    """A head scale's sign turns the scores, zero makes them equal."""
+    c = Case(fmt, [300, 47, 17], 8, 4, Q=Q, seed=11)
+    f = np.array([1, -1, 0, -8], np.float32)
+    c.s *= f
+    c.kval *= f[:, None, None]
+    _check_weights(pk, c, 300)

@@ -824,3 +824,16 @@ def test_decode_scores_of_millions(pk, big):
     for unit in np.linspace(2.4, 3.3, 19):  # of half a code in the log2 domain; 3 units are a jump
         scale = float(np.float32(unit * np.log(2.0) / (big * 2.0 ** -18)))
         _check_weights_range(pk, caches, tab, L, q, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,BS,Q,lens", [(8, 2, 128, 16, 130, [130, 131, 200, 333]),
+                                                (8, 1, 64, 32, 65, [65, 66, 96, 97, 700]),
+                                                (1, 1, 64, 16, 1024, [1024, 1100])])
+def test_decode_prompt_chunks(pk, Hq, Hkv, D, BS, Q, lens):
+    """Chunks of many new tokens: groups of columns in their dozens, up to the longest chunk."""
+    c = Case(lens, Hq, Hkv, D, BS, Q=Q, seed=Q)
+    args, sc = c.cuda()
+    _check(pk, pk.pa_decode(*args, **sc), c)
+    args, sc = c.cuda_cut()
+    _check(pk, pk.pa_decode(*args, **sc), c)
