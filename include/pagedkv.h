@@ -228,11 +228,13 @@ typedef struct {
  * pa_copy_blocks_fp4. One kernel decodes it whatever `variant` says: head_dim
  * 64 or 128, every block size, G in {1, 2, 4, 8}, any number of KV heads,
  * num_seqs * query_len <= 65535 and num_seqs * ceil(query_len / (8 / G)) *
- * num_kv_heads * (max_context_len / 32 + 9) < 2^31 (else PA_ERR_UNSUPPORTED;
- * max_context_len no more than the table holds). The codes are multiplied exactly; the
- * softmax weights are rounded to f16. With several new tokens, up to 8 / G of
- * them share each load of the keys. overlap_prologue and wait_timeout_us are
- * accepted and not used (the kernel waits on no barrier of its own). */
+ * num_kv_heads * (max_context_len / 32 + 9) < 2^31, max_context_len <= 2^31 - 64
+ * (else PA_ERR_UNSUPPORTED; max_context_len here no more than the table holds).
+ * The codes are multiplied exactly; the softmax weights are rounded to f16, by at
+ * most 2^-11 of their value or 2^-32 of the row's largest. With several new
+ * tokens, up to 8 / G of them share each load of the keys. overlap_prologue and
+ * wait_timeout_us are accepted and not used (the kernel waits on no barrier of
+ * its own). */
 #define PA_KV_FP4_E2M1 2
 
 #define PA_DECODE_TENSOR_CORE 0 /* tcgen05 MMAs, TMEM accumulators, tensor-map TMA ring */

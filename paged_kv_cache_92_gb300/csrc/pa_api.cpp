@@ -96,7 +96,7 @@ pa_status check_decode(const pa_decode_params* p, bool need_pointers) {
   if (fp4 && !fp4_stream_ok(p))
     return set_error(PA_ERR_UNSUPPORTED,
                      "pa_decode: the 4-bit cache takes num_seqs * column groups * num_kv_heads * "
-                     "(tokens / 32 + 9) below 2^31");
+                     "(tokens / 32 + 9) below 2^31, and at most 2^31 - 64 tokens a sequence");
   if (p->kv_dtype != PA_KV_BF16) {
     if (need_pointers && p->num_seqs > 0 &&
         (!p->k_scale || !p->v_scale || (reinterpret_cast<uintptr_t>(p->k_scale) & 3u) ||

@@ -46,11 +46,13 @@ struct Fp4Plan {
   bool whole;
 };
 Fp4Plan fp4_plan(const pa_decode_params* p, int num_sms);
-// Stream positions (steps and starts of every item) fit 32 bits.
+// Stream positions (steps and starts of every item) fit 32 bits, and so do the
+// keys of a sequence rounded up to whole steps.
 inline bool fp4_stream_ok(const pa_decode_params* p) {
   const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
   const int64_t cap = p->max_context_len < table ? p->max_context_len : table;
-  return double(p->num_seqs) * fp4_columns(p).n_groups * p->num_kv_heads *
+  return cap <= (int64_t(1) << 31) - 64 &&
+         double(p->num_seqs) * fp4_columns(p).n_groups * p->num_kv_heads *
              double(cap / 32 + 9) < 2147483648.0;
 }
 int launch_decode_fp4(const DecodeLaunch& L, const Fp4Plan& plan, void* stream);

@@ -210,6 +210,18 @@ def test_decode_refusals_name_this_cache(pk, kw, words):
         assert words in got and b"4-bit cache" in got and b"CUDA-core" not in got
 
 
+def test_decode_longest_sequence(pk):
+    """A sequence's steps are counted by rounding its length up in 32 bits."""
+    for blocks, status in ((2 ** 26 - 1, 2), (2 ** 26 - 2, 1)):  # 2^31 - 32 and - 64 tokens
+        p = _lib_params(pk, num_seqs=1, num_kv_heads=1, num_q_heads=1, block_size=32,
+                        max_blocks_per_seq=blocks, max_context_len=2 ** 31 - 1)
+        assert pk.load().pa_decode(ctypes.byref(p), None, 0, None) == status
+        assert (b"2^31 - 64" in pk.load().pa_last_error()) == (status == 2)
+        assert (pk.load().pa_decode_workspace_size(ctypes.byref(p)) > 0) == (status == 1)
+        p.max_context_len = 4096  # the bound on the lengths, whatever the tables hold
+        assert pk.load().pa_decode(ctypes.byref(p), None, 0, None) == 1
+
+
 @pytest.mark.parametrize("name", ["pa_reshape_and_cache_fp4", "pa_gather_fp4"])
 @pytest.mark.parametrize("dims,status", [
     ((-1, 2, 64, 16, 4), 1), ((2, 0, 64, 16, 4), 1), ((2, 2, 96, 16, 4), 2),
