@@ -3,7 +3,8 @@
 Argument marshalling only. Every step of the data path runs in the CUDA
 kernels of ``libpagedkv.so`` (see ``include/pagedkv.h``); torch supplies
 device memory and streams. There is no CPU fallback: if the library has not
-been built, every call raises.
+been built, every call raises. Calls run on the current CUDA device, and refuse
+(``ValueError``) tensors that are not on it.
 
 Names follow the C ABI: ``pa_decode``, ``pa_decode_workspace_size``,
 ``pa_reshape_and_cache``, ``pa_copy_blocks``, ``pa_device_errors`` and the

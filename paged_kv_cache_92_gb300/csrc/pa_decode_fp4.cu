@@ -28,7 +28,7 @@
 //  * P^T comes out of the first product transposed to what the second one
 //    wants; an 8x8 register transpose turns it.
 //  * Queries are scaled by a power of two per row into f16's range (exact for
-//    every element within 2^-30 of the row's largest) and the factor goes to
+//    every element within 2^-29 of the row's largest) and the factor goes to
 //    the softmax scale. P is rounded to f16, eight times finer than bf16 (no
 //    cheaper form exists); the running maximum, the sums and the output stay in
 //    fp32.

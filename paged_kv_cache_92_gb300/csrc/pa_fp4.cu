@@ -19,9 +19,14 @@
 //
 // Both kernels are bound by memory traffic: one thread per group of 16
 // elements reads or writes 32 bytes of bf16 and 9 bytes of cache. The codes of
-// a row are written by head_dim / 16 neighbouring threads, 8 bytes each. At a
-// decode step's sizes the launch is what they cost (64 tokens of 8 heads, d 128:
-// 4.6 us for the two of them, against 0.1 us of traffic).
+// a row are written by head_dim / 16 neighbouring threads, 8 bytes each. Neither
+// reaches the copy rate: past some 3 us of start and end (7 k tokens of 8 heads,
+// d 128, take 10.9 and 9.9 us, 29 k 34.3 and 31.1) they move 4.8 and 5.3 TB/s, with
+// two thirds of the issue slots busy -- the index of a thread is divided by the
+// groups of a row and by the heads, each of the 32 elements by its step -- and each
+// thread's one round of loads before its work. At a decode step's sizes the launch
+// is what they cost (64 tokens: 4.6 us for the two of them, against 0.1 us of
+// traffic).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -129,7 +134,7 @@ __device__ __forceinline__ uint2 quantise_group(const uint4& lo, const uint4& hi
 }
 
 // One thread per group, of K and of V: their loads are in flight together
-// (7 k tokens of 8 heads, dim 128: 11.8 us, 3.6 TB/s; one thread for each
+// (four prompts of 1.5 to 2 k tokens, 8 heads, dim 128: 11.8 us; one thread for each
 // 13.4 us). No pointer is __restrict__ here: what a kernel reads through its
 // read-only path must not change from its start on, and this one may start
 // before the preceding kernel has written it.
@@ -198,8 +203,8 @@ __device__ __forceinline__ void read_group(const uint2& codes, float sf, float s
 }
 
 // One thread per group of a row read back; blockIdx.y = 0 reads K, 1 reads V.
-// (A thread for both, as in the write, took 10.3 us on 7 k tokens of 8 heads
-// where this takes 9.2: here the stores are what is wide.)
+// (A thread for both, as in the write, took 10.3 us on those prompts where this
+// takes 9.2: here the stores are what is wide.)
 __global__ void __launch_bounds__(256)
     gather_fp4_kernel(const uint8_t* k_cache, const uint8_t* v_cache, uint4* k_out, uint4* v_out,
                       const int64_t* slot_mapping, const float* k_scale, const float* v_scale,

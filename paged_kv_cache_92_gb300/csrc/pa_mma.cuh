@@ -213,7 +213,8 @@ __device__ __forceinline__ void query_load(const __nv_bfloat16* row, bool on, in
 // A query row as the products' B operand; all lanes call together. bf16 rows
 // stay as they are and the result is 1. The others are scaled to f16 by a power
 // of two that brings the row's largest magnitude into [2^12, 2^13), exactly for
-// every element within 2^-30 of it, and its inverse is returned.
+// every element within 2^-29 of it (8 significant bits above f16's last, 2^-24),
+// and its inverse is returned.
 template <int FMT, int D>
 __device__ __forceinline__ float query_fragment(const uint4 (&raw)[D / 32],
                                                 uint32_t (&qf)[D / 16][2]) {

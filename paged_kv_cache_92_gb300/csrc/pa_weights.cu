@@ -17,15 +17,18 @@
 // The keys of a (sequence, KV head) are split into partitions, a CTA each, for
 // about 8 CTAs an SM when every sequence is as long as the longest. Measured
 // (GB300, copy rate 6.79 TB/s): 64 sequences of up to 2 k tokens, bf16, 32 / 8
-// heads: 31.4 us for 20.0 us of traffic (4.3 TB/s); 8 of 8 to 32 k, 4-bit, 64 /
-// 8 heads: 38.8 us for 15.6, of which the scores take about 28 (issue slots half
-// busy, DRAM 39 %: starts and the uneven ends of one wave of CTAs) and the sums
-// 10. Dropped: 10 to 16 CTAs an SM (41 to 42 us; for the bf16 batch 30.8 to 31.2),
-// a persistent stream as in the 4-bit decode (49), the partition as the slowest
-// grid index (+5 us), two or three ring stages, with as many more CTAs on an SM or
-// without (+4 to +20).
+// heads: 31.0 us for 20.0 us of traffic (4.3 TB/s), of which the scores take about
+// 26 (three CTAs of four warps on an SM, for the rings' shared memory; DRAM 61 %;
+// a third of the stalls are the lengths, tables and queries that a CTA starts with)
+// and the sums 5; 8 of 8 to 32 k, 4-bit, 64 / 8 heads: 38.8 us for 15.6, of which
+// the scores take about 28 (issue slots half busy, DRAM 39 %: starts and the uneven
+// ends of one wave of CTAs) and the sums 10. Dropped: 10 to 16 CTAs an SM (41 to 42
+// us; for the bf16 batch 30.8 to 31.2), a persistent stream as in the 4-bit decode
+// (49), the partition as the slowest grid index (+5 us), two or three ring stages,
+// with as many more CTAs on an SM or without (+4 to +20).
 // Scores, sums and weights are fp32; 8-bit and 4-bit rows enter the products
-// exactly (f16 holds them), so nothing is rounded below fp32.
+// exactly (f16 holds them), and so do the queries beside them (scaled to f16 by a
+// power of two: exact within 2^-29 of a row's largest element).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
