@@ -39,7 +39,10 @@
 //    value; lesser ones by at most 2^-32 of the largest (f16's subnormals, and zero
 //    below them). With the reference at the largest weight that would be 2^-25: a
 //    flat tail of a long context behind one large weight was lost, or half again as
-//    large as it is.
+//    large as it is. The difference is taken of the raw products, before the scale:
+//    the scaled maximum, rounded, is off by up to 16 units from 2^28 on, which f16
+//    does not hold (outputs were NaN). In pairs it costs what the single multiply-
+//    add did: 144.9 us for the batch below, 147.0 one by one.
 //  * Work is dealt out as a stream: every (sequence, column group, KV head) is
 //    an item of so many 32-key steps plus a start cost, and each of the
 //    persistent CTAs takes an equal stretch of the stream's cost, so ragged
@@ -79,7 +82,7 @@ constexpr int NTHREADS = NWARPS * 32;
 constexpr int KEYS = 32;  // keys of a warp's step
 constexpr int CTAS = 4;   // resident on an SM
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float HEADROOM = 7.0f;  // of the softmax reference below the maximum, log2
+constexpr float HEADROOM = 7.0f;  // log2 of the weight that the reference gets
 
 template <int D, int BS>
 struct Cfg {
@@ -391,10 +394,11 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
   }
 
   float o[D / 16][4];  // O^T: D / 16 tiles of 16 rows
-  // Softmax state of columns 2t and 2t+1, in the log2 domain: a score is
-  // s * factor (s the raw product), ref the reference (0 before the first key that
-  // the column sees), HEADROOM below the score that it was taken from, limit the
-  // raw product beyond which ref moves: 8 above that score.
+  // Softmax state of columns 2t and 2t+1. A score is s * factor in the log2 domain,
+  // s the raw product; ref is the raw product that the reference was taken from (0
+  // before the first key that the column sees), and a key's weight exp2((s - ref) *
+  // factor + HEADROOM): the difference comes first, as the last place of a large
+  // score is many units. limit: the raw product beyond which ref moves, 8 above it.
   float ref[2] = {0.0f, 0.0f}, limit[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
@@ -449,19 +453,17 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
         float x = fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2]));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * factor[c];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
         // no branch here: lanes of different columns decide differently, and
         // the warp-wide instructions below need them together
         const bool first = limit[c] == -INFINITY;
-        // beyond 2^20 the roundings of x and of the limit count: that much less room
-        const float slack = fabsf(x) * 0x1p-20f;
-        const float low = x - fmaxf(HEADROOM - slack, 0.0f);
-        const bool take = x != -INFINITY && (first || low > ref[c]);
-        const float y = take ? low : ref[c];
-        const float b = dev::fast_exp2(ref[c] - y);
+        const bool take = x != -INFINITY && (first || x > ref[c]);
+        const float y = take ? x : ref[c];
+        const float b = dev::fast_exp2((ref[c] - y) * factor[c]);
         const float a = take && first ? 0.0f : b;
         ref[c] = y;
-        limit[c] = take ? __fdividef(x + 8.0f - slack, factor[c]) : limit[c];
+        // rounded down, so that no weight passes 2^15
+        limit[c] = take ? __fadd_rd(x, __fdividef(8.0f - 0x1p-16f, factor[c])) : limit[c];
         l[c] *= a;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -476,9 +478,13 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
     for (int h = 0; h < 2; ++h) {
       float p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[j] = dev::fast_exp2(fmaf(s[h][j], factor[j & 1], -ref[j & 1]));
-        l[j & 1] += p[j];
+      for (int r = 0; r < 4; r += 2) {  // a row's two columns
+        const float2 e = dev::fma_pair(dev::sub_pair(make_float2(s[h][r], s[h][r + 1]), ref),
+                                       factor, HEADROOM);
+        p[r] = dev::fast_exp2(e.x);
+        p[r + 1] = dev::fast_exp2(e.y);
+        l[0] += p[r];
+        l[1] += p[r + 1];
       }
       pf[h][0] = dev::transpose_8x8(dev::pack_f16(p[0], p[1]));
       pf[h][1] = dev::transpose_8x8(dev::pack_f16(p[2], p[3]));
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(NTHREADS, CTAS)
     for (int x = 4; x < 32; x <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], x);
     const int n = warp * C::COLS + 2 * t + c;
     if (g == 0) {
-      sm_m[n] = limit[c] == -INFINITY ? -INFINITY : ref[c];
+      sm_m[n] = limit[c] == -INFINITY ? -INFINITY : fmaf(ref[c], factor[c], -HEADROOM);
       sm_l[n] = l[c];
     }
 #pragma unroll

@@ -82,6 +82,27 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return y;
 }
 
+// Pairs of floats in one instruction, each rounded as by itself.
+__device__ __forceinline__ float2 sub_pair(float2 a, const float (&b)[2]) {
+  float2 y;
+  asm("{\n\t.reg .b64 x, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 z, {%4, %5};\n\t"
+      "sub.rn.f32x2 x, x, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b[0]), "f"(b[1]));
+  return y;
+}
+// a * b + c
+__device__ __forceinline__ float2 fma_pair(float2 a, const float (&b)[2], float c) {
+  float2 y;
+  asm("{\n\t.reg .b64 x, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 z, {%4, %5};\n\tmov.b64 w, {%6, %6};\n\t"
+      "fma.rn.f32x2 x, x, z, w;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b[0]), "f"(b[1]), "f"(c));
+  return y;
+}
+
 // Key row of a 16-key tile that a thread with row index g (0..7) reads (its
 // other row is 8 further on). With 64-byte rows, rows 2i and 2i+1 differ in
 // parity, so the 16-byte reads of K are free of bank conflicts, and rows

@@ -849,3 +849,24 @@ def test_decode_prompt_chunks(pk, Hq, Hkv, D, BS, Q, lens):
     _check(pk, pk.pa_decode(*args, **sc), c)
     args, sc = c.cuda_cut()
     _check(pk, pk.pa_decode(*args, **sc), c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [20, 27, 28, 29, 31, 34, 40, 60])
+@pytest.mark.parametrize("low,high", [(6, 7), (15, 14)])  # codes: 4 and 6, or -6 and -4
+def test_decode_scores_of_any_size(pk, power, low, high):
+    """Scores of 2^power in the log2 domain, where a unit is far below their last place: the
+    largest share the weight and the others get none, as in exact arithmetic."""
+    import torch
+
+    L = 500
+    rng = np.random.default_rng(power)
+    keys = np.zeros((L, 64), np.uint8)
+    keys[:, 0] = low
+    keys[[70, 71, 300, 467], 0] = high
+    values = rng.integers(0, 16, (L, 64)).astype(np.uint8)
+    caches, tab = _ones_case(pk, keys, values)
+    q = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    for m in rng.uniform(1, 2, 12):
+        _check_weights_range(pk, caches, tab, L, q, float(np.float32(m * 2.0 ** power / 6)))
