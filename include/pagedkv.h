@@ -94,7 +94,11 @@ typedef enum {
                                         sequence); that token is not written */
 #define PA_DEVERR_KEEP 0x40u         /* pa_evict_compact: a keep entry that does not ascend or is
                                         past the source table (that row is not moved), or past the
-                                        token weights (that weight becomes 0) */
+                                        token weights (that weight becomes 0);
+                                        pa_decode_selected: a selected entry past the sequence's
+                                        blocks (it is skipped) */
+#define PA_DEVERR_POOL 0x80u         /* pa_update_tables: too few free blocks, or no room in the
+                                        ring for the released ones; nothing is done */
 
 const char* pa_status_string(pa_status s);
 const char* pa_last_error(void);
@@ -608,6 +612,169 @@ typedef struct {
   int32_t kv_dtype;
 } pa_evict_compact_params;
 pa_status pa_evict_compact(const pa_evict_compact_params* p, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Tables on the device: what pa_seq_append_tokens and pa_seq_free do for a batch on
+ * the host ([P1 §One step, end to end: allocate_slots]), where the lengths are on the
+ * device -- after pa_evict_select, or in a captured loop.
+ *
+ * Free blocks are a ring in device memory: of free_ring [ring_size] the `count` entries
+ * from `head` on (wrapping around) are free block ids; ring_state is {head, count, 0, 0}.
+ * Row b of block_tables holds blocks for old_lens[b] tokens and gets them for
+ * new_lens[b], with have = ceil(old_lens[b] / block_size), want = ceil(new_lens[b] /
+ * block_size), sequence after sequence:
+ *  - want > have: entries [have, want) become the next blocks from the ring's head;
+ *  - want < have: the blocks of entries [want, have) go to the ring's tail, in order
+ *    (they can be handed out from the next call on). The entries themselves are left as
+ *    they were: entries past a sequence's length are never read.
+ * The rows of tokens old_lens[b] <= t < new_lens[b], packed sequence after sequence:
+ *  - slot_mapping: block * block_size + offset, what pa_reshape_and_cache takes;
+ *  - positions: t;
+ *  - token_starts[b]: the first row of sequence b; token_starts[num_seqs] the number of
+ *    rows. Rows from there to max_new_tokens get slot and position -1 (padding, which
+ *    the KV writes skip).
+ * Blocks of a row must be its own: the ring knows no reference counts, so a released
+ * block that another row shares would be handed out while that row reads it. A ring may
+ * be filled with blocks that a pa_pool has handed out (pa_pool_alloc).
+ * All or nothing: if the blocks do not suffice (PA_DEVERR_POOL), if a length is negative
+ * or past the table row, or if there are more than max_new_tokens tokens
+ * (PA_DEVERR_CONTEXT_LEN), tables and ring stay as they are, slots and positions are -1
+ * and token_starts 0. new_ring_state is {head, count, short, 0}: short is 0 when the step
+ * was done, the number of missing blocks when they did not suffice, else -1.
+ * A ring entry or a released entry outside [0, num_blocks) sets PA_DEVERR_TABLE_ENTRY
+ * and is passed on as -1; so is an old entry that a new token's slot needs (that slot
+ * is -1).
+ * Lengths and state are read while outputs are written: no output may overlap them
+ * (PA_ERR_INVALID_ARG). A call may be repeated with the same arguments as long as the
+ * tables' old entries are unchanged: it gives the same result. num_seqs up to 65535;
+ * ring_size, max_new_tokens and the tokens of a table row below 2^30.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t* block_tables;       /* int32 [num_seqs][max_blocks_per_seq], updated */
+  const int32_t* old_lens;     /* int32 [num_seqs], tokens that the rows hold blocks for */
+  const int32_t* new_lens;     /* int32 [num_seqs], tokens that they shall hold blocks for */
+  int32_t* free_ring;          /* int32 [ring_size], updated */
+  const int32_t* ring_state;   /* int32 [4]: head, count; the others are not read */
+  int32_t* new_ring_state;     /* int32 [4], written */
+  int64_t* slot_mapping;       /* int64 [max_new_tokens] or NULL */
+  int32_t* positions;          /* int32 [max_new_tokens] or NULL */
+  int32_t* token_starts;       /* int32 [num_seqs + 1] or NULL */
+  int32_t max_blocks_per_seq;
+  int32_t num_seqs;
+  int32_t block_size;          /* 8, 16 or 32 */
+  int32_t num_blocks;          /* of the cache */
+  int32_t ring_size;           /* at least the blocks that the ring ever holds */
+  int32_t max_new_tokens;      /* rows of slot_mapping and positions; 0 if both are NULL */
+} pa_update_tables_params;
+pa_status pa_update_tables(const pa_update_tables_params* p, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over selected blocks. The pages read the whole context for every token; a
+ * long one mostly holds blocks that a query gives no weight to. A step is
+ *   pa_block_bounds    the bounds of the keys of the blocks that it wrote
+ *   pa_block_scores    how high a key of each block can score
+ *   pa_block_select    the blocks to read under a budget
+ *   pa_decode_selected the attention over them
+ * with a list of blocks per sequence and KV head. Every cache type, block size, head_dim
+ * 64 or 128, G in {1, 2, 4, 8}; table rows of up to 2^30 tokens.
+ *
+ * pa_block_bounds -- for every block that holds a token t with old_lens[b] <= t <
+ * context_lens[b] (old_lens NULL: all blocks of the sequences), every KV head and element:
+ * the least and the largest value among the keys of its tokens t < context_lens[b]
+ * (rows behind them do not count).
+ *   bounds  bf16 [num_blocks][num_kv_heads][2][head_dim]: least, largest; for the 8-bit
+ *           and 4-bit caches of code (* group scale), the head's scale left out. Exact
+ *           for every cache type. A NaN among the keys makes both NaN.
+ * Bounds of other blocks are left as they were. Two sequences that share a block write
+ * the same bounds if both hold all of its tokens. max_new_tokens is a host-known upper
+ * bound of context_lens[b] - old_lens[b]; blocks beyond those that so many tokens can
+ * touch are not done, and set PA_DEVERR_CONTEXT_LEN, as a length past the table row does.
+ * After pa_evict_compact or pa_copy_blocks the bounds of the written blocks are stale.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* k_cache;         /* of type kv_dtype, as in pa_decode_params */
+  void* bounds;                /* bf16 [num_blocks][num_kv_heads][2][head_dim], written */
+  const int32_t* block_tables; /* int32 [num_seqs][max_blocks_per_seq] */
+  const int32_t* context_lens; /* int32 [num_seqs] */
+  const int32_t* old_lens;     /* int32 [num_seqs] or NULL (zeros) */
+  int32_t max_blocks_per_seq;
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t max_new_tokens;      /* >= 1 */
+  int32_t kv_dtype;
+} pa_block_bounds_params;
+pa_status pa_block_bounds(const pa_block_bounds_params* p, pa_stream_t stream);
+
+/* pa_block_scores -- for every sequence b, KV head g and block j < ceil(context_lens[b] /
+ * block_size), over the query heads h of g and the new tokens i that see the block's
+ * first token (the causal rule of pa_decode):
+ *   scores[b][g][j] = max over i, h of  sum over d of max(f q_d least_d, f q_d largest_d),
+ *   f = scale * k_scale[g], q = q[b][i][h]
+ * which no logit of a key in the block exceeds. fp32. The sum is taken as f+ times (q's
+ * positive part . largest + q's negative part . least); where that is no number (an
+ * infinite or NaN bound), the score is +infinity. Entries from there on are left as they
+ * were, and so are the rows of a sequence of length 0 or with fewer keys than new tokens
+ * (the latter sets PA_DEVERR_CONTEXT_LEN). */
+typedef struct {
+  const void* q;               /* bf16 [num_seqs][query_len][num_q_heads][head_dim] */
+  const void* bounds;          /* of pa_block_bounds */
+  const float* k_scale;        /* float [num_kv_heads], or NULL (ones: the bf16 cache) */
+  const int32_t* block_tables; /* int32 [num_seqs][max_blocks_per_seq] */
+  const int32_t* context_lens; /* int32 [num_seqs], the new tokens included */
+  float* scores;               /* float [num_seqs][num_kv_heads][scores_stride], written */
+  int32_t scores_stride;       /* >= the blocks of min(max_context_len, a table row) tokens */
+  int32_t max_blocks_per_seq;
+  int32_t num_seqs;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t max_context_len;     /* host-known upper bound of every context_lens[b] (>= 1) */
+  float scale;                 /* the softmax scale: positive, finite */
+  int32_t query_len;           /* new tokens per sequence (0 or 1 = one), up to 1024 */
+} pa_block_scores_params;
+pa_status pa_block_scores(const pa_block_scores_params* p, pa_stream_t stream);
+
+/* pa_block_select -- the blocks that every (sequence, KV head) reads: all n =
+ * ceil(context_lens[b] / block_size) of them if they are at most `budget`, else the first
+ * `sink`, the last `recent` and, of the others, the budget - sink - recent with the
+ * largest scores (ties: the lower index; +0 and -0 are equal, a NaN ranks below every
+ * number).
+ *   selected  int32 [num_seqs][num_kv_heads][budget]: their indices, ascending; -1 behind
+ * scores: float [num_seqs][num_kv_heads][scores_stride]; blocks beyond scores_stride do
+ * not take part and set PA_DEVERR_CONTEXT_LEN. scores_stride and budget in [1, 2^30],
+ * sink and recent >= 0 with sink + recent <= budget. No workspace. */
+pa_status pa_block_select(const float* scores, const int32_t* context_lens, int32_t* selected,
+                          int32_t num_seqs, int32_t num_kv_heads, int32_t scores_stride,
+                          int32_t block_size, int32_t budget, int32_t sink, int32_t recent,
+                          pa_stream_t stream);
+
+/* pa_decode_selected -- pa_decode over the tokens of the selected blocks alone: of
+ * selected [num_seqs][num_kv_heads][num_selected] row (b, g) names the logical blocks (of
+ * sequence b) that the query heads of KV head g attend to. Of a row the first
+ * min(num_selected, ceil(context_lens[b] / block_size)) entries count; negative ones among
+ * them are skipped, one past the sequence's blocks is too and sets PA_DEVERR_KEEP. Any
+ * order; a block that is listed twice counts twice. A query token that sees none of the
+ * listed tokens (or whose every score is -infinity) gets a row of zeros.
+ * p is as in pa_decode: all caches, several new tokens (causal among them); the columns
+ * of a KV head's products are G heads of 8 / G new tokens, more of those read the blocks
+ * again. num_seqs * ceil(query_len / (8 / G)) * num_kv_heads below 2^27, table rows of up
+ * to 2^30 tokens (else PA_ERR_UNSUPPORTED). One kernel whatever `variant` says;
+ * partition_tokens, overlap_prologue and wait_timeout_us are checked like those of
+ * pa_decode and not used.
+ * Softmax weights: two bf16 terms (2^-17 of a weight is lost) with the bf16 cache; f16
+ * with the others, as in the 4-bit decode.
+ * Workspace: pa_decode_selected_workspace_size bytes, 256-byte aligned, contents on entry
+ * do not matter, not shared by two calls in flight; may be NULL where the size is 0 (it
+ * is 0 for params that are invalid, and where the kernel needs none). */
+size_t pa_decode_selected_workspace_size(const pa_decode_params* p, int32_t num_selected);
+pa_status pa_decode_selected(const pa_decode_params* p, const int32_t* selected,
+                             int32_t num_selected, void* workspace, size_t workspace_bytes,
+                             pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Host block pool [P1 §Paged attention; P2 §Prefix Caching and Copy-on-Write;

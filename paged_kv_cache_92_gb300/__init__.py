@@ -11,7 +11,9 @@ Names follow the C ABI: ``pa_decode``, ``pa_decode_workspace_size``,
 ``pa_pool_*`` / ``pa_seq_*`` block-pool calls (wrapped by ``Pool``). The cache
 calls have forms for the 8-bit (``_fp8``) and the 4-bit (``_fp4``) cache;
 ``pa_token_weights``, ``pa_evict_select``, ``pa_evict_compact`` and
-``Pool.compact`` evict tokens.
+``Pool.compact`` evict tokens; ``pa_update_tables`` keeps tables on the device;
+``pa_block_bounds``, ``pa_block_scores``, ``pa_block_select`` and
+``pa_decode_selected`` attend to the blocks that matter.
 """
 from __future__ import annotations
 
@@ -35,6 +37,7 @@ DEVERR_COPY_PAIR = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_APPEND_SLOT = 0x20
 DEVERR_KEEP = 0x40
+DEVERR_POOL = 0x80
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
@@ -49,6 +52,8 @@ EXPORTED_SYMBOLS = [
     "pa_copy_blocks",
     "pa_token_weights_workspace_size", "pa_token_weights", "pa_evict_select",
     "pa_evict_compact", "pa_pool_compact",
+    "pa_update_tables", "pa_block_bounds", "pa_block_scores", "pa_block_select",
+    "pa_decode_selected_workspace_size", "pa_decode_selected",
     "pa_pool_create", "pa_pool_destroy", "pa_pool_alloc", "pa_pool_incref", "pa_pool_decref",
     "pa_pool_refcount", "pa_pool_stats", "pa_seq_create", "pa_seq_free", "pa_seq_fork",
     "pa_seq_append_slot", "pa_seq_append_tokens", "pa_seq_length", "pa_seq_table",
@@ -119,6 +124,44 @@ class EvictCompactParams(ctypes.Structure):
         ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
         ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
         ("kv_dtype", ctypes.c_int32),
+    ]
+
+
+class UpdateTablesParams(ctypes.Structure):
+    _fields_ = [
+        ("block_tables", ctypes.c_void_p), ("old_lens", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p), ("free_ring", ctypes.c_void_p),
+        ("ring_state", ctypes.c_void_p), ("new_ring_state", ctypes.c_void_p),
+        ("slot_mapping", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("token_starts", ctypes.c_void_p),
+        ("max_blocks_per_seq", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+        ("ring_size", ctypes.c_int32), ("max_new_tokens", ctypes.c_int32),
+    ]
+
+
+class BlockBoundsParams(ctypes.Structure):
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p), ("bounds", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+        ("old_lens", ctypes.c_void_p),
+        ("max_blocks_per_seq", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+        ("max_new_tokens", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+    ]
+
+
+class BlockScoresParams(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("bounds", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+        ("scores", ctypes.c_void_p), ("scores_stride", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32), ("max_context_len", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("query_len", ctypes.c_int32),
     ]
 
 
@@ -193,6 +236,12 @@ def load():
         "pa_evict_select": ([vp, vp, vp, vp, i32, i32, i32, i32, vp], ctypes.c_int),
         "pa_evict_compact": ([P(EvictCompactParams), vp], ctypes.c_int),
         "pa_pool_compact": ([vp, vp, vp, i32], ctypes.c_int),
+        "pa_update_tables": ([P(UpdateTablesParams), vp], ctypes.c_int),
+        "pa_block_bounds": ([P(BlockBoundsParams), vp], ctypes.c_int),
+        "pa_block_scores": ([P(BlockScoresParams), vp], ctypes.c_int),
+        "pa_block_select": ([vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp], ctypes.c_int),
+        "pa_decode_selected_workspace_size": ([P(DecodeParams), i32], sz),
+        "pa_decode_selected": ([P(DecodeParams), vp, i32, vp, sz, vp], ctypes.c_int),
         "pa_pool_create": ([i32, i32, vp, P(vp)], ctypes.c_int),
         "pa_pool_destroy": ([vp], None),
         "pa_pool_alloc": ([vp, P(i32)], ctypes.c_int),
@@ -813,6 +862,192 @@ def pa_evict_compact(k_cache, v_cache, block_tables, dst_tables, keep, new_lens,
         0 if token_weights is None else token_weights.shape[1], block_tables.shape[1],
         dst_tables.shape[1], keep.shape[1], B, Hkv, D, BS, NB, fmt)
     _check(load().pa_evict_compact(ctypes.byref(p), _stream_handle(stream)), "pa_evict_compact")
+
+
+def make_free_ring(blocks, num_blocks: int, device="cuda"):
+    """A ring for ``pa_update_tables`` that holds the given free block ids (handed out in
+    this order) and has room for every block of a cache of ``num_blocks``. Returns
+    (free_ring int32 [num_blocks], ring_state int32 [4])."""
+    import torch
+
+    ids = np.asarray(list(blocks), dtype=np.int64)
+    if num_blocks < 1 or ids.ndim != 1 or len(set(ids.tolist())) != len(ids) \
+            or (len(ids) and (ids.min() < 0 or ids.max() >= num_blocks)):
+        raise ValueError("blocks must be distinct ids in [0, num_blocks)")
+    ring = np.full(num_blocks, -1, dtype=np.int32)
+    ring[:len(ids)] = ids
+    state = np.array([0, len(ids), 0, 0], dtype=np.int32)
+    return torch.from_numpy(ring).to(device), torch.from_numpy(state).to(device)
+
+
+def pa_update_tables(block_tables, old_lens, new_lens, free_ring, ring_state, new_ring_state,
+                     num_blocks: int, block_size: int, slot_mapping=None, positions=None,
+                     token_starts=None, stream=None) -> None:
+    """Tables on the device: row b of ``block_tables`` (int32 [B][max_blocks]), which
+    holds blocks for ``old_lens[b]`` tokens, gets them for ``new_lens[b]`` from the ring
+    of free blocks (``make_free_ring``), or gives the blocks behind back to it.
+    ``slot_mapping`` (int64 [T]), ``positions`` (int32 [T]) and ``token_starts`` (int32
+    [B + 1]) get the new tokens, packed, -1 behind; ``new_ring_state`` (int32 [4]) the
+    ring's state: head, count, and 0 where the step was done (see the C header)."""
+    import torch
+
+    B = old_lens.shape[0]
+    i32 = torch.int32
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or old_lens.shape != (B,) \
+            or new_lens.shape != (B,):
+        raise ValueError("block_tables must be [num_seqs][max_blocks], the lengths [num_seqs]")
+    if free_ring.dim() != 1 or ring_state.shape != (4,) or new_ring_state.shape != (4,):
+        raise ValueError("free_ring must be [ring_size], the states [4]")
+    rows = slot_mapping if slot_mapping is not None else positions
+    T = 0 if rows is None else rows.shape[0]
+    if (slot_mapping is not None and slot_mapping.shape != (T,)) \
+            or (positions is not None and positions.shape != (T,)) \
+            or (token_starts is not None and token_starts.shape != (B + 1,)):
+        raise ValueError("slot_mapping and positions must be [max_new_tokens], token_starts "
+                         "[num_seqs + 1]")
+    p = UpdateTablesParams(
+        _dev_ptr(block_tables, i32, "block_tables"), _dev_ptr(old_lens, i32, "old_lens"),
+        _dev_ptr(new_lens, i32, "new_lens"), _dev_ptr(free_ring, i32, "free_ring"),
+        _dev_ptr(ring_state, i32, "ring_state"), _dev_ptr(new_ring_state, i32, "new_ring_state"),
+        None if slot_mapping is None else _dev_ptr(slot_mapping, torch.int64, "slot_mapping"),
+        None if positions is None else _dev_ptr(positions, i32, "positions"),
+        None if token_starts is None else _dev_ptr(token_starts, i32, "token_starts"),
+        block_tables.shape[1], B, int(block_size), int(num_blocks), free_ring.shape[0], T)
+    _check(load().pa_update_tables(ctypes.byref(p), _stream_handle(stream)), "pa_update_tables")
+
+
+def block_bounds_shape(num_blocks: int, num_kv_heads: int, head_dim: int):
+    """Shape of the bounds of a cache's blocks (bf16): least and largest keys."""
+    return (num_blocks, num_kv_heads, 2, head_dim)
+
+
+def pa_block_bounds(k_cache, bounds, block_tables, context_lens, max_new_tokens: int,
+                    old_lens=None, stream=None):
+    """The least and the largest key, element by element, of every (block, KV head) that
+    holds a token from ``old_lens[b]`` on (None: from the first), written into ``bounds``
+    (bf16, ``block_bounds_shape``); returns it. K caches of every type; the head's scale
+    is left out. ``max_new_tokens`` is an upper bound of ``context_lens - old_lens``."""
+    import torch
+
+    fmt, D = kv_cache_format(k_cache)
+    NB, Hkv, BS, _ = k_cache.shape
+    tables = block_tables.shape
+    if tuple(bounds.shape) != (NB, Hkv, 2, D):
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
+    if len(tables) != 2 or context_lens.shape != tables[:1] \
+            or (old_lens is not None and old_lens.shape != tables[:1]):
+        raise ValueError("block_tables must be [num_seqs][max_blocks], the lengths [num_seqs]")
+    p = BlockBoundsParams(
+        _dev_ptr(k_cache, torch.bfloat16 if fmt == KV_BF16 else torch.uint8, "k_cache"),
+        _dev_ptr(bounds, torch.bfloat16, "bounds"),
+        _dev_ptr(block_tables, torch.int32, "block_tables"),
+        _dev_ptr(context_lens, torch.int32, "context_lens"),
+        None if old_lens is None else _dev_ptr(old_lens, torch.int32, "old_lens"),
+        tables[1], tables[0], Hkv, D, BS, NB, int(max_new_tokens), fmt)
+    _check(load().pa_block_bounds(ctypes.byref(p), _stream_handle(stream)), "pa_block_bounds")
+    return bounds
+
+
+def pa_block_scores(q, bounds, block_tables, context_lens, max_context_len: int, block_size: int,
+                    scores=None, scale: Optional[float] = None, k_scale=None, stream=None):
+    """An upper bound of the score that any key of a block reaches with any new token and
+    query head of a KV head: float32 [B][Hkv][stride], of which the blocks of each
+    sequence are written; returns it. q bf16 [B][Hq][D] or [B][Q][Hq][D]; ``k_scale`` is
+    the head scale of the 8-bit and 4-bit caches."""
+    import torch
+
+    shape = q.shape
+    if len(shape) == 4:
+        B, QL, Hq, D = shape
+    else:
+        (B, Hq, D), QL = shape, 0
+    NB, Hkv, two, D2 = bounds.shape
+    tables = block_tables.shape
+    if two != 2 or D2 != D:
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim], head_dim as in q")
+    if len(tables) != 2 or tables[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
+    if k_scale is not None and k_scale.numel() != Hkv:
+        raise ValueError("k_scale must be [num_kv_heads]")
+    if scores is None:
+        scores = _empty(stream, q, (B, Hkv, tables[1]), torch.float32)
+    if scores.dim() != 3 or scores.shape[:2] != (B, Hkv):
+        raise ValueError("scores must be [num_seqs][num_kv_heads][stride]")
+    p = BlockScoresParams(
+        _dev_ptr(q, torch.bfloat16, "q"), _dev_ptr(bounds, torch.bfloat16, "bounds"),
+        None if k_scale is None else _dev_ptr(k_scale, torch.float32, "k_scale"),
+        _dev_ptr(block_tables, torch.int32, "block_tables"),
+        _dev_ptr(context_lens, torch.int32, "context_lens"),
+        _dev_ptr(scores, torch.float32, "scores"), scores.shape[2], tables[1], B, Hq, Hkv, D,
+        int(block_size), NB, int(max_context_len),
+        float(1.0 / math.sqrt(D) if scale is None else scale), int(QL))
+    _check(load().pa_block_scores(ctypes.byref(p), _stream_handle(stream)), "pa_block_scores")
+    return scores
+
+
+def pa_block_select(scores, context_lens, block_size: int, budget: int, sink: int = 1,
+                    recent: int = 1, selected=None, stream=None):
+    """The blocks that every (sequence, KV head) reads under ``budget``: the first ``sink``,
+    the last ``recent`` and those with the largest scores. Returns ``selected`` (int32
+    [B][Hkv][budget], ascending, -1 behind)."""
+    import torch
+
+    if scores.dim() != 3 or context_lens.shape != scores.shape[:1]:
+        raise ValueError("scores must be [num_seqs][num_kv_heads][stride], context_lens [num_seqs]")
+    B, Hkv, stride = scores.shape
+    if selected is None:
+        selected = _empty(stream, scores, (B, Hkv, max(int(budget), 0)), torch.int32)
+    if selected.shape != (B, Hkv, budget):
+        raise ValueError("selected must be [num_seqs][num_kv_heads][budget]")
+    _check(load().pa_block_select(
+        _dev_ptr(scores, torch.float32, "scores"),
+        _dev_ptr(context_lens, torch.int32, "context_lens"),
+        _dev_ptr(selected, torch.int32, "selected"), B, Hkv, stride, int(block_size), int(budget),
+        int(sink), int(recent), _stream_handle(stream)), "pa_block_select")
+    return selected
+
+
+def _selected_shape(q, k_cache, selected) -> int:
+    if selected.dim() != 3 or selected.shape[0] != q.shape[0] \
+            or selected.shape[1] != k_cache.shape[1]:
+        raise ValueError("selected must be [num_seqs][num_kv_heads][num_selected]")
+    return selected.shape[2]
+
+
+def pa_decode_selected_workspace_size(q, k_cache, v_cache, block_tables, context_lens,
+                                      max_context_len: int, selected, k_scale=None,
+                                      v_scale=None) -> int:
+    """Workspace bytes of ``pa_decode_selected`` for these arguments."""
+    p = make_decode_params(q, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                           k_scale=k_scale, v_scale=v_scale)
+    return int(load().pa_decode_selected_workspace_size(
+        ctypes.byref(p), _selected_shape(q, k_cache, selected)))
+
+
+def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
+                       selected, scale: Optional[float] = None, out=None, workspace=None,
+                       stream=None, k_scale=None, v_scale=None):
+    """Paged decode attention over the blocks listed in ``selected`` (int32
+    [B][Hkv][num_selected], logical blocks of the sequence, negative ones skipped) alone;
+    returns ``out`` (bf16, the shape of ``q``). Caches of every type, one or several new
+    tokens, as in ``pa_decode``."""
+    import torch
+
+    lib = load()
+    n = _selected_shape(q, k_cache, selected)
+    if out is None:
+        out = _empty(stream, q, q.shape, q.dtype)
+    p = make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                           scale, k_scale=k_scale, v_scale=v_scale)
+    if workspace is None:
+        need = int(lib.pa_decode_selected_workspace_size(ctypes.byref(p), n))
+        if need > 0:
+            workspace = _empty(stream, q, need, torch.uint8)
+    ws_ptr = _dev_ptr(workspace, torch.uint8, "workspace") if workspace is not None else None
+    ws_bytes = workspace.numel() if workspace is not None else 0
+    _check(lib.pa_decode_selected(ctypes.byref(p), _dev_ptr(selected, torch.int32, "selected"), n,
+                                  ws_ptr, ws_bytes, _stream_handle(stream)), "pa_decode_selected")
+    return out
 
 
 def pa_device_errors(stream=None) -> int:

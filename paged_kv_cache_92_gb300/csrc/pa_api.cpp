@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "pa_blocks.h"
 #include "pa_fp4.h"
 #include "pa_internal.h"
 #include "pa_query_major.h"
@@ -430,7 +431,7 @@ pa_status pa_device_errors(pa_stream_t stream, uint32_t* flags) {
   if (!flags) return pa::set_error(PA_ERR_INVALID_ARG, "pa_device_errors: flags is NULL");
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return pa::set_cuda_error("pa_device_errors: stream sync", int(e));
-  uint32_t a = 0, b = 0, c = 0, d = 0, qm = 0, f4 = 0, d4 = 0, tw = 0, ev = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, qm = 0, f4 = 0, d4 = 0, tw = 0, ev = 0, ta = 0, bl = 0, se = 0;
   int r = pa::read_and_clear_decode_errors(&a);
   if (r == 0) r = pa::read_and_clear_decode_tc_errors(&c);
   if (r == 0) r = pa::read_and_clear_cache_errors(&b);
@@ -440,8 +441,11 @@ pa_status pa_device_errors(pa_stream_t stream, uint32_t* flags) {
   if (r == 0) r = pa::read_and_clear_decode_fp4_errors(&d4);
   if (r == 0) r = pa::read_and_clear_weights_errors(&tw);
   if (r == 0) r = pa::read_and_clear_evict_errors(&ev);
+  if (r == 0) r = pa::read_and_clear_tables_errors(&ta);
+  if (r == 0) r = pa::read_and_clear_blocks_errors(&bl);
+  if (r == 0) r = pa::read_and_clear_selected_errors(&se);
   if (r != 0) return pa::set_cuda_error("pa_device_errors: read", r);
-  *flags = a | b | c | d | qm | f4 | d4 | tw | ev;
+  *flags = a | b | c | d | qm | f4 | d4 | tw | ev | ta | bl | se;
   return PA_OK;
 }
 
@@ -970,6 +974,243 @@ pa_status pa_evict_compact(const pa_evict_compact_params* p, pa_stream_t stream)
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_evict_compact: misaligned pointer");
   const int e = pa::launch_evict_compact(p, stream);
   if (e != 0) return pa::set_cuda_error("pa_evict_compact: launch", e);
+  return PA_OK;
+}
+
+// ---- tables on the device, attention over selected blocks
+
+static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// Byte ranges [a, a + na) and [b, b + nb) meet (NULL meets nothing).
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+pa_status pa_update_tables(const pa_update_tables_params* p, pa_stream_t stream) {
+  constexpr int64_t kLimit = int64_t(1) << 30;
+  if (!p) return pa::set_error(PA_ERR_INVALID_ARG, "pa_update_tables: params is NULL");
+  if (p->num_seqs < 0 || p->num_seqs > 65535 || p->max_blocks_per_seq < 1 || p->num_blocks < 1 ||
+      p->ring_size < 1 || p->max_new_tokens < 0)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_update_tables: num_seqs in [0, 65535], max_new_tokens >= 0, the other "
+                         "counts positive");
+  if (!pa::block_size_ok(p->block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_update_tables: block_size must be 8, 16 or 32");
+  if (int64_t(p->max_blocks_per_seq) * p->block_size >= kLimit || p->ring_size >= kLimit ||
+      p->max_new_tokens >= kLimit)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_update_tables: ring_size, max_new_tokens and the tokens of a table row "
+                         "must be below 2^30");
+  if (!p->free_ring || !p->ring_state || !p->new_ring_state ||
+      (p->num_seqs > 0 && (!p->block_tables || !p->old_lens || !p->new_lens)))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_update_tables: a required pointer is NULL");
+  if (!p->slot_mapping && !p->positions && p->max_new_tokens != 0)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_update_tables: max_new_tokens without slot_mapping or positions");
+  if (misaligned4(p->block_tables) || misaligned4(p->old_lens) || misaligned4(p->new_lens) ||
+      misaligned4(p->free_ring) || misaligned4(p->ring_state) || misaligned4(p->new_ring_state) ||
+      misaligned4(p->positions) || misaligned4(p->token_starts) ||
+      (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_update_tables: misaligned pointer");
+  // every CTA reads all lengths and the state, in no order to the others' writes
+  const size_t lens = size_t(p->num_seqs) * 4;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } in[3] = {{p->old_lens, lens}, {p->new_lens, lens}, {p->ring_state, 16}},
+    out[6] = {{p->block_tables, lens * size_t(p->max_blocks_per_seq)},
+              {p->free_ring, size_t(p->ring_size) * 4},
+              {p->new_ring_state, 16},
+              {p->slot_mapping, size_t(p->max_new_tokens) * 8},
+              {p->positions, size_t(p->max_new_tokens) * 4},
+              {p->token_starts, lens + 4}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (overlap(o.at, o.bytes, i.at, i.bytes))
+        return pa::set_error(PA_ERR_INVALID_ARG,
+                             "pa_update_tables: an output overlaps the lengths or ring_state");
+  const int e = pa::launch_update_tables(p, pa::tc_grid(), stream);
+  if (e != 0) return pa::set_cuda_error("pa_update_tables: launch", e);
+  return PA_OK;
+}
+
+pa_status pa_block_bounds(const pa_block_bounds_params* p, pa_stream_t stream) {
+  if (!p) return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: params is NULL");
+  if (p->num_seqs < 0 || p->num_seqs > 65535 || p->num_kv_heads < 1 || p->num_kv_heads > 65535 ||
+      p->num_blocks < 1 || p->max_blocks_per_seq < 1 || p->max_new_tokens < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_bounds: num_seqs in [0, 65535], num_kv_heads in [1, 65535], the "
+                         "other counts positive");
+  if (!pa::block_size_ok(p->block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_block_bounds: block_size must be 8, 16 or 32");
+  if (p->head_dim != 64 && p->head_dim != 128)
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_block_bounds: head_dim must be 64 or 128");
+  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4_E2M1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_bounds: kv_dtype must be PA_KV_BF16, PA_KV_FP8_E4M3 or "
+                         "PA_KV_FP4_E2M1");
+  if (int64_t(p->max_blocks_per_seq) * p->block_size > kMaxEvictTokens)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: table rows of more than 2^30 tokens");
+  if (p->num_seqs == 0) return PA_OK;
+  if (!p->k_cache || !p->bounds || !p->block_tables || !p->context_lens)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: a required pointer is NULL");
+  if (!pa::aligned16(p->k_cache) || !pa::aligned16(p->bounds) || misaligned4(p->block_tables) ||
+      misaligned4(p->context_lens) || misaligned4(p->old_lens))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: misaligned pointer");
+  const int e = pa::launch_block_bounds(p, pa::tc_grid(), stream);
+  if (e != 0) return pa::set_cuda_error("pa_block_bounds: launch", e);
+  return PA_OK;
+}
+
+pa_status pa_block_scores(const pa_block_scores_params* p, pa_stream_t stream) {
+  if (!p) return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_scores: params is NULL");
+  if (p->num_seqs < 0 || p->num_seqs > 65535 || p->num_kv_heads < 1 || p->num_kv_heads > 65535 ||
+      p->num_q_heads < 1 || p->num_q_heads % p->num_kv_heads != 0 || p->num_blocks < 1 ||
+      p->max_blocks_per_seq < 1 || p->max_context_len < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_scores: num_seqs in [0, 65535], num_q_heads a positive multiple "
+                         "of num_kv_heads (<= 65535), the other counts positive");
+  if (!pa::block_size_ok(p->block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_block_scores: block_size must be 8, 16 or 32");
+  if (p->head_dim != 64 && p->head_dim != 128)
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_block_scores: head_dim must be 64 or 128");
+  const int g = p->num_q_heads / p->num_kv_heads;
+  if (g != 1 && g != 2 && g != 4 && g != 8)
+    return pa::set_error(PA_ERR_UNSUPPORTED,
+                         "pa_block_scores: query heads per KV head must be 1, 2, 4 or 8");
+  if (p->query_len < 0 || p->query_len > 1024)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_scores: query_len must be in [0, 1024]");
+  if (!(p->scale > 0.0f) || std::isinf(p->scale))
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_scores: scale must be a positive finite number");
+  const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
+  if (table > kMaxEvictTokens)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_scores: table rows of more than 2^30 tokens");
+  const int64_t cap = p->max_context_len < table ? p->max_context_len : table;
+  if (p->scores_stride < (cap + p->block_size - 1) / p->block_size)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_scores: scores_stride must cover the blocks of "
+                         "min(max_context_len, max_blocks_per_seq * block_size) tokens");
+  if (p->num_seqs == 0) return PA_OK;
+  if (!p->q || !p->bounds || !p->block_tables || !p->context_lens || !p->scores)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_scores: a required pointer is NULL");
+  if (!pa::aligned16(p->q) || !pa::aligned16(p->bounds) || misaligned4(p->block_tables) ||
+      misaligned4(p->context_lens) || misaligned4(p->scores) || misaligned4(p->k_scale))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_scores: misaligned pointer");
+  const int e = pa::launch_block_scores(p, pa::tc_grid(), stream);
+  if (e != 0) return pa::set_cuda_error("pa_block_scores: launch", e);
+  return PA_OK;
+}
+
+pa_status pa_block_select(const float* scores, const int32_t* context_lens, int32_t* selected,
+                          int32_t num_seqs, int32_t num_kv_heads, int32_t scores_stride,
+                          int32_t block_size, int32_t budget, int32_t sink, int32_t recent,
+                          pa_stream_t stream) {
+  if (num_seqs < 0 || num_seqs > 65535 || num_kv_heads < 1 || scores_stride < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_select: num_seqs in [0, 65535], num_kv_heads and scores_stride "
+                         "positive");
+  if (!pa::block_size_ok(block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_block_select: block_size must be 8, 16 or 32");
+  if (scores_stride > kMaxEvictTokens || budget > kMaxEvictTokens)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_select: scores_stride and budget at most 2^30");
+  if (int64_t(num_seqs) * num_kv_heads > INT32_MAX)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_select: num_seqs * num_kv_heads exceeds 2^31");
+  if (budget < 1 || sink < 0 || recent < 0 || int64_t(sink) + recent > budget)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_select: budget >= 1, sink and recent >= 0, sink + recent <= budget");
+  if (num_seqs == 0) return PA_OK;
+  if (!scores || !context_lens || !selected)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_select: a required pointer is NULL");
+  if (misaligned4(scores) || misaligned4(context_lens) || misaligned4(selected))
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_select: misaligned pointer");
+  const int e = pa::launch_block_select(scores, context_lens, selected, num_seqs, num_kv_heads,
+                                        scores_stride, block_size, budget, sink, recent, stream);
+  if (e != 0) return pa::set_cuda_error("pa_block_select: launch", e);
+  return PA_OK;
+}
+
+// Shapes of the decode over selected blocks. Its limits are its own: those of pa_decode
+// that come from that call's kernels are not asked for.
+static pa_status check_decode_selected(const pa_decode_params* p, int32_t num_selected,
+                                       const int32_t* selected, bool need_pointers) {
+  if (!p) return pa::set_error(PA_ERR_INVALID_ARG, "pa_decode_selected: params is NULL");
+  if (p->num_seqs < 0 || p->num_seqs > 65535)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_decode_selected: num_seqs must be in [0, 65535]");
+  if (p->num_q_heads < 1 || p->num_kv_heads < 1 || p->num_kv_heads > 65535 ||
+      p->num_q_heads % p->num_kv_heads != 0)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_decode_selected: num_q_heads must be a positive multiple of "
+                         "num_kv_heads (<= 65535)");
+  if (!pa::block_size_ok(p->block_size))
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_decode_selected: block_size must be 8, 16 or 32");
+  if (p->head_dim != 64 && p->head_dim != 128)
+    return pa::set_error(PA_ERR_UNSUPPORTED, "pa_decode_selected: head_dim must be 64 or 128");
+  const int g = p->num_q_heads / p->num_kv_heads;
+  if (g != 1 && g != 2 && g != 4 && g != 8)
+    return pa::set_error(PA_ERR_UNSUPPORTED,
+                         "pa_decode_selected: query heads per KV head must be 1, 2, 4 or 8");
+  if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4_E2M1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_decode_selected: kv_dtype must be PA_KV_BF16, PA_KV_FP8_E4M3 or "
+                         "PA_KV_FP4_E2M1");
+  if (p->num_blocks < 1 || p->max_blocks_per_seq < 1 || p->max_context_len < 1 || num_selected < 1)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_decode_selected: num_blocks, max_blocks_per_seq, max_context_len and "
+                         "num_selected must be positive");
+  if (p->query_len < 0 || p->query_len > 1024)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_decode_selected: query_len must be in [0, 1024]");
+  const int pt = pa::resolve_partition_tokens(p);
+  if (pt < pa::kBlockSize || pt > pa::kMaxPartitionTokens || pt % pa::kBlockSize != 0)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_decode_selected: partition_tokens must be 0 or a multiple of 16 in "
+                         "[16, 4096]");
+  if (p->variant != PA_DECODE_TENSOR_CORE && p->variant != PA_DECODE_CUDA_CORE)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_decode_selected: variant must be 0 (tensor core) or 1 (CUDA core)");
+  if (p->wait_timeout_us < 0)
+    return pa::set_error(PA_ERR_INVALID_ARG, "pa_decode_selected: wait_timeout_us must be >= 0");
+  if (!(p->scale > 0.0f) || std::isinf(p->scale))
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_decode_selected: scale must be a positive finite number");
+  if (int64_t(p->max_blocks_per_seq) * p->block_size > kMaxEvictTokens)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_decode_selected: table rows of more than 2^30 tokens");
+  if (int64_t(p->num_seqs) * pa::fp4_columns(p).n_groups * p->num_kv_heads >= (int64_t(1) << 27))
+    return pa::set_error(PA_ERR_UNSUPPORTED,
+                         "pa_decode_selected: num_seqs * ceil(query_len / (8 / G)) * num_kv_heads "
+                         "must be below 2^27");
+  if (need_pointers && p->num_seqs > 0) {
+    if (!p->q || !p->out || !p->k_cache || !p->v_cache || !p->block_tables || !p->context_lens ||
+        !selected || (p->kv_dtype != PA_KV_BF16 && (!p->k_scale || !p->v_scale)))
+      return pa::set_error(PA_ERR_INVALID_ARG, "pa_decode_selected: a required pointer is NULL");
+    if (!pa::aligned16(p->q) || !pa::aligned16(p->out) || !pa::aligned16(p->k_cache) ||
+        !pa::aligned16(p->v_cache) || misaligned4(p->block_tables) ||
+        misaligned4(p->context_lens) || misaligned4(selected) || misaligned4(p->k_scale) ||
+        misaligned4(p->v_scale))
+      return pa::set_error(PA_ERR_INVALID_ARG, "pa_decode_selected: misaligned pointer");
+  }
+  return PA_OK;
+}
+
+size_t pa_decode_selected_workspace_size(const pa_decode_params* p, int32_t num_selected) {
+  (void)check_decode_selected(p, num_selected, nullptr, false);
+  return 0;  // the partial results of a list meet in shared memory
+}
+
+pa_status pa_decode_selected(const pa_decode_params* p, const int32_t* selected,
+                             int32_t num_selected, void* workspace, size_t workspace_bytes,
+                             pa_stream_t stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  const pa_status st = check_decode_selected(p, num_selected, selected, true);
+  if (st != PA_OK) return st;
+  if (p->num_seqs == 0) return PA_OK;
+  const int e = pa::launch_decode_selected(
+      p, selected, num_selected, pa::selected_plan(p, num_selected, pa::tc_grid()), stream);
+  if (e != 0) return pa::set_cuda_error("pa_decode_selected: launch", e);
   return PA_OK;
 }
 
