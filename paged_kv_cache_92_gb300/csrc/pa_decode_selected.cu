@@ -19,12 +19,15 @@
 //    the same product (their queries are those of columns 0 to 3), so they cost none.
 //  * 8-bit and 4-bit codes become f16 pairs in registers (exact), as in the 4-bit
 //    decode, with its scaling of queries and its reference for P in f16.
-//  * `split` CTAs, a cluster, share the list of one (sequence, column group, KV head)
-//    and join their results through distributed shared memory: no workspace, no second
-//    launch.
+//  * Small batches: `split` CTAs, a cluster, share the list of one (sequence, column
+//    group, KV head) and join their results through distributed shared memory: no
+//    workspace, no second launch. Larger ones: the steps of all lists are a stream that
+//    the warps of persistent CTAs take equal stretches of, each by itself, so that no warp
+//    waits for another one and the copies run on from list to list; a second launch joins
+//    the lists that were cut.
 //  * Keys that a column must not see (behind the sequence, or behind one of several new
 //    tokens) have weight 0; where V holds no number there, 0 times it would still be
-//    none, so such steps zero those rows of V, for every new token by itself.
+//    none: in the steps that hold such keys, such elements of V are taken out first.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -47,7 +50,7 @@ __device__ unsigned int g_selected_errors;
 
 constexpr int NWARPS = 4;
 constexpr int NTHREADS = NWARPS * 32;
-constexpr int KEYS = 16;  // keys of a warp's step
+constexpr int TILE_KEYS = 16;  // keys of a product
 constexpr int COLS = 8;
 constexpr int MAX_SPLIT = 8;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -67,6 +70,12 @@ struct Sel {
   float scale_log2;
   int num_selected, max_blocks_per_seq, num_kv_heads, num_blocks, cap;
   int g_log2, q_len, q_group, n_groups;
+  int num_virtual;   // sequences * column groups
+  // of the streams:
+  int32_t* plan;     // [num_virtual + 1]: steps before each, then the total
+  float* part_ml;    // [2 * stretches][part_cols][2]: max, sum
+  float* part_acc;   // [2 * stretches][part_cols][D]
+  int part_cols;
 };
 
 template <int FMT, int D, int BS>
@@ -74,19 +83,26 @@ struct Cfg {
   static constexpr int ROWB = FMT == PA_KV_BF16 ? 2 * D : (FMT == PA_KV_FP8_E4M3 ? D : D / 2);
   static constexpr int SCALES = FMT == PA_KV_FP4_E2M1 ? D / 16 : 0;
   static constexpr int TILE = BS * (ROWB + SCALES);         // of one (block, KV head)
+  // keys of a warp's step: about 8 KB at head_dim 128 (of the codes half as much: what a
+  // step costs beside its keys is a tenth of its instructions)
+  static constexpr int KEYS = FMT == PA_KV_BF16 ? 16 : 32;
+  static constexpr int HALVES = KEYS / TILE_KEYS;           // products of a step
+  static constexpr int LEAST = 64 / KEYS;                   // steps of a stretch, at least
   static constexpr int HALF = KEYS * (ROWB + SCALES);       // K (or V) of a step
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int ST = FMT == PA_KV_BF16 ? 3 : 4;      // stages of a warp's ring
+  static constexpr int ST = 3;                              // stages of a warp's ring
   static constexpr int NBK = BS < KEYS ? KEYS / BS : 1;     // blocks of a step
   static constexpr int SPB = BS > KEYS ? BS / KEYS : 1;     // steps of a block
   static constexpr int WINDOW = 32 / NBK;                   // steps whose entries a warp holds
   static constexpr int RING = NWARPS * ST * STAGE;
+  // CTAs of the streams on an SM: by the rings, then by 65,536 registers
+  static constexpr int CTAS = D == 64 ? 4 : (FMT == PA_KV_FP4_E2M1 ? 3 : 2);
   static constexpr int OROW = D + 4;                        // padded row of the merge
   static constexpr int MERGE = NWARPS * COLS * OROW * 4;    // takes the rings' place at the end
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
-  // key row of a step that is row r (0..15) of the products
+  // key row of 16 that is row r of their product
   __device__ static __forceinline__ int key_of(int r) {
-    if constexpr (FMT == PA_KV_FP8_E4M3 && BS >= KEYS)
+    if constexpr (FMT == PA_KV_FP8_E4M3 && BS >= TILE_KEYS)
       // so that a lane's four keys are 4t to 4t + 3: one read of V^T
       return 4 * ((r & 7) >> 1) + (r & 1) + (r >> 3) * 2;
     else if constexpr (FMT == PA_KV_FP4_E2M1)
@@ -114,144 +130,86 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// A virtual sequence: column group `grp` of sequence b.
+struct Virtual {
+  int b, first_tok, n_tok;  // the group's first new token, its tokens
+  int see0;                 // keys that the first one sees
+  int blocks;               // of the sequence; 0: empty, or without room for the new tokens
+  int entries;              // of a list
+};
+__device__ __forceinline__ Virtual virtual_of(const Sel& P, int v, int bs) {
+  Virtual x;
+  x.b = v / P.n_groups;
+  x.first_tok = (v - x.b * P.n_groups) * P.q_group;
+  x.n_tok = min(P.q_group, P.q_len - x.first_tok);
+  int L = min(P.context_lens[x.b], P.cap);
+  L = L < P.q_len ? 0 : L;
+  x.see0 = L - P.q_len + x.first_tok + 1;
+  x.blocks = (L + bs - 1) / bs;
+  x.entries = min(P.num_selected, x.blocks);
+  return x;
+}
+
+// row of q / out of column n: new token n / G of the group, query head head * G + n % G
+__device__ __forceinline__ int64_t q_row(const Sel& P, const Virtual& v, int head, int n) {
+  return (int64_t(v.b) * P.q_len + v.first_tok + (n >> P.g_log2)) *
+             (int64_t(P.num_kv_heads) << P.g_log2) +
+         (head << P.g_log2) + (n & ((1 << P.g_log2) - 1));
+}
+
+// The queries and scales of a list, on their way: loaded some time before they are used.
 // DUP (bf16): columns 4 to 7 repeat columns 0 to 3 and take the second terms of P.
-template <int FMT, int D, int BS, bool DUP>
-__global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) {
-  using C = Cfg<FMT, D, BS>;
-  constexpr int ST = C::ST;
-  dev::griddep_enter();
-  cg::cluster_group cluster = cg::this_cluster();
-  const int split = int(cluster.num_blocks()), rank = int(cluster.block_rank());
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int G = 1 << P.g_log2;
-  const int num_q_heads = P.num_kv_heads << P.g_log2;
-  const int unit = blockIdx.x / split;
-  const int v = unit / P.num_kv_heads, head = unit - v * P.num_kv_heads;
-  const int b = v / P.n_groups, first_tok = (v - b * P.n_groups) * P.q_group;
-  const int n_tok = min(P.q_group, P.q_len - first_tok);
-  const int n_cols = n_tok << P.g_log2;
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float sm_m[NWARPS][COLS], sm_l[NWARPS][COLS];
-  __shared__ float2 sm_ml[COLS];          // of the CTA, read by the cluster
-  __shared__ int sm_pos[NWARPS][ST][2];   // position of the first key of a step's blocks
-  unsigned char* ring = smem + warp * ST * C::STAGE;
+template <int FMT, int D, bool DUP>
+struct Raw {
+  uint4 q[D / 32];  // column lane / 4; bf16: pairs 2t, 2t + 1 of 8 elements each
+  float k_scale, v_scale;
+  int n_tok, see0;
 
-  int L = P.context_lens[b];
-  if (L > P.cap || (L > 0 && L < P.q_len)) {
-    if (tid == 0 && rank == 0 && head == 0 && first_tok == 0)
-      atomicOr(&g_selected_errors, PA_DEVERR_CONTEXT_LEN);
-    L = L < P.q_len ? 0 : P.cap;
-  }
-  L = max(L, 0);
-  const int see0 = L == 0 ? 0 : L - P.q_len + first_tok + 1;  // keys that the first token sees
-  const int n_blocks = (L + BS - 1) / BS;
-  // this CTA's entries of the list
-  const int n_all = min(P.num_selected, n_blocks);
-  const int e0 = int(int64_t(n_all) * rank / split), e1 = int(int64_t(n_all) * (rank + 1) / split);
-  const int n_steps = C::NBK > 1 ? (e1 - e0 + C::NBK - 1) / C::NBK : (e1 - e0) * C::SPB;
-  const int n_my = n_steps > warp ? (n_steps - warp + NWARPS - 1) / NWARPS : 0;
-  const int32_t* list = P.selected + (int64_t(b) * P.num_kv_heads + head) * P.num_selected;
-  const int32_t* table = P.block_tables + int64_t(b) * P.max_blocks_per_seq;
-
-  // The entries of this warp's steps [w0, w0 + WINDOW), NBK a step, one a lane: the
-  // block's first position (NOWHERE: nothing is read) and its place in the pool.
-  unsigned errors = 0;
-  struct Entry {
-    int pos, block;
-  };
-  auto load_window = [&](int w0) {
-    const int step = warp + NWARPS * (w0 + lane / C::NBK);
-    const int e = e0 + (C::NBK > 1 ? step * C::NBK + lane % C::NBK : step / C::SPB);
-    Entry x{NOWHERE, 0};
-    if (e < e1) {
-      const int j = list[e];
-      if (j >= n_blocks) errors |= PA_DEVERR_KEEP;
-      if (j >= 0 && j < n_blocks) {
-        const int k = table[j];
-        if (k < 0 || k >= P.num_blocks)
-          errors |= PA_DEVERR_TABLE_ENTRY;
-        else
-          x = Entry{j * BS + (C::SPB > 1 ? step % C::SPB * KEYS : 0), k};
+  __device__ __forceinline__ void fetch(const Sel& P, const Virtual& v, int head) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n_cols = v.n_tok << P.g_log2, col = DUP ? g & 3 : g;
+    n_tok = v.n_tok;
+    see0 = v.see0;
+    const __nv_bfloat16* row = P.q + q_row(P, v, head, min(col, n_cols - 1)) * D;
+    // (nothing that needs the values: the warp would wait for them)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      if constexpr (FMT == PA_KV_BF16) {
+        const uint32_t* x = reinterpret_cast<const uint32_t*>(row + 32 * i + 2 * t);
+        q[i] = make_uint4(x[0], x[4], x[8], x[12]);
+      } else {  // the order of the codes' fragments
+        constexpr int E = dev::KeyRow<FMT, D>::E;
+        q[i] = *reinterpret_cast<const uint4*>(row + (4 * (8 * i / E) + t) * E + 8 * i % E);
       }
     }
-    return x;
-  };
-  Entry window = load_window(0);
-  // One copy group: step i of the warp, empty past the last.
-  auto issue = [&](int i, int stage) {
-    unsigned char* st = ring + stage * C::STAGE;
-#pragma unroll
-    for (int n = 0; n < C::NBK; ++n) {
-      const int src = i % C::WINDOW * C::NBK + n;
-      const int pos = __shfl_sync(0xffffffffu, window.pos, src);
-      const int block = __shfl_sync(0xffffffffu, window.block, src);
-      if (i < n_my) {
-        if (lane == 0) sm_pos[warp][stage][n] = pos;
-        const int64_t at = (int64_t(block) * P.num_kv_heads + head) * C::TILE;
-        const int row0 = C::SPB > 1 ? pos % BS : 0;  // of the step in its block
-        const bool on = pos != NOWHERE;
-        constexpr int ROWS = BS < KEYS ? BS : KEYS;   // of the block in a step
-        // rows (of a code's V in 8 bits: columns) in 16-byte chunks
-        constexpr int CHUNKS = ROWS * C::ROWB / 16;
-#pragma unroll
-        for (int c = 0; c < CHUNKS; c += 32) {
-          const int x = c + lane;
-          const bool in = on && (c + 32 <= CHUNKS || x < CHUNKS);
-          constexpr int CPR = C::ROWB / 16;  // chunks of a row
-          const int r = n * ROWS + x / CPR, k = x % CPR;
-          int kd = r * C::ROWB, vd = n * ROWS * C::ROWB + x * 16;
-          if constexpr (FMT == PA_KV_BF16) {
-            kd += (k ^ (r & 7)) * 16;
-            vd = kd;
-          } else if constexpr (FMT == PA_KV_FP8_E4M3 && D == 128) {
-            kd += (k ^ ((r & 1) << 2)) * 16;
-          } else {
-            kd += k * 16;
-          }
-          dev::cp_async16(st + kd, P.k_cache + at + row0 * C::ROWB + x * 16, in);
-          dev::cp_async16(st + C::HALF + vd, P.v_cache + at + row0 * C::ROWB + x * 16, in);
-        }
-        if constexpr (C::SCALES > 0) {
-          constexpr int N = ROWS * C::SCALES / 16;  // chunks of scales, of K then of V
-          const bool of_v = lane >= N;
-          const int x = of_v ? lane - N : lane;
-          const unsigned char* from = (of_v ? P.v_cache : P.k_cache) + at + BS * C::ROWB +
-                                      row0 * C::SCALES + x * 16;
-          dev::cp_async16(st + (of_v ? C::HALF : 0) + KEYS * C::ROWB + n * ROWS * C::SCALES + x * 16,
-                          from, on && lane < 2 * N);
-        }
-      }
-    }
-    dev::cp_async_commit();
-  };
-
-  // row of q / out of column n: new token n / G of the group, query head head * G + n % G
-  auto q_row = [&](int n) {
-    return (int64_t(b) * P.q_len + first_tok + (n >> P.g_log2)) * num_q_heads + head * G +
-           (n & (G - 1));
-  };
-#pragma unroll
-  for (int i = 0; i < ST - 1; ++i) issue(i, i);
-
-  uint32_t qf[D / 16][2];  // the queries as the B operand (column g)
-  float inv_scaling = 1.0f, k_scale = 1.0f;
-  {
-    const int col = DUP ? g & 3 : g;
-    const __nv_bfloat16* row = P.q + q_row(min(col, n_cols - 1)) * D;
-    if constexpr (FMT == PA_KV_BF16) {
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t x = *reinterpret_cast<const uint32_t*>(row + s * 16 + i * 8 + t * 2);
-          qf[s][i] = col < n_cols ? x : 0u;
-        }
-    } else {
-      uint4 raw[D / 32];
-      dev::query_load<FMT, D>(row, col < n_cols, t, raw);
-      inv_scaling = dev::query_fragment<FMT, D>(raw, qf);
+    k_scale = v_scale = 1.0f;
+    if constexpr (FMT != PA_KV_BF16) {
       k_scale = P.k_scale[head];
+      v_scale = P.v_scale[head];
+    }
+  }
+};
+
+// What a warp needs of a list at hand.
+template <int FMT, int D, bool DUP>
+struct Columns {
+  uint32_t qf[D / 16][2];  // the queries as the B operand (column lane / 4)
+  float factor[2];  // of columns 2t and 2t+1: softmax scale * K scale / the row's scaling
+  int see[2];       // keys that they see
+  int see0, n_tok;
+  float v_scale;
+
+  __device__ __forceinline__ void take(const Sel& P, Raw<FMT, D, DUP>& raw) {
+    const int t = threadIdx.x & 3, g = (threadIdx.x & 31) >> 2;
+    if ((DUP ? g & 3 : g) >= raw.n_tok << P.g_log2)  // no query: zeros
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raw.q[i] = uint4{};
+    see0 = raw.see0;
+    n_tok = raw.n_tok;
+    v_scale = raw.v_scale;
+    const float inv_scaling = dev::query_fragment<FMT, D>(raw.q, qf);
+    float k_scale = raw.k_scale;
+    if constexpr (FMT != PA_KV_BF16) {
       // a negative scale turns the queries, so that a larger product stays a larger score
       const uint32_t sign = k_scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
@@ -261,123 +219,225 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
       }
       k_scale = fabsf(k_scale);
     }
-  }
-  float factor[2];  // of columns 2t and 2t+1: softmax scale * K scale / the row's scaling
-  int see[2];       // keys that they see
-  int tok[2];       // their new token, in the group
-  const float row_factor = P.scale_log2 * k_scale * inv_scaling;
+    const float row_factor = P.scale_log2 * k_scale * inv_scaling;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    factor[c] = __shfl_sync(0xffffffffu, row_factor, 4 * (2 * t + c));
-    // A scale of zero makes all scores equal, but 0 * -inf is NaN: below 2^-100 the
-    // products (under 2^35) count as zero either way. The comparison keeps a NaN scale.
-    if (FMT != PA_KV_BF16) factor[c] = factor[c] < 0x1p-100f ? 0x1p-100f : factor[c];
-    const int col = DUP ? (2 * t + c) & 3 : 2 * t + c;
-    tok[c] = min(col >> P.g_log2, n_tok - 1);
-    see[c] = see0 + tok[c];
+    for (int c = 0; c < 2; ++c) {
+      factor[c] = __shfl_sync(0xffffffffu, row_factor, 4 * (2 * t + c));
+      // A scale of zero makes all scores equal, but 0 * -inf is NaN: below 2^-100 the
+      // products (under 2^35) count as zero either way. The comparison keeps a NaN scale.
+      if (FMT != PA_KV_BF16) factor[c] = factor[c] < 0x1p-100f ? 0x1p-100f : factor[c];
+      const int n = DUP ? (2 * t + c) & 3 : 2 * t + c;
+      see[c] = see0 + min(n >> P.g_log2, n_tok - 1);
+    }
   }
+};
 
-  // Softmax state of columns 2t and 2t+1: a key's weight is exp2((s - ref) * factor +
-  // HEADROOM), s the raw product and ref the one that the reference was taken from (0
-  // before the first key that the column sees): the difference comes first, as the last
-  // place of a large score is many units. limit: the raw product beyond which ref moves,
-  // 8 above it, so that no weight passes 2^15.
+// Softmax state of columns 2t and 2t+1: a key's weight is exp2((s - ref) * factor +
+// HEADROOM), s the raw product and ref the one that the reference was taken from (0
+// before the first key that the column sees): the difference comes first, as the last
+// place of a large score is many units. limit: the raw product beyond which ref moves,
+// 8 above it, so that no weight passes 2^15.
+template <int FMT, int D, int BS, bool DUP>
+struct State {
+  using C = Cfg<FMT, D, BS>;
   float o[D / 16][4];  // O^T: D / 16 tiles of 16 rows
-  float ref[2] = {0.0f, 0.0f}, limit[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+  float ref[2], limit[2], l[2];
 
-  // A fragments of V^T: rows d (16 i .. 16 i + 15 in some order), keys of the products' rows.
-  auto v_fragment = [&](const unsigned char* vt, int i, uint32_t (&a)[4]) {
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      ref[c] = l[c] = 0.0f;
+      limit[c] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+  }
+
+  // A fragments of V^T: rows d = 16 i .. 16 i + 15, keys of the products' rows.
+  __device__ static __forceinline__ void v_fragment(const unsigned char* vt, int i,
+                                                    uint32_t (&a)[4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if constexpr (FMT == PA_KV_BF16) {
       // lanes 8 m .. 8 m + 7 name the rows of matrix m: keys (m / 2) * 8 .., chunk 2 i + m % 2
       const int m = lane >> 3, r = (m >> 1) * 8 + (lane & 7);
       ldmatrix_x4_trans(a, vt + r * C::ROWB + (((2 * i + (m & 1)) ^ (r & 7)) * 16));
-    } else if constexpr (FMT == PA_KV_FP8_E4M3) {
-      if constexpr (BS >= KEYS) {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(vt + (16 * i + g) * 16 + 4 * t);
-        const uint32_t y = *reinterpret_cast<const uint32_t*>(vt + (16 * i + g + 8) * 16 + 4 * t);
-        a[0] = dev::e4m3x2_to_f16(x & 0xffffu);
-        a[1] = dev::e4m3x2_to_f16(y & 0xffffu);
-        a[2] = dev::e4m3x2_to_f16(x >> 16);
-        a[3] = dev::e4m3x2_to_f16(y >> 16);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)  // block k / 2, row g or g + 8
-          a[k] = dev::e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(
-              vt + (k >> 1) * BS * D + (16 * i + g + (k & 1) * 8) * BS + 2 * t));
-      }
-    }
-  };
-
-  // One step; with EDGE one that holds keys which some column does not see.
-  auto step = [&](int stage, int pos0, int pos1, auto edge_t) {
-    constexpr bool EDGE = decltype(edge_t)::value;
-    const unsigned char* kt = ring + stage * C::STAGE;
-    const unsigned char* vt = kt + C::HALF;
-    auto position = [&](int r) {  // of row r of the products
-      const int k = C::key_of(r);
-      return C::NBK > 1 ? (k < BS ? pos0 + k : pos1 + k - BS) : pos0 + k;
-    };
-    float s[4];
-    if constexpr (FMT == PA_KV_BF16) {
-      float s2[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s2[h][j] = 0.0f;
-      // matrix m: keys (m % 2) * 8 .., chunk 2 i + m / 2
-      const int m = lane >> 3, r = (m & 1) * 8 + (lane & 7);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t a[4];
-        ldmatrix_x4(a, kt + r * C::ROWB + (((2 * i + (m >> 1)) ^ (r & 7)) * 16));
-        dev::mma_bf16_regs(s2[i & 1], a[0], a[1], a[2], a[3], qf[i][0], qf[i][1]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = s2[0][j] + s2[1][j];
+    } else if constexpr (BS >= TILE_KEYS) {
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(vt + (16 * i + g) * 16 + 4 * t);
+      const uint32_t y = *reinterpret_cast<const uint32_t*>(vt + (16 * i + g + 8) * 16 + 4 * t);
+      a[0] = dev::e4m3x2_to_f16(x & 0xffffu);
+      a[1] = dev::e4m3x2_to_f16(y & 0xffffu);
+      a[2] = dev::e4m3x2_to_f16(x >> 16);
+      a[3] = dev::e4m3x2_to_f16(y >> 16);
     } else {
-      using Row = dev::KeyRow<FMT, D>;
-      Row rows[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = C::key_of(g + 8 * h);
-        if constexpr (FMT == PA_KV_FP8_E4M3 && D == 128) {
-          // (runs t and t + 4 of the row, permuted as they were copied)
-          const uint4 x = *reinterpret_cast<const uint4*>(kt + r * D + ((t ^ ((r & 1) << 2)) * 16));
-          const uint4 y =
-              *reinterpret_cast<const uint4*>(kt + r * D + (((t + 4) ^ ((r & 1) << 2)) * 16));
-          rows[h].w[0] = x.x; rows[h].w[1] = x.y; rows[h].w[2] = x.z; rows[h].w[3] = x.w;
-          rows[h].w[4] = y.x; rows[h].w[5] = y.y; rows[h].w[6] = y.z; rows[h].w[7] = y.w;
+      for (int k = 0; k < 4; ++k)  // block k / 2, row g or g + 8
+        a[k] = dev::e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(
+            vt + (k >> 1) * BS * D + (16 * i + g + (k & 1) * 8) * BS + 2 * t));
+    }
+  }
+
+  // position of row r of product h of a step whose blocks begin at `pos`
+  __device__ static __forceinline__ int position(const int (&pos)[C::NBK], int h, int r) {
+    const int k = C::key_of(r);
+    if constexpr (BS < TILE_KEYS)
+      return k < BS ? pos[2 * h] + k : pos[2 * h + 1] + k - BS;
+    else
+      return pos[h * TILE_KEYS / BS] + h * TILE_KEYS % BS + k;
+  }
+  // The same of key k of the step.
+  __device__ static __forceinline__ int key_position(const int* pos, int k) {
+    return pos[k / BS] + k % BS;
+  }
+
+  // Element d of V's key k in a stage: where it lies (of a 4-bit V its group scale, the
+  // codes being finite), and its value where that is no finite number, else 0.
+  __device__ static __forceinline__ unsigned char* v_place(unsigned char* stage, int k, int d) {
+    unsigned char* vt = stage + C::HALF;
+    if constexpr (FMT == PA_KV_BF16) return vt + k * C::ROWB + ((d / 8) ^ (k & 7)) * 16 + d % 8 * 2;
+    constexpr int W = BS < TILE_KEYS ? BS : TILE_KEYS;  // keys of a sub-tile of V^T
+    if constexpr (FMT == PA_KV_FP8_E4M3) return vt + k / W * W * D + d * W + k % W;
+    return vt + C::KEYS * C::ROWB + k * C::SCALES + d / 16;
+  }
+  __device__ static __forceinline__ float not_finite(const unsigned char* at) {
+    if constexpr (FMT == PA_KV_BF16) {
+      const float x = __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(at)) << 16);
+      return isfinite(x) ? 0.0f : x;
+    } else {
+      return (*at & 0x7F) == 0x7F ? NAN : 0.0f;
+    }
+  }
+
+  // For a step that holds keys which some column does not see: their weight is 0 there,
+  // but 0 times what is no number is none. Rows of V that no column sees become zero. In
+  // those that some see, so do the infinities and NaN, and are added to these columns
+  // here (a weight is positive).
+  __device__ __forceinline__ void clear_unseen(unsigned char* stage, const int* pos,
+                                               const Columns<FMT, D, DUP>& q) {
+    const int lane = threadIdx.x & 31;
+    const int see_last = q.see0 + q.n_tok - 1;
+#pragma unroll 1
+    for (int k = 0; k < C::KEYS; ++k) {
+      const int at = key_position(pos, k);
+      if (at >= see_last) {
+        if constexpr (FMT == PA_KV_FP4_E2M1) {
+          if (lane < C::SCALES) *v_place(stage, k, lane * 16) = 0;
+        } else if constexpr (FMT == PA_KV_BF16) {
+          if (lane < D / 8) *reinterpret_cast<uint4*>(v_place(stage, k, lane * 8)) = uint4{};
         } else {
-          rows[h].load(kt + r * C::ROWB + t * Row::RUN,
-                       kt + KEYS * C::ROWB + r * C::SCALES + t * (D / 64));
+#pragma unroll
+          for (int d = lane; d < D; d += 32) *v_place(stage, k, d) = 0;
+        }
+      } else if (at >= q.see0) {
+        float bad[D / 16][2];
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            bad[i][j] = not_finite(v_place(stage, k, element(i, 2 * j)));
+            any |= bad[i][j] != 0.0f;  // (true of a NaN)
+          }
+        if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (bad[i][j] != 0.0f) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  // (of two equal columns the first takes it)
+                  if (at < q.see[c] && !(DUP && (threadIdx.x & 3) >= 2)) o[i][2 * j + c] += bad[i][j];
+                unsigned char* x = v_place(stage, k, element(i, 2 * j));
+                if constexpr (FMT == PA_KV_BF16)
+                  *reinterpret_cast<uint16_t*>(x) = 0;
+                else
+                  *x = 0;
+              }
         }
       }
-      float s1[1][4] = {{0.0f, 0.0f, 0.0f, 0.0f}};
-      uint32_t q1[1][D / 16][2];
+      __syncwarp();
+    }
+  }
+
+  // One step, its blocks' first positions `blocks`.
+  __device__ __forceinline__ void step(unsigned char* stage, const int* blocks,
+                                       const Columns<FMT, D, DUP>& q) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    int pos[C::NBK];
+    bool edge = false;  // keys that some column does not see
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        q1[0][i][0] = qf[i][0];
-        q1[0][i][1] = qf[i][1];
+    for (int n = 0; n < C::NBK; ++n) {
+      pos[n] = blocks[n];
+      edge |= pos[n] + (BS < C::KEYS ? BS : C::KEYS) > q.see0;
+    }
+    float s[C::HALVES][4];
+#pragma unroll
+    for (int h = 0; h < C::HALVES; ++h) {
+      const unsigned char* kt = stage + h * TILE_KEYS * C::ROWB;
+      float s2[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2[i][j] = 0.0f;
+      if constexpr (FMT == PA_KV_BF16) {
+        // matrix m: keys (m % 2) * 8 .., chunk 2 i + m / 2
+        const int m = lane >> 3, r = (m & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t a[4];
+          ldmatrix_x4(a, kt + r * C::ROWB + (((2 * i + (m >> 1)) ^ (r & 7)) * 16));
+          dev::mma_bf16_regs(s2[i & 1], a[0], a[1], a[2], a[3], q.qf[i][0], q.qf[i][1]);
+        }
+      } else {
+        using Row = dev::KeyRow<FMT, D>;
+        Row rows[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = C::key_of(g + 8 * i);
+          if constexpr (FMT == PA_KV_FP8_E4M3 && D == 128) {
+            // (runs t and t + 4 of the row, permuted as they were copied)
+            const uint4 x =
+                *reinterpret_cast<const uint4*>(kt + r * D + ((t ^ ((r & 1) << 2)) * 16));
+            const uint4 y =
+                *reinterpret_cast<const uint4*>(kt + r * D + (((t + 4) ^ ((r & 1) << 2)) * 16));
+            rows[i].w[0] = x.x; rows[i].w[1] = x.y; rows[i].w[2] = x.z; rows[i].w[3] = x.w;
+            rows[i].w[4] = y.x; rows[i].w[5] = y.y; rows[i].w[6] = y.z; rows[i].w[7] = y.w;
+          } else {
+            rows[i].load(kt + r * C::ROWB + t * Row::RUN,
+                         stage + C::KEYS * C::ROWB + (h * TILE_KEYS + r) * C::SCALES + t * (D / 64));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[4], y[4];
+          rows[0].pairs(c, x);
+          rows[1].pairs(c, y);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            dev::mma_f16(s2[k], x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1],
+                         q.qf[2 * c + k][0], q.qf[2 * c + k][1]);
+        }
       }
-      dev::key_product<FMT, D, 1>(s1, rows[0], rows[1], q1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = s1[0][j];
+      for (int j = 0; j < 4; ++j) s[h][j] = s2[0][j] + s2[1][j];
     }
     // ---- softmax; keys that a column does not see are -inf
     bool over = false;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (EDGE && position(g + (j >> 1) * 8) >= see[j & 1]) s[j] = -INFINITY;
-      over |= s[j] > limit[j & 1];
-    }
+    for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (position(pos, h, g + (j >> 1) * 8) >= q.see[j & 1]) s[h][j] = -INFINITY;
+        over |= s[h][j] > limit[j & 1];
+      }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float x = fmaxf(s[c], s[c + 2]);
+        float x = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < C::HALVES; ++h) x = fmaxf(x, fmaxf(s[h][c], s[h][c + 2]));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -385,10 +445,10 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
         const bool first = limit[c] == -INFINITY;
         const bool take = x != -INFINITY && (first || x > ref[c]);
         const float y = take ? x : ref[c];
-        const float old = dev::fast_exp2((ref[c] - y) * factor[c]);
+        const float old = dev::fast_exp2((ref[c] - y) * q.factor[c]);
         const float a = take && first ? 0.0f : old;
         ref[c] = y;
-        limit[c] = take ? __fadd_rd(x, __fdividef(8.0f - 0x1p-16f, factor[c])) : limit[c];
+        limit[c] = take ? __fadd_rd(x, __fdividef(8.0f - 0x1p-16f, q.factor[c])) : limit[c];
         l[c] *= a;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -398,139 +458,264 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
       }
     }
     __syncwarp();
-    uint32_t pf[2];                   // P^T as the second product's B operand
-    [[maybe_unused]] uint32_t pl[2];  // its second terms
+    uint32_t pf[C::HALVES][2];                   // P^T as the second product's B operand
+    [[maybe_unused]] uint32_t pl[C::HALVES][2];  // its second terms
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 e = dev::fma_pair(dev::sub_pair(make_float2(s[2 * h], s[2 * h + 1]), ref),
-                                     factor, HEADROOM);
-      const float p0 = dev::fast_exp2(e.x), p1 = dev::fast_exp2(e.y);
-      l[0] += p0;
-      l[1] += p1;
-      if constexpr (FMT == PA_KV_BF16) {
-        const uint32_t hi = pack_bf16(p0, p1);
-        const uint32_t lo = pack_bf16(p0 - dev::bf16_lo(hi), p1 - dev::bf16_hi(hi));
-        pf[h] = dev::transpose_8x8(DUP && t >= 2 ? lo : hi);
-        if (!DUP) pl[h] = dev::transpose_8x8(lo);
-      } else {
-        pf[h] = dev::transpose_8x8(dev::pack_f16(p0, p1));
-      }
-    }
-    // ---- O^T += V^T P^T
-    auto product = [&](float (&acc)[4], const uint32_t (&a)[4], uint32_t m0, uint32_t m1) {
-      if constexpr (FMT == PA_KV_BF16) {
-        dev::mma_bf16_regs(acc, a[0] & m0, a[1] & m0, a[2] & m1, a[3] & m1, pf[0], pf[1]);
-        if constexpr (!DUP)
-          dev::mma_bf16_regs(acc, a[0] & m0, a[1] & m0, a[2] & m1, a[3] & m1, pl[0], pl[1]);
-      } else {
-        dev::mma_f16(acc, a[0] & m0, a[1] & m0, a[2] & m1, a[3] & m1, pf[0], pf[1]);
-      }
-    };
-    auto tile_product = [&](int i, const uint32_t (&a)[4]) {
-      if constexpr (!EDGE) {
-        product(o[i], a, 0xffffffffu, 0xffffffffu);
-      } else {
-        for (int n = 0; n < n_tok; ++n) {  // for the columns of token n, rows that it sees
-          const int sees = see0 + n;
-          auto mask = [&](int r) {
-            return (position(r) < sees ? 0xffffu : 0u) | (position(r + 1) < sees ? 0xffff0000u : 0u);
-          };
-          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          product(acc, a, mask(2 * t), mask(2 * t + 8));
+    for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[i][j] += tok[j & 1] == n ? acc[j] : 0.0f;
-        }
-      }
-    };
-    if constexpr (FMT != PA_KV_FP4_E2M1) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t a[4];
-        v_fragment(vt, i, a);
-        tile_product(i, a);
-      }
-    } else {
-      constexpr int VW = D / 64;  // code words of a lane's share of a V row (D / 8 elements)
-      uint32_t w[4][VW], sb[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {  // keys of rows 2t, 2t + 1, 2t + 8, 2t + 9
-        const int k = C::key_of(2 * t + (r & 1) + (r >> 1) * 8);
-        const unsigned char* codes = vt + k * C::ROWB + g * (D / 16);
-        if constexpr (D == 128) {
-          const uint2 x = *reinterpret_cast<const uint2*>(codes);
-          w[r][0] = x.x;
-          w[r][1] = x.y;
+      for (int i = 0; i < 2; ++i) {
+        const float2 e = dev::fma_pair(dev::sub_pair(make_float2(s[h][2 * i], s[h][2 * i + 1]), ref),
+                                       q.factor, HEADROOM);
+        const float p0 = dev::fast_exp2(e.x), p1 = dev::fast_exp2(e.y);
+        l[0] += p0;
+        l[1] += p1;
+        if constexpr (FMT == PA_KV_BF16) {
+          const uint32_t hi = pack_bf16(p0, p1);
+          const uint32_t lo = pack_bf16(p0 - dev::bf16_lo(hi), p1 - dev::bf16_hi(hi));
+          pf[h][i] = dev::transpose_8x8(DUP && t >= 2 ? lo : hi);
+          if (!DUP) pl[h][i] = dev::transpose_8x8(lo);
         } else {
-          w[r][0] = *reinterpret_cast<const uint32_t*>(codes);
+          pf[h][i] = dev::transpose_8x8(dev::pack_f16(p0, p1));
         }
-        sb[r] = vt[KEYS * C::ROWB + k * C::SCALES + (g * VW) / 2];
       }
-      const uint32_t s01 = dev::e4m3x2_to_f16(sb[0] | sb[1] << 8);
-      const uint32_t s23 = dev::e4m3x2_to_f16(sb[2] | sb[3] << 8);
+    if (edge) clear_unseen(stage, blocks, q);
+    // ---- O^T += V^T P^T
 #pragma unroll
-      for (int c = 0; c < VW; ++c) {
-        // the nibbles of two keys in one word, so that a conversion yields one element of both
-        uint32_t x0[4], y0[4], x1[4], y1[4];
-        dev::e2m1x8_to_f16((w[0][c] & 0x0F0F0F0Fu) | ((w[1][c] << 4) & 0xF0F0F0F0u), x0);
-        dev::e2m1x8_to_f16(((w[0][c] >> 4) & 0x0F0F0F0Fu) | (w[1][c] & 0xF0F0F0F0u), y0);
-        dev::e2m1x8_to_f16((w[2][c] & 0x0F0F0F0Fu) | ((w[3][c] << 4) & 0xF0F0F0F0u), x1);
-        dev::e2m1x8_to_f16(((w[2][c] >> 4) & 0x0F0F0F0Fu) | (w[3][c] & 0xF0F0F0F0u), y1);
+    for (int h = 0; h < C::HALVES; ++h) {
+      const unsigned char* vt = stage + C::HALF + h * TILE_KEYS * C::ROWB;
+      auto tile_product = [&](int i, const uint32_t (&a)[4]) {
+        if constexpr (FMT == PA_KV_BF16) {
+          dev::mma_bf16_regs(o[i], a[0], a[1], a[2], a[3], pf[h][0], pf[h][1]);
+          if constexpr (!DUP)
+            dev::mma_bf16_regs(o[i], a[0], a[1], a[2], a[3], pl[h][0], pl[h][1]);
+        } else {
+          dev::mma_f16(o[i], a[0], a[1], a[2], a[3], pf[h][0], pf[h][1]);
+        }
+      };
+      if constexpr (FMT != PA_KV_FP4_E2M1) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a[4] = {dev::mul_f16x2(x0[j], s01), dev::mul_f16x2(y0[j], s01),
-                                 dev::mul_f16x2(x1[j], s23), dev::mul_f16x2(y1[j], s23)};
-          tile_product(c * 4 + j, a);
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t a[4];
+          v_fragment(vt, i, a);
+          tile_product(i, a);
+        }
+      } else {
+        constexpr int VW = D / 64;  // code words of a lane's share of a V row (D / 8 elements)
+        const unsigned char* scales =
+            stage + C::HALF + C::KEYS * C::ROWB + h * TILE_KEYS * C::SCALES;
+        uint32_t w[4][VW], sb[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // keys of rows 2t, 2t + 1, 2t + 8, 2t + 9
+          const int k = C::key_of(2 * t + (r & 1) + (r >> 1) * 8);
+          const unsigned char* codes = vt + k * C::ROWB + g * (D / 16);
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(codes);
+            w[r][0] = x.x;
+            w[r][1] = x.y;
+          } else {
+            w[r][0] = *reinterpret_cast<const uint32_t*>(codes);
+          }
+          sb[r] = scales[k * C::SCALES + (g * VW) / 2];
+        }
+        const uint32_t s01 = dev::e4m3x2_to_f16(sb[0] | sb[1] << 8);
+        const uint32_t s23 = dev::e4m3x2_to_f16(sb[2] | sb[3] << 8);
+#pragma unroll
+        for (int c = 0; c < VW; ++c) {
+          // the nibbles of two keys in one word, so that a conversion yields one element of both
+          uint32_t x0[4], y0[4], x1[4], y1[4];
+          dev::e2m1x8_to_f16((w[0][c] & 0x0F0F0F0Fu) | ((w[1][c] << 4) & 0xF0F0F0F0u), x0);
+          dev::e2m1x8_to_f16(((w[0][c] >> 4) & 0x0F0F0F0Fu) | (w[1][c] & 0xF0F0F0F0u), y0);
+          dev::e2m1x8_to_f16((w[2][c] & 0x0F0F0F0Fu) | ((w[3][c] << 4) & 0xF0F0F0F0u), x1);
+          dev::e2m1x8_to_f16(((w[2][c] >> 4) & 0x0F0F0F0Fu) | (w[3][c] & 0xF0F0F0F0u), y1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a[4] = {dev::mul_f16x2(x0[j], s01), dev::mul_f16x2(y0[j], s01),
+                                   dev::mul_f16x2(x1[j], s23), dev::mul_f16x2(y1[j], s23)};
+            tile_product(c * 4 + j, a);
+          }
         }
       }
     }
-  };
+  }
+  // The warp's result: sums over the lanes of a column, second terms to the first ones.
+  // maximum[c]: in the log2 domain; +inf where the sum is NaN, so that it reaches the end.
+  __device__ __forceinline__ void finish(const Columns<FMT, D, DUP>& q, float (&maximum)[2]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], x);
+      maximum[c] = l[c] != l[c] ? INFINITY
+                                : (limit[c] == -INFINITY ? -INFINITY
+                                                         : fmaf(ref[c], q.factor[c], -HEADROOM));
+    }
+    if constexpr (DUP)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[k][j] += __shfl_xor_sync(0xffffffffu, o[k][j], 2);
+  }
+  // element of O that o[k][j] is, of column 2t + j % 2
+  __device__ static __forceinline__ int element(int k, int j) {
+    const int g = (threadIdx.x & 31) >> 2;
+    // rows g and g + 8 of tile k; of a 4-bit V elements g D/8 + 2k, + 1
+    return FMT == PA_KV_FP4_E2M1 ? g * (D / 8) + 2 * k + (j >> 1) : 16 * k + g + (j >> 1) * 8;
+  }
+};
 
+// A block of a step: its first position there (NOWHERE: nothing is read) and its tile
+// (block * num_kv_heads + head).
+struct Entry {
+  int pos, tile;
+};
+// Entry e of the list of (v, head), from its row `row0` on.
+template <int BS>
+__device__ __forceinline__ Entry entry_of(const Sel& P, const Virtual& v, int head, int e, int row0,
+                                          unsigned& errors) {
+  Entry x{NOWHERE, 0};
+  const int j = P.selected[(int64_t(v.b) * P.num_kv_heads + head) * P.num_selected + e];
+  if (j >= v.blocks) errors |= PA_DEVERR_KEEP;
+  if (j >= 0 && j < v.blocks) {
+    const int k = P.block_tables[int64_t(v.b) * P.max_blocks_per_seq + j];
+    if (k < 0 || k >= P.num_blocks)
+      errors |= PA_DEVERR_TABLE_ENTRY;
+    else
+      x = Entry{j * BS + row0, k * P.num_kv_heads + head};
+  }
+  return x;
+}
+// Copies block n of a step (K and V) into its stage.
+template <int FMT, int D, int BS>
+__device__ __forceinline__ void copy_block(const Sel& P, unsigned char* st, int n, Entry e) {
+  using C = Cfg<FMT, D, BS>;
+  const int lane = threadIdx.x & 31;
+  const bool on = e.pos != NOWHERE;
+  const int row0 = C::SPB > 1 ? e.pos % BS : 0;  // of the step in the block
+  const int64_t at = int64_t(e.tile) * C::TILE + row0 * C::ROWB + lane * 16;
+  constexpr int ROWS = BS < C::KEYS ? BS : C::KEYS;  // of the block in a step
+  constexpr int CHUNKS = ROWS * C::ROWB / 16;   // 16-byte chunks
+  constexpr int CPR = C::ROWB / 16;             // of a row (of V in 8 bits: just so many bytes)
+#pragma unroll
+  for (int c = 0; c < CHUNKS; c += 32) {
+    const int x = c + lane;
+    const bool in = on && (c + 32 <= CHUNKS || x < CHUNKS);
+    const int r = n * ROWS + x / CPR, k = x % CPR;
+    int kd = r * C::ROWB + k * 16, vd = n * ROWS * C::ROWB + x * 16;
+    if constexpr (FMT == PA_KV_BF16) {
+      kd = r * C::ROWB + (k ^ (r & 7)) * 16;
+      vd = kd;
+    } else if constexpr (FMT == PA_KV_FP8_E4M3 && D == 128) {
+      kd = r * C::ROWB + (k ^ ((r & 1) << 2)) * 16;
+    }
+    dev::cp_async16(st + kd, P.k_cache + at + c * 16, in);
+    dev::cp_async16(st + C::HALF + vd, P.v_cache + at + c * 16, in);
+  }
+  if constexpr (C::SCALES > 0) {
+    constexpr int N = ROWS * C::SCALES / 16;  // chunks of scales, of K then of V
+    const bool of_v = lane >= N;
+    const int x = of_v ? lane - N : lane;
+    const unsigned char* from = (of_v ? P.v_cache : P.k_cache) + int64_t(e.tile) * C::TILE +
+                                BS * C::ROWB + row0 * C::SCALES + x * 16;
+    dev::cp_async16(st + (of_v ? C::HALF : 0) + C::KEYS * C::ROWB + n * ROWS * C::SCALES + x * 16,
+                    from, on && lane < 2 * N);
+  }
+}
+
+// Lengths that are too long or too short, flagged by the first CTA.
+__device__ __forceinline__ void report_lengths(const Sel& P) {
+  for (int b = blockIdx.x * NTHREADS + threadIdx.x; b < P.num_virtual / P.n_groups;
+       b += gridDim.x * NTHREADS) {
+    const int L = P.context_lens[b];
+    if (L > P.cap || (L > 0 && L < P.q_len)) atomicOr(&g_selected_errors, PA_DEVERR_CONTEXT_LEN);
+  }
+}
+
+// One list per cluster: its CTAs take equal stretches and join their results.
+template <int FMT, int D, int BS, bool DUP>
+__global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) {
+  using C = Cfg<FMT, D, BS>;
+  constexpr int ST = C::ST;
+  dev::griddep_enter();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int split = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int unit = blockIdx.x / split;
+  const int head = unit % P.num_kv_heads;
+  const Virtual v = virtual_of(P, unit / P.num_kv_heads, BS);
+  const int n_cols = v.n_tok << P.g_log2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float sm_m[NWARPS][COLS], sm_l[NWARPS][COLS];
+  __shared__ float2 sm_ml[COLS];          // of the CTA, read by the cluster
+  __shared__ int sm_pos[NWARPS][ST][C::NBK];  // position of the first key of a step's blocks
+  unsigned char* ring = smem + warp * ST * C::STAGE;
+
+  // this CTA's entries of the list
+  const int e0 = int(int64_t(v.entries) * rank / split);
+  const int e1 = int(int64_t(v.entries) * (rank + 1) / split);
+  const int n_steps = C::NBK > 1 ? (e1 - e0 + C::NBK - 1) / C::NBK : (e1 - e0) * C::SPB;
+  const int n_my = n_steps > warp ? (n_steps - warp + NWARPS - 1) / NWARPS : 0;
+  // The entries of this warp's steps [w0, w0 + WINDOW), NBK a step, one a lane.
+  unsigned errors = 0;
+  auto load_window = [&](int w0) {
+    const int step = warp + NWARPS * (w0 + lane / C::NBK);
+    const int e = e0 + (C::NBK > 1 ? step * C::NBK + lane % C::NBK : step / C::SPB);
+    return e < e1 ? entry_of<BS>(P, v, head, e, step % C::SPB * C::KEYS, errors)
+                  : Entry{NOWHERE, 0};
+  };
+  Entry window = load_window(0);
+  Raw<FMT, D, DUP> raw;
+  raw.fetch(P, v, head);
+  // One copy group: step i of the warp, empty past the last.
+  auto issue = [&](int i, int stage) {
+#pragma unroll
+    for (int n = 0; n < C::NBK; ++n) {
+      const int src = i % C::WINDOW * C::NBK + n;
+      const Entry e{__shfl_sync(0xffffffffu, window.pos, src),
+                    __shfl_sync(0xffffffffu, window.tile, src)};
+      if (i < n_my) {
+        if (lane == 0) sm_pos[warp][stage][n] = e.pos;
+        copy_block<FMT, D, BS>(P, ring + stage * C::STAGE, n, e);
+      }
+    }
+    dev::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) issue(i, i);
+
+  Columns<FMT, D, DUP> cols;
+  State<FMT, D, BS, DUP> st;
+  cols.take(P, raw);
+  st.clear();
   for (int i = 0, stage = 0; i < n_my; ++i) {
     dev::cp_async_wait<ST - 2>();
     __syncwarp();  // the step's copies by all lanes, and its positions
     const int ahead = i + ST - 1;
     if (ahead % C::WINDOW == 0) window = load_window(ahead);
     issue(ahead, stage == 0 ? ST - 1 : stage - 1);
-    const int pos0 = sm_pos[warp][stage][0], pos1 = C::NBK > 1 ? sm_pos[warp][stage][1] : 0;
-    const bool inner = pos0 + (C::NBK > 1 ? BS : KEYS) <= see0 && (C::NBK == 1 || pos1 + BS <= see0);
-    if (inner)
-      step(stage, pos0, pos1, std::false_type{});
-    else
-      step(stage, pos0, pos1, std::true_type{});
+    st.step(ring + stage * C::STAGE, sm_pos[warp][stage], cols);
     __syncwarp();  // the stage has been read
     stage = stage + 1 == ST ? 0 : stage + 1;
   }
   dev::cp_async_wait<0>();
   if (errors) atomicOr(&g_selected_errors, errors);
+  report_lengths(P);
   __syncthreads();  // the rings give way to the merge
 
   // ---- the warps' results, then the CTA's, then the cluster's
   float* rows = reinterpret_cast<float*>(smem);  // [NWARPS][COLS][OROW]
+  float maximum[2];
+  st.finish(cols, maximum);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], x);
+  for (int c = 0; c < 2; ++c)
     if (g == 0) {
-      // (a sum of NaN without a maximum has to reach the result: +inf carries it)
-      sm_m[warp][2 * t + c] = l[c] != l[c] ? INFINITY
-                              : (limit[c] == -INFINITY ? -INFINITY
-                                                       : fmaf(ref[c], factor[c], -HEADROOM));
-      sm_l[warp][2 * t + c] = l[c];
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    if constexpr (DUP) {  // first and second terms
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[k][j] += __shfl_xor_sync(0xffffffffu, o[k][j], 2);
+      sm_m[warp][2 * t + c] = maximum[c];
+      sm_l[warp][2 * t + c] = st.l[c];
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // rows g and g + 8 of tile k; of a 4-bit V elements g D/8 + 2k, + 1
-      const int d = FMT == PA_KV_FP4_E2M1 ? g * (D / 8) + 2 * k + (j >> 1) : 16 * k + g + (j >> 1) * 8;
-      rows[(warp * COLS + 2 * t + (j & 1)) * C::OROW + d] = o[k][j];
-    }
-  }
+  for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      rows[(warp * COLS + 2 * t + (j & 1)) * C::OROW + st.element(k, j)] = st.o[k][j];
   __syncthreads();
   constexpr int TPC = NTHREADS / COLS, E = D / TPC;  // threads of a column, their elements
   {
@@ -558,8 +743,7 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
   }
   cluster.sync();
   {
-    // a CTA writes every split-th element pair of the rows
-    const float scale_v = FMT == PA_KV_BF16 ? 1.0f : P.v_scale[head];
+    // a CTA writes every split-th stretch of element pairs
     for (int i = rank * NTHREADS + tid; i < n_cols * (D / 2); i += split * NTHREADS) {
       const int n = i / (D / 2), d = i % (D / 2) * 2;
       float2 ml[MAX_SPLIT], x[MAX_SPLIT];
@@ -582,16 +766,324 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
           sum.x = fmaf(w, x[k].x, sum.x);
           sum.y = fmaf(w, x[k].y, sum.y);
         }
-      const float norm = den == 0.0f ? 0.0f : scale_v / den;  // no key: a row of zeros
-      *reinterpret_cast<__nv_bfloat162*>(P.out + q_row(n) * D + d) =
+      const float norm = den == 0.0f ? 0.0f : cols.v_scale / den;  // no key: a row of zeros
+      *reinterpret_cast<__nv_bfloat162*>(P.out + q_row(P, v, head, n) * D + d) =
           __floats2bfloat162_rn(sum.x * norm, sum.y * norm);
     }
   }
   if (split > 1) cluster.sync();  // no CTA leaves while another reads its rows
 }
 
+// ---------------------------------------------------------------- streams
+
+// The steps of all lists, one after the other, are dealt out to the warps of a
+// persistent grid in equal stretches: T positions, T / n or one more each, and `least` at
+// least (a stretch costs its queries and a partial).
+struct Deal {
+  int n, base, longer;  // stretches; positions of one; how many hold one more
+  __device__ __forceinline__ Deal(int T, int most, int least) {
+    n = T > 0 ? max(1, min(T / least, most)) : 0;
+    base = n > 0 ? T / n : 0;
+    longer = T - base * n;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * base + min(c, longer); }
+  __device__ __forceinline__ int owner(int x) const {  // the stretch that holds position x
+    const int cut = longer * (base + 1);
+    return x < cut ? x / (base + 1) : longer + (x - cut) / base;
+  }
+};
+template <class C>
+__device__ __forceinline__ int steps_of(const Virtual& v) {
+  return (v.entries + C::NBK - 1) / C::NBK * C::SPB;
+}
+
+// Every warp works through its stretch by itself, its ring running on from list to list;
+// a list that a stretch's end cuts leaves partials, at most two a warp, which
+// merge_selected_kernel joins.
 template <int FMT, int D, int BS, bool DUP>
-int launch_t(const Sel& P, int split, int64_t units, cudaStream_t stream) {
+__global__ void __launch_bounds__(NTHREADS, Cfg<FMT, D, BS>::CTAS)
+    stream_selected_kernel(const Sel P) {
+  using C = Cfg<FMT, D, BS>;
+  constexpr int ST = C::ST;
+  dev::griddep_enter();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* ring = smem + warp * ST * C::STAGE;
+  struct Begin {
+    int before, v;  // steps before virtual sequence v, which holds a stretch's first one
+  };
+  // of a step in the ring: its blocks' positions, its list (virtual sequence and KV head),
+  // and its place there
+  struct Step {
+    int pos[C::NBK], v, head, at;
+  };
+  __shared__ Begin sm_begin[NWARPS];
+  __shared__ int warp_tot[NWARPS];
+  __shared__ Step sm_step[NWARPS][ST];
+
+  // ---- where the warps' stretches begin
+  int x0, n_my;
+  {
+    const int per = (P.num_virtual + NTHREADS - 1) / NTHREADS;
+    const int v0 = min(P.num_virtual, tid * per), v1 = min(P.num_virtual, v0 + per);
+    int sum = 0;
+    for (int v = v0; v < v1; ++v) sum += steps_of<C>(virtual_of(P, v, BS)) * P.num_kv_heads;
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_tot[warp] = inc;
+    __syncthreads();
+    int before = inc - sum, T = 0;
+#pragma unroll
+    for (int w = 0; w < NWARPS; ++w) {
+      if (w < warp) before += warp_tot[w];
+      T += warp_tot[w];
+    }
+    const Deal deal(T, gridDim.x * NWARPS, C::LEAST);
+    const int c0 = blockIdx.x * NWARPS;
+    int start[NWARPS];
+    bool mine = blockIdx.x == 0;  // (CTA 0 writes the plan for the merge)
+#pragma unroll
+    for (int w = 0; w < NWARPS; ++w) {
+      start[w] = c0 + w < deal.n ? deal.start(c0 + w) : T;
+      mine |= before <= start[w] && start[w] < before + sum;
+    }
+    if (mine) {
+      int at = before;
+      for (int v = v0; v < v1; ++v) {
+        const int all = steps_of<C>(virtual_of(P, v, BS)) * P.num_kv_heads;
+        if (blockIdx.x == 0) P.plan[v] = at;
+#pragma unroll
+        for (int w = 0; w < NWARPS; ++w)
+          if (at <= start[w] && start[w] < at + all) sm_begin[w] = Begin{at, v};
+        at += all;
+      }
+    }
+    if (blockIdx.x == 0 && tid == 0) P.plan[P.num_virtual] = T;
+    __syncthreads();
+    const int c = c0 + warp;
+    x0 = c < deal.n ? deal.start(c) : T;
+    n_my = (c < deal.n ? deal.start(c + 1) : T) - x0;
+  }
+
+  // The entries of steps [w0, w0 + WINDOW) of the stretch, NBK a step, one a lane; the
+  // lanes walk on from the virtual sequence that held the previous window's last step.
+  Begin cursor = n_my > 0 ? sm_begin[warp] : Begin{0, 0};
+  unsigned errors = 0;
+  struct Place {
+    Entry e;
+    int v, head, at;
+  };
+  auto load_window = [&](int w0) {
+    Place p{{NOWHERE, 0}, 0, 0, 0};
+    const int i = w0 + lane / C::NBK;
+    Begin c = cursor;
+    if (i < n_my) {
+      const int x = x0 + i;
+      Virtual q = virtual_of(P, c.v, BS);
+      int steps = steps_of<C>(q);
+      while (x >= c.before + steps * P.num_kv_heads) {
+        c.before += steps * P.num_kv_heads;
+        q = virtual_of(P, ++c.v, BS);
+        steps = steps_of<C>(q);
+      }
+      p.v = c.v;
+      p.head = (x - c.before) / steps;
+      p.at = x - c.before - p.head * steps;
+      const int e = C::NBK > 1 ? p.at * C::NBK + lane % C::NBK : p.at / C::SPB;
+      if (e < q.entries)
+        p.e = entry_of<BS>(P, q, p.head, e, p.at % C::SPB * C::KEYS, errors);
+    }
+    cursor.before = __shfl_sync(0xffffffffu, c.before, 31);
+    cursor.v = __shfl_sync(0xffffffffu, c.v, 31);
+    return p;
+  };
+  Place window = load_window(0);
+  // The queries of the list at hand when it begins, of the next one from then on: under
+  // the copies' load they take 3 to 4 us.
+  Raw<FMT, D, DUP> raw;
+  int v = __shfl_sync(0xffffffffu, window.v, 0), head = __shfl_sync(0xffffffffu, window.head, 0);
+  if (n_my > 0) raw.fetch(P, virtual_of(P, v, BS), head);
+  auto issue = [&](int i, int stage) {
+#pragma unroll
+    for (int n = 0; n < C::NBK; ++n) {
+      const int src = i % C::WINDOW * C::NBK + n;
+      const Entry e{__shfl_sync(0xffffffffu, window.e.pos, src),
+                    __shfl_sync(0xffffffffu, window.e.tile, src)};
+      if (i < n_my) {
+        if (lane == src) {
+          sm_step[warp][stage].pos[n] = window.e.pos;
+          if (n == 0) {
+            sm_step[warp][stage].v = window.v;
+            sm_step[warp][stage].head = window.head;
+            sm_step[warp][stage].at = window.at;
+          }
+        }
+        copy_block<FMT, D, BS>(P, ring + stage * C::STAGE, n, e);
+      }
+    }
+    dev::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) issue(i, i);
+  Place coming = n_my > C::WINDOW ? load_window(C::WINDOW) : window;
+
+  Columns<FMT, D, DUP> cols;
+  State<FMT, D, BS, DUP> st;
+  int first = 0, done = 0;  // the steps of the list at hand that are done
+  int left = 0;             // those that are not (of the list, and of the stretch)
+  // the list's end, or the stretch's: a row of the result, or a partial
+  auto flush = [&]() {
+    const Virtual q = virtual_of(P, v, BS);
+    float maximum[2];
+    st.finish(cols, maximum);
+    const int n_cols = q.n_tok << P.g_log2;
+    const bool whole = first == 0 && done == steps_of<C>(q);
+    const float scale_v = cols.v_scale;
+    const int64_t slot = 2 * int64_t(blockIdx.x * NWARPS + warp) + (first == 0);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int n = 2 * t + c;
+      if (n < n_cols) {
+        if (whole) {
+          const float norm = st.l[c] == 0.0f ? 0.0f : scale_v / st.l[c];  // no key: zeros
+          __nv_bfloat16* out = P.out + q_row(P, q, head, n) * D;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int j = c; j < 4; j += 2)
+              out[st.element(k, j)] = __float2bfloat16_rn(st.o[k][j] * norm);
+        } else {
+          float* acc = P.part_acc + (slot * P.part_cols + n) * D;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int j = c; j < 4; j += 2) acc[st.element(k, j)] = st.o[k][j] * scale_v;
+          if (g == 0)
+            *reinterpret_cast<float2*>(P.part_ml + (slot * P.part_cols + n) * 2) =
+                make_float2(maximum[c], st.l[c]);
+        }
+      }
+    }
+  };
+  for (int i = 0, stage = 0; i < n_my; ++i) {
+    dev::cp_async_wait<ST - 2>();
+    __syncwarp();  // the step's copies by all lanes, and what is known of it
+    const int ahead = i + ST - 1;
+    if (ahead % C::WINDOW == 0) {
+      window = coming;
+      if (ahead + C::WINDOW < n_my) coming = load_window(ahead + C::WINDOW);
+    }
+    issue(ahead, stage == 0 ? ST - 1 : stage - 1);
+    const Step& now = sm_step[warp][stage];
+    if (left == 0) {  // a list begins
+      if (i > 0) flush();
+      v = now.v;
+      head = now.head;
+      first = done = now.at;
+      cols.take(P, raw);
+      st.clear();
+      Virtual q = virtual_of(P, v, BS);
+      left = min(steps_of<C>(q) - first, n_my - i);
+      if (i + left < n_my) {  // the stretch holds the beginning of the next list
+        int next = v, h = head + 1;
+        if (h == P.num_kv_heads) {
+          h = 0;
+          do q = virtual_of(P, ++next, BS);
+          while (q.entries == 0);
+        }
+        raw.fetch(P, q, h);
+      }
+    }
+    st.step(ring + stage * C::STAGE, now.pos, cols);
+    ++done;
+    --left;
+    __syncwarp();  // the stage has been read
+    stage = stage + 1 == ST ? 0 : stage + 1;
+  }
+  if (n_my > 0) flush();
+  if (errors) atomicOr(&g_selected_errors, errors);
+
+  // bad lengths are flagged, and rows of sequences without keys zeroed, by the CTAs in turn
+  report_lengths(P);
+  for (int u = blockIdx.x; u < P.num_virtual; u += gridDim.x) {
+    const Virtual q = virtual_of(P, u, BS);
+    if (q.entries > 0) continue;
+    const int num_q_heads = P.num_kv_heads << P.g_log2;
+    __nv_bfloat16* row = P.out + (int64_t(q.b) * P.q_len + q.first_tok) * num_q_heads * D;
+    for (int i = tid; i < q.n_tok * num_q_heads * D; i += NTHREADS) row[i] = __float2bfloat16_rn(0.0f);
+  }
+}
+
+// Joins the pieces of the lists that were cut: one warp per (list, column).
+template <int FMT, int D, int BS>
+__global__ void __launch_bounds__(128) merge_selected_kernel(const Sel P, int stretches) {
+  using C = Cfg<FMT, D, BS>;
+  constexpr int E = D / 32;  // elements of a lane
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int n = int(row % P.part_cols);
+  const int item = int(row / P.part_cols);
+  const int v = item / P.num_kv_heads, head = item - v * P.num_kv_heads;
+  if (v >= P.num_virtual) return;
+  const Virtual q = virtual_of(P, v, BS);
+  dev::griddep_wait();
+  if (q.entries == 0 || n >= (q.n_tok << P.g_log2)) return;
+  const int steps = steps_of<C>(q);
+  const int base = P.plan[v] + head * steps;
+  const Deal deal(P.plan[P.num_virtual], stretches, C::LEAST);
+  const int c0 = deal.owner(base), c1 = deal.owner(base + steps - 1);
+  if (c0 == c1) return;  // one piece: written by the stream
+  // eight pieces at a time, their loads in flight together
+  constexpr int BATCH = 8;
+  float M = -INFINITY, den = 0.0f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+  for (int c = c0; c <= c1; c += BATCH) {
+    float2 ml[BATCH], x[BATCH][E / 2];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int64_t slot = (int64_t(2) * min(c + k, c1) + (c + k == c0)) * P.part_cols + n;
+      ml[k] = *reinterpret_cast<const float2*>(P.part_ml + slot * 2);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e)
+        x[k][e] = *reinterpret_cast<const float2*>(P.part_acc + slot * D + lane * E + 2 * e);
+      if (c + k > c1) ml[k].x = -INFINITY;
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+    const float a = M == -INFINITY ? 0.0f : dev::fast_exp2(M - top);
+    M = top;
+    den *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (ml[k].x == -INFINITY) continue;  // no keys of this column in the piece
+      const float wt = dev::fast_exp2(ml[k].x - M);
+      den = fmaf(wt, ml[k].y, den);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        acc[2 * e] = fmaf(wt, x[k][e].x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(wt, x[k][e].y, acc[2 * e + 1]);
+      }
+    }
+  }
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+  const int64_t out = q_row(P, q, head, n);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(P.out + out * D + lane * E + e) =
+        __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <int FMT, int D, int BS, bool DUP>
+int launch_t(const Sel& P, const SelectedPlan& plan, cudaStream_t stream) {
   using C = Cfg<FMT, D, BS>;
   // the opt-in to large shared memory is per device
   static std::atomic<uint64_t> configured{0};
@@ -602,33 +1094,56 @@ int launch_t(const Sel& P, int split, int64_t units, cudaStream_t stream) {
   if (!(configured.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(decode_selected_kernel<FMT, D, BS, DUP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(stream_selected_kernel<FMT, D, BS, DUP>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::RING);
     if (e != cudaSuccess) return int(e);
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_ordered(decode_selected_kernel<FMT, D, BS, DUP>, dim3(unsigned(units * split)),
-                        NTHREADS, C::SMEM, stream, unsigned(split), P);
+  const int64_t lists = int64_t(P.num_virtual) * P.num_kv_heads;
+  if (plan.grid == 0)
+    return launch_ordered(decode_selected_kernel<FMT, D, BS, DUP>,
+                          dim3(unsigned(lists * plan.split)), NTHREADS, C::SMEM, stream,
+                          unsigned(plan.split), P);
+  const int err = launch_ordered(stream_selected_kernel<FMT, D, BS, DUP>, dim3(unsigned(plan.grid)),
+                                 NTHREADS, C::RING, stream, 1, P);
+  if (err) return err;
+  return launch_ordered(merge_selected_kernel<FMT, D, BS>,
+                        dim3(unsigned((lists * P.part_cols + 3) / 4)), 128, 0, stream, 1, P,
+                        plan.grid * NWARPS);
 }
 
 template <int FMT, int D, int BS>
-int launch_dup(const Sel& P, int split, int64_t units, cudaStream_t s) {
+int launch_dup(const Sel& P, const SelectedPlan& plan, cudaStream_t s) {
   if constexpr (FMT == PA_KV_BF16)
-    if ((P.q_group << P.g_log2) <= 4) return launch_t<FMT, D, BS, true>(P, split, units, s);
-  return launch_t<FMT, D, BS, false>(P, split, units, s);
+    if ((P.q_group << P.g_log2) <= 4) return launch_t<FMT, D, BS, true>(P, plan, s);
+  return launch_t<FMT, D, BS, false>(P, plan, s);
 }
 template <int FMT, int D>
-int launch_bs(const Sel& P, int block_size, int split, int64_t units, cudaStream_t s) {
+int launch_bs(const Sel& P, int block_size, const SelectedPlan& plan, cudaStream_t s) {
   switch (block_size) {
-    case 8: return launch_dup<FMT, D, 8>(P, split, units, s);
-    case 16: return launch_dup<FMT, D, 16>(P, split, units, s);
-    case 32: return launch_dup<FMT, D, 32>(P, split, units, s);
+    case 8: return launch_dup<FMT, D, 8>(P, plan, s);
+    case 16: return launch_dup<FMT, D, 16>(P, plan, s);
+    case 32: return launch_dup<FMT, D, 32>(P, plan, s);
     default: return int(cudaErrorInvalidValue);
   }
 }
 template <int FMT>
-int launch_d(const Sel& P, int head_dim, int block_size, int split, int64_t units, cudaStream_t s) {
-  return head_dim == 64 ? launch_bs<FMT, 64>(P, block_size, split, units, s)
-                        : launch_bs<FMT, 128>(P, block_size, split, units, s);
+int launch_d(const Sel& P, int head_dim, int block_size, const SelectedPlan& plan, cudaStream_t s) {
+  return head_dim == 64 ? launch_bs<FMT, 64>(P, block_size, plan, s)
+                        : launch_bs<FMT, 128>(P, block_size, plan, s);
 }
+
+int stream_ctas(int kv_dtype, int d) {
+  switch (kv_dtype) {
+    case PA_KV_BF16: return d == 64 ? Cfg<PA_KV_BF16, 64, 16>::CTAS : Cfg<PA_KV_BF16, 128, 16>::CTAS;
+    case PA_KV_FP8_E4M3:
+      return d == 64 ? Cfg<PA_KV_FP8_E4M3, 64, 16>::CTAS : Cfg<PA_KV_FP8_E4M3, 128, 16>::CTAS;
+    default: return d == 64 ? Cfg<PA_KV_FP4_E2M1, 64, 16>::CTAS : Cfg<PA_KV_FP4_E2M1, 128, 16>::CTAS;
+  }
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -637,19 +1152,27 @@ SelectedPlan selected_plan(const pa_decode_params* p, int num_selected, int num_
   r.cols = fp4_columns(p);
   const int64_t table = int64_t(p->max_blocks_per_seq) * p->block_size;
   r.cap = int(p->max_context_len < table ? p->max_context_len : table);
-  // CTAs for two an SM several times over, each with two steps a warp at least
-  const int64_t units = int64_t(p->num_seqs) * r.cols.n_groups * p->num_kv_heads;
-  const int64_t blocks = (int64_t(r.cap) + p->block_size - 1) / p->block_size;
-  const int64_t keys = (blocks < num_selected ? blocks : num_selected) * p->block_size;
+  const int64_t lists = int64_t(p->num_seqs) * r.cols.n_groups * p->num_kv_heads;
+  const int64_t steps = selected_steps(p, num_selected);  // of a list, at most
+  const int sms = num_sms > 0 ? num_sms : 152;
+  const int resident = stream_ctas(p->kv_dtype, p->head_dim);
+  // Where one wave of CTAs takes all lists: clusters, with two steps a warp at least.
   r.split = 1;
-  while (r.split < MAX_SPLIT && units * r.split < int64_t(num_sms) * 8 &&
-         keys / (2 * r.split) >= 2 * NWARPS * KEYS)
+  while (r.split < MAX_SPLIT && lists * r.split * 2 <= int64_t(sms) * resident &&
+         steps >= 4 * NWARPS * r.split)
     r.split *= 2;
+  if (lists * r.split <= int64_t(sms) * resident && steps <= 8 * NWARPS * r.split) return r;
+  r.grid = sms * resident;
+  r.part_cols = r.cols.q_group * (p->num_q_heads / p->num_kv_heads);
+  const size_t rows = size_t(2) * r.grid * NWARPS * r.part_cols;
+  r.ml = kWorkspaceHeaderBytes + round256((size_t(p->num_seqs) * r.cols.n_groups + 1) * 4);
+  r.acc = r.ml + round256(rows * 8);
+  r.total = r.acc + round256(rows * p->head_dim * 4);
   return r;
 }
 
 int launch_decode_selected(const pa_decode_params* p, const int32_t* selected, int num_selected,
-                           const SelectedPlan& plan, void* stream) {
+                           const SelectedPlan& plan, unsigned char* ws, void* stream) {
   Sel P;
   P.q = static_cast<const __nv_bfloat16*>(p->q);
   P.out = static_cast<__nv_bfloat16*>(p->out);
@@ -670,15 +1193,16 @@ int launch_decode_selected(const pa_decode_params* p, const int32_t* selected, i
   P.q_len = query_len_of(p);
   P.q_group = plan.cols.q_group;
   P.n_groups = plan.cols.n_groups;
-  const int64_t units = int64_t(p->num_seqs) * plan.cols.n_groups * p->num_kv_heads;
+  P.num_virtual = p->num_seqs * plan.cols.n_groups;
+  P.plan = plan.grid ? reinterpret_cast<int32_t*>(ws + kWorkspaceHeaderBytes) : nullptr;
+  P.part_ml = plan.grid ? reinterpret_cast<float*>(ws + plan.ml) : nullptr;
+  P.part_acc = plan.grid ? reinterpret_cast<float*>(ws + plan.acc) : nullptr;
+  P.part_cols = plan.part_cols;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (p->kv_dtype) {
-    case PA_KV_BF16:
-      return launch_d<PA_KV_BF16>(P, p->head_dim, p->block_size, plan.split, units, s);
-    case PA_KV_FP8_E4M3:
-      return launch_d<PA_KV_FP8_E4M3>(P, p->head_dim, p->block_size, plan.split, units, s);
-    default:
-      return launch_d<PA_KV_FP4_E2M1>(P, p->head_dim, p->block_size, plan.split, units, s);
+    case PA_KV_BF16: return launch_d<PA_KV_BF16>(P, p->head_dim, p->block_size, plan, s);
+    case PA_KV_FP8_E4M3: return launch_d<PA_KV_FP8_E4M3>(P, p->head_dim, p->block_size, plan, s);
+    default: return launch_d<PA_KV_FP4_E2M1>(P, p->head_dim, p->block_size, plan, s);
   }
 }
 
