@@ -282,14 +282,38 @@ def _check(status: int, where: str) -> None:
 # torch's calls for the current device, looked up once: the checks below run for
 # every tensor of every call, and a step is a few microseconds
 _device = _raw_stream = None
+_i32 = _i64 = _f32 = _bf16 = _u8 = None
 
 
 def _bind_torch() -> None:
-    global _device, _raw_stream
+    global _device, _raw_stream, _i32, _i64, _f32, _bf16, _u8
     import torch
 
+    _i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
+    _bf16, _u8 = torch.bfloat16, torch.uint8
     _raw_stream = torch._C._cuda_getCurrentRawStream
     _device = torch._C._cuda_getDevice
+
+
+def _current() -> Optional[int]:
+    """The current device, for ``_ptr``; None where there is none (every tensor is then
+    refused by ``_dev_ptr``). Binds torch."""
+    if _device is None:
+        _bind_torch()
+    try:
+        return _device()
+    except Exception:
+        return None
+
+
+def _ptr(t, dtype, name: str, device: Optional[int]) -> int:
+    """``_dev_ptr`` for a call of many tensors: the current device is looked up once."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev_ptr(t, dtype, name)
 
 
 def _dev_ptr(t, dtype, name: str) -> int:
@@ -342,13 +366,13 @@ def kv_cache_format(k_cache) -> Tuple[int, int]:
     """(kv_dtype, head_dim) of a K cache tensor: bf16 [NB][Hkv][BS][D]; uint8
     [NB][Hkv][BS][D] for the 8-bit cache, [NB][Hkv][BS][D * 9 / 16] for the
     4-bit one (36 or 72 bytes a row: no 8-bit head_dim)."""
-    import torch
-
+    if _u8 is None:
+        _bind_torch()
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError("a cache is [num_blocks][num_kv_heads][block_size][row]")
     row = shape[3]
-    if k_cache.dtype is torch.uint8:
+    if k_cache.dtype is _u8:
         return (KV_FP4_E2M1, row * 16 // 9) if row in (36, 72) else (KV_FP8_E4M3, row)
     return KV_BF16, row
 
@@ -378,8 +402,7 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
     (K [NB][Hkv][BS][D], V^T in 16-key sub-tiles [NB][Hkv][BS/16][D][16]) or,
     with D * 9 / 16 bytes a row, the 4-bit cache (``fp4_cache_shape``); both
     need k_scale / v_scale, float32 CUDA tensors [Hkv]."""
-    import torch
-
+    dev = _current()
     shape = q.shape
     if len(shape) == 4:
         B, QL, Hq, D = shape
@@ -392,20 +415,20 @@ def make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens,
     tables = block_tables.shape
     if len(tables) != 2 or tables[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
-    fmt_dtype = torch.bfloat16 if fmt == KV_BF16 else torch.uint8
+    fmt_dtype = _bf16 if fmt == KV_BF16 else _u8
     ks = vs = None
     if fmt != KV_BF16:
         if k_scale is None or v_scale is None:
             raise ValueError("the 8-bit and 4-bit caches need k_scale and v_scale")
-        ks = _dev_ptr(k_scale, torch.float32, "k_scale")
-        vs = _dev_ptr(v_scale, torch.float32, "v_scale")
+        ks = _ptr(k_scale, _f32, "k_scale", dev)
+        vs = _ptr(v_scale, _f32, "v_scale", dev)
         if fmt == KV_FP4_E2M1 and (k_scale.numel() != Hkv or v_scale.numel() != Hkv):
             raise ValueError("k_scale and v_scale must be [num_kv_heads]")
     return DecodeParams(
-        _dev_ptr(q, torch.bfloat16, "q"), _dev_ptr(out, torch.bfloat16, "out"),
-        _dev_ptr(k_cache, fmt_dtype, "k_cache"), _dev_ptr(v_cache, fmt_dtype, "v_cache"),
-        _dev_ptr(block_tables, torch.int32, "block_tables"),
-        _dev_ptr(context_lens, torch.int32, "context_lens"),
+        _ptr(q, _bf16, "q", dev), _ptr(out, _bf16, "out", dev),
+        _ptr(k_cache, fmt_dtype, "k_cache", dev), _ptr(v_cache, fmt_dtype, "v_cache", dev),
+        _ptr(block_tables, _i32, "block_tables", dev),
+        _ptr(context_lens, _i32, "context_lens", dev),
         tables[1], B, Hq, Hkv, D, BS, NB, int(max_context_len),
         float(1.0 / math.sqrt(D) if scale is None else scale), int(partition_tokens),
         int(variant), int(bool(overlap_prologue)), fmt, ks, vs, int(QL), int(wait_timeout_us))
@@ -889,10 +912,8 @@ def pa_update_tables(block_tables, old_lens, new_lens, free_ring, ring_state, ne
     ``slot_mapping`` (int64 [T]), ``positions`` (int32 [T]) and ``token_starts`` (int32
     [B + 1]) get the new tokens, packed, -1 behind; ``new_ring_state`` (int32 [4]) the
     ring's state: head, count, and 0 where the step was done (see the C header)."""
-    import torch
-
+    dev = _current()
     B = old_lens.shape[0]
-    i32 = torch.int32
     if block_tables.dim() != 2 or block_tables.shape[0] != B or old_lens.shape != (B,) \
             or new_lens.shape != (B,):
         raise ValueError("block_tables must be [num_seqs][max_blocks], the lengths [num_seqs]")
@@ -906,12 +927,12 @@ def pa_update_tables(block_tables, old_lens, new_lens, free_ring, ring_state, ne
         raise ValueError("slot_mapping and positions must be [max_new_tokens], token_starts "
                          "[num_seqs + 1]")
     p = UpdateTablesParams(
-        _dev_ptr(block_tables, i32, "block_tables"), _dev_ptr(old_lens, i32, "old_lens"),
-        _dev_ptr(new_lens, i32, "new_lens"), _dev_ptr(free_ring, i32, "free_ring"),
-        _dev_ptr(ring_state, i32, "ring_state"), _dev_ptr(new_ring_state, i32, "new_ring_state"),
-        None if slot_mapping is None else _dev_ptr(slot_mapping, torch.int64, "slot_mapping"),
-        None if positions is None else _dev_ptr(positions, i32, "positions"),
-        None if token_starts is None else _dev_ptr(token_starts, i32, "token_starts"),
+        _ptr(block_tables, _i32, "block_tables", dev), _ptr(old_lens, _i32, "old_lens", dev),
+        _ptr(new_lens, _i32, "new_lens", dev), _ptr(free_ring, _i32, "free_ring", dev),
+        _ptr(ring_state, _i32, "ring_state", dev), _ptr(new_ring_state, _i32, "new_ring_state", dev),
+        None if slot_mapping is None else _ptr(slot_mapping, _i64, "slot_mapping", dev),
+        None if positions is None else _ptr(positions, _i32, "positions", dev),
+        None if token_starts is None else _ptr(token_starts, _i32, "token_starts", dev),
         block_tables.shape[1], B, int(block_size), int(num_blocks), free_ring.shape[0], T)
     _check(load().pa_update_tables(ctypes.byref(p), _stream_handle(stream)), "pa_update_tables")
 
@@ -927,8 +948,7 @@ def pa_block_bounds(k_cache, bounds, block_tables, context_lens, max_new_tokens:
     holds a token from ``old_lens[b]`` on (None: from the first), written into ``bounds``
     (bf16, ``block_bounds_shape``); returns it. K caches of every type; the head's scale
     is left out. ``max_new_tokens`` is an upper bound of ``context_lens - old_lens``."""
-    import torch
-
+    dev = _current()
     fmt, D = kv_cache_format(k_cache)
     NB, Hkv, BS, _ = k_cache.shape
     tables = block_tables.shape
@@ -938,11 +958,11 @@ def pa_block_bounds(k_cache, bounds, block_tables, context_lens, max_new_tokens:
             or (old_lens is not None and old_lens.shape != tables[:1]):
         raise ValueError("block_tables must be [num_seqs][max_blocks], the lengths [num_seqs]")
     p = BlockBoundsParams(
-        _dev_ptr(k_cache, torch.bfloat16 if fmt == KV_BF16 else torch.uint8, "k_cache"),
-        _dev_ptr(bounds, torch.bfloat16, "bounds"),
-        _dev_ptr(block_tables, torch.int32, "block_tables"),
-        _dev_ptr(context_lens, torch.int32, "context_lens"),
-        None if old_lens is None else _dev_ptr(old_lens, torch.int32, "old_lens"),
+        _ptr(k_cache, _bf16 if fmt == KV_BF16 else _u8, "k_cache", dev),
+        _ptr(bounds, _bf16, "bounds", dev),
+        _ptr(block_tables, _i32, "block_tables", dev),
+        _ptr(context_lens, _i32, "context_lens", dev),
+        None if old_lens is None else _ptr(old_lens, _i32, "old_lens", dev),
         tables[1], tables[0], Hkv, D, BS, NB, int(max_new_tokens), fmt)
     _check(load().pa_block_bounds(ctypes.byref(p), _stream_handle(stream)), "pa_block_bounds")
     return bounds
@@ -954,8 +974,7 @@ def pa_block_scores(q, bounds, block_tables, context_lens, max_context_len: int,
     query head of a KV head: float32 [B][Hkv][stride], of which the blocks of each
     sequence are written; returns it. q bf16 [B][Hq][D] or [B][Q][Hq][D]; ``k_scale`` is
     the head scale of the 8-bit and 4-bit caches."""
-    import torch
-
+    dev = _current()
     shape = q.shape
     if len(shape) == 4:
         B, QL, Hq, D = shape
@@ -970,15 +989,15 @@ def pa_block_scores(q, bounds, block_tables, context_lens, max_context_len: int,
     if k_scale is not None and k_scale.numel() != Hkv:
         raise ValueError("k_scale must be [num_kv_heads]")
     if scores is None:
-        scores = _empty(stream, q, (B, Hkv, tables[1]), torch.float32)
+        scores = _empty(stream, q, (B, Hkv, tables[1]), _f32)
     if scores.dim() != 3 or scores.shape[:2] != (B, Hkv):
         raise ValueError("scores must be [num_seqs][num_kv_heads][stride]")
     p = BlockScoresParams(
-        _dev_ptr(q, torch.bfloat16, "q"), _dev_ptr(bounds, torch.bfloat16, "bounds"),
-        None if k_scale is None else _dev_ptr(k_scale, torch.float32, "k_scale"),
-        _dev_ptr(block_tables, torch.int32, "block_tables"),
-        _dev_ptr(context_lens, torch.int32, "context_lens"),
-        _dev_ptr(scores, torch.float32, "scores"), scores.shape[2], tables[1], B, Hq, Hkv, D,
+        _ptr(q, _bf16, "q", dev), _ptr(bounds, _bf16, "bounds", dev),
+        None if k_scale is None else _ptr(k_scale, _f32, "k_scale", dev),
+        _ptr(block_tables, _i32, "block_tables", dev),
+        _ptr(context_lens, _i32, "context_lens", dev),
+        _ptr(scores, _f32, "scores", dev), scores.shape[2], tables[1], B, Hq, Hkv, D,
         int(block_size), NB, int(max_context_len),
         float(1.0 / math.sqrt(D) if scale is None else scale), int(QL))
     _check(load().pa_block_scores(ctypes.byref(p), _stream_handle(stream)), "pa_block_scores")
@@ -990,19 +1009,18 @@ def pa_block_select(scores, context_lens, block_size: int, budget: int, sink: in
     """The blocks that every (sequence, KV head) reads under ``budget``: the first ``sink``,
     the last ``recent`` and those with the largest scores. Returns ``selected`` (int32
     [B][Hkv][budget], ascending, -1 behind)."""
-    import torch
-
+    dev = _current()
     if scores.dim() != 3 or context_lens.shape != scores.shape[:1]:
         raise ValueError("scores must be [num_seqs][num_kv_heads][stride], context_lens [num_seqs]")
     B, Hkv, stride = scores.shape
     if selected is None:
-        selected = _empty(stream, scores, (B, Hkv, max(int(budget), 0)), torch.int32)
+        selected = _empty(stream, scores, (B, Hkv, max(int(budget), 0)), _i32)
     if selected.shape != (B, Hkv, budget):
         raise ValueError("selected must be [num_seqs][num_kv_heads][budget]")
     _check(load().pa_block_select(
-        _dev_ptr(scores, torch.float32, "scores"),
-        _dev_ptr(context_lens, torch.int32, "context_lens"),
-        _dev_ptr(selected, torch.int32, "selected"), B, Hkv, stride, int(block_size), int(budget),
+        _ptr(scores, _f32, "scores", dev),
+        _ptr(context_lens, _i32, "context_lens", dev),
+        _ptr(selected, _i32, "selected", dev), B, Hkv, stride, int(block_size), int(budget),
         int(sink), int(recent), _stream_handle(stream)), "pa_block_select")
     return selected
 
@@ -1031,8 +1049,7 @@ def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, max_cont
     [B][Hkv][num_selected], logical blocks of the sequence, negative ones skipped) alone;
     returns ``out`` (bf16, the shape of ``q``). Caches of every type, one or several new
     tokens, as in ``pa_decode``."""
-    import torch
-
+    dev = _current()
     lib = load()
     n = _selected_shape(q, k_cache, selected)
     if out is None:
@@ -1042,10 +1059,10 @@ def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, max_cont
     if workspace is None:
         need = int(lib.pa_decode_selected_workspace_size(ctypes.byref(p), n))
         if need > 0:
-            workspace = _empty(stream, q, need, torch.uint8)
-    ws_ptr = _dev_ptr(workspace, torch.uint8, "workspace") if workspace is not None else None
+            workspace = _empty(stream, q, need, _u8)
+    ws_ptr = _ptr(workspace, _u8, "workspace", dev) if workspace is not None else None
     ws_bytes = workspace.numel() if workspace is not None else 0
-    _check(lib.pa_decode_selected(ctypes.byref(p), _dev_ptr(selected, torch.int32, "selected"), n,
+    _check(lib.pa_decode_selected(ctypes.byref(p), _ptr(selected, _i32, "selected", dev), n,
                                   ws_ptr, ws_bytes, _stream_handle(stream)), "pa_decode_selected")
     return out
 

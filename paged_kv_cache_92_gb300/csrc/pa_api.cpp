@@ -1052,13 +1052,16 @@ pa_status pa_block_bounds(const pa_block_bounds_params* p, pa_stream_t stream) {
                          "PA_KV_FP4_E2M1");
   if (int64_t(p->max_blocks_per_seq) * p->block_size > kMaxEvictTokens)
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: table rows of more than 2^30 tokens");
+  if (int64_t(p->max_blocks_per_seq) * p->num_kv_heads > INT32_MAX)
+    return pa::set_error(PA_ERR_INVALID_ARG,
+                         "pa_block_bounds: max_blocks_per_seq * num_kv_heads exceeds 2^31");
   if (p->num_seqs == 0) return PA_OK;
   if (!p->k_cache || !p->bounds || !p->block_tables || !p->context_lens)
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: a required pointer is NULL");
   if (!pa::aligned16(p->k_cache) || !pa::aligned16(p->bounds) || misaligned4(p->block_tables) ||
       misaligned4(p->context_lens) || misaligned4(p->old_lens))
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: misaligned pointer");
-  const int e = pa::launch_block_bounds(p, pa::tc_grid(), stream);
+  const int e = pa::launch_block_bounds(p, stream);
   if (e != 0) return pa::set_cuda_error("pa_block_bounds: launch", e);
   return PA_OK;
 }

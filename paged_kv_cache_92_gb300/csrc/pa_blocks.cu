@@ -36,7 +36,10 @@ __device__ unsigned int g_blocks_errors;
 
 // ---------------------------------------------------------------- bounds
 
-constexpr int BOUND_WARPS = 8;
+// Warps of a CTA (64 sequences' prompts in bf16, 32 in 4 bits, d 128: with 8 106.8 and
+// 73.7 us, with 4 108.9 and 58.4, with 2 133.6 and 67.3).
+template <int FMT>
+constexpr int bound_warps = FMT == PA_KV_BF16 ? 8 : 4;
 
 struct Bounds {
   const unsigned char* k_cache;
@@ -68,15 +71,19 @@ __device__ __forceinline__ uint32_t bf16_of_f16(uint32_t x) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// Lanes take 16-byte chunks of the rows: LPR lanes a row, 32 / LPR rows at a time.
+// Lanes take chunks of the rows: LPR lanes a row, 32 / LPR rows at a time. 16 bytes, of
+// 4-bit codes 8 (a group of 16 elements): those are bound by the ALU, and the fewer
+// elements a lane has of more rows, the fewer have to meet between lanes.
 template <int FMT, int D, int BS>
-__global__ void __launch_bounds__(BOUND_WARPS * 32) block_bounds_kernel(const Bounds P) {
+__global__ void __launch_bounds__(bound_warps<FMT> * 32) block_bounds_kernel(const Bounds P) {
+  constexpr int WARPS = bound_warps<FMT>;
   constexpr int ROWB = FMT == PA_KV_BF16 ? 2 * D : (FMT == PA_KV_FP8_E4M3 ? D : D / 2);
   constexpr int SCALES = FMT == PA_KV_FP4_E2M1 ? D / 16 : 0;
   constexpr int TILE = BS * (ROWB + SCALES);
-  constexpr int LPR = ROWB / 16, RPL = 32 / LPR;       // lanes of a row, rows of a load
+  constexpr int CHUNK = FMT == PA_KV_FP4_E2M1 ? 8 : 16, WORDS = CHUNK / 4;
+  constexpr int LPR = ROWB / CHUNK, RPL = 32 / LPR;    // lanes of a row, rows of a load
   constexpr int LOADS = (BS + RPL - 1) / RPL;
-  constexpr int PAIRS = FMT == PA_KV_BF16 ? 4 : (FMT == PA_KV_FP8_E4M3 ? 8 : 16);  // of a chunk
+  constexpr int PAIRS = FMT == PA_KV_BF16 ? 4 : 8;     // of a chunk
   dev::griddep_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y;
@@ -86,10 +93,9 @@ __global__ void __launch_bounds__(BOUND_WARPS * 32) block_bounds_kernel(const Bo
   if (blockIdx.x == 0 && threadIdx.x == 0 && (L > cap || last - first > P.per_seq))
     atomicOr(&g_blocks_errors, PA_DEVERR_CONTEXT_LEN);
   const int n = min(last - first, P.per_seq);
-  const int64_t units = int64_t(max(n, 0)) * P.num_kv_heads;
-  for (int64_t u = int64_t(blockIdx.x) * BOUND_WARPS + warp; u < units;
-       u += int64_t(gridDim.x) * BOUND_WARPS) {
-    const int k = int(u / P.num_kv_heads), head = int(u - int64_t(k) * P.num_kv_heads);
+  const uint32_t heads = uint32_t(P.num_kv_heads), units = uint32_t(max(n, 0)) * heads;
+  for (uint32_t u = blockIdx.x * WARPS + warp; u < units; u += gridDim.x * WARPS) {
+    const int k = int(u / heads), head = int(u - k * heads);
     const int j = first + k;
     const int e = P.block_tables[int64_t(b) * P.max_blocks_per_seq + j];
     if (e < 0 || e >= P.num_blocks) {
@@ -100,19 +106,35 @@ __global__ void __launch_bounds__(BOUND_WARPS * 32) block_bounds_kernel(const Bo
     const int64_t at = int64_t(e) * P.num_kv_heads + head;
     const unsigned char* tile = P.k_cache + at * TILE;
     const int row0 = lane / LPR, chunk = lane % LPR;
-    uint4 raw[LOADS];
-    uint16_t sf[LOADS];
+    uint32_t raw[LOADS][WORDS];
+    uint8_t sf[LOADS];
+    auto load = [&](int i, const unsigned char* codes, const unsigned char* scale) {
+      if constexpr (CHUNK == 16) {
+        const uint4 y = *reinterpret_cast<const uint4*>(codes);
+        raw[i][0] = y.x; raw[i][1] = y.y; raw[i][2] = y.z; raw[i][3] = y.w;
+      } else {
+        const uint2 y = *reinterpret_cast<const uint2*>(codes);
+        raw[i][0] = y.x; raw[i][1] = y.y;
+        sf[i] = *scale;
+      }
+    };
+    const unsigned char* scales = tile + BS * ROWB + chunk;
+    if (BS >= RPL && rows == BS) {  // addresses apart by constants
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int r = min(row0 + i * RPL, rows - 1);  // (a row that counts twice changes nothing)
-      raw[i] = *reinterpret_cast<const uint4*>(tile + r * ROWB + chunk * 16);
-      if constexpr (FMT == PA_KV_FP4_E2M1)
-        sf[i] = *reinterpret_cast<const uint16_t*>(tile + BS * ROWB + r * SCALES + chunk * 2);
+      for (int i = 0; i < LOADS; ++i)
+        load(i, tile + row0 * ROWB + chunk * CHUNK + i * RPL * ROWB,
+             scales + row0 * SCALES + i * RPL * SCALES);
+    } else {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int r = min(row0 + i * RPL, rows - 1);  // (a row that counts twice changes nothing)
+        load(i, tile + r * ROWB + chunk * CHUNK, scales + r * SCALES);
+      }
     }
-    uint32_t lo[PAIRS], hi[PAIRS];
+    uint32_t v[2 * PAIRS];  // least, then largest
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      const uint32_t(&w)[WORDS] = raw[i];
       uint32_t x[PAIRS];
       if constexpr (FMT == PA_KV_BF16) {
 #pragma unroll
@@ -121,50 +143,58 @@ __global__ void __launch_bounds__(BOUND_WARPS * 32) block_bounds_kernel(const Bo
 #pragma unroll
         for (int p = 0; p < 8; ++p) x[p] = dev::e4m3x2_to_f16((w[p / 2] >> (16 * (p & 1))) & 0xffffu);
       } else {
-        const uint32_t s = dev::e4m3x2_to_f16(sf[i]);
-        const uint32_t s0 = __byte_perm(s, 0, 0x1010), s1 = __byte_perm(s, 0, 0x3232);
+        const uint32_t s = __byte_perm(dev::e4m3x2_to_f16(sf[i]), 0, 0x1010);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t y[4];
           dev::e2m1x8_to_f16(w[c], y);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) x[4 * c + p] = dev::mul_f16x2(y[p], c < 2 ? s0 : s1);
+          for (int p = 0; p < 4; ++p) x[4 * c + p] = dev::mul_f16x2(y[p], s);
         }
       }
 #pragma unroll
       for (int p = 0; p < PAIRS; ++p) {
         if (i == 0) {
-          lo[p] = hi[p] = x[p];
+          v[p] = v[PAIRS + p] = x[p];
         } else {
-          lower<FMT>(lo[p], x[p]);
-          raise<FMT>(hi[p], x[p]);
+          lower<FMT>(v[p], x[p]);
+          raise<FMT>(v[PAIRS + p], x[p]);
         }
       }
     }
+    // Over the lanes of a chunk (one per row0). The largest become least of the negated,
+    // so that both halves reduce alike: at every exchange a lane keeps half of what it
+    // has, until it has 4 pairs, the 16-byte piece row0 % PIECES of the chunk's result.
 #pragma unroll
-    for (int o = LPR; o < 32; o <<= 1)
-#pragma unroll
-      for (int p = 0; p < PAIRS; ++p) {
-        lower<FMT>(lo[p], __shfl_xor_sync(0xffffffffu, lo[p], o));
-        raise<FMT>(hi[p], __shfl_xor_sync(0xffffffffu, hi[p], o));
-      }
-    // every lane of a chunk has its result; lanes of row r write its 16-byte piece r
+    for (int p = 0; p < PAIRS; ++p) v[PAIRS + p] ^= 0x80008000u;
     constexpr int PIECES = 2 * PAIRS / 4;
-    unsigned char* out = reinterpret_cast<unsigned char*>(P.bounds) + at * (4 * D) + chunk * PAIRS * 4;
-#pragma unroll
-    for (int p = 0; p < PIECES; ++p) {
-      const int q = p % (PIECES / 2) * 4;
-      uint32_t y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i] = p < PIECES / 2 ? lo[q + i] : hi[q + i];
-        if constexpr (FMT != PA_KV_BF16) y[i] = bf16_of_f16(y[i]);
-      }
-      if (row0 == p)
-        *reinterpret_cast<uint4*>(out + (p < PIECES / 2 ? 0 : 2 * D) + q * 4) =
-            make_uint4(y[0], y[1], y[2], y[3]);
-    }
     static_assert(PIECES <= RPL, "a lane for every piece");
+#pragma unroll
+    for (int half = PAIRS, o = LPR * PIECES / 2; half >= 4; half /= 2, o /= 2) {
+      const bool upper = lane & o;
+#pragma unroll
+      for (int p = 0; p < half; ++p) {
+        const uint32_t mine = upper ? v[half + p] : v[p], other = upper ? v[p] : v[half + p];
+        v[p] = mine;
+        lower<FMT>(v[p], __shfl_xor_sync(0xffffffffu, other, o));
+      }
+    }
+#pragma unroll
+    for (int o = LPR * PIECES; o < 32; o <<= 1)
+#pragma unroll
+      for (int p = 0; p < 4; ++p) lower<FMT>(v[p], __shfl_xor_sync(0xffffffffu, v[p], o));
+    const bool largest = row0 & (PIECES / 2);
+    uint4 piece;
+    uint32_t* y = reinterpret_cast<uint32_t*>(&piece);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      y[p] = largest ? v[p] ^ 0x80008000u : v[p];
+      if constexpr (FMT != PA_KV_BF16) y[p] = bf16_of_f16(y[p]);
+    }
+    if (row0 < PIECES)
+      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(P.bounds) + at * (4 * D) +
+                                (largest ? 2 * D : 0) + chunk * PAIRS * 4 +
+                                row0 % (PIECES / 2) * 16) = piece;
   }
 }
 
@@ -434,23 +464,27 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
 }
 
 template <int FMT, int D>
-int launch_bounds_bs(const Bounds& P, int block_size, dim3 grid, cudaStream_t s) {
+int launch_bounds_bs(const Bounds& P, int block_size, int num_seqs, cudaStream_t s) {
+  constexpr int WARPS = bound_warps<FMT>, threads = WARPS * 32;
+  int64_t x = (int64_t(P.per_seq) * P.num_kv_heads + WARPS - 1) / WARPS;
+  if (x > 65535) x = 65535;  // (warps go on by the grid's width)
+  const dim3 grid{unsigned(x), unsigned(num_seqs)};
   switch (block_size) {
-    case 8: return launch_ordered(block_bounds_kernel<FMT, D, 8>, grid, BOUND_WARPS * 32, 0, s, 1, P);
-    case 16: return launch_ordered(block_bounds_kernel<FMT, D, 16>, grid, BOUND_WARPS * 32, 0, s, 1, P);
-    case 32: return launch_ordered(block_bounds_kernel<FMT, D, 32>, grid, BOUND_WARPS * 32, 0, s, 1, P);
+    case 8: return launch_ordered(block_bounds_kernel<FMT, D, 8>, grid, threads, 0, s, 1, P);
+    case 16: return launch_ordered(block_bounds_kernel<FMT, D, 16>, grid, threads, 0, s, 1, P);
+    case 32: return launch_ordered(block_bounds_kernel<FMT, D, 32>, grid, threads, 0, s, 1, P);
     default: return int(cudaErrorInvalidValue);
   }
 }
 template <int FMT>
-int launch_bounds_d(const Bounds& P, int head_dim, int block_size, dim3 grid, cudaStream_t s) {
-  return head_dim == 64 ? launch_bounds_bs<FMT, 64>(P, block_size, grid, s)
-                        : launch_bounds_bs<FMT, 128>(P, block_size, grid, s);
+int launch_bounds_d(const Bounds& P, const pa_block_bounds_params* p, cudaStream_t s) {
+  return p->head_dim == 64 ? launch_bounds_bs<FMT, 64>(P, p->block_size, p->num_seqs, s)
+                           : launch_bounds_bs<FMT, 128>(P, p->block_size, p->num_seqs, s);
 }
 
 }  // namespace
 
-int launch_block_bounds(const pa_block_bounds_params* p, int num_sms, void* stream) {
+int launch_block_bounds(const pa_block_bounds_params* p, void* stream) {
   Bounds P;
   P.k_cache = static_cast<const unsigned char*>(p->k_cache);
   P.bounds = static_cast<__nv_bfloat16*>(p->bounds);
@@ -463,17 +497,11 @@ int launch_block_bounds(const pa_block_bounds_params* p, int num_sms, void* stre
   // blocks that max_new_tokens tokens can touch, wherever they begin
   const int64_t touched = (int64_t(p->max_new_tokens) + 2 * p->block_size - 2) / p->block_size;
   P.per_seq = int(touched < p->max_blocks_per_seq ? touched : p->max_blocks_per_seq);
-  const int64_t units = int64_t(P.per_seq) * p->num_kv_heads;
-  int64_t x = (units + BOUND_WARPS - 1) / BOUND_WARPS;
-  if (x > 65535) x = 65535;  // (warps go on by the grid's width)
-  const dim3 grid(unsigned(x), unsigned(p->num_seqs));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  (void)num_sms;
   switch (p->kv_dtype) {
-    case PA_KV_BF16: return launch_bounds_d<PA_KV_BF16>(P, p->head_dim, p->block_size, grid, s);
-    case PA_KV_FP8_E4M3:
-      return launch_bounds_d<PA_KV_FP8_E4M3>(P, p->head_dim, p->block_size, grid, s);
-    default: return launch_bounds_d<PA_KV_FP4_E2M1>(P, p->head_dim, p->block_size, grid, s);
+    case PA_KV_BF16: return launch_bounds_d<PA_KV_BF16>(P, p, s);
+    case PA_KV_FP8_E4M3: return launch_bounds_d<PA_KV_FP8_E4M3>(P, p, s);
+    default: return launch_bounds_d<PA_KV_FP4_E2M1>(P, p, s);
   }
 }
 
