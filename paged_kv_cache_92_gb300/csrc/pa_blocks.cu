@@ -16,9 +16,10 @@
 //    order of a contraction is free, so a lane takes 16-byte runs), B the query rows
 //    of a KV head. fp32 sums of exact products. Bound by the bytes of the bounds.
 //  * block_select_kernel: one CTA per (sequence, KV head) with the row's scores as
-//    ordered 32-bit keys in registers; the key of the budget's rank is found bit by bit
-//    from the first bit in which keys differ, a count over the CTA each, until a count
-//    meets the budget. Ties go to the lowest index through ranks. Bound by latency.
+//    ordered 32-bit keys in registers; the key of the budget's rank is found by histograms
+//    in shared memory, the first over the range that the keys span, the next over the bin
+//    that holds it, until a bin is kept whole (for scores that differ, two). Ties go to the
+//    lowest index through ranks. Bound by latency.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -200,7 +201,11 @@ __global__ void __launch_bounds__(bound_warps<FMT> * 32) block_bounds_kernel(con
 
 // ---------------------------------------------------------------- scores
 
-constexpr int SCORE_WARPS = 4;
+// Warps of a CTA. With one tile of query rows they share nothing, and the more CTAs the
+// evener the SMs' ends: 64 long contexts take 61 us with four, 56 with two, 54 with one.
+template <bool ONE>
+constexpr int score_warps = ONE ? 1 : 4;
+constexpr int SCORE_RUN = 4;  // 16-block tiles of a warp
 
 struct Scores {
   const __nv_bfloat16* q;
@@ -221,15 +226,43 @@ __device__ __forceinline__ uint32_t part_of(uint32_t x, bool neg) {
   return x & ((s >> 15) * 0xffffu);
 }
 
-// grid (partition, KV head, sequence)
+// A lane's runs of a row of bounds. In order, all before the products that use them: left
+// to the compiler some are put off, and 64 long contexts take 67 us instead of 58.
 template <int D>
-__global__ void __launch_bounds__(SCORE_WARPS * 32) block_scores_kernel(const Scores P) {
+__device__ __forceinline__ void load_bounds(dev::KeyRow<PA_KV_BF16, D>& x, const unsigned char* at) {
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.w[4 * j]), "=r"(x.w[4 * j + 1]), "=r"(x.w[4 * j + 2]), "=r"(x.w[4 * j + 3])
+                 : "l"(at + j * 64)
+                 : "memory");
+}
+
+// grid (partition, KV head, sequence). A warp takes 16 blocks at a time, whose bounds are
+// read into fragments; the next 16 blocks' table entries are on their way meanwhile. ONE:
+// one tile of 8 query rows, in registers; else up to MAX_SHARED tiles of them in shared
+// memory (both parts of every row), more tiles in turn, with the bounds read again.
+constexpr int MAX_SHARED = 8;
+template <int D, bool ONE>
+__global__ void __launch_bounds__(score_warps<ONE> * 32, 16 / score_warps<ONE>)
+    block_scores_kernel(const Scores P) {
+  constexpr int WARPS = score_warps<ONE>;
   using Row = dev::KeyRow<PA_KV_BF16, D>;
   dev::griddep_enter();
+  extern __shared__ __align__(16) uint4 sm_q[];  // [tile][part][D / 32][32 lanes]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int head = blockIdx.y, b = blockIdx.z;
   const int BS = 1 << P.bs_log2, G = 1 << P.g_log2;
+  // the first tile's entries are on their way while the length is
+  const int32_t* table = P.block_tables + int64_t(b) * P.max_blocks_per_seq;
+  const int first = blockIdx.x * P.part_tiles + warp;
+  auto entry = [&](int tile, int r) {
+    const int j = tile * 16 + r * 8 + g;
+    return j < P.max_blocks_per_seq ? table[j] : 0;
+  };
+  int e[2] = {entry(first, 0), entry(first, 1)};
+  const float f = P.k_scale != nullptr ? P.scale * P.k_scale[head] : P.scale;
   int L = P.context_lens[b];
   if (L > P.cap || (L > 0 && L < P.q_len)) {
     if (blockIdx.x == 0 && head == 0 && threadIdx.x == 0)
@@ -239,17 +272,19 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) block_scores_kernel(const Sc
   }
   if (L < P.q_len || L <= 0) return;
   const int n_blocks = (L + BS - 1) >> P.bs_log2;
-  const int n_cols = P.q_len << P.g_log2;
-  const float f = P.k_scale != nullptr ? P.scale * P.k_scale[head] : P.scale;
+  const int tiles = (n_blocks + 15) / 16;
+  const int tile1 = min(tiles, (int(blockIdx.x) + 1) * P.part_tiles);
+  if (int(blockIdx.x) * P.part_tiles >= tiles) return;
+  const int n_cols = P.q_len << P.g_log2, col_tiles = ONE ? 1 : (n_cols + 7) / 8;
   // a negative factor turns the queries instead
   const uint32_t turn = f < 0.0f ? 0x80008000u : 0u;
   const float factor = fabsf(f);
-  auto load_queries = [&](int c0, uint32_t (&up)[1][D / 16][2], uint32_t (&down)[1][D / 16][2]) {
-    const int n = c0 + g;
-    const int64_t row = (int64_t(b) * P.q_len + (min(n, n_cols - 1) >> P.g_log2)) *
-                            (P.num_kv_heads << P.g_log2) + head * G + (min(n, n_cols - 1) & (G - 1));
+  auto load_queries = [&](int ct, uint32_t (&up)[1][D / 16][2], uint32_t (&down)[1][D / 16][2]) {
+    const int n = min(ct * 8 + g, n_cols - 1);
+    const int64_t row = (int64_t(b) * P.q_len + (n >> P.g_log2)) * (P.num_kv_heads << P.g_log2) +
+                        head * G + (n & (G - 1));
     uint4 raw[D / 32];
-    dev::query_load<PA_KV_BF16, D>(P.q + row * D, n < n_cols, t, raw);
+    dev::query_load<PA_KV_BF16, D>(P.q + row * D, ct * 8 + g < n_cols, t, raw);
     uint32_t qf[D / 16][2];
     dev::query_fragment<PA_KV_BF16, D>(raw, qf);
 #pragma unroll
@@ -260,47 +295,81 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) block_scores_kernel(const Sc
         down[0][s][i] = part_of(qf[s][i] ^ turn, true);
       }
   };
-  uint32_t up[1][D / 16][2], down[1][D / 16][2];
-  load_queries(0, up, down);
-  int loaded = 0;  // the columns at hand
-  const int tiles = (n_blocks + 15) / 16;
-  const int tile1 = min(tiles, (int(blockIdx.x) + 1) * P.part_tiles);
-  const int32_t* table = P.block_tables + int64_t(b) * P.max_blocks_per_seq;
   float* out = P.scores + (int64_t(b) * P.num_kv_heads + head) * P.scores_stride;
   bool bad_entry = false;
-  for (int tile = blockIdx.x * P.part_tiles + warp; tile < tile1; tile += SCORE_WARPS) {
-    Row lo[2], hi[2];  // of blocks g and g + 8 of the tile
+  uint32_t up[1][D / 16][2], down[1][D / 16][2];
+  if (ONE) load_queries(0, up, down);
+  for (int c0 = 0; c0 < col_tiles; c0 += MAX_SHARED) {
+    const int n_ct = ONE ? 1 : min(MAX_SHARED, col_tiles - c0);
+    if (!ONE) {
+      if (c0 > 0) __syncthreads();  // the previous rows have been read
+      for (int ct = warp; ct < n_ct; ct += WARPS) {
+        load_queries(c0 + ct, up, down);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int j = min(tile * 16 + r * 8 + g, n_blocks - 1);
-      int e = table[j];
-      bad_entry |= e < 0 || e >= P.num_blocks;
-      e = e < 0 || e >= P.num_blocks ? 0 : e;
-      const unsigned char* at = P.bounds + (int64_t(e) * P.num_kv_heads + head) * (4 * D) + t * 16;
-      lo[r].load(at, nullptr);
-      hi[r].load(at + 2 * D, nullptr);
-    }
-    float best[2] = {-INFINITY, -INFINITY};
-    for (int c0 = 0; c0 < n_cols; c0 += 8) {
-      if (c0 != loaded) load_queries(loaded = c0, up, down);
-      float s[1][4] = {{0.0f, 0.0f, 0.0f, 0.0f}};
-      dev::key_product<PA_KV_BF16, D, 1>(s, hi[0], hi[1], up);
-      dev::key_product<PA_KV_BF16, D, 1>(s, lo[0], lo[1], down);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = c0 + 2 * t + (i & 1), j = tile * 16 + (i >> 1) * 8 + g;
-        const bool sees = n < n_cols && (j << P.bs_log2) <= L - P.q_len + (n >> P.g_log2);
-        float x = s[0][i] * factor;
-        x = x != x ? INFINITY : x;  // a bound that is no number hides nothing
-        if (sees) best[i >> 1] = fmaxf(best[i >> 1], x);
+        for (int c = 0; c < D / 32; ++c) {
+          uint4* at = sm_q + (ct * 2 * (D / 32) + c) * 32 + lane;
+          at[0] = make_uint4(up[0][2 * c][0], up[0][2 * c][1], up[0][2 * c + 1][0], up[0][2 * c + 1][1]);
+          at[D / 32 * 32] =
+              make_uint4(down[0][2 * c][0], down[0][2 * c][1], down[0][2 * c + 1][0], down[0][2 * c + 1][1]);
+        }
       }
+      __syncthreads();
     }
+    for (int tile = first; tile < tile1; tile += WARPS) {
+      Row lo[2], hi[2];  // of blocks g and g + 8 of the tile
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
-      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-      const int j = tile * 16 + r * 8 + g;
-      if (t == 0 && j < n_blocks) out[j] = best[r];
+      for (int r = 0; r < 2; ++r) {
+        const bool there = tile * 16 + r * 8 + g < n_blocks;
+        const bool bad = there && (e[r] < 0 || e[r] >= P.num_blocks);
+        bad_entry |= bad;
+        const unsigned char* at =
+            P.bounds + (int64_t(!there || bad ? 0 : e[r]) * P.num_kv_heads + head) * (4 * D) + t * 16;
+        load_bounds<D>(lo[r], at);
+        load_bounds<D>(hi[r], at + 2 * D);
+      }
+      const int next = tile + WARPS < tile1 ? tile + WARPS : first;
+      e[0] = entry(next, 0);
+      e[1] = entry(next, 1);
+      float best[2] = {-INFINITY, -INFINITY};
+      for (int ct = 0; ct < n_ct; ++ct) {
+        float s[2][1][4];  // of largest and least, apart: half the chain
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[0][0][i] = s[1][0][i] = 0.0f;
+        if constexpr (ONE) {
+          dev::key_product<PA_KV_BF16, D, 1>(s[0], hi[0], hi[1], up);
+          dev::key_product<PA_KV_BF16, D, 1>(s[1], lo[0], lo[1], down);
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const uint4* at = sm_q + (ct * 2 * (D / 32) + c) * 32 + lane;
+            const uint4 x = at[0], y = at[D / 32 * 32];
+            uint32_t a[4], z[4];
+            hi[0].pairs(c, a);
+            hi[1].pairs(c, z);
+            dev::mma_bf16_regs(s[0][0], a[0], z[0], a[1], z[1], x.x, x.y);
+            dev::mma_bf16_regs(s[0][0], a[2], z[2], a[3], z[3], x.z, x.w);
+            lo[0].pairs(c, a);
+            lo[1].pairs(c, z);
+            dev::mma_bf16_regs(s[1][0], a[0], z[0], a[1], z[1], y.x, y.y);
+            dev::mma_bf16_regs(s[1][0], a[2], z[2], a[3], z[3], y.z, y.w);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = (c0 + ct) * 8 + 2 * t + (i & 1), j = tile * 16 + (i >> 1) * 8 + g;
+          const bool sees = n < n_cols && (j << P.bs_log2) <= L - P.q_len + (n >> P.g_log2);
+          float x = (s[0][0][i] + s[1][0][i]) * factor;
+          x = x != x ? INFINITY : x;  // a bound that is no number hides nothing
+          if (sees) best[i >> 1] = fmaxf(best[i >> 1], x);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+        const int j = tile * 16 + r * 8 + g;
+        if (t == 0 && j < n_blocks) out[j] = c0 == 0 ? best[r] : fmaxf(out[j], best[r]);
+      }
     }
   }
   if (bad_entry) atomicOr(&g_blocks_errors, PA_DEVERR_TABLE_ENTRY);
@@ -324,17 +393,24 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, KV head). Warp w holds candidates [w * 32 E, (w + 1) * 32 E)
-// of a span, key e of a lane the e-th run of 32.
+constexpr int LOG_BINS = 10, BINS = 1 << LOG_BINS;
+
+// One CTA per (sequence, KV head). Of a span a warp holds `runs` runs of 32 candidates, no
+// more than the span needs, key e of a lane in the e-th of them.
 template <int WARPS, int E>
 __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P) {
-  constexpr int THREADS = WARPS * 32, SPAN = THREADS * E;
+  constexpr int THREADS = WARPS * 32, OWN = BINS / THREADS;
+  __shared__ int hist[BINS];
   __shared__ int counts[2][WARPS];
   __shared__ uint32_t ends[2][WARPS];
+  __shared__ int found[3];  // a bin, how many of its keys are kept, whether all are
   dev::griddep_enter();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x, b = row / P.num_kv_heads;
   const int BS = 1 << P.bs_log2;
+#pragma unroll
+  for (int k = 0; k < OWN; ++k) hist[tid + k * THREADS] = 0;
+  const float* scores = P.scores + int64_t(row) * P.scores_stride;
   const int L = max(P.context_lens[b], 0);
   int64_t blocks = (int64_t(L) + BS - 1) >> P.bs_log2;
   if (blocks > P.scores_stride) {
@@ -348,42 +424,38 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
     for (int j = tid; j < n; j += THREADS) out[j] = j;
     return;
   }
-  const float* scores = P.scores + int64_t(row) * P.scores_stride;
   const int c0 = P.sink, c1 = n - P.recent;         // the candidates
   const int need = P.budget - P.sink - P.recent;    // of them, fewer than there are
   for (int j = tid; j < P.sink; j += THREADS) out[j] = j;
   for (int j = tid; j < P.recent; j += THREADS) out[P.sink + need + j] = c1 + j;
   if (need == 0) return;
 
-  const int spans = (c1 - c0 + SPAN - 1) / SPAN;
-  auto index = [&](int span, int e) { return c0 + span * SPAN + (warp * E + e) * 32 + lane; };
+  const int runs = min(E, (c1 - c0 + THREADS - 1) / THREADS), span = runs * THREADS;
+  const int spans = (c1 - c0 + span - 1) / span;
+  const int mine0 = c0 + warp * runs * 32 + lane;
+  auto index = [&](int s, int e) { return mine0 + s * span + e * 32; };
   uint32_t key[E];
-  auto load = [&](int span) {
+  auto load = [&](int s) {  // all on their way together
+    float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int j = index(span, e);
-      key[e] = j < c1 ? score_key(scores[j]) : 0u;
+      const int j = index(s, e);
+      x[e] = 0.0f;
+      if (e < runs && j < c1) x[e] = scores[j];
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) key[e] = score_key(x[e]);
   };
-  int turn = 0;
-  // sum over the CTA; one barrier, two buffers
-  auto total = [&](int x) {
-    x = __reduce_add_sync(0xffffffffu, x);
-    if (lane == 0) counts[turn][warp] = x;
-    __syncthreads();
-    x = __reduce_add_sync(0xffffffffu, lane < WARPS ? counts[turn][lane] : 0);
-    turn ^= 1;
-    return x;
-  };
-  // the least and the largest key: bits above the first that differs are known
+  // the least and the largest key
   uint32_t least = 0xffffffffu, most = 0u;
   for (int s = 0; s < spans; ++s) {
     load(s);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      most = max(most, key[e]);
-      if (index(s, e) < c1) least = min(least, key[e]);
-    }
+    for (int e = 0; e < E; ++e)
+      if (e < runs && index(s, e) < c1) {
+        most = max(most, key[e]);
+        least = min(least, key[e]);
+      }
   }
   least = __reduce_min_sync(0xffffffffu, least);
   most = __reduce_max_sync(0xffffffffu, most);
@@ -394,35 +466,63 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
   __syncthreads();
   least = __reduce_min_sync(0xffffffffu, lane < WARPS ? ends[0][lane] : 0xffffffffu);
   most = __reduce_max_sync(0xffffffffu, lane < WARPS ? ends[1][lane] : 0u);
-  // threshold: the largest key that at least `need` candidates reach
-  int bit = 31 - __clz(least ^ most);  // -1: all alike
-  uint32_t threshold = bit < 0 ? most : most >> bit >> 1 << bit << 1;
-  bool exact = false;  // exactly `need` reach it
-  for (; bit >= 0 && !exact; --bit) {
-    const uint32_t x = threshold | 1u << bit;
-    int c = 0;
+  // The key of rank `need`: the range [least, most] in up to BINS bins, then the bin that
+  // holds it, until a bin is kept whole or is one key. `left`: how many of the range's keys
+  // are kept.
+  uint32_t threshold = least, width = most - least;
+  int left = need;
+  bool whole = false;
+  while (width > 0) {
+    const int shift = max(0, 32 - __clz(width) - LOG_BINS);
     for (int s = 0; s < spans; ++s) {
       if (spans > 1) load(s);
 #pragma unroll
-      for (int e = 0; e < E; ++e) c += key[e] >= x;  // (x > 0: not what lies past the row)
+      for (int e = 0; e < E; ++e) {
+        if (e >= runs) break;
+        const uint32_t x = key[e] - threshold;
+        if (index(s, e) < c1 && x <= width) atomicAdd(&hist[x >> shift], 1);
+      }
     }
-    c = total(c);
-    if (c >= need) threshold = x;
-    exact = c == need;
-  }
-  // of the keys that equal the threshold the first `ties` are kept
-  int ties = need;
-  if (!exact) {
-    int c = 0;
-    for (int s = 0; s < spans; ++s) {
-      if (spans > 1) load(s);
+    __syncthreads();
+    // bins from the top, OWN a thread: where the count reaches `left`
+    int mine[OWN], sum = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) c += key[e] > threshold;
+    for (int k = 0; k < OWN; ++k) {
+      mine[k] = hist[BINS - 1 - (tid * OWN + k)];
+      sum += mine[k];
     }
-    ties = need - total(c);
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) counts[0][warp] = upto;
+    __syncthreads();
+    upto += __reduce_add_sync(0xffffffffu, lane < warp ? counts[0][lane] : 0);
+    int above = upto - sum;
+    if (above < left && left <= upto) {
+#pragma unroll
+      for (int k = 0; k < OWN; ++k) {
+        if (above < left && left <= above + mine[k]) {
+          found[0] = BINS - 1 - (tid * OWN + k);
+          found[1] = left - above;
+          found[2] = left - above == mine[k];
+        }
+        above += mine[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) hist[BINS - 1 - (tid * OWN + k)] = 0;
+    __syncthreads();
+    threshold += uint32_t(found[0]) << shift;
+    left = found[1];
+    whole = found[2];
+    width = whole ? 0 : (1u << shift) - 1u;
   }
-  // ranks in index order
-  int equal_base = 0, keep_base = P.sink;
+  // kept: keys above the threshold (from it on, where its bin is kept whole), and the first
+  // `left` of those that equal it
+  int equal_base = 0, keep_base = P.sink, turn = 0;
   const uint32_t below = (1u << lane) - 1u;
   // exclusive prefix over the warps; `all` is the total
   auto prefix = [&](int x, int& all) {
@@ -435,26 +535,38 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
   };
   for (int s = 0; s < spans; ++s) {
     if (spans > 1) load(s);
-    uint32_t equal[E], kept[E];
-    int n_equal = 0, n_kept = 0;
+    uint32_t kept[E];
+    int n_kept = 0, all_equal = 0, all_kept;
+    if (whole) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      equal[e] = __ballot_sync(0xffffffffu, index(s, e) < c1 && key[e] == threshold);
-      n_equal += __popc(equal[e]);
+      for (int e = 0; e < E; ++e) {
+        if (e >= runs) break;
+        kept[e] = __ballot_sync(0xffffffffu, index(s, e) < c1 && key[e] >= threshold);
+        n_kept += __popc(kept[e]);
+      }
+    } else {
+      int n_equal = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (e >= runs) break;
+        n_equal += __popc(__ballot_sync(0xffffffffu, index(s, e) < c1 && key[e] == threshold));
+      }
+      int at = equal_base + prefix(n_equal, all_equal);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (e >= runs) break;
+        const bool in = index(s, e) < c1, same = in && key[e] == threshold;
+        const uint32_t equal = __ballot_sync(0xffffffffu, same);
+        const bool tie = same && at + __popc(equal & below) < left;
+        kept[e] = __ballot_sync(0xffffffffu, tie || (in && key[e] > threshold));
+        at += __popc(equal);
+        n_kept += __popc(kept[e]);
+      }
     }
-    int all_equal, all_kept;
-    int at = equal_base + prefix(n_equal, all_equal);
+    int at = keep_base + prefix(n_kept, all_kept);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const bool in = index(s, e) < c1;
-      const bool tie = in && key[e] == threshold && at + __popc(equal[e] & below) < ties;
-      kept[e] = __ballot_sync(0xffffffffu, tie || (in && key[e] > threshold));
-      at += __popc(equal[e]);
-      n_kept += __popc(kept[e]);
-    }
-    at = keep_base + prefix(n_kept, all_kept);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
+      if (e >= runs) break;
       if (kept[e] >> lane & 1u) out[at + __popc(kept[e] & below)] = index(s, e);
       at += __popc(kept[e]);
     }
@@ -480,6 +592,21 @@ template <int FMT>
 int launch_bounds_d(const Bounds& P, const pa_block_bounds_params* p, cudaStream_t s) {
   return p->head_dim == 64 ? launch_bounds_bs<FMT, 64>(P, p->block_size, p->num_seqs, s)
                            : launch_bounds_bs<FMT, 128>(P, p->block_size, p->num_seqs, s);
+}
+
+template <int D, bool ONE>
+int launch_scores_t(Scores P, int64_t tiles, int num_seqs, int num_sms, cudaStream_t s) {
+  constexpr int WARPS = score_warps<ONE>;
+  // SCORE_RUN tiles a warp, fewer where that leaves fewer than 16 warps an SM
+  const int64_t rows = int64_t(num_seqs) * P.num_kv_heads;
+  int64_t run = SCORE_RUN;
+  while (run > 1 && (tiles + run - 1) / run * rows < int64_t(num_sms) * 16) run /= 2;
+  P.part_tiles = int(run * WARPS);
+  const dim3 grid{unsigned((tiles + P.part_tiles - 1) / P.part_tiles), unsigned(P.num_kv_heads),
+                  unsigned(num_seqs)};
+  const int col_tiles = ((P.q_len << P.g_log2) + 7) / 8;
+  const size_t smem = ONE ? 0 : size_t(col_tiles < MAX_SHARED ? col_tiles : MAX_SHARED) * 32 * D;
+  return launch_ordered(block_scores_kernel<D, ONE>, grid, WARPS * 32, smem, s, 1, P);
 }
 
 }  // namespace
@@ -523,18 +650,13 @@ int launch_block_scores(const pa_block_scores_params* p, int num_sms, void* stre
   P.bs_log2 = log2_of(p->block_size);
   P.g_log2 = log2_of(p->num_q_heads / p->num_kv_heads);
   P.q_len = p->query_len > 1 ? p->query_len : 1;
-  // four tiles a warp, fewer where that leaves SMs idle
   const int64_t tiles = ((P.cap + p->block_size - 1) / p->block_size + 15) / 16;
-  const int64_t rows = int64_t(p->num_seqs) * p->num_kv_heads;
-  int64_t per = 4 * SCORE_WARPS;
-  while (per > SCORE_WARPS && (tiles + per - 1) / per * rows < int64_t(num_sms) * 4) per /= 2;
-  P.part_tiles = int(per);
-  const dim3 grid(unsigned((tiles + per - 1) / per), unsigned(p->num_kv_heads),
-                  unsigned(p->num_seqs));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p->head_dim == 64)
-    return launch_ordered(block_scores_kernel<64>, grid, SCORE_WARPS * 32, 0, s, 1, P);
-  return launch_ordered(block_scores_kernel<128>, grid, SCORE_WARPS * 32, 0, s, 1, P);
+  if ((P.q_len << P.g_log2) <= 8)
+    return p->head_dim == 64 ? launch_scores_t<64, true>(P, tiles, p->num_seqs, num_sms, s)
+                             : launch_scores_t<128, true>(P, tiles, p->num_seqs, num_sms, s);
+  return p->head_dim == 64 ? launch_scores_t<64, false>(P, tiles, p->num_seqs, num_sms, s)
+                           : launch_scores_t<128, false>(P, tiles, p->num_seqs, num_sms, s);
 }
 
 int launch_block_select(const float* scores, const int32_t* context_lens, int32_t* selected,
@@ -553,9 +675,13 @@ int launch_block_select(const float* scores, const int32_t* context_lens, int32_
   P.recent = recent;
   const dim3 grid(unsigned(num_seqs) * unsigned(num_kv_heads));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // a row in registers where it fits; longer ones are read again for every count
-  if (scores_stride <= 8 * 32 * 8)
+  // a row in registers where it fits; longer ones are read again for every range
+  if (scores_stride <= 2048)
     return launch_ordered(block_select_kernel<8, 8>, grid, 8 * 32, 0, s, 1, P);
+  if (scores_stride <= 4096)
+    return launch_ordered(block_select_kernel<8, 16>, grid, 8 * 32, 0, s, 1, P);
+  if (scores_stride <= 8192)
+    return launch_ordered(block_select_kernel<16, 16>, grid, 16 * 32, 0, s, 1, P);
   return launch_ordered(block_select_kernel<32, 16>, grid, 32 * 32, 0, s, 1, P);
 }
 
