@@ -317,19 +317,46 @@ struct State {
                                                const Columns<FMT, D, DUP>& q) {
     const int lane = threadIdx.x & 31;
     const int see_last = q.see0 + q.n_tok - 1;
-#pragma unroll 1
-    for (int k = 0; k < C::KEYS; ++k) {
-      const int at = key_position(pos, k);
-      if (at >= see_last) {
-        if constexpr (FMT == PA_KV_FP4_E2M1) {
-          if (lane < C::SCALES) *v_place(stage, k, lane * 16) = 0;
-        } else if constexpr (FMT == PA_KV_BF16) {
-          if (lane < D / 8) *reinterpret_cast<uint4*>(v_place(stage, k, lane * 8)) = uint4{};
-        } else {
+    unsigned char* vt = stage + C::HALF;
+    if constexpr (FMT == PA_KV_BF16) {
 #pragma unroll
-          for (int d = lane; d < D; d += 32) *v_place(stage, k, d) = 0;
+      for (int x = lane; x < C::KEYS * C::ROWB / 16; x += 32)
+        if (key_position(pos, x / (C::ROWB / 16)) >= see_last)
+          reinterpret_cast<uint4*>(vt)[x] = uint4{};
+    } else if constexpr (FMT == PA_KV_FP8_E4M3) {
+      constexpr int W = BS < TILE_KEYS ? BS : TILE_KEYS;  // keys of a sub-tile of V^T
+#pragma unroll 1
+      for (int u = 0; u < C::KEYS / W; ++u) {
+        const int seen = see_last - key_position(pos, u * W);  // of its keys, from the first
+        if (seen >= W) continue;
+        uint32_t keep[W / 4];
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+          const int n = min(max(seen - 4 * i, 0), 4);
+          keep[i] = n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
         }
-      } else if (at >= q.see0) {
+#pragma unroll
+        for (int d = lane; d < D; d += 32) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(vt + (u * D + d) * W);
+#pragma unroll
+          for (int i = 0; i < W / 4; ++i) x[i] &= keep[i];
+        }
+      }
+    } else {
+      static_assert(C::KEYS <= 32, "a lane for every key");
+      if (lane < C::KEYS && key_position(pos, lane) >= see_last)
+#pragma unroll
+        for (int i = 0; i < C::SCALES; i += 4)
+          *reinterpret_cast<uint32_t*>(vt + C::KEYS * C::ROWB + lane * C::SCALES + i) = 0;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int at = q.see0; at < see_last; ++at)  // keys that some see, block by block
+#pragma unroll 1
+      for (int n = 0; n < C::NBK; ++n) {
+        const int in = at - pos[n];
+        if (in < 0 || in >= (BS < C::KEYS ? BS : C::KEYS)) continue;
+        const int k = n * BS + in;
         float bad[D / 16][2];
         bool any = false;
 #pragma unroll
@@ -356,9 +383,8 @@ struct State {
                   *x = 0;
               }
         }
+        __syncwarp();
       }
-      __syncwarp();
-    }
   }
 
   // One step, its blocks' first positions `blocks`.
@@ -567,12 +593,15 @@ struct State {
 struct Entry {
   int pos, tile;
 };
-// Entry e of the list of (v, head), from its row `row0` on.
+// Entry e of the list of (sequence b, head): a logical block.
+__device__ __forceinline__ int listed(const Sel& P, int b, int head, int e) {
+  return P.selected[(int64_t(b) * P.num_kv_heads + head) * P.num_selected + e];
+}
+// Logical block j of v, from its row `row0` on.
 template <int BS>
-__device__ __forceinline__ Entry entry_of(const Sel& P, const Virtual& v, int head, int e, int row0,
+__device__ __forceinline__ Entry entry_of(const Sel& P, const Virtual& v, int head, int j, int row0,
                                           unsigned& errors) {
   Entry x{NOWHERE, 0};
-  const int j = P.selected[(int64_t(v.b) * P.num_kv_heads + head) * P.num_selected + e];
   if (j >= v.blocks) errors |= PA_DEVERR_KEEP;
   if (j >= 0 && j < v.blocks) {
     const int k = P.block_tables[int64_t(v.b) * P.max_blocks_per_seq + j];
@@ -640,8 +669,16 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int unit = blockIdx.x / split;
-  const int head = unit % P.num_kv_heads;
-  const Virtual v = virtual_of(P, unit / P.num_kv_heads, BS);
+  const int head = unit % P.num_kv_heads, vseq = unit / P.num_kv_heads;
+  // The list's entry for this lane's place in the warp's first steps (place_of below) if
+  // the sequence fills the list: on its way while the length is.
+  auto place_of = [&](int w0, int e0) {
+    const int step = warp + NWARPS * (w0 + lane / C::NBK);
+    return e0 + (C::NBK > 1 ? step * C::NBK + lane % C::NBK : step / C::SPB);
+  };
+  const int guess = place_of(0, int(int64_t(P.num_selected) * rank / split));
+  const int early = guess < P.num_selected ? listed(P, vseq / P.n_groups, head, guess) : -1;
+  const Virtual v = virtual_of(P, vseq, BS);
   const int n_cols = v.n_tok << P.g_log2;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[NWARPS][COLS], sm_l[NWARPS][COLS];
@@ -657,10 +694,11 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
   // The entries of this warp's steps [w0, w0 + WINDOW), NBK a step, one a lane.
   unsigned errors = 0;
   auto load_window = [&](int w0) {
+    const int e = place_of(w0, e0);
+    if (e >= e1) return Entry{NOWHERE, 0};
+    const int j = w0 == 0 && v.entries == P.num_selected ? early : listed(P, v.b, head, e);
     const int step = warp + NWARPS * (w0 + lane / C::NBK);
-    const int e = e0 + (C::NBK > 1 ? step * C::NBK + lane % C::NBK : step / C::SPB);
-    return e < e1 ? entry_of<BS>(P, v, head, e, step % C::SPB * C::KEYS, errors)
-                  : Entry{NOWHERE, 0};
+    return entry_of<BS>(P, v, head, j, step % C::SPB * C::KEYS, errors);
   };
   Entry window = load_window(0);
   Raw<FMT, D, DUP> raw;
@@ -896,7 +934,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<FMT, D, BS>::CTAS)
       p.at = x - c.before - p.head * steps;
       const int e = C::NBK > 1 ? p.at * C::NBK + lane % C::NBK : p.at / C::SPB;
       if (e < q.entries)
-        p.e = entry_of<BS>(P, q, p.head, e, p.at % C::SPB * C::KEYS, errors);
+        p.e = entry_of<BS>(P, q, p.head, listed(P, q.b, p.head, e), p.at % C::SPB * C::KEYS, errors);
     }
     cursor.before = __shfl_sync(0xffffffffu, c.before, 31);
     cursor.v = __shfl_sync(0xffffffffu, c.v, 31);
