@@ -1185,14 +1185,9 @@ static pa_status check_decode_selected(const pa_decode_params* p, int32_t num_se
     return pa::set_error(PA_ERR_UNSUPPORTED,
                          "pa_decode_selected: num_seqs * ceil(query_len / (8 / G)) * num_kv_heads "
                          "must be below 2^27");
-  // 32-bit indices of tiles, and of steps of all lists
   if (int64_t(p->num_blocks) * p->num_kv_heads > INT32_MAX)
     return pa::set_error(PA_ERR_INVALID_ARG,
                          "pa_decode_selected: num_blocks * num_kv_heads exceeds 2^31");
-  if (int64_t(p->num_seqs) * pa::fp4_columns(p).n_groups * p->num_kv_heads >
-      INT32_MAX / pa::selected_steps(p, num_selected))
-    return pa::set_error(PA_ERR_UNSUPPORTED,
-                         "pa_decode_selected: more than 2^31 steps of 16 keys in all lists");
   if (need_pointers && p->num_seqs > 0) {
     if (!p->q || !p->out || !p->k_cache || !p->v_cache || !p->block_tables || !p->context_lens ||
         !selected || (p->kv_dtype != PA_KV_BF16 && (!p->k_scale || !p->v_scale)))
@@ -1207,26 +1202,20 @@ static pa_status check_decode_selected(const pa_decode_params* p, int32_t num_se
 }
 
 size_t pa_decode_selected_workspace_size(const pa_decode_params* p, int32_t num_selected) {
-  if (check_decode_selected(p, num_selected, nullptr, false) != PA_OK) return 0;
-  return pa::selected_plan(p, num_selected, pa::tc_grid()).total;
+  (void)check_decode_selected(p, num_selected, nullptr, false);
+  return 0;  // the results of a list's CTAs meet in shared memory
 }
 
 pa_status pa_decode_selected(const pa_decode_params* p, const int32_t* selected,
                              int32_t num_selected, void* workspace, size_t workspace_bytes,
                              pa_stream_t stream) {
+  (void)workspace;
+  (void)workspace_bytes;
   const pa_status st = check_decode_selected(p, num_selected, selected, true);
   if (st != PA_OK) return st;
   if (p->num_seqs == 0) return PA_OK;
-  const pa::SelectedPlan plan = pa::selected_plan(p, num_selected, pa::tc_grid());
-  if (plan.total > 0 && (!workspace || workspace_bytes < plan.total))
-    return pa::set_error(PA_ERR_INVALID_ARG,
-                         "pa_decode_selected: workspace smaller than "
-                         "pa_decode_selected_workspace_size()");
-  if (plan.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
-    return pa::set_error(PA_ERR_INVALID_ARG,
-                         "pa_decode_selected: workspace must be 256-byte aligned");
-  const int e = pa::launch_decode_selected(p, selected, num_selected, plan,
-                                           static_cast<unsigned char*>(workspace), stream);
+  const int e = pa::launch_decode_selected(
+      p, selected, num_selected, pa::selected_plan(p, num_selected, pa::tc_grid()), stream);
   if (e != 0) return pa::set_cuda_error("pa_decode_selected: launch", e);
   return PA_OK;
 }

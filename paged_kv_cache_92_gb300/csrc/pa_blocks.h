@@ -21,16 +21,12 @@ int launch_block_select(const float* scores, const int32_t* context_lens, int32_
 int read_and_clear_blocks_errors(uint32_t* flags);
 
 // Attention over selected blocks (pa_decode_selected.cu): the query rows of a KV head
-// are the 8 columns of its products, as in the 4-bit decode. Small batches take `split`
-// CTAs, a cluster, for every list (a (sequence, column group, KV head)'s); others a stream
-// of all lists' steps over `grid` persistent CTAs, with two partials a warp for what is cut.
+// are the 8 columns of its products, as in the 4-bit decode; `split` CTAs, a cluster, take
+// the list of one (sequence, column group, KV head).
 struct SelectedPlan {
   MmaColumns cols;
   int cap;    // keys a sequence may have
   int split;  // CTAs of a cluster: 1, 2, 4 or 8
-  int grid;   // CTAs of the stream; 0: clusters
-  int part_cols;          // columns of a partial
-  size_t ml, acc, total;  // workspace: byte offsets of the partials, size (0: none)
 };
 // 16-key steps of a list, at most.
 inline int64_t selected_steps(const pa_decode_params* p, int num_selected) {
@@ -42,7 +38,7 @@ inline int64_t selected_steps(const pa_decode_params* p, int num_selected) {
 }
 SelectedPlan selected_plan(const pa_decode_params* p, int num_selected, int num_sms);
 int launch_decode_selected(const pa_decode_params* p, const int32_t* selected, int num_selected,
-                           const SelectedPlan& plan, unsigned char* ws, void* stream);
+                           const SelectedPlan& plan, void* stream);
 int read_and_clear_selected_errors(uint32_t* flags);
 
 }  // namespace pa

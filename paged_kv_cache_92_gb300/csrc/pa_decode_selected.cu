@@ -19,12 +19,10 @@
 //    the same product (their queries are those of columns 0 to 3), so they cost none.
 //  * 8-bit and 4-bit codes become f16 pairs in registers (exact), as in the 4-bit
 //    decode, with its scaling of queries and its reference for P in f16.
-//  * Small batches: `split` CTAs, a cluster, share the list of one (sequence, column
-//    group, KV head) and join their results through distributed shared memory: no
-//    workspace, no second launch. Larger ones: the steps of all lists are a stream that
-//    the warps of persistent CTAs take equal stretches of, each by itself, so that no warp
-//    waits for another one and the copies run on from list to list; a second launch joins
-//    the lists that were cut.
+//  * A CTA takes the list of one (sequence, column group, KV head); of few lists a
+//    cluster of up to eight, which join their results through distributed shared memory: no
+//    workspace, no second launch. The GPU deals out the CTAs as others end, which evens out
+//    ragged contexts.
 //  * Keys that a column must not see (behind the sequence, or behind one of several new
 //    tokens) have weight 0; where V holds no number there, 0 times it would still be
 //    none: in the steps that hold such keys, such elements of V are taken out first.
@@ -70,12 +68,7 @@ struct Sel {
   float scale_log2;
   int num_selected, max_blocks_per_seq, num_kv_heads, num_blocks, cap;
   int g_log2, q_len, q_group, n_groups;
-  int num_virtual;   // sequences * column groups
-  // of the streams:
-  int32_t* plan;     // [num_virtual + 1]: steps before each, then the total
-  float* part_ml;    // [2 * stretches][part_cols][2]: max, sum
-  float* part_acc;   // [2 * stretches][part_cols][D]
-  int part_cols;
+  int num_virtual;  // sequences * column groups
 };
 
 template <int FMT, int D, int BS>
@@ -87,7 +80,6 @@ struct Cfg {
   // step costs beside its keys is a tenth of its instructions)
   static constexpr int KEYS = FMT == PA_KV_BF16 ? 16 : 32;
   static constexpr int HALVES = KEYS / TILE_KEYS;           // products of a step
-  static constexpr int LEAST = 64 / KEYS;                   // steps of a stretch, at least
   static constexpr int HALF = KEYS * (ROWB + SCALES);       // K (or V) of a step
   static constexpr int STAGE = 2 * HALF;
   static constexpr int ST = 3;                              // stages of a warp's ring
@@ -95,7 +87,7 @@ struct Cfg {
   static constexpr int SPB = BS > KEYS ? BS / KEYS : 1;     // steps of a block
   static constexpr int WINDOW = 32 / NBK;                   // steps whose entries a warp holds
   static constexpr int RING = NWARPS * ST * STAGE;
-  // CTAs of the streams on an SM: by the rings, then by 65,536 registers
+  // CTAs on an SM: by the rings, then by 65,536 registers
   static constexpr int CTAS = D == 64 ? 4 : (FMT == PA_KV_FP4_E2M1 ? 3 : 2);
   static constexpr int OROW = D + 4;                        // padded row of the merge
   static constexpr int MERGE = NWARPS * COLS * OROW * 4;    // takes the rings' place at the end
@@ -660,7 +652,8 @@ __device__ __forceinline__ void report_lengths(const Sel& P) {
 
 // One list per cluster: its CTAs take equal stretches and join their results.
 template <int FMT, int D, int BS, bool DUP>
-__global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) {
+__global__ void __launch_bounds__(NTHREADS, Cfg<FMT, D, BS>::CTAS)
+    decode_selected_kernel(const Sel P) {
   using C = Cfg<FMT, D, BS>;
   constexpr int ST = C::ST;
   dev::griddep_enter();
@@ -812,314 +805,6 @@ __global__ void __launch_bounds__(NTHREADS) decode_selected_kernel(const Sel P) 
   if (split > 1) cluster.sync();  // no CTA leaves while another reads its rows
 }
 
-// ---------------------------------------------------------------- streams
-
-// The steps of all lists, one after the other, are dealt out to the warps of a
-// persistent grid in equal stretches: T positions, T / n or one more each, and `least` at
-// least (a stretch costs its queries and a partial).
-struct Deal {
-  int n, base, longer;  // stretches; positions of one; how many hold one more
-  __device__ __forceinline__ Deal(int T, int most, int least) {
-    n = T > 0 ? max(1, min(T / least, most)) : 0;
-    base = n > 0 ? T / n : 0;
-    longer = T - base * n;
-  }
-  __device__ __forceinline__ int start(int c) const { return c * base + min(c, longer); }
-  __device__ __forceinline__ int owner(int x) const {  // the stretch that holds position x
-    const int cut = longer * (base + 1);
-    return x < cut ? x / (base + 1) : longer + (x - cut) / base;
-  }
-};
-template <class C>
-__device__ __forceinline__ int steps_of(const Virtual& v) {
-  return (v.entries + C::NBK - 1) / C::NBK * C::SPB;
-}
-
-// Every warp works through its stretch by itself, its ring running on from list to list;
-// a list that a stretch's end cuts leaves partials, at most two a warp, which
-// merge_selected_kernel joins.
-template <int FMT, int D, int BS, bool DUP>
-__global__ void __launch_bounds__(NTHREADS, Cfg<FMT, D, BS>::CTAS)
-    stream_selected_kernel(const Sel P) {
-  using C = Cfg<FMT, D, BS>;
-  constexpr int ST = C::ST;
-  dev::griddep_enter();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  extern __shared__ __align__(128) unsigned char smem[];
-  unsigned char* ring = smem + warp * ST * C::STAGE;
-  struct Begin {
-    int before, v;  // steps before virtual sequence v, which holds a stretch's first one
-  };
-  // of a step in the ring: its blocks' positions, its list (virtual sequence and KV head),
-  // and its place there
-  struct Step {
-    int pos[C::NBK], v, head, at;
-  };
-  __shared__ Begin sm_begin[NWARPS];
-  __shared__ int warp_tot[NWARPS];
-  __shared__ Step sm_step[NWARPS][ST];
-
-  // ---- where the warps' stretches begin
-  int x0, n_my;
-  {
-    const int per = (P.num_virtual + NTHREADS - 1) / NTHREADS;
-    const int v0 = min(P.num_virtual, tid * per), v1 = min(P.num_virtual, v0 + per);
-    int sum = 0;
-    for (int v = v0; v < v1; ++v) sum += steps_of<C>(virtual_of(P, v, BS)) * P.num_kv_heads;
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) warp_tot[warp] = inc;
-    __syncthreads();
-    int before = inc - sum, T = 0;
-#pragma unroll
-    for (int w = 0; w < NWARPS; ++w) {
-      if (w < warp) before += warp_tot[w];
-      T += warp_tot[w];
-    }
-    const Deal deal(T, gridDim.x * NWARPS, C::LEAST);
-    const int c0 = blockIdx.x * NWARPS;
-    int start[NWARPS];
-    bool mine = blockIdx.x == 0;  // (CTA 0 writes the plan for the merge)
-#pragma unroll
-    for (int w = 0; w < NWARPS; ++w) {
-      start[w] = c0 + w < deal.n ? deal.start(c0 + w) : T;
-      mine |= before <= start[w] && start[w] < before + sum;
-    }
-    if (mine) {
-      int at = before;
-      for (int v = v0; v < v1; ++v) {
-        const int all = steps_of<C>(virtual_of(P, v, BS)) * P.num_kv_heads;
-        if (blockIdx.x == 0) P.plan[v] = at;
-#pragma unroll
-        for (int w = 0; w < NWARPS; ++w)
-          if (at <= start[w] && start[w] < at + all) sm_begin[w] = Begin{at, v};
-        at += all;
-      }
-    }
-    if (blockIdx.x == 0 && tid == 0) P.plan[P.num_virtual] = T;
-    __syncthreads();
-    const int c = c0 + warp;
-    x0 = c < deal.n ? deal.start(c) : T;
-    n_my = (c < deal.n ? deal.start(c + 1) : T) - x0;
-  }
-
-  // The entries of steps [w0, w0 + WINDOW) of the stretch, NBK a step, one a lane; the
-  // lanes walk on from the virtual sequence that held the previous window's last step.
-  Begin cursor = n_my > 0 ? sm_begin[warp] : Begin{0, 0};
-  unsigned errors = 0;
-  struct Place {
-    Entry e;
-    int v, head, at;
-  };
-  auto load_window = [&](int w0) {
-    Place p{{NOWHERE, 0}, 0, 0, 0};
-    const int i = w0 + lane / C::NBK;
-    Begin c = cursor;
-    if (i < n_my) {
-      const int x = x0 + i;
-      Virtual q = virtual_of(P, c.v, BS);
-      int steps = steps_of<C>(q);
-      while (x >= c.before + steps * P.num_kv_heads) {
-        c.before += steps * P.num_kv_heads;
-        q = virtual_of(P, ++c.v, BS);
-        steps = steps_of<C>(q);
-      }
-      p.v = c.v;
-      p.head = (x - c.before) / steps;
-      p.at = x - c.before - p.head * steps;
-      const int e = C::NBK > 1 ? p.at * C::NBK + lane % C::NBK : p.at / C::SPB;
-      if (e < q.entries)
-        p.e = entry_of<BS>(P, q, p.head, listed(P, q.b, p.head, e), p.at % C::SPB * C::KEYS, errors);
-    }
-    cursor.before = __shfl_sync(0xffffffffu, c.before, 31);
-    cursor.v = __shfl_sync(0xffffffffu, c.v, 31);
-    return p;
-  };
-  Place window = load_window(0);
-  // The queries of the list at hand when it begins, of the next one from then on: under
-  // the copies' load they take 3 to 4 us.
-  Raw<FMT, D, DUP> raw;
-  int v = __shfl_sync(0xffffffffu, window.v, 0), head = __shfl_sync(0xffffffffu, window.head, 0);
-  if (n_my > 0) raw.fetch(P, virtual_of(P, v, BS), head);
-  auto issue = [&](int i, int stage) {
-#pragma unroll
-    for (int n = 0; n < C::NBK; ++n) {
-      const int src = i % C::WINDOW * C::NBK + n;
-      const Entry e{__shfl_sync(0xffffffffu, window.e.pos, src),
-                    __shfl_sync(0xffffffffu, window.e.tile, src)};
-      if (i < n_my) {
-        if (lane == src) {
-          sm_step[warp][stage].pos[n] = window.e.pos;
-          if (n == 0) {
-            sm_step[warp][stage].v = window.v;
-            sm_step[warp][stage].head = window.head;
-            sm_step[warp][stage].at = window.at;
-          }
-        }
-        copy_block<FMT, D, BS>(P, ring + stage * C::STAGE, n, e);
-      }
-    }
-    dev::cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < ST - 1; ++i) issue(i, i);
-  Place coming = n_my > C::WINDOW ? load_window(C::WINDOW) : window;
-
-  Columns<FMT, D, DUP> cols;
-  State<FMT, D, BS, DUP> st;
-  int first = 0, done = 0;  // the steps of the list at hand that are done
-  int left = 0;             // those that are not (of the list, and of the stretch)
-  // the list's end, or the stretch's: a row of the result, or a partial
-  auto flush = [&]() {
-    const Virtual q = virtual_of(P, v, BS);
-    float maximum[2];
-    st.finish(cols, maximum);
-    const int n_cols = q.n_tok << P.g_log2;
-    const bool whole = first == 0 && done == steps_of<C>(q);
-    const float scale_v = cols.v_scale;
-    const int64_t slot = 2 * int64_t(blockIdx.x * NWARPS + warp) + (first == 0);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int n = 2 * t + c;
-      if (n < n_cols) {
-        if (whole) {
-          const float norm = st.l[c] == 0.0f ? 0.0f : scale_v / st.l[c];  // no key: zeros
-          __nv_bfloat16* out = P.out + q_row(P, q, head, n) * D;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int j = c; j < 4; j += 2)
-              out[st.element(k, j)] = __float2bfloat16_rn(st.o[k][j] * norm);
-        } else {
-          float* acc = P.part_acc + (slot * P.part_cols + n) * D;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int j = c; j < 4; j += 2) acc[st.element(k, j)] = st.o[k][j] * scale_v;
-          if (g == 0)
-            *reinterpret_cast<float2*>(P.part_ml + (slot * P.part_cols + n) * 2) =
-                make_float2(maximum[c], st.l[c]);
-        }
-      }
-    }
-  };
-  for (int i = 0, stage = 0; i < n_my; ++i) {
-    dev::cp_async_wait<ST - 2>();
-    __syncwarp();  // the step's copies by all lanes, and what is known of it
-    const int ahead = i + ST - 1;
-    if (ahead % C::WINDOW == 0) {
-      window = coming;
-      if (ahead + C::WINDOW < n_my) coming = load_window(ahead + C::WINDOW);
-    }
-    issue(ahead, stage == 0 ? ST - 1 : stage - 1);
-    const Step& now = sm_step[warp][stage];
-    if (left == 0) {  // a list begins
-      if (i > 0) flush();
-      v = now.v;
-      head = now.head;
-      first = done = now.at;
-      cols.take(P, raw);
-      st.clear();
-      Virtual q = virtual_of(P, v, BS);
-      left = min(steps_of<C>(q) - first, n_my - i);
-      if (i + left < n_my) {  // the stretch holds the beginning of the next list
-        int next = v, h = head + 1;
-        if (h == P.num_kv_heads) {
-          h = 0;
-          do q = virtual_of(P, ++next, BS);
-          while (q.entries == 0);
-        }
-        raw.fetch(P, q, h);
-      }
-    }
-    st.step(ring + stage * C::STAGE, now.pos, cols);
-    ++done;
-    --left;
-    __syncwarp();  // the stage has been read
-    stage = stage + 1 == ST ? 0 : stage + 1;
-  }
-  if (n_my > 0) flush();
-  if (errors) atomicOr(&g_selected_errors, errors);
-
-  // bad lengths are flagged, and rows of sequences without keys zeroed, by the CTAs in turn
-  report_lengths(P);
-  for (int u = blockIdx.x; u < P.num_virtual; u += gridDim.x) {
-    const Virtual q = virtual_of(P, u, BS);
-    if (q.entries > 0) continue;
-    const int num_q_heads = P.num_kv_heads << P.g_log2;
-    __nv_bfloat16* row = P.out + (int64_t(q.b) * P.q_len + q.first_tok) * num_q_heads * D;
-    for (int i = tid; i < q.n_tok * num_q_heads * D; i += NTHREADS) row[i] = __float2bfloat16_rn(0.0f);
-  }
-}
-
-// Joins the pieces of the lists that were cut: one warp per (list, column).
-template <int FMT, int D, int BS>
-__global__ void __launch_bounds__(128) merge_selected_kernel(const Sel P, int stretches) {
-  using C = Cfg<FMT, D, BS>;
-  constexpr int E = D / 32;  // elements of a lane
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int n = int(row % P.part_cols);
-  const int item = int(row / P.part_cols);
-  const int v = item / P.num_kv_heads, head = item - v * P.num_kv_heads;
-  if (v >= P.num_virtual) return;
-  const Virtual q = virtual_of(P, v, BS);
-  dev::griddep_wait();
-  if (q.entries == 0 || n >= (q.n_tok << P.g_log2)) return;
-  const int steps = steps_of<C>(q);
-  const int base = P.plan[v] + head * steps;
-  const Deal deal(P.plan[P.num_virtual], stretches, C::LEAST);
-  const int c0 = deal.owner(base), c1 = deal.owner(base + steps - 1);
-  if (c0 == c1) return;  // one piece: written by the stream
-  // eight pieces at a time, their loads in flight together
-  constexpr int BATCH = 8;
-  float M = -INFINITY, den = 0.0f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int c = c0; c <= c1; c += BATCH) {
-    float2 ml[BATCH], x[BATCH][E / 2];
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int64_t slot = (int64_t(2) * min(c + k, c1) + (c + k == c0)) * P.part_cols + n;
-      ml[k] = *reinterpret_cast<const float2*>(P.part_ml + slot * 2);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e)
-        x[k][e] = *reinterpret_cast<const float2*>(P.part_acc + slot * D + lane * E + 2 * e);
-      if (c + k > c1) ml[k].x = -INFINITY;
-    }
-    float top = M;
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
-    const float a = M == -INFINITY ? 0.0f : dev::fast_exp2(M - top);
-    M = top;
-    den *= a;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= a;
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (ml[k].x == -INFINITY) continue;  // no keys of this column in the piece
-      const float wt = dev::fast_exp2(ml[k].x - M);
-      den = fmaf(wt, ml[k].y, den);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        acc[2 * e] = fmaf(wt, x[k][e].x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(wt, x[k][e].y, acc[2 * e + 1]);
-      }
-    }
-  }
-  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-  const int64_t out = q_row(P, q, head, n);
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(P.out + out * D + lane * E + e) =
-        __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-}
-
 template <int FMT, int D, int BS, bool DUP>
 int launch_t(const Sel& P, const SelectedPlan& plan, cudaStream_t stream) {
   using C = Cfg<FMT, D, BS>;
@@ -1132,23 +817,13 @@ int launch_t(const Sel& P, const SelectedPlan& plan, cudaStream_t stream) {
   if (!(configured.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(decode_selected_kernel<FMT, D, BS, DUP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(stream_selected_kernel<FMT, D, BS, DUP>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::RING);
     if (e != cudaSuccess) return int(e);
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   const int64_t lists = int64_t(P.num_virtual) * P.num_kv_heads;
-  if (plan.grid == 0)
-    return launch_ordered(decode_selected_kernel<FMT, D, BS, DUP>,
-                          dim3(unsigned(lists * plan.split)), NTHREADS, C::SMEM, stream,
-                          unsigned(plan.split), P);
-  const int err = launch_ordered(stream_selected_kernel<FMT, D, BS, DUP>, dim3(unsigned(plan.grid)),
-                                 NTHREADS, C::RING, stream, 1, P);
-  if (err) return err;
-  return launch_ordered(merge_selected_kernel<FMT, D, BS>,
-                        dim3(unsigned((lists * P.part_cols + 3) / 4)), 128, 0, stream, 1, P,
-                        plan.grid * NWARPS);
+  return launch_ordered(decode_selected_kernel<FMT, D, BS, DUP>,
+                        dim3(unsigned(lists * plan.split)), NTHREADS, C::SMEM, stream,
+                        unsigned(plan.split), P);
 }
 
 template <int FMT, int D, int BS>
@@ -1172,7 +847,7 @@ int launch_d(const Sel& P, int head_dim, int block_size, const SelectedPlan& pla
                         : launch_bs<FMT, 128>(P, block_size, plan, s);
 }
 
-int stream_ctas(int kv_dtype, int d) {
+int resident_ctas(int kv_dtype, int d) {
   switch (kv_dtype) {
     case PA_KV_BF16: return d == 64 ? Cfg<PA_KV_BF16, 64, 16>::CTAS : Cfg<PA_KV_BF16, 128, 16>::CTAS;
     case PA_KV_FP8_E4M3:
@@ -1180,8 +855,6 @@ int stream_ctas(int kv_dtype, int d) {
     default: return d == 64 ? Cfg<PA_KV_FP4_E2M1, 64, 16>::CTAS : Cfg<PA_KV_FP4_E2M1, 128, 16>::CTAS;
   }
 }
-
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -1192,25 +865,19 @@ SelectedPlan selected_plan(const pa_decode_params* p, int num_selected, int num_
   r.cap = int(p->max_context_len < table ? p->max_context_len : table);
   const int64_t lists = int64_t(p->num_seqs) * r.cols.n_groups * p->num_kv_heads;
   const int64_t steps = selected_steps(p, num_selected);  // of a list, at most
-  const int sms = num_sms > 0 ? num_sms : 152;
-  const int resident = stream_ctas(p->kv_dtype, p->head_dim);
-  // Where one wave of CTAs takes all lists: clusters, with two steps a warp at least.
+  // CTAs a list: as many as are resident at once if it is few lists, with two steps a warp
+  // at least; lists beyond that are worked off as CTAs end, whole (512 lists of 128 blocks in
+  // bf16, 304 CTAs resident: 82.9 us whole, 90.4 in halves).
+  const int64_t slots =
+      int64_t(num_sms > 0 ? num_sms : 152) * resident_ctas(p->kv_dtype, p->head_dim);
   r.split = 1;
-  while (r.split < MAX_SPLIT && lists * r.split * 2 <= int64_t(sms) * resident &&
-         steps >= 4 * NWARPS * r.split)
+  while (r.split < MAX_SPLIT && lists * r.split * 2 <= slots && steps >= 4 * NWARPS * r.split)
     r.split *= 2;
-  if (lists * r.split <= int64_t(sms) * resident && steps <= 8 * NWARPS * r.split) return r;
-  r.grid = sms * resident;
-  r.part_cols = r.cols.q_group * (p->num_q_heads / p->num_kv_heads);
-  const size_t rows = size_t(2) * r.grid * NWARPS * r.part_cols;
-  r.ml = kWorkspaceHeaderBytes + round256((size_t(p->num_seqs) * r.cols.n_groups + 1) * 4);
-  r.acc = r.ml + round256(rows * 8);
-  r.total = r.acc + round256(rows * p->head_dim * 4);
   return r;
 }
 
 int launch_decode_selected(const pa_decode_params* p, const int32_t* selected, int num_selected,
-                           const SelectedPlan& plan, unsigned char* ws, void* stream) {
+                           const SelectedPlan& plan, void* stream) {
   Sel P;
   P.q = static_cast<const __nv_bfloat16*>(p->q);
   P.out = static_cast<__nv_bfloat16*>(p->out);
@@ -1232,10 +899,6 @@ int launch_decode_selected(const pa_decode_params* p, const int32_t* selected, i
   P.q_group = plan.cols.q_group;
   P.n_groups = plan.cols.n_groups;
   P.num_virtual = p->num_seqs * plan.cols.n_groups;
-  P.plan = plan.grid ? reinterpret_cast<int32_t*>(ws + kWorkspaceHeaderBytes) : nullptr;
-  P.part_ml = plan.grid ? reinterpret_cast<float*>(ws + plan.ml) : nullptr;
-  P.part_acc = plan.grid ? reinterpret_cast<float*>(ws + plan.acc) : nullptr;
-  P.part_cols = plan.part_cols;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (p->kv_dtype) {
     case PA_KV_BF16: return launch_d<PA_KV_BF16>(P, p->head_dim, p->block_size, plan, s);
