@@ -913,27 +913,31 @@ def pa_update_tables(block_tables, old_lens, new_lens, free_ring, ring_state, ne
     [B + 1]) get the new tokens, packed, -1 behind; ``new_ring_state`` (int32 [4]) the
     ring's state: head, count, and 0 where the step was done (see the C header)."""
     dev = _current()
-    B = old_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or old_lens.shape != (B,) \
-            or new_lens.shape != (B,):
+    tables, lens, ring = block_tables.shape, old_lens.shape, free_ring.shape
+    if len(tables) != 2 or lens != tables[:1] or new_lens.shape != lens:
         raise ValueError("block_tables must be [num_seqs][max_blocks], the lengths [num_seqs]")
-    if free_ring.dim() != 1 or ring_state.shape != (4,) or new_ring_state.shape != (4,):
+    if len(ring) != 1 or ring_state.shape != (4,) or new_ring_state.shape != (4,):
         raise ValueError("free_ring must be [ring_size], the states [4]")
-    rows = slot_mapping if slot_mapping is not None else positions
-    T = 0 if rows is None else rows.shape[0]
-    if (slot_mapping is not None and slot_mapping.shape != (T,)) \
-            or (positions is not None and positions.shape != (T,)) \
-            or (token_starts is not None and token_starts.shape != (B + 1,)):
+    B = lens[0]
+    slots = pos = starts = None
+    T = 0
+    if slot_mapping is not None:
+        slots, rows = _ptr(slot_mapping, _i64, "slot_mapping", dev), slot_mapping.shape
+        T = rows[0] if len(rows) == 1 else -1
+    if positions is not None:
+        pos, rows = _ptr(positions, _i32, "positions", dev), positions.shape
+        T = rows[0] if len(rows) == 1 and (slots is None or rows[0] == T) else -1
+    if token_starts is not None:
+        starts = _ptr(token_starts, _i32, "token_starts", dev)
+        T = T if token_starts.shape == (B + 1,) else -1
+    if T < 0:
         raise ValueError("slot_mapping and positions must be [max_new_tokens], token_starts "
                          "[num_seqs + 1]")
     p = UpdateTablesParams(
         _ptr(block_tables, _i32, "block_tables", dev), _ptr(old_lens, _i32, "old_lens", dev),
         _ptr(new_lens, _i32, "new_lens", dev), _ptr(free_ring, _i32, "free_ring", dev),
         _ptr(ring_state, _i32, "ring_state", dev), _ptr(new_ring_state, _i32, "new_ring_state", dev),
-        None if slot_mapping is None else _ptr(slot_mapping, _i64, "slot_mapping", dev),
-        None if positions is None else _ptr(positions, _i32, "positions", dev),
-        None if token_starts is None else _ptr(token_starts, _i32, "token_starts", dev),
-        block_tables.shape[1], B, int(block_size), int(num_blocks), free_ring.shape[0], T)
+        slots, pos, starts, tables[1], B, int(block_size), int(num_blocks), ring[0], T)
     _check(load().pa_update_tables(ctypes.byref(p), _stream_handle(stream)), "pa_update_tables")
 
 
