@@ -851,3 +851,69 @@ def test_two_streams_at_once(pk):
     for pair in outs:
         for got, (_, (want, W, A, V), _) in zip(pair, sets):
             close(got.double().cpu().numpy()[:, None], want, W, A, V, "bf16", 90 * 16)
+
+
+@pytest.mark.gpu
+def test_decode_block_listed_twice_counts_twice(pk):
+    lens = [90]
+    tables, NB, poison = layout(lens, 16, 6)
+    c = Cache("bf16", NB, 1, 16, 128, 6, poison)
+    q = workloads.bf16_normal((1, 4, 128), 6)
+    sel = np.array([[[5, 2, 5, 5, 0, 2]]], np.int32)
+    want, W, A, V = plain_attend(c, q.double().numpy()[:, None], tables, lens, sel, 128 ** -0.5)
+    got = pk.pa_decode_selected(q.cuda(), c.k.cuda(), c.v.cuda(), dev(tables),
+                                dev(np.array(lens, np.int32)), 90, dev(sel))
+    close(got.double().cpu().numpy()[:, None], want, W, A, V, "bf16", 96)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS)
+def test_decode_many_new_tokens(pk, fmt):
+    """1,024 of them, a column group each at eight query heads a KV head."""
+    import torch
+
+    L, Q, G = 1100, 1024, 8
+    tables, NB, poison = layout([L], 32, 4)
+    c = Cache(fmt, NB, 1, 32, 64, 4, poison)
+    q = workloads.bf16_normal((1, Q, G, 64), 4)
+    sel = np.arange(35, dtype=np.int32)[None, None].copy()
+    sel[0, 0, 3:9] = -1
+    got = pk.pa_decode_selected(q.cuda(), c.k.cuda(), c.v.cuda(), dev(tables),
+                                dev(np.array([L], np.int32)), L, dev(sel), **c.scales())
+    got = got.double().cpu().numpy()
+    some = [0, 1, 19, 20, 211, 212, 700, 1023]
+    for i in some:  # token i as the only new one of a shorter sequence
+        n = L - Q + i + 1
+        want, W, A, V = plain_attend(c, q.double().numpy()[:, i:i + 1], tables, [n], sel, 0.125)
+        close(got[:, i:i + 1], want, W, A, V, fmt, L)
+    assert torch.isfinite(torch.from_numpy(got)).all() and pk.pa_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_most_sequences(pk):
+    """65,535 sequences that read one block."""
+    import torch
+
+    B, BS, D = 65535, 8, 64
+    c = Cache("bf16", 2, 1, BS, D, 1, poison=[(1, o) for o in range(5, 8)])
+    q = workloads.bf16_normal((B, 1, D), 2).cuda()
+    tables = torch.ones(B, 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), 5, dtype=torch.int32, device="cuda")
+    bounds = torch.zeros(pk.block_bounds_shape(2, 1, D), dtype=torch.bfloat16, device="cuda")
+    pk.pa_block_bounds(c.k.cuda(), bounds, tables, lens, 5)
+    x = c.k_codes[1, 0, :5]
+    assert np.array_equal(bounds[1, 0].double().cpu().numpy(), np.stack([x.min(0), x.max(0)]))
+    scores = pk.pa_block_scores(q, bounds, tables, lens, 5, BS)
+    qd = q.double().cpu().numpy()
+    want, mag = plain_scores(qd[-3:, None], bounds.double().cpu().numpy(), None,
+                             np.ones((3, 1), np.int32), [5] * 3, BS, D ** -0.5)
+    assert all(abs(scores[B - 3 + i[0], 0, 0].item() - s) <= 2.0 ** -17 * mag[i]
+               for i, s in want.items())
+    sel = pk.pa_block_select(scores, lens, BS, 3, 1, 1)
+    assert (sel == torch.tensor([0, -1, -1], dtype=torch.int32, device="cuda")).all()
+    out = pk.pa_decode_selected(q, c.k.cuda(), c.v.cuda(), tables, lens, 5, sel)
+    for b in (0, 1, 40000, B - 1):
+        want, W, A, V = plain_attend(c, qd[b:b + 1, None], np.ones((1, 1), np.int32), [5],
+                                     np.zeros((1, 1, 1), np.int32), D ** -0.5)
+        close(out[b:b + 1].double().cpu().numpy()[:, None], want, W, A, V, "bf16", 8)
+    assert torch.isfinite(out).all() and pk.pa_device_errors() == 0
