@@ -442,14 +442,17 @@ struct State {
       for (int j = 0; j < 4; ++j) s[h][j] = s2[0][j] + s2[1][j];
     }
     // ---- softmax; keys that a column does not see are -inf
+    if (edge)
+#pragma unroll
+      for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (position(pos, h, g + (j >> 1) * 8) >= q.see[j & 1]) s[h][j] = -INFINITY;
     bool over = false;
 #pragma unroll
     for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (position(pos, h, g + (j >> 1) * 8) >= q.see[j & 1]) s[h][j] = -INFINITY;
-        over |= s[h][j] > limit[j & 1];
-      }
+      for (int j = 0; j < 4; ++j) over |= s[h][j] > limit[j & 1];
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
