@@ -685,7 +685,8 @@ pa_status pa_update_tables(const pa_update_tables_params* p, pa_stream_t stream)
  *   bounds  bf16 [num_blocks][num_kv_heads][2][head_dim]: least, largest; for the 8-bit
  *           and 4-bit caches of code (* group scale), the head's scale left out. Exact
  *           for every cache type. A NaN among the keys makes both NaN.
- * Bounds of other blocks are left as they were. Two sequences that share a block write
+ * Bounds of other blocks are left as they were (max_blocks_per_seq * num_kv_heads below
+ * 2^31). Two sequences that share a block write
  * the same bounds if both hold all of its tokens. max_new_tokens is a host-known upper
  * bound of context_lens[b] - old_lens[b]; blocks beyond those that so many tokens can
  * touch are not done, and set PA_DEVERR_CONTEXT_LEN, as a length past the table row does.
@@ -762,15 +763,15 @@ pa_status pa_block_select(const float* scores, const int32_t* context_lens, int3
  * listed tokens (or whose every score is -infinity) gets a row of zeros.
  * p is as in pa_decode: all caches, several new tokens (causal among them); the columns
  * of a KV head's products are G heads of 8 / G new tokens, more of those read the blocks
- * again. num_seqs * ceil(query_len / (8 / G)) * num_kv_heads below 2^27, table rows of up
- * to 2^30 tokens (else PA_ERR_UNSUPPORTED). One kernel whatever `variant` says;
+ * again. num_seqs * ceil(query_len / (8 / G)) * num_kv_heads below 2^27 (else
+ * PA_ERR_UNSUPPORTED), num_blocks * num_kv_heads below 2^31, table rows of up to 2^30
+ * tokens. One kernel whatever `variant` says;
  * partition_tokens, overlap_prologue and wait_timeout_us are checked like those of
  * pa_decode and not used.
  * Softmax weights: two bf16 terms (2^-17 of a weight is lost) with the bf16 cache; f16
  * with the others, as in the 4-bit decode.
- * Workspace: pa_decode_selected_workspace_size bytes, 256-byte aligned, contents on entry
- * do not matter, not shared by two calls in flight; may be NULL where the size is 0 (it
- * is 0 for params that are invalid, and where the kernel needs none). */
+ * The kernel needs no workspace: pa_decode_selected_workspace_size is 0, and `workspace`,
+ * there as in pa_decode, may be NULL and is not looked at. */
 size_t pa_decode_selected_workspace_size(const pa_decode_params* p, int32_t num_selected);
 pa_status pa_decode_selected(const pa_decode_params* p, const int32_t* selected,
                              int32_t num_selected, void* workspace, size_t workspace_bytes,

@@ -9,8 +9,8 @@
 // a tile is one (block, KV head), 4 KB of a bf16 cache at block size 16 and head_dim
 // 128, anywhere in the pool.
 //  * The query rows of a KV head (G heads of up to 8 / G new tokens) are the 8 columns
-//    of m16n8k16 products: S^T = K Q^T, O^T += V^T P^T, a warp taking 16 keys a step.
-//    Its lanes copy the keys' K and V rows into the warp's own ring with 16-byte
+//    of m16n8k16 products: S^T = K Q^T, O^T += V^T P^T, a warp taking 16 keys a step (of
+//    codes 32). Its lanes copy the keys' K and V rows into the warp's own ring with 16-byte
 //    asynchronous copies, which may go to any place of a stage, so 16-byte chunks are
 //    permuted where the fragments' reads would meet in a bank. No CTA-wide barrier
 //    until the end.
@@ -26,6 +26,20 @@
 //  * Keys that a column must not see (behind the sequence, or behind one of several new
 //    tokens) have weight 0; where V holds no number there, 0 times it would still be
 //    none: in the steps that hold such keys, such elements of V are taken out first.
+//
+// Measured (GB300, in a graph; the floor is the bytes at the copy rate of 6.68 TB/s): 64
+// contexts of 8 to 32 k, 128 blocks of 16 each, bf16, 32 / 8 heads 81.9 us (floor 80.6; the
+// whole decode 769; the tensor-core decode over a table per KV head, its making left out,
+// 95.0); 32 of 32 to 128 k, 256 blocks, 8-bit, 64 / 8 heads 46.6 us (40.4: a start of some 3
+// us, and the ends of 256 lists on 152 SMs); one sequence, two new tokens, 64 blocks, 4-bit,
+// d 64 4.7 us (a chain of list, table, copies, products and the cluster's two barriers).
+// 456 lists of 256 blocks in 4 bits 50.5 us (40.5): 600 instructions a step of 32 keys.
+// Tried: the lists of all sequences as a stream over persistent warps with a merge of what
+// was cut (89.0, 53.8 us for the first two); 2 and 8 warps a CTA (84.2, 89.0); twice the
+// ring or two thirds of it (no faster, or slower: codes with two stages and a third more
+// CTAs 52.8 for 47.1); steps of 16 keys for the codes (4-bit: a third more time a key); a
+// form of the step of its own for steps without unseen keys (twice the code: 1.5 us more
+// for 8-bit, from instruction fetches).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -23,6 +23,9 @@
 // What bounds it: latency. A step of 64 sequences moves under 2 KB; the kernel is a
 // chain of the lengths' load, a scan, a search and the dependent loads of a table or
 // ring entry. One launch; a second one to hold the sums would cost as much again.
+// Measured (GB300, in a graph): a decode step of 64 sequences 3.4 us; 256 sequences, of
+// which a quarter end and a quarter begin with prompts of up to 4 k tokens (116 k slots
+// and positions, 1.5 MB), 4.4 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -917,3 +917,21 @@ def test_most_sequences(pk):
                                      np.zeros((1, 1, 1), np.int32), D ** -0.5)
         close(out[b:b + 1].double().cpu().numpy()[:, None], want, W, A, V, "bf16", 8)
     assert torch.isfinite(out).all() and pk.pa_device_errors() == 0
+
+
+@pytest.mark.parametrize("source", ["pa_tables.cu", "pa_blocks.cu", "pa_decode_selected.cu"])
+def test_kernels_do_not_spill(source, tmp_path):
+    """Launch bounds were chosen so that ptxas keeps every kernel in registers."""
+    import os
+    import re
+    import subprocess
+
+    from paged_kv_cache_92_gb300 import build
+
+    got = subprocess.run([build._nvcc(), *build.ARCH, "-O3", "-std=c++17", f"-I{build.INCLUDE}",
+                          "-lineinfo", "-Xptxas", "-v", "-cubin", "-o", str(tmp_path / "k.cubin"),
+                          os.path.join(build.CSRC, source)], capture_output=True, text=True,
+                         check=True)
+    lines = re.findall(r"function '(\w+)'.*?(\d+) bytes spill stores, (\d+) bytes spill loads",
+                       got.stderr, flags=re.S)
+    assert lines and [x for x in lines if x[1:] != ("0", "0")] == []
