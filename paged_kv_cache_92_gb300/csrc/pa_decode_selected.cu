@@ -13,7 +13,9 @@
 //    codes 32). Its lanes copy the keys' K and V rows into the warp's own ring with 16-byte
 //    asynchronous copies, which may go to any place of a stage, so 16-byte chunks are
 //    permuted where the fragments' reads would meet in a bank. No CTA-wide barrier
-//    until the end.
+//    until the end. (Warp-level products: with 8 columns they take 10 to 25 % of the matrix
+//    unit, and their operands come converted from registers; products from tensor memory
+//    would want 128 rows of keys a tile, more than a list's short end has.)
 //  * bf16: fragments by ldmatrix, V's transposed. P is split into two bf16 terms (2^-17
 //    of it is lost); with up to four query rows the second terms are columns 4 to 7 of
 //    the same product (their queries are those of columns 0 to 3), so they cost none.
@@ -658,7 +660,7 @@ __device__ __forceinline__ void copy_block(const Sel& P, unsigned char* st, int 
   }
 }
 
-// Lengths that are too long or too short, flagged by the first CTA.
+// Lengths that are too long or too short, flagged by the CTAs in turn.
 __device__ __forceinline__ void report_lengths(const Sel& P) {
   for (int b = blockIdx.x * NTHREADS + threadIdx.x; b < P.num_virtual / P.n_groups;
        b += gridDim.x * NTHREADS) {
