@@ -1061,7 +1061,7 @@ pa_status pa_block_bounds(const pa_block_bounds_params* p, pa_stream_t stream) {
   if (!pa::aligned16(p->k_cache) || !pa::aligned16(p->bounds) || misaligned4(p->block_tables) ||
       misaligned4(p->context_lens) || misaligned4(p->old_lens))
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_bounds: misaligned pointer");
-  const int e = pa::launch_block_bounds(p, stream);
+  const int e = pa::launch_block_bounds(p, pa::tc_grid(), stream);
   if (e != 0) return pa::set_cuda_error("pa_block_bounds: launch", e);
   return PA_OK;
 }

@@ -23,10 +23,10 @@
 //
 // Measured (GB300, in a graph; the floor is the bytes at the copy rate of 6.68 TB/s):
 //  * bounds, 8 KV heads, d 128: the last blocks of 64 sequences 1.8 us; 16 prompts of 8 to
-//    32 k tokens, bf16, 106.5 us (floor 106.9); 32 contexts of 4 to 16 k, 4-bit, block size
-//    32, 58.2 us (35.8): the ALU is 73 % busy, with a conversion, a minimum and a maximum
-//    a pair of codes. Tried for the codes: 16-byte chunks (66 us with eight warps a CTA),
-//    the next tile's loads ahead of this one's work (64.7).
+//    32 k tokens, bf16, 102.5 us (floor 106.9: a copy writes as much as it reads); 32
+//    contexts of 4 to 16 k, 4-bit, block size 32, 49.5 us (35.8): the ALU, with a conversion,
+//    a minimum and a maximum a pair of codes. Tried: several tiles' loads in flight (103.8
+//    and 52.9), the next tile's ahead of this one's work (115 and 64.7).
 //  * scores: 64 contexts of 8 to 32 k, block size 16, 32 / 8 heads 53.9 us (52.1); two of
 //    64 to 128 k with four new tokens, 64 / 8 heads 14.5 us (9.2): a warp's chain of length,
 //    table, rows twice over, and 1.7 waves of CTAs. Query rows of several tiles loaded from
@@ -52,10 +52,7 @@ __device__ unsigned int g_blocks_errors;
 
 // ---------------------------------------------------------------- bounds
 
-// Warps of a CTA (64 sequences' prompts in bf16, 32 in 4 bits, d 128: with 8 106.8 and
-// 73.7 us, with 4 108.9 and 58.4, with 2 133.6 and 67.3).
-template <int FMT>
-constexpr int bound_warps = FMT == PA_KV_BF16 ? 8 : 4;
+constexpr int BOUND_WARPS = 4;
 
 struct Bounds {
   const unsigned char* k_cache;
@@ -91,8 +88,7 @@ __device__ __forceinline__ uint32_t bf16_of_f16(uint32_t x) {
 // 4-bit codes 8 (a group of 16 elements): those are bound by the ALU, and the fewer
 // elements a lane has of more rows, the fewer have to meet between lanes.
 template <int FMT, int D, int BS>
-__global__ void __launch_bounds__(bound_warps<FMT> * 32) block_bounds_kernel(const Bounds P) {
-  constexpr int WARPS = bound_warps<FMT>;
+__global__ void __launch_bounds__(BOUND_WARPS * 32) block_bounds_kernel(const Bounds P) {
   constexpr int ROWB = FMT == PA_KV_BF16 ? 2 * D : (FMT == PA_KV_FP8_E4M3 ? D : D / 2);
   constexpr int SCALES = FMT == PA_KV_FP4_E2M1 ? D / 16 : 0;
   constexpr int TILE = BS * (ROWB + SCALES);
@@ -110,7 +106,7 @@ __global__ void __launch_bounds__(bound_warps<FMT> * 32) block_bounds_kernel(con
     atomicOr(&g_blocks_errors, PA_DEVERR_CONTEXT_LEN);
   const int n = min(last - first, P.per_seq);
   const uint32_t heads = uint32_t(P.num_kv_heads), units = uint32_t(max(n, 0)) * heads;
-  for (uint32_t u = blockIdx.x * WARPS + warp; u < units; u += gridDim.x * WARPS) {
+  for (uint32_t u = blockIdx.x * BOUND_WARPS + warp; u < units; u += gridDim.x * BOUND_WARPS) {
     const int k = int(u / heads), head = int(u - k * heads);
     const int j = first + k;
     const int e = P.block_tables[int64_t(b) * P.max_blocks_per_seq + j];
@@ -590,23 +586,35 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
   }
 }
 
-template <int FMT, int D>
-int launch_bounds_bs(const Bounds& P, int block_size, int num_seqs, cudaStream_t s) {
-  constexpr int WARPS = bound_warps<FMT>, threads = WARPS * 32;
-  int64_t x = (int64_t(P.per_seq) * P.num_kv_heads + WARPS - 1) / WARPS;
+template <int FMT, int D, int BS>
+int launch_bounds_t(const Bounds& P, int num_seqs, int num_sms, cudaStream_t s) {
+  constexpr int TILE = BS * (FMT == PA_KV_BF16 ? 2 * D : (FMT == PA_KV_FP8_E4M3 ? D : D * 9 / 16));
+  // Tiles a warp, one after the other: 16 KB of them, of 4-bit codes 8 (the GPU starts about
+  // a CTA a nanosecond: with a tile a warp 106.5 for 102.5 us, 58.2 for 49.5 in 4 bits, and
+  // blocks of 8 tokens in 4 bits 129 for 72), fewer where that leaves fewer than 32 warps an
+  // SM.
+  constexpr int BYTES = FMT == PA_KV_FP4_E2M1 ? 8192 : 16384;
+  const int64_t units = int64_t(P.per_seq) * P.num_kv_heads;
+  int64_t run = units * num_seqs / (int64_t(num_sms > 0 ? num_sms : 152) * 32);
+  run = run < 1 ? 1 : (run > BYTES / TILE ? (BYTES + TILE - 1) / TILE : run);
+  int64_t x = (units + BOUND_WARPS * run - 1) / (BOUND_WARPS * run);
   if (x > 65535) x = 65535;  // (warps go on by the grid's width)
   const dim3 grid{unsigned(x), unsigned(num_seqs)};
+  return launch_ordered(block_bounds_kernel<FMT, D, BS>, grid, BOUND_WARPS * 32, 0, s, 1, P);
+}
+template <int FMT, int D>
+int launch_bounds_bs(const Bounds& P, int block_size, int num_seqs, int num_sms, cudaStream_t s) {
   switch (block_size) {
-    case 8: return launch_ordered(block_bounds_kernel<FMT, D, 8>, grid, threads, 0, s, 1, P);
-    case 16: return launch_ordered(block_bounds_kernel<FMT, D, 16>, grid, threads, 0, s, 1, P);
-    case 32: return launch_ordered(block_bounds_kernel<FMT, D, 32>, grid, threads, 0, s, 1, P);
+    case 8: return launch_bounds_t<FMT, D, 8>(P, num_seqs, num_sms, s);
+    case 16: return launch_bounds_t<FMT, D, 16>(P, num_seqs, num_sms, s);
+    case 32: return launch_bounds_t<FMT, D, 32>(P, num_seqs, num_sms, s);
     default: return int(cudaErrorInvalidValue);
   }
 }
 template <int FMT>
-int launch_bounds_d(const Bounds& P, const pa_block_bounds_params* p, cudaStream_t s) {
-  return p->head_dim == 64 ? launch_bounds_bs<FMT, 64>(P, p->block_size, p->num_seqs, s)
-                           : launch_bounds_bs<FMT, 128>(P, p->block_size, p->num_seqs, s);
+int launch_bounds_d(const Bounds& P, const pa_block_bounds_params* p, int num_sms, cudaStream_t s) {
+  return p->head_dim == 64 ? launch_bounds_bs<FMT, 64>(P, p->block_size, p->num_seqs, num_sms, s)
+                           : launch_bounds_bs<FMT, 128>(P, p->block_size, p->num_seqs, num_sms, s);
 }
 
 template <int D, bool ONE>
@@ -626,7 +634,7 @@ int launch_scores_t(Scores P, int64_t tiles, int num_seqs, int num_sms, cudaStre
 
 }  // namespace
 
-int launch_block_bounds(const pa_block_bounds_params* p, void* stream) {
+int launch_block_bounds(const pa_block_bounds_params* p, int num_sms, void* stream) {
   Bounds P;
   P.k_cache = static_cast<const unsigned char*>(p->k_cache);
   P.bounds = static_cast<__nv_bfloat16*>(p->bounds);
@@ -641,9 +649,9 @@ int launch_block_bounds(const pa_block_bounds_params* p, void* stream) {
   P.per_seq = int(touched < p->max_blocks_per_seq ? touched : p->max_blocks_per_seq);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (p->kv_dtype) {
-    case PA_KV_BF16: return launch_bounds_d<PA_KV_BF16>(P, p, s);
-    case PA_KV_FP8_E4M3: return launch_bounds_d<PA_KV_FP8_E4M3>(P, p, s);
-    default: return launch_bounds_d<PA_KV_FP4_E2M1>(P, p, s);
+    case PA_KV_BF16: return launch_bounds_d<PA_KV_BF16>(P, p, num_sms, s);
+    case PA_KV_FP8_E4M3: return launch_bounds_d<PA_KV_FP8_E4M3>(P, p, num_sms, s);
+    default: return launch_bounds_d<PA_KV_FP4_E2M1>(P, p, num_sms, s);
   }
 }
 

@@ -12,7 +12,7 @@ int launch_update_tables(const pa_update_tables_params* p, int num_sms, void* st
 int read_and_clear_tables_errors(uint32_t* flags);
 
 // Bounds, scores and choice of blocks (pa_blocks.cu)
-int launch_block_bounds(const pa_block_bounds_params* p, void* stream);
+int launch_block_bounds(const pa_block_bounds_params* p, int num_sms, void* stream);
 int launch_block_scores(const pa_block_scores_params* p, int num_sms, void* stream);
 int launch_block_select(const float* scores, const int32_t* context_lens, int32_t* selected,
                         int32_t num_seqs, int32_t num_kv_heads, int32_t scores_stride,
