@@ -24,9 +24,9 @@
 // Measured (GB300, in a graph; the floor is the bytes at the copy rate of 6.68 TB/s):
 //  * bounds, 8 KV heads, d 128: the last blocks of 64 sequences 1.8 us; 16 prompts of 8 to
 //    32 k tokens, bf16, 102.5 us (floor 106.9: a copy writes as much as it reads); 32
-//    contexts of 4 to 16 k, 4-bit, block size 32, 49.5 us (35.8): the ALU is 83 % busy, with a
-//    conversion, a minimum and a maximum a pair of codes. Tried: several tiles' loads in flight (103.8
-//    and 52.9), the next tile's ahead of this one's work (115 and 64.7).
+//    contexts of 4 to 16 k, 4-bit, block size 32, 49.5 us (35.8): the ALU is 83 % busy, with
+//    a conversion, a minimum and a maximum a pair of codes. Tried: several tiles' loads in
+//    flight (103.8 and 52.9), the next tile's ahead of this one's work (115 and 64.7).
 //  * scores: 64 contexts of 8 to 32 k, block size 16, 32 / 8 heads 53.9 us (52.1); two of
 //    64 to 128 k with four new tokens, 64 / 8 heads 14.5 us (9.2): a warp's chain of length,
 //    table, rows twice over, and 1.7 waves of CTAs. Query rows of several tiles loaded from
