@@ -17,9 +17,11 @@
 //    of a KV head. fp32 sums of exact products. Bound by the bytes of the bounds.
 //  * block_select_kernel: one CTA per (sequence, KV head) with the row's scores as
 //    ordered 32-bit keys in registers; the key of the budget's rank is found by histograms
-//    in shared memory, the first over the range that the keys span, the next over the bin
-//    that holds it, until a bin is kept whole (for scores that differ, two). Ties go to the
-//    lowest index through ranks. Bound by latency.
+//    in shared memory, the first over the range that the scores span, in bins of equal
+//    widths, the next over the bin that holds it, until that has 32 keys or fewer, which
+//    are ranked one against the other (mostly after one histogram). Ties go to the lowest
+//    index through ranks. Bound by latency: straight code without branches a key, since an
+//    instruction runs once a warp.
 //
 // Measured (GB300, in a graph; the floor is the bytes at the copy rate of 6.68 TB/s):
 //  * bounds, 8 KV heads, d 128: the last blocks of 64 sequences 1.8 us; 16 prompts of 8 to
@@ -31,10 +33,11 @@
 //    64 to 128 k with four new tokens, 64 / 8 heads 14.5 us (9.2): a warp's chain of length,
 //    table, rows twice over, and 1.7 waves of CTAs. Query rows of several tiles loaded from
 //    memory for every 16 blocks: 23.2.
-//  * choice: 512 rows of up to 2,048 blocks, 128 kept 8.6 us (4.4 from a CTA's start to its
-//    end: length 0.8, scores 0.6, two histograms 1.8, ranks 0.7), 32 rows of up to 16,384,
-//    512 kept 9.0 us. Bit by bit instead: 10.9 and 18.8; a warp's equal bins counted at once
-//    10.7 for the latter (equal scores cost a third more without).
+//  * choice: 512 rows of up to 2,048 blocks, 128 kept 5.7 us (8.9 k cycles a CTA: length
+//    1.6, scores 1.7, a histogram 1.4, its scan 1.1, the last bin 1.5, lists 1.1), 32 rows of
+//    up to 16,384, 512 kept 8.6 us. Histograms over the keys' bits only: 8.6 and 9.0; bit by
+//    bit: 10.9 and 18.8; a warp's equal bins counted at once: 10.7 for the latter (equal
+//    scores cost a third more without).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -393,7 +396,7 @@ struct Choose {
   const int32_t* context_lens;
   int32_t* selected;
   int64_t scores_stride;
-  int num_kv_heads, bs_log2, budget, sink, recent;
+  int bs_log2, budget, sink, recent;
 };
 
 // Order-preserving map of a score to an unsigned key; NaN below everything, both
@@ -402,6 +405,20 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x + 0.0f);  // -0 + 0 = +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// The score of a key that is no NaN's.
+__device__ __forceinline__ float key_score(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// A count in shared memory, without a branch.
+__device__ __forceinline__ void count_if(int* at, bool here) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p red.shared.add.u32 [%0], 1;\n}\n" ::"r"(
+          uint32_t(__cvta_generic_to_shared(at))),
+      "r"(uint32_t(here))
+      : "memory");
 }
 
 constexpr int LOG_BINS = 10, BINS = 1 << LOG_BINS;
@@ -414,22 +431,24 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
   __shared__ int hist[BINS];
   __shared__ int counts[2][WARPS];
   __shared__ uint32_t ends[2][WARPS];
-  __shared__ int found[3];  // a bin, how many of its keys are kept, whether all are
+  __shared__ int found[3];  // a bin, how many of its keys are kept, how many it has
+  __shared__ uint32_t few[32];
+  __shared__ int n_few;
   dev::griddep_enter();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x, b = row / P.num_kv_heads;
-  const int BS = 1 << P.bs_log2;
+  const int L = max(P.context_lens[blockIdx.y], 0), BS = 1 << P.bs_log2;
+  const int64_t row = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
 #pragma unroll
   for (int k = 0; k < OWN; ++k) hist[tid + k * THREADS] = 0;
-  const float* scores = P.scores + int64_t(row) * P.scores_stride;
-  const int L = max(P.context_lens[b], 0);
+  if (tid == 0) n_few = 0;
+  const float* scores = P.scores + row * P.scores_stride;
   int64_t blocks = (int64_t(L) + BS - 1) >> P.bs_log2;
   if (blocks > P.scores_stride) {
     if (tid == 0) atomicOr(&g_blocks_errors, PA_DEVERR_CONTEXT_LEN);
     blocks = P.scores_stride;
   }
   const int n = int(blocks), n_keep = min(n, P.budget);
-  int32_t* out = P.selected + int64_t(row) * P.budget;
+  int32_t* out = P.selected + row * P.budget;
   for (int j = n_keep + tid; j < P.budget; j += THREADS) out[j] = -1;
   if (n <= P.budget) {
     for (int j = tid; j < n; j += THREADS) out[j] = j;
@@ -446,52 +465,89 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
   const int mine0 = c0 + warp * runs * 32 + lane;
   auto index = [&](int s, int e) { return mine0 + s * span + e * 32; };
   uint32_t key[E];
+  int there;                // of the keys, the first so many are
   auto load = [&](int s) {  // all on their way together
+    there = min(runs, (c1 - index(s, 0) + 31) >> 5);
     float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int j = index(s, e);
       x[e] = 0.0f;
-      if (e < runs && j < c1) x[e] = scores[j];
+      if (e < there) x[e] = scores[index(s, e)];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) key[e] = score_key(x[e]);
   };
-  // the least and the largest key
-  uint32_t least = 0xffffffffu, most = 0u;
-  for (int s = 0; s < spans; ++s) {
-    load(s);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (e < runs && index(s, e) < c1) {
-        most = max(most, key[e]);
-        least = min(least, key[e]);
-      }
-  }
-  least = __reduce_min_sync(0xffffffffu, least);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) {
-    ends[0][warp] = least;
-    ends[1][warp] = most;
-  }
-  __syncthreads();
-  least = __reduce_min_sync(0xffffffffu, lane < WARPS ? ends[0][lane] : 0xffffffffu);
-  most = __reduce_max_sync(0xffffffffu, lane < WARPS ? ends[1][lane] : 0u);
-  // The key of rank `need`: the range [least, most] in up to BINS bins, then the bin that
-  // holds it, until a bin is kept whole or is one key. `left`: how many of the range's keys
-  // are kept.
-  uint32_t threshold = least, width = most - least;
-  int left = need;
-  bool whole = false;
-  while (width > 0) {
-    const int shift = max(0, 32 - __clz(width) - LOG_BINS);
-    for (int s = 0; s < spans; ++s) {
-      if (spans > 1) load(s);
+  // The key of rank `need`: the range of the keys in up to BINS bins, then that of the keys
+  // in the bin that holds it, until a bin is kept whole, is one key, or has no more than 32
+  // keys, which every warp ranks for itself. The bins are first of equal widths in score,
+  // where the ends are finite, then in key, which ends after four. `left`: how many of the
+  // range's keys are kept.
+  uint32_t threshold = 0, width = 0xffffffffu;
+  int left = need, shift = 0, bin = 0;
+  float low = 0.0f, scale = 0.0f;
+  bool whole = false, linear = false;
+  int slot[E];  // the keys' bins, -1 of one outside the range
+  auto place = [&]() {
+    if (linear) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (e >= runs) break;
+        if (e % 4 == 0 && e >= runs) break;
+        const int k = min(int((key_score(key[e]) - low) * scale), BINS - 1);
+        slot[e] = e < there ? k : -1;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (e % 4 == 0 && e >= runs) break;
         const uint32_t x = key[e] - threshold;
-        if (index(s, e) < c1 && x <= width) atomicAdd(&hist[x >> shift], 1);
+        slot[e] = e < there && x <= width ? int(x >> shift) : -1;
+      }
+    }
+  };
+  auto members = [&]() {  // which of the keys are in the bin, a bit each
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (e % 4 == 0 && e >= runs) break;
+      m |= (slot[e] == bin ? 1u : 0u) << e;
+    }
+    return m;
+  };
+  for (int level = 0; level < 6; ++level) {  // (an end even for scores that change meanwhile)
+    uint32_t least = 0xffffffffu, most = 0u;
+    for (int s = 0; s < spans; ++s) {
+      if (level == 0 || spans > 1) load(s);
+      if (level > 0 && spans > 1) place();
+      const uint32_t m = level == 0 ? ~(~0u << max(there, 0)) : members();
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (e % 4 == 0 && e >= runs) break;
+        most = max(most, m >> e & 1u ? key[e] : 0u);
+        least = min(least, m >> e & 1u ? key[e] : 0xffffffffu);
+      }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      ends[0][warp] = least;
+      ends[1][warp] = most;
+    }
+    __syncthreads();
+    threshold = __reduce_min_sync(0xffffffffu, lane < WARPS ? ends[0][lane] : 0xffffffffu);
+    width = __reduce_max_sync(0xffffffffu, lane < WARPS ? ends[1][lane] : 0u) - threshold;
+    if (whole || width == 0) break;
+    shift = max(0, 32 - __clz(width) - LOG_BINS);
+    low = key_score(threshold);
+    scale = __fdividef(float(BINS - 1), key_score(threshold + width) - low);
+    // (of a NaN or an infinity among the ends the scale is no number or zero)
+    linear = level == 0 && scale > 0.0f && scale < INFINITY;
+    for (int s = 0; s < spans; ++s) {
+      if (spans > 1) load(s);
+      place();
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (e % 4 == 0 && e >= runs) break;
+        count_if(&hist[max(slot[e], 0)], slot[e] >= 0);
       }
     }
     __syncthreads();
@@ -518,7 +574,7 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
         if (above < left && left <= above + mine[k]) {
           found[0] = BINS - 1 - (tid * OWN + k);
           found[1] = left - above;
-          found[2] = left - above == mine[k];
+          found[2] = mine[k];
         }
         above += mine[k];
       }
@@ -526,10 +582,35 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
 #pragma unroll
     for (int k = 0; k < OWN; ++k) hist[BINS - 1 - (tid * OWN + k)] = 0;
     __syncthreads();
-    threshold += uint32_t(found[0]) << shift;
+    bin = found[0];
     left = found[1];
-    whole = found[2];
-    width = whole ? 0 : (1u << shift) - 1u;
+    const int held = found[2];
+    whole = left == held;
+    if (held > 32) continue;
+    for (int s = 0; s < spans; ++s) {
+      if (spans > 1) {
+        load(s);
+        place();
+      }
+      const uint32_t m = members();
+      if (m == 0) continue;
+      const int at = atomicAdd(&n_few, __popc(m));
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (m >> e & 1u) few[(at + __popc(m & ((1u << e) - 1u))) & 31] = key[e];
+    }
+    __syncthreads();
+    const uint32_t x = few[min(lane, held - 1)];
+    int larger = 0, as_large = 0;
+    for (int i = 0; i < held; ++i) {
+      larger += few[i] > x;
+      as_large += few[i] >= x;
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, larger < left && left <= as_large)) - 1;
+    threshold = __shfl_sync(0xffffffffu, x, at);
+    whole = left == __shfl_sync(0xffffffffu, as_large, at);
+    left -= __shfl_sync(0xffffffffu, larger, at);
+    break;
   }
   // kept: keys above the threshold (from it on, where its bin is kept whole), and the first
   // `left` of those that equal it
@@ -551,25 +632,25 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
     if (whole) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (e >= runs) break;
-        kept[e] = __ballot_sync(0xffffffffu, index(s, e) < c1 && key[e] >= threshold);
+        if (e % 4 == 0 && e >= runs) break;
+        kept[e] = __ballot_sync(0xffffffffu, e < there && key[e] >= threshold);
         n_kept += __popc(kept[e]);
       }
     } else {
       int n_equal = 0;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (e >= runs) break;
-        n_equal += __popc(__ballot_sync(0xffffffffu, index(s, e) < c1 && key[e] == threshold));
+        if (e % 4 == 0 && e >= runs) break;
+        n_equal += __popc(__ballot_sync(0xffffffffu, e < there && key[e] == threshold));
       }
       int at = equal_base + prefix(n_equal, all_equal);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (e >= runs) break;
-        const bool in = index(s, e) < c1, same = in && key[e] == threshold;
+        if (e % 4 == 0 && e >= runs) break;
+        const bool same = e < there && key[e] == threshold;
         const uint32_t equal = __ballot_sync(0xffffffffu, same);
         const bool tie = same && at + __popc(equal & below) < left;
-        kept[e] = __ballot_sync(0xffffffffu, tie || (in && key[e] > threshold));
+        kept[e] = __ballot_sync(0xffffffffu, tie || (e < there && key[e] > threshold));
         at += __popc(equal);
         n_kept += __popc(kept[e]);
       }
@@ -577,7 +658,7 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
     int at = keep_base + prefix(n_kept, all_kept);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      if (e >= runs) break;
+      if (e % 4 == 0 && e >= runs) break;
       if (kept[e] >> lane & 1u) out[at + __popc(kept[e] & below)] = index(s, e);
       at += __popc(kept[e]);
     }
@@ -691,12 +772,11 @@ int launch_block_select(const float* scores, const int32_t* context_lens, int32_
   P.context_lens = context_lens;
   P.selected = selected;
   P.scores_stride = scores_stride;
-  P.num_kv_heads = num_kv_heads;
   P.bs_log2 = log2_of(block_size);
   P.budget = budget;
   P.sink = sink;
   P.recent = recent;
-  const dim3 grid(unsigned(num_seqs) * unsigned(num_kv_heads));
+  const dim3 grid{unsigned(num_kv_heads), unsigned(num_seqs)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // a row in registers where it fits; longer ones are read again for every range
   if (scores_stride <= 2048)

@@ -558,6 +558,43 @@ def test_select_of_long_rows(pk, stride, n, kind):
         assert np.array_equal(got.cpu().numpy(), plain_select(x, lens, 8, budget, sink, recent))
 
 
+def _spread(rng, B, H, n, kind):
+    """Scores that no one width of bin suits."""
+    x = rng.standard_normal((B, H, n)).astype(np.float32)
+    if kind == "outlier":  # all but one in a bin of equal widths
+        x[..., n // 3] = 1e30
+    elif kind == "outliers":
+        x[..., n // 3], x[..., n // 2] = 1e30, -1e30
+    elif kind == "exponents":
+        x = np.ldexp(np.sign(x), rng.integers(-149, 128, x.shape)).astype(np.float32)
+    elif kind == "subnormal":
+        x = (x * 1e-42).astype(np.float32)
+    elif kind == "ends":  # a difference that overflows
+        x[..., n // 3], x[..., n // 2] = 3.4e38, -3.4e38
+    elif kind == "halves":  # a difference near the largest number
+        x[..., n // 3], x[..., n // 2] = 1.5e38, -1.5e38
+    elif kind == "clusters":  # runs of 31 to 34 neighbours in the last place, far apart
+        at = np.cumsum(rng.integers(31, 35, n))
+        which = np.searchsorted(at, np.arange(n), side="right")
+        step = np.arange(n) - np.concatenate([[0], at])[which]
+        base = (which + 1).astype(np.float32)
+        x = np.broadcast_to((base.view(np.int32) + step.astype(np.int32)).view(np.float32), x.shape)
+        x = rng.permuted(x, axis=-1)
+    return np.ascontiguousarray(x, np.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["outlier", "outliers", "exponents", "subnormal", "ends", "halves",
+                                  "clusters"])
+@pytest.mark.parametrize("n", [70, 1027, 2048, 4095, 8000, 16384, 20001])
+def test_select_of_scores_of_all_sizes(pk, kind, n):
+    x = _spread(np.random.default_rng(n), 2, 3, n, kind)
+    lens = [16 * n, 16 * (n - 1) - 5]
+    for budget, sink, recent in ((1, 0, 0), (33, 1, 1), (64, 0, 4), (n // 2, 1, 0), (n - 1, 0, 0)):
+        got = pk.pa_block_select(dev(x), dev(np.array(lens, np.int32)), 16, budget, sink, recent)
+        assert np.array_equal(got.cpu().numpy(), plain_select(x, lens, 16, budget, sink, recent))
+
+
 @pytest.mark.gpu
 def test_select_of_a_row_that_is_too_short(pk):
     x = np.arange(20, dtype=np.float32).reshape(1, 2, 10)
