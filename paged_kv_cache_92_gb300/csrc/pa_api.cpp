@@ -1130,7 +1130,8 @@ pa_status pa_block_select(const float* scores, const int32_t* context_lens, int3
   if (misaligned4(scores) || misaligned4(context_lens) || misaligned4(selected))
     return pa::set_error(PA_ERR_INVALID_ARG, "pa_block_select: misaligned pointer");
   const int e = pa::launch_block_select(scores, context_lens, selected, num_seqs, num_kv_heads,
-                                        scores_stride, block_size, budget, sink, recent, stream);
+                                        scores_stride, block_size, budget, sink, recent,
+                                        pa::tc_grid(), stream);
   if (e != 0) return pa::set_cuda_error("pa_block_select: launch", e);
   return PA_OK;
 }

@@ -15,13 +15,13 @@
 //    A the bounds (16 blocks a tile, read from memory straight into fragments: the
 //    order of a contraction is free, so a lane takes 16-byte runs), B the query rows
 //    of a KV head. fp32 sums of exact products. Bound by the bytes of the bounds.
-//  * block_select_kernel: one CTA per (sequence, KV head) with the row's scores as
-//    ordered 32-bit keys in registers; the key of the budget's rank is found by histograms
-//    in shared memory, the first over the range that the scores span, in bins of equal
-//    widths, the next over the bin that holds it, until that has 32 keys or fewer, which
-//    are ranked one against the other (mostly after one histogram). Ties go to the lowest
-//    index through ranks. Bound by latency: straight code without branches a key, since an
-//    instruction runs once a warp.
+//  * block_select_kernel: one CTA per (sequence, KV head), or a cluster of four for few long
+//    rows, with the row's scores as ordered 32-bit keys in registers; the key of the budget's
+//    rank is found by histograms in shared memory, the first over the range that the scores
+//    span, in bins of equal widths, the next over the bin that holds it, until that has 32
+//    keys or fewer, which are ranked one against the other (mostly after one histogram). Ties
+//    go to the lowest index through ranks. Bound by latency: straight code without branches a
+//    key, since an instruction runs once a warp.
 //
 // Measured (GB300, in a graph; the floor is the bytes at the copy rate of 6.68 TB/s):
 //  * bounds, 8 KV heads, d 128: the last blocks of 64 sequences 1.8 us; 16 prompts of 8 to
@@ -33,11 +33,13 @@
 //    64 to 128 k with four new tokens, 64 / 8 heads 14.5 us (9.2): a warp's chain of length,
 //    table, rows twice over, and 1.7 waves of CTAs. Query rows of several tiles loaded from
 //    memory for every 16 blocks: 23.2.
-//  * choice: 512 rows of up to 2,048 blocks, 128 kept 5.7 us (8.9 k cycles a CTA: length
-//    1.6, scores 1.7, a histogram 1.4, its scan 1.1, the last bin 1.5, lists 1.1), 32 rows of
-//    up to 16,384, 512 kept 8.6 us. Histograms over the keys' bits only: 8.6 and 9.0; bit by
-//    bit: 10.9 and 18.8; a warp's equal bins counted at once: 10.7 for the latter (equal
-//    scores cost a third more without).
+//  * choice: 512 rows of up to 2,048 blocks, 128 kept 5.4 us (length, scores, the histogram,
+//    its scan, the last bin and the lists take 1,100 to 1,700 cycles each), 32 rows of up to
+//    16,384, 512 kept 6.5 us. Histograms over the keys' bits only: 8.6 and 9.0; bit by bit:
+//    10.9 and 18.8; a warp's equal bins counted at once: 10.7 for the latter (equal scores
+//    cost a third more without). The next kernel's CTAs come with this one's end: dispatched
+//    at the start they take the room unevenly (7.0 for 5.4).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -50,6 +52,8 @@
 
 namespace pa {
 namespace {
+
+namespace cg = cooperative_groups;
 
 __device__ unsigned int g_blocks_errors;
 
@@ -423,44 +427,68 @@ __device__ __forceinline__ void count_if(int* at, bool here) {
 
 constexpr int LOG_BINS = 10, BINS = 1 << LOG_BINS;
 
-// One CTA per (sequence, KV head). Of a span a warp holds `runs` runs of 32 candidates, no
-// more than the span needs, key e of a lane in the e-th of them.
-template <int WARPS, int E>
-__global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P) {
-  constexpr int THREADS = WARPS * 32, OWN = BINS / THREADS;
-  __shared__ int hist[BINS];
+// A cluster of C CTAs per (sequence, KV head). Of a span a warp holds `runs` runs of 32
+// candidates, no more than the span needs, key e of a lane in the e-th of them. What a warp
+// or a CTA finds is written to all CTAs, or read from all; the rest they do alike.
+template <int W, int E, int C>
+__global__ void __launch_bounds__(W * 32) block_select_kernel(const Choose P) {
+  constexpr int THREADS = W * 32, WARPS = W * C, OWN = BINS / THREADS;
+  static_assert(WARPS <= 32 && (C == 1 || OWN == 4));
+  constexpr bool PAIRS = W * E >= 512;  // two bins a register: there are 64 a thread
+  __shared__ __align__(16) int hist[C > 1 ? 2 : 1][BINS];
   __shared__ int counts[2][WARPS];
   __shared__ uint32_t ends[2][WARPS];
   __shared__ int found[3];  // a bin, how many of its keys are kept, how many it has
   __shared__ uint32_t few[32];
   __shared__ int n_few;
-  dev::griddep_enter();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int32_t* list;  // (64 registers a thread do not hold it as well)
+  dev::griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31;
   const int L = max(P.context_lens[blockIdx.y], 0), BS = 1 << P.bs_log2;
-  const int64_t row = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  const int row = int(blockIdx.y * (gridDim.x / C) + blockIdx.x / C);
+  const int first = int(blockIdx.x % C) * THREADS + tid, warp = first >> 5;  // in the cluster
+  cg::cluster_group cluster = cg::this_cluster();
+  auto sync_row = [&]() {
+    if constexpr (C > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
+  // x to *at of every CTA, by the first lanes of a warp
+  auto put = [&](auto* at, auto x) {
+    if constexpr (C > 1) {
+      if (lane < C) *cluster.map_shared_rank(at, unsigned(lane)) = x;
+    } else {
+      if (lane == 0) *at = x;
+    }
+  };
 #pragma unroll
-  for (int k = 0; k < OWN; ++k) hist[tid + k * THREADS] = 0;
-  if (tid == 0) n_few = 0;
-  const float* scores = P.scores + row * P.scores_stride;
+  for (int k = 0; k < (C > 1 ? 2 : 1) * OWN; ++k) hist[k / OWN][tid + k % OWN * THREADS] = 0;
+  const float* scores = P.scores + int64_t(row) * P.scores_stride;
   int64_t blocks = (int64_t(L) + BS - 1) >> P.bs_log2;
   if (blocks > P.scores_stride) {
-    if (tid == 0) atomicOr(&g_blocks_errors, PA_DEVERR_CONTEXT_LEN);
+    if (first == 0) atomicOr(&g_blocks_errors, PA_DEVERR_CONTEXT_LEN);
     blocks = P.scores_stride;
   }
   const int n = int(blocks), n_keep = min(n, P.budget);
-  int32_t* out = P.selected + row * P.budget;
-  for (int j = n_keep + tid; j < P.budget; j += THREADS) out[j] = -1;
+  int32_t* out = P.selected + int64_t(row) * P.budget;
+  if (tid == 0) {
+    n_few = 0;
+    list = out;
+  }
+  for (int j = n_keep + first; j < P.budget; j += WARPS * 32) out[j] = -1;
   if (n <= P.budget) {
-    for (int j = tid; j < n; j += THREADS) out[j] = j;
+    for (int j = first; j < n; j += WARPS * 32) out[j] = j;
     return;
   }
   const int c0 = P.sink, c1 = n - P.recent;         // the candidates
   const int need = P.budget - P.sink - P.recent;    // of them, fewer than there are
-  for (int j = tid; j < P.sink; j += THREADS) out[j] = j;
-  for (int j = tid; j < P.recent; j += THREADS) out[P.sink + need + j] = c1 + j;
+  for (int j = first; j < P.sink; j += WARPS * 32) out[j] = j;
+  for (int j = first; j < P.recent; j += WARPS * 32) out[P.sink + need + j] = c1 + j;
   if (need == 0) return;
+  if constexpr (C > 1) cluster.barrier_arrive();
 
-  const int runs = min(E, (c1 - c0 + THREADS - 1) / THREADS), span = runs * THREADS;
+  const int runs = min(E, (c1 - c0 + WARPS * 32 - 1) / (WARPS * 32)), span = runs * WARPS * 32;
   const int spans = (c1 - c0 + span - 1) / span;
   const int mine0 = c0 + warp * runs * 32 + lane;
   auto index = [&](int s, int e) { return mine0 + s * span + e * 32; };
@@ -483,24 +511,39 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
   // where the ends are finite, then in key, which ends after four. `left`: how many of the
   // range's keys are kept.
   uint32_t threshold = 0, width = 0xffffffffu;
-  int left = need, shift = 0, bin = 0;
-  float low = 0.0f, scale = 0.0f;
-  bool whole = false, linear = false;
-  int slot[E];  // the keys' bins, -1 of one outside the range
+  uint32_t bin = 0;
+  int left = need, shift = 0;
+  float scale = 0.0f;  // of bins in score, or zero
+  bool whole = false;
+  constexpr uint32_t NONE = 0xffffu;
+  uint32_t slots[PAIRS ? E / 2 : E];  // the keys' bins, NONE of one outside the range
+  auto set_slot = [&](int e, uint32_t x) {
+    if constexpr (PAIRS)
+      slots[e / 2] = e % 2 ? slots[e / 2] | x << 16 : x;
+    else
+      slots[e] = x;
+  };
+  auto slot = [&](int e) -> uint32_t {
+    if constexpr (PAIRS)
+      return e % 2 ? slots[e / 2] >> 16 : slots[e / 2] & 0xffffu;
+    else
+      return slots[e];
+  };
   auto place = [&]() {
-    if (linear) {
+    if (scale > 0.0f) {
+      const float low = key_score(threshold);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (e % 4 == 0 && e >= runs) break;
         const int k = min(int((key_score(key[e]) - low) * scale), BINS - 1);
-        slot[e] = e < there ? k : -1;
+        set_slot(e, e < there ? uint32_t(k) : NONE);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (e % 4 == 0 && e >= runs) break;
         const uint32_t x = key[e] - threshold;
-        slot[e] = e < there && x <= width ? int(x >> shift) : -1;
+        set_slot(e, e < there && x <= width ? x >> shift : NONE);
       }
     }
   };
@@ -509,7 +552,7 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       if (e % 4 == 0 && e >= runs) break;
-      m |= (slot[e] == bin ? 1u : 0u) << e;
+      m |= (slot(e) == bin ? 1u : 0u) << e;
     }
     return m;
   };
@@ -528,45 +571,64 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
     }
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) {
-      ends[0][warp] = least;
-      ends[1][warp] = most;
+    if constexpr (C > 1) {  // (all of the cluster's CTAs run, and have cleared)
+      if (level == 0) cluster.barrier_wait();
     }
-    __syncthreads();
+    put(&ends[0][warp], least);
+    put(&ends[1][warp], most);
+    sync_row();
     threshold = __reduce_min_sync(0xffffffffu, lane < WARPS ? ends[0][lane] : 0xffffffffu);
     width = __reduce_max_sync(0xffffffffu, lane < WARPS ? ends[1][lane] : 0u) - threshold;
     if (whole || width == 0) break;
     shift = max(0, 32 - __clz(width) - LOG_BINS);
-    low = key_score(threshold);
-    scale = __fdividef(float(BINS - 1), key_score(threshold + width) - low);
-    // (of a NaN or an infinity among the ends the scale is no number or zero)
-    linear = level == 0 && scale > 0.0f && scale < INFINITY;
+    scale = __fdividef(float(BINS - 1), key_score(threshold + width) - key_score(threshold));
+    // (of a NaN or an infinity among the ends it is no number or zero)
+    if (level > 0 || !(scale < INFINITY)) scale = 0.0f;
+    int* bins = hist[C > 1 ? level & 1 : 0];
+    if constexpr (C > 1) {  // (what the other one held has been read)
+      if (level > 0)
+        reinterpret_cast<int4*>(hist[~level & 1])[tid] = make_int4(0, 0, 0, 0);
+    }
     for (int s = 0; s < spans; ++s) {
       if (spans > 1) load(s);
       place();
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (e % 4 == 0 && e >= runs) break;
-        count_if(&hist[max(slot[e], 0)], slot[e] >= 0);
+        count_if(&bins[slot(e) & (BINS - 1)], slot(e) != NONE);
       }
     }
-    __syncthreads();
+    sync_row();
     // bins from the top, OWN a thread: where the count reaches `left`
     int mine[OWN], sum = 0;
+    if constexpr (C > 1) {
+      const int4* at = reinterpret_cast<int4*>(bins) + THREADS - 1 - tid;
+      int4 x[C];
 #pragma unroll
-    for (int k = 0; k < OWN; ++k) {
-      mine[k] = hist[BINS - 1 - (tid * OWN + k)];
-      sum += mine[k];
+      for (int c = 0; c < C; ++c) x[c] = *cluster.map_shared_rank(at, unsigned(c));
+      mine[0] = mine[1] = mine[2] = mine[3] = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        mine[0] += x[c].w, mine[1] += x[c].z, mine[2] += x[c].y, mine[3] += x[c].x;
+    } else {
+#pragma unroll
+      for (int k = 0; k < OWN; ++k) {
+        int& at = bins[BINS - 1 - (tid * OWN + k)];
+        mine[k] = at;
+        at = 0;
+      }
     }
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) sum += mine[k];
     int upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
-    if (lane == 31) counts[0][warp] = upto;
+    if (lane == 31) counts[0][tid >> 5] = upto;
     __syncthreads();
-    upto += __reduce_add_sync(0xffffffffu, lane < warp ? counts[0][lane] : 0);
+    upto += __reduce_add_sync(0xffffffffu, lane < tid >> 5 ? counts[0][lane] : 0);
     int above = upto - sum;
     if (above < left && left <= upto) {
 #pragma unroll
@@ -579,10 +641,8 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
         above += mine[k];
       }
     }
-#pragma unroll
-    for (int k = 0; k < OWN; ++k) hist[BINS - 1 - (tid * OWN + k)] = 0;
     __syncthreads();
-    bin = found[0];
+    bin = uint32_t(found[0]);
     left = found[1];
     const int held = found[2];
     whole = left == held;
@@ -594,12 +654,24 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
       }
       const uint32_t m = members();
       if (m == 0) continue;
-      const int at = atomicAdd(&n_few, __popc(m));
+      if constexpr (C > 1) {
+        const int at = atomicAdd(cluster.map_shared_rank(&n_few, 0), __popc(m));
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (m >> e & 1u) few[(at + __popc(m & ((1u << e) - 1u))) & 31] = key[e];
+        for (int e = 0; e < E; ++e) {
+          if (m >> e & 1u) {
+            uint32_t* to = &few[(at + __popc(m & ((1u << e) - 1u))) & 31];
+#pragma unroll
+            for (int c = 0; c < C; ++c) *cluster.map_shared_rank(to, unsigned(c)) = key[e];
+          }
+        }
+      } else {
+        const int at = atomicAdd(&n_few, __popc(m));
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (m >> e & 1u) few[(at + __popc(m & ((1u << e) - 1u))) & 31] = key[e];
+      }
     }
-    __syncthreads();
+    sync_row();
     const uint32_t x = few[min(lane, held - 1)];
     int larger = 0, as_large = 0;
     for (int i = 0; i < held; ++i) {
@@ -618,8 +690,8 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
   const uint32_t below = (1u << lane) - 1u;
   // exclusive prefix over the warps; `all` is the total
   auto prefix = [&](int x, int& all) {
-    if (lane == 0) counts[turn][warp] = x;
-    __syncthreads();
+    put(&counts[turn][warp], x);
+    sync_row();
     const int y = lane < WARPS ? counts[turn][lane] : 0;
     all = __reduce_add_sync(0xffffffffu, y);
     turn ^= 1;
@@ -656,10 +728,11 @@ __global__ void __launch_bounds__(WARPS * 32) block_select_kernel(const Choose P
       }
     }
     int at = keep_base + prefix(n_kept, all_kept);
+    int32_t* to = list;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       if (e % 4 == 0 && e >= runs) break;
-      if (kept[e] >> lane & 1u) out[at + __popc(kept[e] & below)] = index(s, e);
+      if (kept[e] >> lane & 1u) to[at + __popc(kept[e] & below)] = index(s, e);
       at += __popc(kept[e]);
     }
     equal_base += all_equal;
@@ -766,7 +839,7 @@ int launch_block_scores(const pa_block_scores_params* p, int num_sms, void* stre
 int launch_block_select(const float* scores, const int32_t* context_lens, int32_t* selected,
                         int32_t num_seqs, int32_t num_kv_heads, int32_t scores_stride,
                         int32_t block_size, int32_t budget, int32_t sink, int32_t recent,
-                        void* stream) {
+                        int num_sms, void* stream) {
   Choose P;
   P.scores = scores;
   P.context_lens = context_lens;
@@ -776,16 +849,21 @@ int launch_block_select(const float* scores, const int32_t* context_lens, int32_
   P.budget = budget;
   P.sink = sink;
   P.recent = recent;
-  const dim3 grid{unsigned(num_kv_heads), unsigned(num_seqs)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // a row in registers where it fits; longer ones are read again for every range
-  if (scores_stride <= 2048)
-    return launch_ordered(block_select_kernel<8, 8>, grid, 8 * 32, 0, s, 1, P);
-  if (scores_stride <= 4096)
-    return launch_ordered(block_select_kernel<8, 16>, grid, 8 * 32, 0, s, 1, P);
-  if (scores_stride <= 8192)
-    return launch_ordered(block_select_kernel<16, 16>, grid, 16 * 32, 0, s, 1, P);
-  return launch_ordered(block_select_kernel<32, 16>, grid, 32 * 32, 0, s, 1, P);
+  auto launch = [&](auto kernel, unsigned warps, unsigned ctas) {
+    const dim3 grid{unsigned(num_kv_heads) * ctas, unsigned(num_seqs)};
+    return launch_ordered(kernel, grid, warps * 32, 0, s, ctas, P);
+  };
+  // A row in registers where it fits; longer ones are read again for every range. A cluster
+  // pays where a CTA a row leaves half of the SMs idle: up to 16,384 blocks 6.8 for 8.9 us at
+  // 8 rows, 8.3 for 9.0 at 72, but 10.3 for 9.2 at 80; of two CTAs, up to 8,192 blocks, it does
+  // not (6.4 for 5.8).
+  if (scores_stride <= 2048) return launch(block_select_kernel<8, 8, 1>, 8, 1);
+  if (scores_stride <= 4096) return launch(block_select_kernel<8, 16, 1>, 8, 1);
+  if (scores_stride <= 8192) return launch(block_select_kernel<16, 16, 1>, 16, 1);
+  if (int64_t(num_seqs) * num_kv_heads * 2 <= (num_sms > 0 ? num_sms : 152))
+    return launch(block_select_kernel<8, 16, 4>, 8, 4);
+  return launch(block_select_kernel<32, 16, 1>, 32, 1);
 }
 
 int read_and_clear_blocks_errors(uint32_t* flags) {

@@ -17,7 +17,7 @@ int launch_block_scores(const pa_block_scores_params* p, int num_sms, void* stre
 int launch_block_select(const float* scores, const int32_t* context_lens, int32_t* selected,
                         int32_t num_seqs, int32_t num_kv_heads, int32_t scores_stride,
                         int32_t block_size, int32_t budget, int32_t sink, int32_t recent,
-                        void* stream);
+                        int num_sms, void* stream);
 int read_and_clear_blocks_errors(uint32_t* flags);
 
 // Attention over selected blocks (pa_decode_selected.cu): the query rows of a KV head
