@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(score_warps<ONE> * 32, 16 / score_warps<ONE>)
     block_scores_kernel(const Scores P) {
   constexpr int WARPS = score_warps<ONE>;
   using Row = dev::KeyRow<PA_KV_BF16, D>;
-  dev::griddep_enter();
+  dev::griddep_wait();
   extern __shared__ __align__(16) uint4 sm_q[];  // [tile][part][D / 32][32 lanes]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;

@@ -35,6 +35,9 @@
 // 95.0); 32 of 32 to 128 k, 256 blocks, 8-bit, 64 / 8 heads 46.6 us (40.4: a start of some 3
 // us, and the ends of 256 lists on 152 SMs); one sequence, two new tokens, 64 blocks, 4-bit,
 // d 64 4.7 us (a chain of list, table, copies, products and the cluster's two barriers).
+// The next kernel is not dispatched ahead of the end: scores, choice and attention layer
+// after layer take 145 us, the sum of the three, for 161 with CTAs of the next scores waiting
+// beside the attention's last (alone, a kernel is as fast either way).
 // 456 lists of 256 blocks in 4 bits 50.5 us (40.5): 600 instructions a step of 32 keys.
 // Tried: the lists of all sequences as a stream over persistent warps with a merge of what
 // was cut (89.0, 53.8 us for the first two); 2 and 8 warps a CTA (84.2, 89.0); twice the
@@ -675,7 +678,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<FMT, D, BS>::CTAS)
     decode_selected_kernel(const Sel P) {
   using C = Cfg<FMT, D, BS>;
   constexpr int ST = C::ST;
-  dev::griddep_enter();
+  dev::griddep_wait();  // (the next kernel's CTAs come as these end: see above)
   cg::cluster_group cluster = cg::this_cluster();
   const int split = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
