@@ -1030,10 +1030,10 @@ def pa_block_select(scores, context_lens, block_size: int, budget: int, sink: in
 
 
 def _selected_shape(q, k_cache, selected) -> int:
-    if selected.dim() != 3 or selected.shape[0] != q.shape[0] \
-            or selected.shape[1] != k_cache.shape[1]:
+    shape = selected.shape
+    if len(shape) != 3 or shape[0] != q.shape[0] or shape[1] != k_cache.shape[1]:
         raise ValueError("selected must be [num_seqs][num_kv_heads][num_selected]")
-    return selected.shape[2]
+    return shape[2]
 
 
 def pa_decode_selected_workspace_size(q, k_cache, v_cache, block_tables, context_lens,
