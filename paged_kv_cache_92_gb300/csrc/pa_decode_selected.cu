@@ -663,13 +663,12 @@ __device__ __forceinline__ void copy_block(const Sel& P, unsigned char* st, int 
   }
 }
 
-// Lengths that are too long or too short, flagged by the CTAs in turn.
-__device__ __forceinline__ void report_lengths(const Sel& P) {
-  for (int b = blockIdx.x * NTHREADS + threadIdx.x; b < P.num_virtual / P.n_groups;
-       b += gridDim.x * NTHREADS) {
-    const int L = P.context_lens[b];
-    if (L > P.cap || (L > 0 && L < P.q_len)) atomicOr(&g_selected_errors, PA_DEVERR_CONTEXT_LEN);
-  }
+// A length that is too long or too short, flagged once: by the first CTA of the sequence's
+// first list. (No index of its own: CTAs times threads passes 32 bits with 2^24 lists.)
+__device__ __forceinline__ void report_length(const Sel& P, const Virtual& v, int head, int rank) {
+  if (threadIdx.x != 0 || rank != 0 || head != 0 || v.first_tok != 0) return;
+  const int L = P.context_lens[v.b];
+  if (L > P.cap || (L > 0 && L < P.q_len)) atomicOr(&g_selected_errors, PA_DEVERR_CONTEXT_LEN);
 }
 
 // One list per cluster: its CTAs take equal stretches and join their results.
@@ -751,7 +750,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<FMT, D, BS>::CTAS)
   }
   dev::cp_async_wait<0>();
   if (errors) atomicOr(&g_selected_errors, errors);
-  report_lengths(P);
+  report_length(P, v, head, rank);
   __syncthreads();  // the rings give way to the merge
 
   // ---- the warps' results, then the CTA's, then the cluster's
