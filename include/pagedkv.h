@@ -685,9 +685,10 @@ pa_status pa_update_tables(const pa_update_tables_params* p, pa_stream_t stream)
  *   bounds  bf16 [num_blocks][num_kv_heads][2][head_dim]: least, largest; for the 8-bit
  *           and 4-bit caches of code (* group scale), the head's scale left out. Exact
  *           for every cache type. A NaN among the keys makes both NaN.
- * Bounds of other blocks are left as they were (max_blocks_per_seq * num_kv_heads below
- * 2^31). Two sequences that share a block write
- * the same bounds if both hold all of its tokens. max_new_tokens is a host-known upper
+ * Bounds of other blocks are left as they were, those of a sequence that gains no token
+ * (old_lens[b] >= context_lens[b]) among them (max_blocks_per_seq * num_kv_heads below
+ * 2^31). Two sequences that share a block and both gain tokens in it write the same bounds
+ * if both hold all of its tokens. max_new_tokens is a host-known upper
  * bound of context_lens[b] - old_lens[b]; blocks beyond those that so many tokens can
  * touch are not done, and set PA_DEVERR_CONTEXT_LEN, as a length past the table row does.
  * After pa_evict_compact or pa_copy_blocks the bounds of the written blocks are stale.

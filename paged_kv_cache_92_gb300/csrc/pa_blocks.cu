@@ -108,11 +108,13 @@ __global__ void __launch_bounds__(BOUND_WARPS * 32) block_bounds_kernel(const Bo
   const int b = blockIdx.y;
   const int L = P.context_lens[b], old = P.old_lens != nullptr ? max(P.old_lens[b], 0) : 0;
   const int cap = P.max_blocks_per_seq * BS;
-  const int first = old / BS, last = (min(L, cap) + BS - 1) / BS;  // the blocks to do
+  const int end = min(L, cap), first = old / BS, last = (end + BS - 1) / BS;  // the blocks to do
   if (blockIdx.x == 0 && threadIdx.x == 0 && (L > cap || last - first > P.per_seq))
     atomicOr(&g_blocks_errors, PA_DEVERR_CONTEXT_LEN);
-  const int n = min(last - first, P.per_seq);
-  const uint32_t heads = uint32_t(P.num_kv_heads), units = uint32_t(max(n, 0)) * heads;
+  // (without a new token none, though `first` may be a block with tokens: another sequence that
+  // shares it may have gained some)
+  const int n = old < end ? min(last - first, P.per_seq) : 0;
+  const uint32_t heads = uint32_t(P.num_kv_heads), units = uint32_t(n) * heads;
   for (uint32_t u = blockIdx.x * BOUND_WARPS + warp; u < units; u += gridDim.x * BOUND_WARPS) {
     const int k = int(u / heads), head = int(u - k * heads);
     const int j = first + k;

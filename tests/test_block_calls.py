@@ -69,3 +69,106 @@ def test_decode_reports_each_sequence(pk, B, Q, G, H):
             lens[b] = n
             pk.pa_decode_selected(q, k, v, tables, lens, 640, sel)
             assert pk.pa_device_errors() == (pk.DEVERR_CONTEXT_LEN if bit else 0), (b, n)
+
+
+# ------------------------------------------------------------------ bounds: whose blocks
+
+
+def token_bounds(codes, bounds, tables, old, lens, BS):
+    """`bounds` (float64) with those of the blocks that hold a token old <= t < lens, over the
+    block's tokens t < lens."""
+    out = bounds.copy()
+    for b, n in enumerate(lens):
+        for j in sorted({t // BS for t in range(max(old[b], 0), n)}):
+            x = codes[tables[b, j], :, :min(BS, n - j * BS)]
+            out[tables[b, j], :, 0], out[tables[b, j], :, 1] = x.min(1), x.max(1)
+    return out
+
+
+def cache_of(fmt, NB, H, BS, D, seed):
+    """A K cache on the host, and its values without the head's scale."""
+    import torch
+
+    import oracle
+
+    rng = np.random.default_rng(seed)
+    if fmt == "bf16":
+        k = torch.from_numpy(rng.standard_normal((NB, H, BS, D)).astype(np.float32)).bfloat16()
+        return k, k.double().numpy()
+    if fmt == "fp8":
+        k = rng.integers(0, 256, (NB, H, BS, D), dtype=np.uint8)
+        k[(k & 0x7F) == 0x7F] = 0
+        return torch.from_numpy(k), oracle.e4m3_to_f64(k)
+    k = rng.integers(0, 256, (NB, H, BS, D * 9 // 16), dtype=np.uint8)
+    f = k.reshape(NB, H, -1)[..., BS * D // 2:]
+    f[:] = rng.integers(0x28, 0x48, f.shape)
+    return torch.from_numpy(k), oracle.fp4_values(k, np.ones(H, np.float32), D)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("D,BS,H", [(64, 8, 3), (128, 16, 8), (64, 32, 1), (128, 32, 2)])
+def test_bounds_of_blocks_with_new_tokens_alone(pk, fmt, D, BS, H):
+    """Sequences that gain tokens, none, or fewer than they had (in the same block, in another):
+    blocks without a new token are left as they were."""
+    import torch
+
+    lens = [0, 1, BS, BS + 1, 7 * BS - 1, 100, 333, 3 * BS + 2, 2 * BS, 50]
+    blocks = [-(-n // BS) + 1 for n in lens]
+    NB = sum(blocks) + 2
+    ids = np.random.default_rng(BS).permutation(NB).astype(np.int32)
+    tables, at = np.full((len(lens), max(blocks)), -1, np.int32), 0
+    for b, n in enumerate(blocks):
+        tables[b, :n], at = ids[at:at + n], at + n
+    k, codes = cache_of(fmt, NB, H, BS, D, 7)
+    olds = {"all new": ([0] * 10, 333), "none new": (list(lens), 1),
+            "some": ([0, 0, BS - 1, BS, 6 * BS, 100, 333, 3 * BS, 2 * BS - 1, 49], BS),
+            "fewer": ([3, 2, BS + 1, BS + 2, 7 * BS, 101, 336, 3 * BS + 4, 2 * BS + 1, 64], 1),
+            "some idle": ([0, 1, BS, BS, 7 * BS - 1, 99, 333, 3 * BS + 1, 2 * BS, 0], 50)}
+    for name, (old, most) in olds.items():
+        start = torch.randn(NB, H, 2, D).bfloat16()
+        got = start.cuda()
+        pk.pa_block_bounds(k.cuda(), got, dev(tables), dev(np.array(lens, np.int32)), most,
+                           old_lens=dev(np.array(old, np.int32)))
+        want = token_bounds(codes, start.double().numpy(), tables, old, lens, BS)
+        assert np.array_equal(got.double().cpu().numpy(), want), name
+        assert pk.pa_device_errors() == 0, name
+
+
+@pytest.mark.gpu
+def test_bounds_of_a_block_that_an_idle_sequence_shares(pk):
+    """300 sequences of 20 tokens that gain none share the second block of one that grew to 32:
+    the block's bounds are the grown one's, whoever comes last."""
+    import torch
+
+    k, codes = cache_of("bf16", 303, 2, 16, 128, 5)
+    B = 301
+    tables = np.stack([np.arange(B), np.full(B, 302)], 1).astype(np.int32)
+    lens, old = np.full(B, 20, np.int32), np.full(B, 20, np.int32)
+    for at in (0, 150, 300):  # the one that grew
+        n = lens.copy()
+        n[at] = 32
+        start = torch.randn(303, 2, 2, 128).bfloat16()
+        want = token_bounds(codes, start.double().numpy(), tables, old, n, 16)
+        for _ in range(5):
+            got = start.cuda()
+            pk.pa_block_bounds(k.cuda(), got, dev(tables), dev(n), 12, old_lens=dev(old))
+            assert np.array_equal(got.double().cpu().numpy(), want)
+    assert pk.pa_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_bounds_still_report_lengths(pk):
+    """A length past the table row is reported, with new tokens and without."""
+    import torch
+
+    k, _ = cache_of("bf16", 4, 1, 16, 64, 5)
+    tables = dev(np.array([[0, 1], [2, 3]], np.int32))
+    for lens, old, most, bit in (([40, 20], [40, 20], 1, True), ([20, 33], [20, 20], 13, True),
+                                 ([2**31 - 1, 1], [2**31 - 1, 1], 1, True),
+                                 ([32, 32], [32, 32], 1, False), ([32, 32], [0, 32], 1, True),
+                                 ([-4, 3], [7, -2], 3, False)):
+        got = torch.zeros(4, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+        pk.pa_block_bounds(k.cuda(), got, tables, dev(np.array(lens, np.int32)), most,
+                           old_lens=dev(np.array(old, np.int32)))
+        assert pk.pa_device_errors() == (pk.DEVERR_CONTEXT_LEN if bit else 0), (lens, old)
