@@ -664,7 +664,8 @@ typedef struct {
   int32_t block_size;          /* 8, 16 or 32 */
   int32_t num_blocks;          /* of the cache */
   int32_t ring_size;           /* at least the blocks that the ring ever holds */
-  int32_t max_new_tokens;      /* rows of slot_mapping and positions; 0 if both are NULL */
+  int32_t max_new_tokens;      /* rows of slot_mapping and positions; 0 if both are NULL (then
+                                  any number of new tokens is taken) */
 } pa_update_tables_params;
 pa_status pa_update_tables(const pa_update_tables_params* p, pa_stream_t stream);
 

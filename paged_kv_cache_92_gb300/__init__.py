@@ -903,6 +903,9 @@ def make_free_ring(blocks, num_blocks: int, device="cuda"):
     return torch.from_numpy(ring).to(device), torch.from_numpy(state).to(device)
 
 
+_NO_ROWS = 256  # stands for the address of an array of no bytes
+
+
 def pa_update_tables(block_tables, old_lens, new_lens, free_ring, ring_state, new_ring_state,
                      num_blocks: int, block_size: int, slot_mapping=None, positions=None,
                      token_starts=None, stream=None) -> None:
@@ -921,11 +924,12 @@ def pa_update_tables(block_tables, old_lens, new_lens, free_ring, ring_state, ne
     B = lens[0]
     slots = pos = starts = None
     T = 0
+    # (torch has no address for a tensor without rows, and NULL would say that it is not wanted)
     if slot_mapping is not None:
-        slots, rows = _ptr(slot_mapping, _i64, "slot_mapping", dev), slot_mapping.shape
+        slots, rows = _ptr(slot_mapping, _i64, "slot_mapping", dev) or _NO_ROWS, slot_mapping.shape
         T = rows[0] if len(rows) == 1 else -1
     if positions is not None:
-        pos, rows = _ptr(positions, _i32, "positions", dev), positions.shape
+        pos, rows = _ptr(positions, _i32, "positions", dev) or _NO_ROWS, positions.shape
         T = rows[0] if len(rows) == 1 and (slots is None or rows[0] == T) else -1
     if token_starts is not None:
         starts = _ptr(token_starts, _i32, "token_starts", dev)

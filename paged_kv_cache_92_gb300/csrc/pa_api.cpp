@@ -981,10 +981,10 @@ pa_status pa_evict_compact(const pa_evict_compact_params* p, pa_stream_t stream)
 
 static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
-// Byte ranges [a, a + na) and [b, b + nb) meet (NULL meets nothing).
+// Byte ranges [a, a + na) and [b, b + nb) meet (NULL and a range of no bytes meet nothing).
 static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
+  return a && b && na && nb && x < y + nb && y < x + na;
 }
 
 pa_status pa_update_tables(const pa_update_tables_params* p, pa_stream_t stream) {

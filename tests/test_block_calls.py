@@ -172,3 +172,61 @@ def test_bounds_still_report_lengths(pk):
         pk.pa_block_bounds(k.cuda(), got, tables, dev(np.array(lens, np.int32)), most,
                            old_lens=dev(np.array(old, np.int32)))
         assert pk.pa_device_errors() == (pk.DEVERR_CONTEXT_LEN if bit else 0), (lens, old)
+
+
+# ------------------------------------------------------------------ tables: outputs without rows
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("slots,positions", [(True, False), (False, True), (True, True)])
+def test_tables_without_rows_for_new_tokens(pk, slots, positions):
+    """An output that is given and has no rows has no room for a new token: the step is refused
+    and changes nothing, as with any other number of rows. A step that gains none is done."""
+    import torch
+
+    def go(old, new):
+        tables = torch.tensor([[3, -1, -1], [1, 2, -1]], dtype=torch.int32, device="cuda")
+        ring, state = pk.make_free_ring([0, 4, 5], 6)
+        out = torch.full((4,), 9, dtype=torch.int32, device="cuda")
+        before = tables.tolist(), ring.tolist()
+        rows = dict(slot_mapping=torch.empty(0, dtype=torch.int64, device="cuda") if slots else None,
+                    positions=torch.empty(0, dtype=torch.int32, device="cuda") if positions else None)
+        pk.pa_update_tables(tables, dev(np.array(old, np.int32)), dev(np.array(new, np.int32)), ring,
+                            state, out, 6, 16, **rows)
+        return out.tolist(), before == (tables.tolist(), ring.tolist()), pk.pa_device_errors()
+
+    assert go([16, 20], [17, 20]) == ([0, 3, -1, 0], True, pk.DEVERR_CONTEXT_LEN)
+    assert go([16, 20], [16, 21]) == ([0, 3, -1, 0], True, pk.DEVERR_CONTEXT_LEN)
+    assert go([16, 20], [16, 20]) == ([0, 3, 0, 0], True, 0)
+    assert go([16, 20], [16, 3]) == ([0, 4, 0, 0], False, 0)
+
+
+@pytest.mark.gpu
+def test_tables_without_rows_or_outputs_grow(pk):
+    """Without slots and positions (None) any number of new tokens is taken."""
+    import torch
+
+    tables = torch.tensor([[3, -1, -1]], dtype=torch.int32, device="cuda")
+    ring, state = pk.make_free_ring([0, 4, 5], 6)
+    out = torch.full((4,), 9, dtype=torch.int32, device="cuda")
+    pk.pa_update_tables(tables, dev(np.array([16], np.int32)), dev(np.array([40], np.int32)), ring,
+                        state, out, 6, 16)
+    assert tables.tolist() == [[3, 0, 4]] and out.tolist() == [2, 1, 0, 0]
+    assert pk.pa_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_tables_arrays_of_no_bytes_overlap_nothing(pk):
+    """No sequences and no rows: arrays of no bytes may point anywhere, into an output too."""
+    import ctypes
+
+    import torch
+
+    ring, state = pk.make_free_ring([0, 4, 5], 6)
+    out = torch.full((4,), 9, dtype=torch.int32, device="cuda")
+    p = pk.UpdateTablesParams(
+        ring.data_ptr(), ring.data_ptr() + 4, ring.data_ptr() + 8, ring.data_ptr(),
+        state.data_ptr(), out.data_ptr(), state.data_ptr() + 8, state.data_ptr() + 4, None, 3, 0, 16,
+        6, 6, 0)
+    assert pk.load().pa_update_tables(ctypes.byref(p), pk._stream_handle(None)) == 0
+    assert out.tolist() == [0, 3, 0, 0] and pk.pa_device_errors() == 0
