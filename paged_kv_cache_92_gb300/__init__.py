@@ -309,7 +309,7 @@ def _current() -> Optional[int]:
 def _ptr(t, dtype, name: str, device: Optional[int]) -> int:
     """``_dev_ptr`` for a call of many tensors: the current device is looked up once."""
     try:
-        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        if t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.get_device() == device:
             return t.data_ptr()
     except AttributeError:
         pass

@@ -230,3 +230,23 @@ def test_tables_arrays_of_no_bytes_overlap_nothing(pk):
         6, 6, 0)
     assert pk.load().pa_update_tables(ctypes.byref(p), pk._stream_handle(None)) == 0
     assert out.tolist() == [0, 3, 0, 0] and pk.pa_device_errors() == 0
+
+
+# ------------------------------------------------------------------ the binding
+
+
+def test_another_kind_of_device_is_refused(pk, monkeypatch):
+    """A tensor of another accelerator whose index is the current CUDA device's."""
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    pk._current()  # (binds torch's calls)
+    monkeypatch.setattr(pk, "_device", lambda: 0)
+    x = torch.zeros(4, dtype=torch.int32).as_subclass(Elsewhere)
+    assert x.get_device() == 0 and x.data_ptr() != 0
+    for call in (lambda: pk._ptr(x, torch.int32, "x", 0), lambda: pk._dev_ptr(x, torch.int32, "x")):
+        with pytest.raises(ValueError, match="x must live on a CUDA device"):
+            call()
