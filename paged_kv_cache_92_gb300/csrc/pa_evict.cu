@@ -574,7 +574,7 @@ int read_and_clear_evict_errors(uint32_t* flags) {
   unsigned int v = 0, zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_evict_errors, sizeof(v));
   if (e != cudaSuccess) return int(e);
-  e = cudaMemcpyToSymbol(g_evict_errors, &zero, sizeof(zero));
+  if (v != 0) e = cudaMemcpyToSymbol(g_evict_errors, &zero, sizeof(zero));
   *flags = v;
   return int(e);
 }

@@ -290,7 +290,7 @@ int read_and_clear_fp8_errors(uint32_t* flags) {
   unsigned int v = 0, zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_errors, sizeof(v));
   if (e != cudaSuccess) return int(e);
-  e = cudaMemcpyToSymbol(g_fp8_errors, &zero, sizeof(zero));
+  if (v != 0) e = cudaMemcpyToSymbol(g_fp8_errors, &zero, sizeof(zero));
   *flags = v;
   return int(e);
 }

@@ -268,7 +268,7 @@ int read_and_clear_tables_errors(uint32_t* flags) {
   unsigned int v = 0, zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_tables_errors, sizeof(v));
   if (e != cudaSuccess) return int(e);
-  e = cudaMemcpyToSymbol(g_tables_errors, &zero, sizeof(zero));
+  if (v != 0) e = cudaMemcpyToSymbol(g_tables_errors, &zero, sizeof(zero));
   *flags = v;
   return int(e);
 }

@@ -250,3 +250,31 @@ def test_another_kind_of_device_is_refused(pk, monkeypatch):
     for call in (lambda: pk._ptr(x, torch.int32, "x", 0), lambda: pk._dev_ptr(x, torch.int32, "x")):
         with pytest.raises(ValueError, match="x must live on a CUDA device"):
             call()
+
+
+@pytest.mark.gpu
+def test_device_errors_of_several_kernels_at_once(pk):
+    """The bits of all kernels since the last call, once; what none has set stays clear."""
+    import torch
+
+    i = lambda *x: dev(np.array(x, np.int32))  # noqa: E731
+    ring, state = pk.make_free_ring([0], 4)
+    k = torch.zeros(4, 1, 8, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    bounds = torch.zeros(pk.block_bounds_shape(4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    calls = [  # more blocks than there are; a table entry; a list past the blocks; a short row
+        (lambda: pk.pa_update_tables(i([-1, -1]), i(0), i(16), ring, state, i(0, 0, 0, 0), 4, 8),
+         pk.DEVERR_POOL),
+        (lambda: pk.pa_block_bounds(k, bounds, i([9, 1]), i(16), 16), pk.DEVERR_TABLE_ENTRY),
+        (lambda: pk.pa_decode_selected(q, k, k, i([0, 1]), i(8), 16, i([[1]])), pk.DEVERR_KEEP),
+        (lambda: pk.pa_block_select(torch.zeros(1, 1, 2, device="cuda"), i(99), 8, 1, 0, 0),
+         pk.DEVERR_CONTEXT_LEN)]
+    torch.cuda.synchronize()
+    assert pk.pa_device_errors() == 0
+    for chosen in range(1 << len(calls)):
+        want = 0
+        for n, (call, bit) in enumerate(calls):
+            if chosen >> n & 1:
+                call()
+                want |= bit
+        assert pk.pa_device_errors() == want and pk.pa_device_errors() == 0
