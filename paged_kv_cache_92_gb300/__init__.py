@@ -1056,7 +1056,7 @@ def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, max_cont
     """Paged decode attention over the blocks listed in ``selected`` (int32
     [B][Hkv][num_selected], logical blocks of the sequence, negative ones skipped) alone;
     returns ``out`` (bf16, the shape of ``q``). Caches of every type, one or several new
-    tokens, as in ``pa_decode``."""
+    tokens, as in ``pa_decode``. No workspace is needed; one that is given is not used."""
     dev = _current()
     lib = load()
     n = _selected_shape(q, k_cache, selected)
@@ -1064,10 +1064,6 @@ def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, max_cont
         out = _empty(stream, q, q.shape, q.dtype)
     p = make_decode_params(q, out, k_cache, v_cache, block_tables, context_lens, max_context_len,
                            scale, k_scale=k_scale, v_scale=v_scale)
-    if workspace is None:
-        need = int(lib.pa_decode_selected_workspace_size(ctypes.byref(p), n))
-        if need > 0:
-            workspace = _empty(stream, q, need, _u8)
     ws_ptr = _ptr(workspace, _u8, "workspace", dev) if workspace is not None else None
     ws_bytes = workspace.numel() if workspace is not None else 0
     _check(lib.pa_decode_selected(ctypes.byref(p), _ptr(selected, _i32, "selected", dev), n,
