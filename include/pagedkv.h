@@ -716,7 +716,8 @@ pa_status pa_block_bounds(const pa_block_bounds_params* p, pa_stream_t stream);
  * first token (the causal rule of pa_decode):
  *   scores[b][g][j] = max over i, h of  sum over d of max(f q_d least_d, f q_d largest_d),
  *   f = scale * k_scale[g], q = q[b][i][h]
- * which no logit of a key in the block exceeds. fp32. The sum is taken as f+ times (q's
+ * In exact arithmetic no logit of a key in the block exceeds it; it is held in fp32, within
+ * 2^-17 times the sum of its terms' magnitudes. The sum is taken as f+ times (q's
  * positive part . largest + q's negative part . least); where that is no number (an
  * infinite or NaN bound), the score is +infinity. Entries from there on are left as they
  * were, and so are the rows of a sequence of length 0 or with fewer keys than new tokens

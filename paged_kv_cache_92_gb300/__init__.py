@@ -978,8 +978,8 @@ def pa_block_bounds(k_cache, bounds, block_tables, context_lens, max_new_tokens:
 
 def pa_block_scores(q, bounds, block_tables, context_lens, max_context_len: int, block_size: int,
                     scores=None, scale: Optional[float] = None, k_scale=None, stream=None):
-    """An upper bound of the score that any key of a block reaches with any new token and
-    query head of a KV head: float32 [B][Hkv][stride], of which the blocks of each
+    """An upper bound (up to fp32 rounding) of the score that any key of a block reaches with
+    any new token and query head of a KV head: float32 [B][Hkv][stride], of which the blocks of each
     sequence are written; returns it. q bf16 [B][Hq][D] or [B][Q][Hq][D]; ``k_scale`` is
     the head scale of the 8-bit and 4-bit caches."""
     dev = _current()

@@ -25,20 +25,23 @@
 //
 // Measured (GB300, in a graph; the floor is the bytes at the copy rate of 6.68 TB/s):
 //  * bounds, 8 KV heads, d 128: the last blocks of 64 sequences 1.8 us; 16 prompts of 8 to
-//    32 k tokens, bf16, 102.5 us (floor 106.9: a copy writes as much as it reads); 32
-//    contexts of 4 to 16 k, 4-bit, block size 32, 49.5 us (35.8): the ALU is 83 % busy, with
+//    32 k tokens, bf16, 102.5 us (floor 106.9: a copy writes as much as it reads), 8-bit 62.3
+//    (59.4); 32 contexts of 4 to 16 k, 4-bit, block size 32, 49.5 us (35.8): the ALU is 83 % busy, with
 //    a conversion, a minimum and a maximum a pair of codes. Tried: several tiles' loads in
 //    flight (103.8 and 52.9), the next tile's ahead of this one's work (115 and 64.7).
 //  * scores: 64 contexts of 8 to 32 k, block size 16, 32 / 8 heads 53.9 us (52.1); two of
 //    64 to 128 k with four new tokens, 64 / 8 heads 14.5 us (9.2): a warp's chain of length,
 //    table, rows twice over, and 1.7 waves of CTAs. Query rows of several tiles loaded from
-//    memory for every 16 blocks: 23.2.
+//    memory for every 16 blocks: 23.2. 32 contexts of 32 to 128 k, 64 / 8 heads: one new token
+//    149 us, four 109.5 (96): the form for one tile of query rows is far from memory there.
 //  * choice: 512 rows of up to 2,048 blocks, 128 kept 5.4 us (length, scores, the histogram,
 //    its scan, the last bin and the lists take 1,100 to 1,700 cycles each), 32 rows of up to
 //    16,384, 512 kept 6.5 us. Histograms over the keys' bits only: 8.6 and 9.0; bit by bit:
 //    10.9 and 18.8; a warp's equal bins counted at once: 10.7 for the latter (equal scores
 //    cost a third more without). The next kernel's CTAs come with this one's end: dispatched
-//    at the start they take the room unevenly (7.0 for 5.4).
+//    at the start they take the room unevenly (7.0 for 5.4). Many long rows are far from their
+//    bytes: of 16,000 blocks, 256 kept, 304 rows 16.2 us (3.0), 512 rows 30.8 (5.0), 1,024 rows
+//    57.5 (10.0): one CTA of 32 warps an SM, whose steps are latencies that nothing overlaps.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -859,7 +862,9 @@ int launch_block_select(const float* scores, const int32_t* context_lens, int32_
   // A row in registers where it fits; longer ones are read again for every range. A cluster
   // pays where a CTA a row leaves half of the SMs idle: up to 16,384 blocks 6.8 for 8.9 us at
   // 8 rows, 8.3 for 9.0 at 72, but 10.3 for 9.2 at 80; of two CTAs, up to 8,192 blocks, it does
-  // not (6.4 for 5.8).
+  // not (6.4 for 5.8). The stride stands for the rows' length, which the host does not know:
+  // rows much shorter than it take a wider form than they need (512 rows of 8,000 blocks in a
+  // stride of 16,384: 22.6 us).
   if (scores_stride <= 2048) return launch(block_select_kernel<8, 8, 1>, 8, 1);
   if (scores_stride <= 4096) return launch(block_select_kernel<8, 16, 1>, 8, 1);
   if (scores_stride <= 8192) return launch(block_select_kernel<16, 16, 1>, 16, 1);

@@ -39,6 +39,10 @@
 // after layer take 145 us, the sum of the three, for 161 with CTAs of the next scores waiting
 // beside the attention's last (alone, a kernel is as fast either way).
 // 456 lists of 256 blocks in 4 bits 50.5 us (40.5): 600 instructions a step of 32 keys.
+// More new tokens than 8 / G are groups of columns, each of which reads and converts the list
+// again (from L2): 32 sequences, four new tokens, 256 blocks, 64 / 8 heads (four groups): bf16
+// 149 us (81), 8-bit 131 (41), 4-bit 116 (23); 128 blocks, 32 / 8 heads (two groups), bf16 51.9
+// (40.5).
 // Tried: the lists of all sequences as a stream over persistent warps with a merge of what
 // was cut (89.0, 53.8 us for the first two); 2 and 8 warps a CTA (84.2, 89.0); twice the
 // ring or two thirds of it (no faster, or slower: codes with two stages and a third more
